@@ -11,13 +11,15 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgdn_gb300.so")
 
-GDN_FP32, GDN_BF16 = 0, 1
+GDN_FP32, GDN_BF16, GDN_FP16 = 0, 1, 2
 GDN_DEV_BAD_SLOT, GDN_DEV_BAD_CU_SEQLENS, GDN_DEV_WAIT_TIMEOUT = 0x1, 0x2, 0x4
 GDN_FP32_STATE = 0x1   # gdn_dims.flags: fp32 state products in prefill
 GDN_CHECK_FINITE = 0x2  # gdn_dims.flags: per-stage NaN/Inf probe of prefill
 GDN_TEST_WAIT_TIMEOUT = 0x4  # gdn_dims.flags (tests only): 2 ms waits, one chunk withheld
 GDN_BF16_OPERANDS = 0x8      # gdn_dims.flags: bf16 instead of fp16 tensor-core operands
 GDN_DEV_NONFINITE_FRONTEND, GDN_DEV_NONFINITE_CHUNK, GDN_DEV_NONFINITE_OUT = 0x8, 0x10, 0x20
+GDN_DEV_BAD_PAGE, GDN_DEV_BAD_LENGTH = 0x40, 0x80   # full attention over a paged cache
+GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
 STATUS = {0: "GDN_OK", -1: "GDN_EINVAL", -2: "GDN_EUNSUPPORTED", -3: "GDN_ECUDA",
           -4: "GDN_EWORKSPACE", -5: "GDN_EALIGN"}
 
@@ -40,6 +42,29 @@ class gdn_dims(ctypes.Structure):
 class gdn_params(ctypes.Structure):
     _fields_ = [("conv_weight", ctypes.c_void_p), ("A_log", ctypes.c_void_p),
                 ("dt_bias", ctypes.c_void_p)]
+
+
+class gdn_attn_dims(ctypes.Structure):
+    _fields_ = [("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("io", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("rope", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("norm_eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class gdn_view(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class gdn_rope_params(ctypes.Structure):
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("rope_scale", ctypes.c_float)]
+
+
+class gdn_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32)]
 
 
 GDN_NUM_STAGES = 3
@@ -107,6 +132,18 @@ def load() -> ctypes.CDLL:
     lib.gdn_decode_step_gated_norm.restype = ctypes.c_int
     lib.gdn_gate_projection.argtypes = [D, P, P, I32, I64, P, P, P, P]
     lib.gdn_gate_projection.restype = ctypes.c_int
+    A, V = ctypes.POINTER(gdn_attn_dims), ctypes.POINTER(gdn_view)
+    RP, KV = ctypes.POINTER(gdn_rope_params), ctypes.POINTER(gdn_kv_cache)
+    lib.gdn_qk_norm_rope.argtypes = [A, RP, V, V, P, I64, P, P, P]
+    lib.gdn_qk_norm_rope.restype = ctypes.c_int
+    lib.gdn_kv_append.argtypes = [A, RP, V, V, V, P, P, I64, KV, P, P, P]
+    lib.gdn_kv_append.restype = ctypes.c_int
+    lib.gdn_attn_prefill.argtypes = [A, V, V, V, P, P, I32, I64, I64, V, P, P, P]
+    lib.gdn_attn_prefill.restype = ctypes.c_int
+    lib.gdn_attn_decode_workspace_size.argtypes = [A, I32, I64]
+    lib.gdn_attn_decode_workspace_size.restype = SZ
+    lib.gdn_attn_decode.argtypes = [A, V, KV, P, I32, I64, V, P, P, SZ, P, P]
+    lib.gdn_attn_decode.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -436,3 +473,222 @@ def gdn_gate_projection(dims, hidden, w_ba, a=None, b=None, d_status=None, strea
                                     _ptr(a), _ptr(b), _ptr(d_status), _stream(stream))
     _check("gdn_gate_projection", rc)
     return a, b
+
+
+# ---- full attention ---------------------------------------------------------
+
+
+def make_attn_dims(h_q, h_kv, d, io="bf16", rot_dim=0, rope="half", page_size=64, norm_eps=1e-6,
+                   scale=None, flags=0) -> gdn_attn_dims:
+    """gdn_attn_dims: scale None is 1 / sqrt(d)."""
+    io_code = {"fp32": GDN_FP32, "bf16": GDN_BF16, "fp16": GDN_FP16}[io] if isinstance(io, str) \
+        else int(io)
+    rope_code = {"half": GDN_ROPE_HALF, "interleaved": GDN_ROPE_INTERLEAVED}[rope] \
+        if isinstance(rope, str) else int(rope)
+    return gdn_attn_dims(h_q, h_kv, d, io_code, rot_dim, rope_code, page_size, norm_eps,
+                         0.0 if scale is None else scale, flags)
+
+
+def rope_frequencies(rot_dim, theta=1e4, scaling=None, factor=1.0, original_len=None,
+                     beta_fast=32.0, beta_slow=1.0, device="cpu"):
+    """(inv_freq, rope_scale) for gdn_qk_norm_rope and gdn_kv_append: the
+    frequencies theta^(-2 i / rot_dim) in fp64 (radians per position), scaled
+    for contexts `factor` times as long as the trained `original_len`:
+      None      as trained;
+      "linear"  every frequency divided by factor (positions interpolated);
+      "ntk"     theta raised to theta * factor^(rot_dim / (rot_dim - 2)), so
+                that the highest frequency stays and the lowest is interpolated;
+      "yarn"    frequencies that turn more than beta_fast times over
+                original_len stay, those that turn less than beta_slow times
+                are interpolated, a linear ramp between (Peng et al., YaRN);
+                rope_scale = 0.1 ln(factor) + 1."""
+    import math
+
+    import torch
+    if rot_dim % 2 or rot_dim < 2:
+        raise ValueError(f"rot_dim must be even and positive, got {rot_dim}")
+    if not theta > 0 or not factor > 0:
+        raise ValueError("theta and factor must be positive")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim >= 4")
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    freq = theta ** (-2.0 * i / rot_dim)
+    rope_scale = 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        if original_len is None or not original_len > 0 or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn scaling needs original_len > 0 and beta_fast > beta_slow > 0")
+
+        def index(turns):   # the (fractional) pair that turns this often over original_len
+            return rot_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(theta))
+        lo = max(math.floor(index(beta_fast)), 0)
+        hi = min(math.ceil(index(beta_slow)), rot_dim - 1)
+        keep = 1 - ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        freq = freq / factor * (1 - keep) + freq * keep
+        rope_scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freq.to(device), rope_scale
+
+
+def _attn_dtype(d: gdn_attn_dims):
+    import torch
+    return {GDN_BF16: torch.bfloat16, GDN_FP16: torch.float16}.get(d.io, torch.float32)
+
+
+def _view(t, name, dtype, heads, d, n=None):
+    """gdn_view of a [tokens, heads, d] tensor whose channels are contiguous."""
+    if t is None:
+        return None
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be [{'n' if n is None else n}, {heads}, {d}], got "
+                         f"{list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    ts, hs, cs = t.stride()
+    if cs != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    return gdn_view(t.data_ptr(), ts, hs)
+
+
+def _ref(v):
+    return None if v is None else ctypes.byref(v)
+
+
+def _cache(d, dtype, k_cache, v_cache, block_table):
+    import torch
+    _expect(k_cache, "k_cache", dtype)
+    _expect(v_cache, "v_cache", dtype, k_cache.numel())
+    _expect(block_table, "block_table", torch.int32)
+    if k_cache.dim() != 4 or tuple(k_cache.shape[1:]) != (d.h_kv, d.page_size, d.d):
+        raise ValueError(f"k_cache must be [num_pages, {d.h_kv}, {d.page_size}, {d.d}], got "
+                         f"{list(k_cache.shape)}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_seqs, pages_per_seq]")
+    return gdn_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                        k_cache.shape[0], block_table.shape[0], block_table.shape[1])
+
+
+def _rope_params(d, q_norm, k_norm, inv_freq, rope_scale):
+    import torch
+    _expect(q_norm, "q_norm", torch.float32, d.d)
+    _expect(k_norm, "k_norm", torch.float32, d.d)
+    _expect(inv_freq, "inv_freq", torch.float64, d.rot_dim // 2)
+    return gdn_rope_params(*(None if t is None else t.data_ptr() for t in (q_norm, k_norm, inv_freq)),
+                           rope_scale)
+
+
+def gdn_qk_norm_rope(dims, q, k, q_norm, k_norm, inv_freq, positions, q_out=None, k_out=None,
+                     rope_scale=1.0, stream=None):
+    """Per-head norm and rotation of queries and keys (see gdn_qk_norm_rope in
+    include/gdn.h): q [n, h_q, d], k [n, h_kv, d] (either may be None), norm
+    weights [d] fp32 or None, inv_freq [rot_dim / 2] fp64, positions [n] int32.
+    Outputs are allocated when not given.  Returns (q_out, k_out)."""
+    import torch
+    n = positions.numel()
+    dt = _attn_dtype(dims)
+    qv, kv = _view(q, "q", dt, dims.h_q, dims.d, n), _view(k, "k", dt, dims.h_kv, dims.d, n)
+    p = _rope_params(dims, q_norm, k_norm, inv_freq, rope_scale)
+    _expect(positions, "positions", torch.int32)
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = torch.empty((n, dims.h_q, dims.d), dtype=dt, device=q.device)
+    else:
+        _expect(q_out, "q_out", dt, n * dims.h_q * dims.d)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = torch.empty((n, dims.h_kv, dims.d), dtype=dt, device=k.device)
+    else:
+        _expect(k_out, "k_out", dt, n * dims.h_kv * dims.d)
+    _check("gdn_qk_norm_rope", load().gdn_qk_norm_rope(
+        ctypes.byref(dims), ctypes.byref(p), _ref(qv), _ref(kv), _ptr(positions), n, _ptr(q_out),
+        _ptr(k_out), _stream(stream)))
+    return q_out, k_out
+
+
+def gdn_kv_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions, k_cache, v_cache, block_table,
+                  row_seq=None, q_out=None, rope_scale=1.0, d_status=None, stream=None):
+    """gdn_qk_norm_rope with the keys, and the values, going into the paged
+    cache (see gdn_kv_append in include/gdn.h): caches [num_pages, h_kv,
+    page_size, d], block_table [num_seqs, pages_per_seq] int32, row_seq [n]
+    int32 (None: row t is sequence t).  Returns q_out (None when q is None)."""
+    import torch
+    n = positions.numel()
+    dt = _attn_dtype(dims)
+    qv = _view(q, "q", dt, dims.h_q, dims.d, n)
+    kv, vv = _view(k, "k", dt, dims.h_kv, dims.d, n), _view(v, "v", dt, dims.h_kv, dims.d, n)
+    p = _rope_params(dims, q_norm, k_norm, inv_freq, rope_scale)
+    c = _cache(dims, dt, k_cache, v_cache, block_table)
+    _expect(positions, "positions", torch.int32)
+    _expect(row_seq, "row_seq", torch.int32, n)
+    _expect(d_status, "d_status", torch.int32, 1)
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = torch.empty((n, dims.h_q, dims.d), dtype=dt, device=q.device)
+    else:
+        _expect(q_out, "q_out", dt, n * dims.h_q * dims.d)
+    _check("gdn_kv_append", load().gdn_kv_append(
+        ctypes.byref(dims), ctypes.byref(p), _ref(qv), _ref(kv), _ref(vv), _ptr(positions),
+        _ptr(row_seq), n, ctypes.byref(c), _ptr(q_out), _ptr(d_status), _stream(stream)))
+    return q_out
+
+
+def gdn_attn_prefill(dims, q, k, v, cu_seqlens, cu_seqlens_kv=None, gate=None, o=None,
+                     d_status=None, stream=None):
+    """Causal attention over packed prompts (see gdn_attn_prefill in
+    include/gdn.h): q [total_q, h_q, d], k, v [total_kv, h_kv, d], cu_seqlens
+    [num_seqs + 1] int32 (cu_seqlens_kv None: the same for the keys), gate
+    [total_q, h_q, d] or None.  o is allocated when not given.  Returns o."""
+    import torch
+    dt = _attn_dtype(dims)
+    tq, tk = int(q.shape[0]), int(k.shape[0])
+    qv, gv = _view(q, "q", dt, dims.h_q, dims.d), _view(gate, "gate", dt, dims.h_q, dims.d, tq)
+    kv, vv = _view(k, "k", dt, dims.h_kv, dims.d), _view(v, "v", dt, dims.h_kv, dims.d, tk)
+    _expect(cu_seqlens, "cu_seqlens", torch.int32)
+    _expect(cu_seqlens_kv, "cu_seqlens_kv", torch.int32, cu_seqlens.numel())
+    _expect(d_status, "d_status", torch.int32, 1)
+    if o is None:
+        o = torch.empty((tq, dims.h_q, dims.d), dtype=dt, device=q.device)
+    else:
+        _expect(o, "o", dt, tq * dims.h_q * dims.d)
+    _check("gdn_attn_prefill", load().gdn_attn_prefill(
+        ctypes.byref(dims), ctypes.byref(qv), ctypes.byref(kv), ctypes.byref(vv),
+        _ptr(cu_seqlens), _ptr(cu_seqlens_kv), cu_seqlens.numel() - 1, tq, tk, _ref(gv), _ptr(o),
+        _ptr(d_status), _stream(stream)))
+    return o
+
+
+def gdn_attn_decode_workspace_size(dims, n: int, shared_len: int = 0) -> int:
+    return int(load().gdn_attn_decode_workspace_size(ctypes.byref(dims), int(n), int(shared_len)))
+
+
+def gdn_attn_decode(dims, q, k_cache, v_cache, block_table, seq_lens, workspace, shared_len=0,
+                    gate=None, o=None, d_status=None, stream=None):
+    """One query token per sequence against the paged cache (see
+    gdn_attn_decode in include/gdn.h): q [n, h_q, d], caches [num_pages, h_kv,
+    page_size, d], block_table [num_seqs, pages_per_seq] int32, seq_lens [n]
+    int32; the first shared_len tokens (whole pages) are common to all rows.
+    o is allocated when not given.  Returns o."""
+    import torch
+    dt = _attn_dtype(dims)
+    n = int(q.shape[0])
+    qv, gv = _view(q, "q", dt, dims.h_q, dims.d), _view(gate, "gate", dt, dims.h_q, dims.d, n)
+    c = _cache(dims, dt, k_cache, v_cache, block_table)
+    _expect(seq_lens, "seq_lens", torch.int32, n)
+    _expect(d_status, "d_status", torch.int32, 1)
+    if o is None:
+        o = torch.empty((n, dims.h_q, dims.d), dtype=dt, device=q.device)
+    else:
+        _expect(o, "o", dt, n * dims.h_q * dims.d)
+    _expect(workspace, "workspace")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("gdn_attn_decode", load().gdn_attn_decode(
+        ctypes.byref(dims), ctypes.byref(qv), ctypes.byref(c), _ptr(seq_lens), n, int(shared_len),
+        _ref(gv), _ptr(o), _ptr(workspace), ws_bytes, _ptr(d_status), _stream(stream)))
+    return o

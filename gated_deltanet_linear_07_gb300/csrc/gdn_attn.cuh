@@ -1,0 +1,138 @@
+// gdn_attn.cuh -- what the full-attention kernels share: 16-bit and 32-bit
+// element vectors and the launch descriptors between the API translation unit
+// and the kernels.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+namespace attn {
+
+// Eight consecutive channels of a row: one 16-byte access (16-bit types) or
+// two (fp32).
+template <typename IO>
+struct Vec8;
+
+template <>
+struct Vec8<float> {
+  float4 lo, hi;
+  __device__ __forceinline__ void load(const float* p) {
+    lo = *reinterpret_cast<const float4*>(p);
+    hi = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    *reinterpret_cast<float4*>(p) = lo;
+    *reinterpret_cast<float4*>(p + 4) = hi;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w;
+    f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    lo = make_float4(f[0], f[1], f[2], f[3]);
+    hi = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+template <typename IO>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename IO>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+template <typename IO>
+struct Vec8 {
+  uint4 w;
+  __device__ __forceinline__ void load(const IO* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(IO* p) const { *reinterpret_cast<uint4*>(p) = w; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2<IO>(u[i]);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    w = make_uint4(pack2<IO>(f[0], f[1]), pack2<IO>(f[2], f[3]), pack2<IO>(f[4], f[5]),
+                   pack2<IO>(f[6], f[7]));
+  }
+};
+
+// sigmoid(x) with the exponential and the quotient on the special-function
+// unit: a few ulp, 0 and 1 at the ends.
+__device__ __forceinline__ float gate_sigmoid(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
+  return __fdividef(1.0f, 1.0f + e);
+}
+
+}  // namespace attn
+}  // namespace gdn
+
+// One call of gdn_qk_norm_rope or gdn_kv_append.
+struct GdnRopeArgs {
+  gdn_view q, k, v;            // null data: left out (v: no append)
+  void* q_out;
+  void* k_out;                 // null with an append: k goes to the cache
+  const float* q_norm;
+  const float* k_norm;
+  const double* inv_freq;
+  const int32_t* positions;
+  const int32_t* row_seq;
+  gdn_kv_cache cache;
+  int32_t* d_status;
+  int64_t n;
+  int32_t h_q, h_kv, d, rot_dim, interleaved, page_shift;
+  float eps, rope_scale;
+};
+
+// One attention call; the prefix pass of gdn_attn_decode uses the same kernel
+// as gdn_attn_prefill, with the batch's rows as its tokens.
+struct GdnAttnArgs {
+  gdn_view q, k, v;            // k, v: packed keys and values (prefill)
+  gdn_view gate;               // null data: none
+  void* o;
+  const int32_t* cu_q;
+  const int32_t* cu_kv;
+  gdn_kv_cache cache;          // decode
+  const int32_t* seq_lens;     // decode
+  int32_t* d_status;
+  float* part_o;               // decode workspace: partial outputs, [slot][d] fp32,
+  float2* part_ml;             // and their (reference maximum in log2 units, sum)
+  int64_t total_q, total_kv, shared_len;
+  uint64_t wait_ns;
+  float scale_log2;            // scale * log2(e)
+  int32_t h_q, h_kv, d, num_seqs, page_shift;
+  int32_t splits;              // prefix pass: how many CTA groups share the prefix
+};
+
+cudaError_t gdn_launch_rope(const GdnRopeArgs& a, int io, cudaStream_t s);
+cudaError_t gdn_launch_attn_prefill(const GdnAttnArgs& a, int io, cudaStream_t s);
+// Decode: slots of partial results that n rows behind shared_len shared tokens
+// need, and the launches (prefix pass, per-sequence pass, merge).
+int64_t gdn_attn_decode_slots(int h_q, int h_kv, int d, int n, int64_t shared_len);
+cudaError_t gdn_launch_attn_decode(const GdnAttnArgs& a, int io, cudaStream_t s);
+// How many CTA groups share the keys of the prefix pass (0: no pass).
+int gdn_attn_prefix_splits(int h_q, int h_kv, int d, int n, int64_t shared_len);
+cudaError_t gdn_launch_attn_prefix(const GdnAttnArgs& a, int io, cudaStream_t s);

@@ -1,0 +1,853 @@
+// gdn_attn_tc.cu -- attention of many query rows over the same keys on the
+// tensor cores: causal attention over packed prompts (gdn_attn_prefill), and
+// the pass of gdn_attn_decode over a prefix that the whole batch shares.
+//
+// For a block of 128 query rows per CTA and blocks of 128 keys, one pass:
+//   S = Q K^T,  m' = max(m, rowmax S),  P = 2^(c (S - m')),  c = scale log2 e
+//   l = l 2^(c (m - m')) + rowsum P,    O = O 2^(c (m - m')) + P V,
+// and o = O / l at the end.  S and O live in tensor memory (fp32); P goes
+// back there in the I/O type as the A operand of the second product.  The
+// reference maximum m may lag behind the true one by up to 2^RESCALE_LOG2: P
+// is then larger than one but the quotient is the same, and O is rescaled
+// only when a row really passes that, which is rare after the first blocks.
+//
+// Rows: a key/value head's query heads are packed with the tokens, so that
+// one block of 128 rows covers 128 / gp tokens x gp heads (gp the largest
+// power of two that divides the group) and every key block that is loaded
+// serves gp heads at once.
+//
+// CTA pairs (CG = 2): the two CTAs of a cluster take 256 rows of the same
+// key/value head and each loads one half of every K and V block; one
+// tcgen05.mma.cta_group::2 works on both CTAs' tensor memories.  That halves
+// both the bytes fetched from L2 per product and the operand bytes read from
+// shared memory, which at head dim 256 would otherwise be the bound (128 keys
+// x 256 channels x 2 operands = 128 KB per 2048 cycles of products).
+//
+// Warps: 0-7 softmax (warps w and w + 4 share 32 rows, 64 of a block's 128
+// columns each), 8 the TMA loads, 9 the MMAs.  K and V blocks run through one
+// ring in the order K0 K1 V0 K2 V1 ..., which is the order the MMA warp
+// consumes: S(i+1) is formed while the softmax works on S(i).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "gdn_attn.cuh"
+#include "gdn_tc.cuh"
+
+namespace gdn {
+namespace attn {
+
+using namespace gdn::tc;
+
+constexpr int BM = 128;            // query rows per CTA (tensor-memory lanes)
+constexpr int BN = 128;            // keys per block
+constexpr int TC_THREADS = 320;
+constexpr int WARP_LOAD = 8, WARP_MMA = 9;
+constexpr float RESCALE_LOG2 = 8.0f;
+constexpr uint32_t MISC_BYTES = 3072;
+constexpr int MAX_RING = 8;
+
+template <int D, int CG>
+struct TcCfg {
+  static constexpr uint32_t Q_BYTES = BM * D * 2;
+  static constexpr uint32_t STAGE = BN * D * 2 / CG;
+  static constexpr int FIT = (int)((232448u - MISC_BYTES - Q_BYTES) / STAGE);
+  static constexpr int RING = FIT < MAX_RING ? FIT : MAX_RING;
+  static constexpr uint32_t SMEM = MISC_BYTES + Q_BYTES + RING * STAGE;
+  static constexpr uint32_t TMEM_O = 256;   // after the two S buffers
+};
+
+struct __align__(16) TcShared {
+  uint64_t full[MAX_RING], empty[MAX_RING];
+  uint64_t q_full, s_full[2], p_ready[2], o_done, v_tail;
+  uint32_t tmem;
+  int32_t seq, tile, bad;
+  int32_t scan[12];
+  float red[2][2][BM];   // row maxima of the two column halves, two turns
+};
+static_assert(sizeof(TcShared) <= MISC_BYTES, "shared bookkeeping");
+
+// ---- PTX: clusters and the pair forms of the tensor-core operations --------
+
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+template <int CG>
+__device__ __forceinline__ bool try_wait_scope(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if (CG == 2) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  }
+  return ok != 0;
+}
+// Bounded wait; once one has run out (ok false) the later ones return at once.
+template <int CG>
+__device__ __forceinline__ void wait_on(bool& ok, uint64_t* bar, uint32_t parity,
+                                        uint64_t budget_ns) {
+  if (!ok) return;
+  const uint32_t addr = smem_u32(bar);
+  if (try_wait_scope<CG>(addr, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (!try_wait_scope<CG>(addr, parity))
+    if (globaltimer_ns() - t0 > budget_ns) {
+      ok = false;
+      return;
+    }
+}
+template <int CG>
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                           int c2, int c3, uint32_t cluster_bar) {
+  if (CG == 2) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+        "r"(cluster_bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+        "r"(cluster_bar)
+        : "memory");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_alloc_cg(uint32_t* dst, uint32_t ncols) {
+  if (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(dst)),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, ncols);
+    tmem_relinquish();
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) {
+  if (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                 : "memory");
+  else
+    tmem_dealloc(taddr, ncols);
+}
+template <int CG>
+__device__ __forceinline__ void mma_ss_cg(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+  if (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    mma_ss(d, a, b, idesc, acc);
+}
+template <int CG>
+__device__ __forceinline__ void mma_ts_cg(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
+  if (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    mma_ts(d, a, b, idesc, acc);
+}
+// Arrive on `bar` of every CTA of the pair when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit_cg(uint64_t* bar) {
+  if (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    mma_commit(bar);
+}
+// 32 consecutive columns of this thread's lane, without the wait.
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+      "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]),
+      "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]),
+      "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void pair_bar(int id) {   // the two warps that share 32 rows
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+template <typename IO>
+__host__ __device__ constexpr uint32_t idesc_io(int M, int N, bool b_mn);
+template <>
+__host__ __device__ constexpr uint32_t idesc_io<__nv_bfloat16>(int M, int N, bool b_mn) {
+  return idesc_bf16(M, N, false, b_mn);
+}
+template <>
+__host__ __device__ constexpr uint32_t idesc_io<__half>(int M, int N, bool b_mn) {
+  return idesc_f16(M, N, false, b_mn);
+}
+
+// ---- the kernel ---------------------------------------------------------------
+
+struct TcLaunch {
+  GdnAttnArgs a;
+  int32_t gp_shift;       // log2 of the query heads packed into a row block
+  int32_t subs;           // groups of 2^gp_shift query heads per key/value head
+  int32_t k_rows, v_rows; // rows of one K / V box
+};
+
+// Which sequence and which of its row blocks is block j, counting from the
+// last one; by all threads.  False: there is none (or cu_seqlens is bad).
+__device__ __forceinline__ bool find_tile(const GdnAttnArgs& a, TcShared* sh, int64_t j, int tokens,
+                                          int64_t& q0, int64_t& len_q, int64_t& k0,
+                                          int64_t& len_k, int64_t& tile) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    sh->seq = -1;
+    sh->bad = 0;
+  }
+  __syncthreads();
+  // Last sequences and last blocks first: within a sequence the longest rows
+  // start first, so the tail of the grid is made of short ones.
+  int64_t before = 0;
+  for (int base = 0; base < a.num_seqs; base += TC_THREADS) {
+    const int i = base + tid;                   // sequence num_seqs - 1 - i
+    int64_t nt = 0;
+    if (i < a.num_seqs) {
+      const int b = a.num_seqs - 1 - i;
+      const int64_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
+      const int64_t klo = a.cu_kv[b], khi = a.cu_kv[b + 1];
+      if (hi < lo || lo < 0 || hi > a.total_q || khi < klo || klo < 0 || khi > a.total_kv ||
+          (b == 0 && (lo != 0 || klo != 0)) ||
+          (b == a.num_seqs - 1 && (hi != a.total_q || khi != a.total_kv)))
+        sh->bad = 1;
+      else
+        nt = (hi - lo + tokens - 1) / tokens;
+    }
+    int incl = (int)nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh->scan[warp] = incl;
+    __syncthreads();
+    int64_t off = before;
+    int64_t all = 0;
+    for (int w = 0; w < TC_THREADS / 32; ++w) {
+      if (w < warp) off += sh->scan[w];
+      all += sh->scan[w];
+    }
+    const int64_t first = off + incl - nt;
+    if (nt > 0 && j >= first && j < first + nt) {
+      sh->seq = a.num_seqs - 1 - i;
+      sh->tile = (int)(nt - 1 - (j - first));
+    }
+    before += all;
+    __syncthreads();
+  }
+  if (sh->bad) {
+    if (tid == 0) set_status(a.d_status, GDN_DEV_BAD_CU_SEQLENS);
+    return false;
+  }
+  if (sh->seq < 0) return false;
+  const int b = sh->seq;
+  q0 = a.cu_q[b];
+  len_q = a.cu_q[b + 1] - q0;
+  k0 = a.cu_kv[b];
+  len_k = a.cu_kv[b + 1] - k0;
+  tile = sh->tile;
+  return true;
+}
+
+template <typename IO, int D, int CG, bool PREFIX>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    attn_tc_kernel(const __grid_constant__ TcLaunch p, const __grid_constant__ CUtensorMap qmap,
+                   const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap) {
+  using C = TcCfg<D, CG>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  TcShared* sh = reinterpret_cast<TcShared*>(smem);
+  const GdnAttnArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CG == 2 ? cta_rank() : 0u;
+  const uint32_t q_smem = smem_u32(smem) + MISC_BYTES;
+  const uint32_t ring = q_smem + C::Q_BYTES;
+
+  // ---- which rows and which keys ----
+  const int gp = 1 << p.gp_shift;
+  const int cta_tokens = BM >> p.gp_shift;
+  const int64_t item = blockIdx.x / CG;
+  const int heads = a.h_kv * p.subs;             // row groups that share a tile of tokens
+  const int head = (int)(item % heads);
+  const int kvh = head / p.subs;
+  const int h0 = kvh * (a.h_q / a.h_kv) + (head % p.subs) * gp;   // first packed query head
+  int64_t q0, len_q, k0, len_k, tile;
+  int split = 0, first_block = 0, blocks;
+  if (PREFIX) {
+    const int64_t rest = item / heads;
+    split = (int)(rest % a.splits);
+    tile = rest / a.splits;
+    q0 = 0;
+    len_q = a.total_q;
+    k0 = 0;
+    len_k = a.shared_len;
+    const int64_t all = (len_k + BN - 1) / BN;
+    first_block = (int)(all * split / a.splits);
+    blocks = (int)(all * (split + 1) / a.splits) - first_block;
+  } else {
+    if (!find_tile(a, sh, item / heads, cta_tokens * CG, q0, len_q, k0, len_k, tile)) return;
+    blocks = 0;
+  }
+  const int64_t tok0 = (tile * CG + rank) * cta_tokens;      // this CTA's first token
+  const int64_t off = len_k - len_q;                         // causal: token t sees t + off + 1
+  if (!PREFIX) {
+    // the keys that the last token of the pair's rows sees
+    const int64_t last = min(len_q, (tile + 1) * CG * cta_tokens) - 1;
+    const int64_t seen = last + off + 1;
+    blocks = seen > 0 ? (int)((seen + BN - 1) / BN) : 0;
+  }
+  // keys past `key_end` are another sequence's, or none
+  const int64_t key_end = len_k;
+  const bool tail = (int64_t)(first_block + blocks) * BN > key_end;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::RING; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
+    }
+    mbar_init(&sh->q_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh->s_full[s], 1);
+      mbar_init(&sh->p_ready[s], 8 * CG);
+    }
+    mbar_init(&sh->o_done, 1);
+    mbar_init(&sh->v_tail, 1);
+    fence_mbar_init();
+  }
+  if (warp == WARP_MMA) tmem_alloc_cg<CG>(&sh->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  bool ok = (smem_u32(smem) & 1023u) == 0 && blocks >= 0;
+
+  if (warp == WARP_LOAD && lane == 0 && blocks > 0 && ok) {
+    // ---- TMA loads; in a pair every copy reports to the first CTA's barrier ----
+    auto lead = [&](uint64_t* bar) {
+      return CG == 2 ? map_cta(smem_u32(bar), 0) : smem_u32(bar);
+    };
+    if (rank == 0) mbar_expect_tx(&sh->q_full, C::Q_BYTES * CG);
+    tma_load_4d<CG>(q_smem, &qmap, 0, h0, (int)(q0 + tok0), 0, lead(&sh->q_full));
+    // rows of [t, t + n) that exist, in whole boxes
+    auto rows_of = [&](int64_t t, int n, int box) -> int {
+      const int64_t left = PREFIX ? key_end - t : (int64_t)n;
+      return left <= 0 ? 0 : (int)min((int64_t)n, (left + box - 1) / box * box);
+    };
+    auto load_rows = [&](uint32_t dst, const CUtensorMap* map, int64_t t, int n, int box, int kb0,
+                         int kbs, uint32_t bar) {
+      if (!PREFIX) tma_load_4d<CG>(dst, map, 0, (int)(k0 + t), kb0, kvh, bar);
+      for (int r = 0; PREFIX && r < n && t + r < key_end; r += box) {
+        const int64_t pos = t + r;
+        int32_t page = __ldg(a.cache.block_table + (pos >> a.page_shift));
+        if (page < 0 || page >= a.cache.num_pages) {
+          set_status(a.d_status, GDN_DEV_BAD_PAGE);
+          page = 0;
+        }
+        const int64_t row = (((int64_t)page * a.h_kv + kvh) << a.page_shift) +
+                            (pos & ((1 << a.page_shift) - 1));
+        for (int kb = 0; kb < kbs; ++kb)
+          tma_load_4d<CG>(dst + (uint32_t)(kb * n + r) * 128u, map, 0, (int)row, kb0 + kb, 0, bar);
+      }
+    };
+    int j = 0;
+    for (int i = 0; i <= blocks && ok; ++i) {
+      if (i < blocks) {   // K block i: this CTA's share of its rows
+        const int s = j % C::RING;
+        if (j >= C::RING) wait_on<CG>(ok, &sh->empty[s], ((j / C::RING) - 1) & 1, a.wait_ns);
+        if (!ok) break;
+        const int64_t t = (int64_t)(first_block + i) * BN;
+        const int n = BN / CG;
+        if (rank == 0) {
+          int rows = 0;
+          for (int c = 0; c < CG; ++c) rows += rows_of(t + c * n, n, p.k_rows);
+          mbar_expect_tx(&sh->full[s], (uint32_t)rows * D * 2);
+        }
+        load_rows(ring + (uint32_t)s * C::STAGE, &kmap, t + (int64_t)rank * n, n, p.k_rows, 0,
+                  D / 64, lead(&sh->full[s]));
+        ++j;
+      }
+      if (i > 0) {        // V block i - 1: this CTA's share of its channels
+        const int s = j % C::RING;
+        if (j >= C::RING) wait_on<CG>(ok, &sh->empty[s], ((j / C::RING) - 1) & 1, a.wait_ns);
+        if (!ok) break;
+        const int64_t t = (int64_t)(first_block + i - 1) * BN;
+        const uint32_t bytes = (uint32_t)rows_of(t, BN, p.v_rows) * (D / CG) * 2;
+        const bool own = tail && i == blocks;   // reports here: this CTA clears its rows past the end
+        if (own)
+          mbar_expect_tx(&sh->v_tail, bytes);
+        else if (rank == 0)
+          mbar_expect_tx(&sh->full[s], bytes * CG);
+        const uint32_t own_bar = CG == 2 ? map_cta(smem_u32(&sh->v_tail), rank)
+                                         : smem_u32(&sh->v_tail);
+        load_rows(ring + (uint32_t)s * C::STAGE, &vmap, t, BN, p.v_rows,
+                  (int)rank * (D / 64 / CG), D / 64 / CG, own ? own_bar : lead(&sh->full[s]));
+        ++j;
+      }
+    }
+  } else if (warp == WARP_MMA && lane == 0 && rank == 0 && blocks > 0 && ok) {
+    // ---- MMAs, for both CTAs of a pair ----
+    constexpr uint32_t id_s = idesc_io<IO>(BM * CG, BN, false);
+    constexpr uint32_t id_o = idesc_io<IO>(BM * CG, D, true);
+    int j = 0;
+    auto scores = [&](int i) {
+      const int s = j % C::RING;
+      wait_on<CG>(ok, &sh->full[s], (j / C::RING) & 1, a.wait_ns);
+      ++j;
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t kt = ring + (uint32_t)s * C::STAGE;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        mma_ss_cg<CG>(tmem + (uint32_t)(i & 1) * BN, sdesc_kmaj(q_smem, BM, ks),
+                      sdesc_kmaj(kt, BN / CG, ks), id_s, ks > 0 ? 1u : 0u);
+      commit_cg<CG>(&sh->empty[s]);
+      commit_cg<CG>(&sh->s_full[i & 1]);
+    };
+    wait_on<CG>(ok, &sh->q_full, 0, a.wait_ns);
+    if (ok) scores(0);
+    for (int i = 0; i < blocks && ok; ++i) {
+      if (i + 1 < blocks) scores(i + 1);
+      const int s = j % C::RING;
+      if (!(tail && i == blocks - 1)) wait_on<CG>(ok, &sh->full[s], (j / C::RING) & 1, a.wait_ns);
+      ++j;
+      wait_on<CG>(ok, &sh->p_ready[i & 1], (i >> 1) & 1, a.wait_ns);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t vt = ring + (uint32_t)s * C::STAGE;
+      const uint32_t pt = tmem + (uint32_t)(i & 1) * BN;
+#pragma unroll
+      for (int ks = 0; ks < BN / 16; ++ks)
+        mma_ts_cg<CG>(tmem + C::TMEM_O, pt + (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8),
+                      sdesc_mnmaj(vt, BN, ks), id_o, (i > 0 || ks > 0) ? 1u : 0u);
+      commit_cg<CG>(&sh->empty[s]);
+      commit_cg<CG>(&sh->o_done);
+    }
+  } else if (warp < 8) {
+    // ---- softmax: warps w and w + 4 share rows 32 (w % 4) .. + 31 ----
+    const int quarter = warp & 3, half = warp >> 2;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const int64_t tok = tok0 + (row >> p.gp_shift);
+    const bool live = tok < len_q;
+    // how many keys this row sees; rows past the end follow the last one, so
+    // that they ask for no mask of their own
+    const int64_t vt = live ? tok : len_q - 1;
+    int64_t lim;
+    if (PREFIX) {
+      lim = min((int64_t)max(a.seq_lens[vt], 0), len_k);
+    } else {
+      lim = vt + off + 1;
+      lim = lim < 0 ? 0 : lim;
+    }
+    int64_t low = lim;   // the least of the warp's rows
+    if (PREFIX) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) low = min(low, (int64_t)__shfl_xor_sync(0xffffffffu, low, o));
+    } else {
+      low = __shfl_sync(0xffffffffu, lim, 0);
+    }
+    const float c = a.scale_log2;
+    float m = -INFINITY;      // reference maximum of the raw scores
+    float l = 0.f;            // this thread's half of the row sum
+    uint32_t ready[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      ready[b] = CG == 2 ? map_cta(smem_u32(&sh->p_ready[b]), 0) : smem_u32(&sh->p_ready[b]);
+
+    for (int i = 0; i < blocks; ++i) {
+      const int b = i & 1;
+      wait_on<CG>(ok, &sh->s_full[b], (i >> 1) & 1, a.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) ok = false;
+      tc_fence_after();
+      const uint32_t st = tmem + lanes + (uint32_t)b * BN + (uint32_t)half * 64;
+      uint32_t r0[32], r1[32];
+      tmem_ld32_nowait(st, r0);
+      tmem_ld32_nowait(st + 32, r1);
+      tmem_wait_ld(r0);
+      tmem_wait_ld(r1);
+      const int64_t key = (int64_t)(first_block + i) * BN + half * 64;
+      if (low < key + 64) {
+        const int seen = (int)max((int64_t)-1, min((int64_t)64, lim - key));
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          if (k >= seen) r0[k] = 0xff800000u;
+          if (k + 32 >= seen) r1[k] = 0xff800000u;
+        }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        mx[k / 2 % 2] = fmaxf(mx[k / 2 % 2], fmaxf(__uint_as_float(r0[k]), __uint_as_float(r0[k + 1])));
+        mx[2 + k / 2 % 2] =
+            fmaxf(mx[2 + k / 2 % 2], fmaxf(__uint_as_float(r1[k]), __uint_as_float(r1[k + 1])));
+      }
+      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      sh->red[b][half][row] = mt;
+      pair_bar(1 + quarter);
+      mt = fmaxf(mt, sh->red[b][half ^ 1][row]);
+      // both warps of a row see the same maxima and so decide alike
+      const bool far = mt > m && (m == -INFINITY || (mt - m) * c > RESCALE_LOG2);
+      if (__any_sync(0xffffffffu, far)) {
+        const float mn = fmaxf(m, mt);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float f = fast_exp2((m - base) * c);    // 0 for a first maximum
+        if (i > 0) {   // S(i) was formed after product i - 2: only i - 1 may be under way
+          wait_on<CG>(ok, &sh->o_done, (i - 1) & 1, a.wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) ok = false;
+          tc_fence_after();
+#pragma unroll 1
+          for (int n = 0; n < D / 2; n += 32) {
+            uint32_t o[32];
+            const uint32_t at = tmem + lanes + C::TMEM_O + (uint32_t)(half * (D / 2) + n);
+            tmem_ld32_nowait(at, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(at, o);
+          }
+        }
+        l *= f;
+        m = mn;
+      }
+      const float nm = m == -INFINITY ? 0.f : -m * c;
+      uint32_t w[32];
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        const float e0 = fast_exp2(fmaf(__uint_as_float(r0[k]), c, nm));
+        const float e1 = fast_exp2(fmaf(__uint_as_float(r0[k + 1]), c, nm));
+        const float e2 = fast_exp2(fmaf(__uint_as_float(r1[k]), c, nm));
+        const float e3 = fast_exp2(fmaf(__uint_as_float(r1[k + 1]), c, nm));
+        sum[0] += e0;
+        sum[1] += e1;
+        sum[2] += e2;
+        sum[3] += e3;
+        w[k / 2] = pack2<IO>(e0, e1);
+        w[16 + k / 2] = pack2<IO>(e2, e3);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      // over this half's own scores, which are in registers by now
+      tmem_st32(st, w);
+      tmem_wait_st();
+      if (tail && i == blocks - 1) {
+        // the rows of V past the end are someone else's, or nothing: clear them
+        wait_on<CG>(ok, &sh->v_tail, 0, a.wait_ns);
+        const int s = (2 * blocks - 1) % C::RING;
+        const int from = (int)(key_end - (int64_t)(first_block + i) * BN);
+        const uint32_t vt2 = ring + (uint32_t)s * C::STAGE;
+        constexpr int ATOMS = D / 64 / CG;
+        for (int x = from * 8 + tid; x < BN * 8; x += 256)
+#pragma unroll
+          for (int at = 0; at < ATOMS; ++at)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             vt2 + (uint32_t)(at * BN * 128 + x * 16)),
+                         "r"(0)
+                         : "memory");
+        fence_async_smem();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          arrive_cluster(ready[b]);
+        else
+          mbar_arrive(&sh->p_ready[b]);
+      }
+    }
+
+    // ---- the end: o = O / l ----
+    if (blocks > 0) {
+      // S(blocks - 1) was formed after product blocks - 3: the last two may be
+      // under way, and a parity tells only one phase from the next
+      if (blocks > 1) wait_on<CG>(ok, &sh->o_done, (blocks - 2) & 1, a.wait_ns);
+      wait_on<CG>(ok, &sh->o_done, (blocks - 1) & 1, a.wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) ok = false;
+      tc_fence_after();
+    }
+    sh->red[blocks & 1][half][row] = l;
+    pair_bar(1 + quarter);
+    l += sh->red[blocks & 1][half ^ 1][row];
+    const int h = h0 + (row & (gp - 1));
+    if (PREFIX) {
+      const int64_t slot = ((int64_t)split * a.total_q + (live ? tok : 0)) * a.h_q + h;
+      if (live && half == 0) a.part_ml[slot] = make_float2(m * c, l);
+#pragma unroll 1
+      for (int n = 0; n < D / 2 && blocks > 0; n += 32) {
+        uint32_t o[32];
+        const int col = half * (D / 2) + n;
+        tmem_ld32_nowait(tmem + lanes + C::TMEM_O + (uint32_t)col, o);
+        tmem_wait_ld(o);
+        if (live && l > 0.f) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + col);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+        }
+      }
+    } else {
+      const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no key: zeros; NaN stays
+      const int64_t t = q0 + tok;
+      const IO* gate = a.gate.data && live
+                           ? reinterpret_cast<const IO*>(a.gate.data) + t * a.gate.token_stride +
+                                 h * a.gate.head_stride
+                           : nullptr;
+      IO* out = reinterpret_cast<IO*>(a.o) + (t * a.h_q + h) * D;
+#pragma unroll 1
+      for (int n = 0; n < D / 2; n += 32) {
+        uint32_t o[32];
+        const int col = half * (D / 2) + n;
+        if (blocks > 0) {
+          tmem_ld32_nowait(tmem + lanes + C::TMEM_O + (uint32_t)col, o);
+          tmem_wait_ld(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (live) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[k + e]) * inv;
+            if (l == 0.f)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = 0.f;
+            if (gate) {
+              Vec8<IO> gv;
+              gv.load(gate + col + k);
+              float g[8];
+              gv.get(g);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] *= gate_sigmoid(g[e]);
+            }
+            Vec8<IO> ov;
+            ov.set(f);
+            ov.store(out + col + k);
+          }
+        }
+      }
+    }
+  }
+  if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
+  __syncwarp();
+  // nothing of the pair is still to arrive at the other's barriers
+  tc_fence_before();
+  __syncthreads();
+  if (CG == 2) cluster_sync_all();
+  tc_fence_after();
+  if (warp == WARP_MMA) tmem_dealloc_cg<CG>(tmem, 512);
+}
+
+// ---- host -------------------------------------------------------------------------
+
+static cudaError_t encode(CUtensorMap* map, int io, const void* ptr, const cuuint64_t (&dims)[4],
+                          const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn_tensor_map_encoder());
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r =
+      enc(map, io == GDN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+          4, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Strides of axes of extent one are never used: any legal value does.
+static cuuint64_t stride_bytes(int64_t elements, int64_t extent) {
+  return extent > 1 ? (cuuint64_t)elements * 2 : 16;
+}
+
+template <typename IO, int D, int CG, bool PREFIX>
+static cudaError_t launch_tc(const GdnAttnArgs& a, int io, cudaStream_t s) {
+  using C = TcCfg<D, CG>;
+  cudaError_t e = cudaSuccess;
+  TcLaunch p;
+  p.a = a;
+  const int group = a.h_q / a.h_kv;
+  p.gp_shift = 0;
+  while ((group >> p.gp_shift) % 2 == 0 && p.gp_shift < 7) ++p.gp_shift;
+  const int gp = 1 << p.gp_shift;
+  p.subs = group / gp;
+  const int cta_tokens = BM / gp;
+  CUtensorMap qmap, kmap, vmap;
+  {   // Q: (64 channels, head, token, 64-channel block): rows token-major, then heads
+    const cuuint64_t dims[4] = {64, (cuuint64_t)a.h_q, (cuuint64_t)a.total_q, D / 64};
+    const cuuint64_t str[3] = {stride_bytes(a.q.head_stride, a.h_q),
+                               stride_bytes(a.q.token_stride, a.total_q), 128};
+    const cuuint32_t box[4] = {64, (cuuint32_t)gp, (cuuint32_t)cta_tokens, D / 64};
+    if ((e = encode(&qmap, io, a.q.data, dims, str, box)) != cudaSuccess) return e;
+  }
+  if (PREFIX) {   // cache rows: (64 channels, row of the pool, 64-channel block, -)
+    const cuuint64_t rows = (cuuint64_t)a.cache.num_pages * a.h_kv << a.page_shift;
+    const cuuint64_t dims[4] = {64, rows, D / 64, 1};
+    const cuuint64_t str[3] = {D * 2, 128, 16};
+    const int page = 1 << a.page_shift;
+    p.k_rows = page < BN / CG ? page : BN / CG;
+    p.v_rows = page < BN ? page : BN;
+    const cuuint32_t kbox[4] = {64, (cuuint32_t)p.k_rows, 1, 1};
+    const cuuint32_t vbox[4] = {64, (cuuint32_t)p.v_rows, 1, 1};
+    if ((e = encode(&kmap, io, a.cache.k, dims, str, kbox)) != cudaSuccess) return e;
+    if ((e = encode(&vmap, io, a.cache.v, dims, str, vbox)) != cudaSuccess) return e;
+  } else {        // packed: (64 channels, token, 64-channel block, head)
+    const cuuint64_t rows = a.total_kv > 0 ? (cuuint64_t)a.total_kv : 1;   // none: never loaded
+    const cuuint64_t dims[4] = {64, rows, D / 64, (cuuint64_t)a.h_kv};
+    const cuuint64_t kstr[3] = {stride_bytes(a.k.token_stride, a.total_kv), 128,
+                                stride_bytes(a.k.head_stride, a.h_kv)};
+    const cuuint64_t vstr[3] = {stride_bytes(a.v.token_stride, a.total_kv), 128,
+                                stride_bytes(a.v.head_stride, a.h_kv)};
+    const cuuint32_t kbox[4] = {64, BN / CG, D / 64, 1};
+    const cuuint32_t vbox[4] = {64, BN, D / 64 / CG, 1};
+    p.k_rows = BN / CG;
+    p.v_rows = BN;
+    if ((e = encode(&kmap, io, a.k.data, dims, kstr, kbox)) != cudaSuccess) return e;
+    if ((e = encode(&vmap, io, a.v.data, dims, vstr, vbox)) != cudaSuccess) return e;
+  }
+  auto kernel = attn_tc_kernel<IO, D, CG, PREFIX>;
+  static int opted_in[64] = {};
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !opted_in[dev]) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)C::SMEM)) != cudaSuccess)
+      return e;
+    if (dev >= 0 && dev < 64) opted_in[dev] = 1;
+  }
+  const int64_t tokens = (int64_t)cta_tokens * CG;
+  const int64_t tiles = PREFIX ? (a.total_q + tokens - 1) / tokens * a.splits
+                               : a.total_q / tokens + a.num_seqs;   // sum of the rounded-up counts
+  const int64_t grid = tiles * a.h_kv * p.subs * CG;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(TC_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, qmap, kmap, vmap);
+}
+
+template <typename IO, bool PREFIX>
+static cudaError_t launch_tc_d(const GdnAttnArgs& a, int io, cudaStream_t s) {
+  // Head dim 64 has no pair form: half of its 64 value channels would not fill
+  // a 128-byte operand row.
+  switch (a.d) {
+    case 64: return launch_tc<IO, 64, 1, PREFIX>(a, io, s);
+    case 128: return launch_tc<IO, 128, 2, PREFIX>(a, io, s);
+    default: return launch_tc<IO, 256, 2, PREFIX>(a, io, s);
+  }
+}
+
+}  // namespace attn
+}  // namespace gdn
+
+cudaError_t gdn_launch_attn_prefill(const GdnAttnArgs& a, int io, cudaStream_t s) {
+  using namespace gdn::attn;
+  return io == GDN_BF16 ? launch_tc_d<__nv_bfloat16, false>(a, io, s)
+                        : launch_tc_d<__half, false>(a, io, s);
+}
+
+// Enough CTA groups to give every SM (pair) one, each with at least two key
+// blocks: a partial output costs h_q d floats per row to write and to merge.
+int gdn_attn_prefix_splits(int h_q, int h_kv, int d, int n, int64_t shared_len) {
+  // one row alone shares nothing: its own pass covers the prefix too
+  if (shared_len <= 0 || n <= 1) return 0;
+  const int cg = d == 64 ? 1 : 2;
+  int gp = 1;
+  while ((h_q / h_kv) % (2 * gp) == 0 && gp < 128) gp *= 2;
+  const int64_t rows = (int64_t)gdn::attn::BM / gp * cg;
+  const int64_t items = ((n + rows - 1) / rows) * (h_q / gp);
+  const int64_t blocks = (shared_len + gdn::attn::BN - 1) / gdn::attn::BN;
+  int64_t splits = (152 / cg) / items;
+  if (splits > (blocks + 1) / 2) splits = (blocks + 1) / 2;
+  if (splits < 1) splits = 1;
+  return (int)splits;
+}
+
+cudaError_t gdn_launch_attn_prefix(const GdnAttnArgs& a, int io, cudaStream_t s) {
+  using namespace gdn::attn;
+  return io == GDN_BF16 ? launch_tc_d<__nv_bfloat16, true>(a, io, s)
+                        : launch_tc_d<__half, true>(a, io, s);
+}

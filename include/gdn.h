@@ -75,7 +75,8 @@ typedef enum {
   GDN_EALIGN = -5         /* a device pointer is not 16-byte aligned */
 } gdn_status;
 
-typedef enum { GDN_FP32 = 0, GDN_BF16 = 1 } gdn_dtype;
+/* GDN_FP16 is taken by the full-attention entry points only. */
+typedef enum { GDN_FP32 = 0, GDN_BF16 = 1, GDN_FP16 = 2 } gdn_dtype;
 
 /* Bits of *d_status. */
 #define GDN_DEV_BAD_SLOT 0x1        /* slot index out of range (prefill: < 0 or >= num_slots;
@@ -86,6 +87,9 @@ typedef enum { GDN_FP32 = 0, GDN_BF16 = 1 } gdn_dtype;
 #define GDN_DEV_NONFINITE_FRONTEND 0x8  /* the front end's q, k (and v, gates on the SIMT path) */
 #define GDN_DEV_NONFINITE_CHUNK 0x10    /* the chunk factors: P, U, Wk, decays */
 #define GDN_DEV_NONFINITE_OUT 0x20      /* the layer output o (y) or a final state */
+/* Full attention over a paged cache. */
+#define GDN_DEV_BAD_PAGE 0x40    /* a block-table entry outside [0, num_pages) was needed */
+#define GDN_DEV_BAD_LENGTH 0x80  /* a position, sequence index or length the block table cannot hold */
 
 /* Bits of gdn_dims.flags.
  * GDN_FP32_STATE: prefill keeps every product with the fp32 state in fp32
@@ -434,6 +438,163 @@ int gdn_decode_step_gated_norm(const gdn_dims* dims, const gdn_params* params,
                                void* conv_pool, int64_t num_slots, const void* z,
                                const float* norm_weight, float eps, void* y,
                                int32_t* d_status, gdn_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Full attention: the layers between the Gated DeltaNet ones.  A hybrid model
+ * of this family runs gated full attention with per-head query/key norms and
+ * partial rotary positions in every fourth layer (Vallmo README, "What's
+ * here": gated full attention; oxydllm release notes, New Features, "GGUF
+ * qwen35 architecture": 24 of the 32 layers are linear attention).  For token
+ * t, query head h and key/value head j = h / (h_q / h_kv):
+ *   1. q and k per head: x / sqrt(mean_i x_i^2 + norm_eps) * weight, then the
+ *      first rot_dim channels turned by the token's position (gdn_qk_norm_rope);
+ *   2. k and v stored in a paged cache (gdn_kv_append does 1 on the way);
+ *   3. o = softmax(scale * q k^T over the visible keys) v, optionally times
+ *      sigmoid(gate) (gdn_attn_prefill, gdn_attn_decode).
+ *
+ * Layouts:
+ *   gdn_view     rows of a tensor [tokens][heads][d] whose channels are
+ *                contiguous: element (t, h, i) at data + t * token_stride +
+ *                h * head_stride + i, strides in elements, so that q, k, v and
+ *                the gate may be slices of one projection's output.  Address
+ *                and strides must be multiples of 16 bytes (GDN_EALIGN).
+ *   paged cache  k, v [num_pages][h_kv][page_size][d] IO: the rows of one page
+ *                and head are contiguous.  Token p of sequence b is row
+ *                p % page_size of page block_table[b][p / page_size].
+ * The norm weights are applied as stored, in fp32.  Ownership, streams, graph
+ * capture and errors follow the rules at the top of this file.
+ * ------------------------------------------------------------------------- */
+#define GDN_ROPE_HALF 0         /* channel i turns with channel i + rot_dim / 2 */
+#define GDN_ROPE_INTERLEAVED 1  /* channel 2 i turns with channel 2 i + 1 */
+
+typedef struct {
+  int32_t h_q;       /* query heads; multiple of h_kv */
+  int32_t h_kv;      /* key/value heads */
+  int32_t d;         /* head dim: 64, 128 or 256 */
+  int32_t io;        /* gdn_dtype of q, k, v, gate, o and the cache: GDN_BF16 or GDN_FP16
+                        (gdn_qk_norm_rope and gdn_kv_append: GDN_FP32 too) */
+  int32_t rot_dim;   /* channels rotated: 0 (none) .. d, a multiple of 16 */
+  int32_t rope;      /* GDN_ROPE_HALF or GDN_ROPE_INTERLEAVED */
+  int32_t page_size; /* tokens per cache page: 16, 32, 64 or 128 */
+  float norm_eps;    /* added to the mean of squares inside the root, >= 0 */
+  float scale;       /* softmax scale, > 0; 0 means 1 / sqrt(d) */
+  int32_t flags;     /* 0 or GDN_TEST_WAIT_TIMEOUT (the waits of the attention kernels give up
+                        after 2 ms instead of 4 s); other bits: GDN_EINVAL */
+} gdn_attn_dims;
+
+typedef struct {
+  const void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} gdn_view;
+
+typedef struct {
+  const float* q_norm;    /* [d] fp32, or NULL: q is not normalised */
+  const float* k_norm;    /* [d] fp32, or NULL: k is not normalised */
+  const double* inv_freq; /* [rot_dim / 2] fp64: radians per position of each pair, after any
+                             scaling for long contexts (may be NULL when rot_dim is 0) */
+  float rope_scale;       /* factor on the rotated channels (1 unless the scaling has one) */
+} gdn_rope_params;
+
+typedef struct {
+  void* k;                    /* [num_pages][h_kv][page_size][d] IO, 16-byte aligned */
+  void* v;                    /* the same */
+  const int32_t* block_table; /* [num_seqs][pages_per_seq] int32 (device) */
+  int64_t num_pages;
+  int32_t num_seqs;
+  int32_t pages_per_seq;
+} gdn_kv_cache;
+
+/*
+ * gdn_qk_norm_rope -- per-head RMS norm of queries and keys and the rotation
+ * by position, in one pass: with c, s the cosine and sine of
+ * positions[t] * inv_freq[i] (the angle is reduced in fp64, so positions of
+ * any size keep fp32 accuracy), pair (a, b) -> rope_scale * (a c - b s,
+ * a s + b c); channels from rot_dim on are only normalised.
+ *   q, k       views [n][h_q][d] and [n][h_kv][d] IO; a view with null data
+ *              is left out (its output too)
+ *   positions  [n] int32 (device)
+ *   q_out      [n][h_q][d] IO, k_out [n][h_kv][d] IO, contiguous, 16-byte
+ *              aligned; each may be its own input where that is contiguous
+ * IO is fp32, bf16 or fp16; everything between is fp32, rounded once.
+ */
+int gdn_qk_norm_rope(const gdn_attn_dims* dims, const gdn_rope_params* params, const gdn_view* q,
+                     const gdn_view* k, const int32_t* positions, int64_t n, void* q_out,
+                     void* k_out, gdn_stream_t stream);
+
+/*
+ * gdn_kv_append -- the new tokens' keys and values go into the paged cache,
+ * the keys normed and rotated on the way as gdn_qk_norm_rope defines it; the
+ * queries too, into q_out, when q is given: one launch for a decode step or
+ * a prompt.
+ *   q, k, v    views [n][h_q or h_kv][d] IO (q with null data: left out)
+ *   positions  [n] int32 (device): position of row t in its sequence, which is
+ *              also its place in the cache; < 0 marks a padding row (q_out
+ *              zeroed, nothing stored)
+ *   row_seq    [n] int32 (device): the row's sequence; NULL: row t is
+ *              sequence t (then n <= cache->num_seqs, else GDN_EINVAL)
+ * A row whose sequence is outside [0, num_seqs) or whose position its block
+ * table row cannot hold sets GDN_DEV_BAD_LENGTH; one whose page is outside
+ * [0, num_pages) sets GDN_DEV_BAD_PAGE.  Such a row is not stored (its q_out
+ * is written).  Two rows of one call must not have the same place.
+ */
+int gdn_kv_append(const gdn_attn_dims* dims, const gdn_rope_params* params, const gdn_view* q,
+                  const gdn_view* k, const gdn_view* v, const int32_t* positions,
+                  const int32_t* row_seq, int64_t n, const gdn_kv_cache* cache, void* q_out,
+                  int32_t* d_status, gdn_stream_t stream);
+
+/*
+ * gdn_attn_prefill -- causal attention over packed prompts with grouped heads.
+ * Sequence b has the queries cu_seqlens_q[b] .. cu_seqlens_q[b+1] and the keys
+ * cu_seqlens_kv[b] .. cu_seqlens_kv[b+1]; its queries are the last ones of its
+ * keys, so query i of len_q sees the keys 0 .. i + len_kv - len_q (a query
+ * that sees none gives a row of zeros).
+ *   q, k, v    views [total_q][h_q][d], [total_kv][h_kv][d] IO
+ *   cu_seqlens_q, cu_seqlens_kv  [num_seqs+1] int32 (device); cu_seqlens_kv
+ *              NULL: the same as cu_seqlens_q (then total_kv = total_q).
+ *              0 = cu[0] <= cu[1] <= ... = total, else
+ *              GDN_DEV_BAD_CU_SEQLENS and nothing is written
+ *   gate       view [total_q][h_q][d] IO, or null data: o is multiplied by
+ *              sigmoid(gate)
+ *   o          [total_q][h_q][d] IO, contiguous, 16-byte aligned, not an input
+ * Scores, softmax statistics and the accumulated output are fp32; the softmax
+ * weights are rounded to IO for the product with v.  Keys and values outside a
+ * sequence never reach it, whatever they hold; within one, a non-finite v can
+ * reach the earlier queries of its sequence that share its block of 128 keys
+ * (a weight of zero times it).
+ */
+int gdn_attn_prefill(const gdn_attn_dims* dims, const gdn_view* q, const gdn_view* k,
+                     const gdn_view* v, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                     int32_t num_seqs, int64_t total_q, int64_t total_kv, const gdn_view* gate,
+                     void* o, int32_t* d_status, gdn_stream_t stream);
+
+/* Bytes of device workspace gdn_attn_decode needs for n rows behind a shared
+ * prefix of shared_len tokens (0 on bad arguments). */
+size_t gdn_attn_decode_workspace_size(const gdn_attn_dims* dims, int32_t n, int64_t shared_len);
+
+/*
+ * gdn_attn_decode -- one query token for each of n rows against the paged
+ * cache: row b sees the first seq_lens[b] tokens of sequence b of the cache
+ * (its own token included, once appended).
+ *   q          view [n][h_q][d] IO; n <= cache->num_seqs
+ *   seq_lens   [n] int32 (device); 0 (or less) marks a padding row (o zeroed).
+ *              A length that the block table cannot hold sets
+ *              GDN_DEV_BAD_LENGTH and is cut to what it holds; a page outside
+ *              [0, num_pages) sets GDN_DEV_BAD_PAGE and that row's o is not valid
+ *   shared_len tokens at the start that every sequence of the call shares, a
+ *              multiple of page_size (0: none).  Their pages are read from row
+ *              0 of the block table, once for the whole batch; the entries of
+ *              the other rows there are not looked at
+ *   gate       as in gdn_attn_prefill, [n][h_q][d]
+ *   o          [n][h_q][d] IO, contiguous, 16-byte aligned
+ *   workspace  gdn_attn_decode_workspace_size() bytes, 256-byte aligned,
+ *              clobbered; it needs no initial value
+ * What the cache holds beyond a sequence's length never reaches its output.
+ */
+int gdn_attn_decode(const gdn_attn_dims* dims, const gdn_view* q, const gdn_kv_cache* cache,
+                    const int32_t* seq_lens, int32_t n, int64_t shared_len, const gdn_view* gate,
+                    void* o, void* workspace, size_t workspace_bytes, int32_t* d_status,
+                    gdn_stream_t stream);
 
 /* Static description of a gdn_status code (library plumbing).  The string is
  * owned by the library and valid for the life of the process. */
