@@ -30,6 +30,13 @@ struct Vec8<float> {
     f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w;
     f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
   }
+  // The same channels of lane `src` of a group of `width` lanes.
+  __device__ __forceinline__ void exchange(uint32_t mask, int src, int width) {
+    lo = make_float4(__shfl_sync(mask, lo.x, src, width), __shfl_sync(mask, lo.y, src, width),
+                     __shfl_sync(mask, lo.z, src, width), __shfl_sync(mask, lo.w, src, width));
+    hi = make_float4(__shfl_sync(mask, hi.x, src, width), __shfl_sync(mask, hi.y, src, width),
+                     __shfl_sync(mask, hi.z, src, width), __shfl_sync(mask, hi.w, src, width));
+  }
   __device__ __forceinline__ void set(const float (&f)[8]) {
     lo = make_float4(f[0], f[1], f[2], f[3]);
     hi = make_float4(f[4], f[5], f[6], f[7]);
@@ -72,6 +79,10 @@ struct Vec8 {
       f[2 * i] = v.x;
       f[2 * i + 1] = v.y;
     }
+  }
+  __device__ __forceinline__ void exchange(uint32_t mask, int src, int width) {
+    w = make_uint4(__shfl_sync(mask, w.x, src, width), __shfl_sync(mask, w.y, src, width),
+                   __shfl_sync(mask, w.z, src, width), __shfl_sync(mask, w.w, src, width));
   }
   __device__ __forceinline__ void set(const float (&f)[8]) {
     w = make_uint4(pack2<IO>(f[0], f[1]), pack2<IO>(f[2], f[3]), pack2<IO>(f[4], f[5]),

@@ -34,23 +34,27 @@ constexpr int ROWS = 16;              // query heads per item, at most
 constexpr int DEC_WARPS = 4;          // consumer warps, 16 keys of a block each
 constexpr int DEC_THREADS = 32 * (DEC_WARPS + 1);
 constexpr int DEC_MAX_STAGES = 8;
+constexpr int DEC_CTAS = 152;         // one per SM: the ring takes an SM's shared memory
 
 template <int D>
 struct DecCfg {
   static constexpr uint32_t TILE = KEYS * D * 2;           // one of K, V
   static constexpr uint32_t STAGE = 2 * TILE;
   static constexpr uint32_t OBUF = ROWS * D * 4;           // joining the four warps' O
-  static constexpr int FIT = (int)((232448u - 4096u - OBUF) / STAGE);
+  static constexpr uint32_t Q_ROW = D * 2 + 16;            // padded: no bank conflicts in ldmatrix
+  static constexpr uint32_t HEAD = (1024 + ROWS * Q_ROW + OBUF + 1023) / 1024 * 1024;
+  static constexpr int FIT = (int)((232448u - HEAD) / STAGE);
   static constexpr int STAGES = FIT < DEC_MAX_STAGES ? FIT : DEC_MAX_STAGES;
-  static constexpr uint32_t SMEM = 4096 + OBUF + STAGES * STAGE;
+  static constexpr uint32_t SMEM = HEAD + STAGES * STAGE;
 };
 
 struct __align__(16) DecShared {
-  uint64_t full[DEC_MAX_STAGES], empty[DEC_MAX_STAGES];
+  uint64_t full[DEC_MAX_STAGES], empty[DEC_MAX_STAGES], q_full, q_empty;
   float m[DEC_WARPS][ROWS], l[DEC_WARPS][ROWS];
   int64_t sum[DEC_WARPS + 1], found_first;
   int32_t found;
 };
+static_assert(sizeof(DecShared) <= 1024, "shared bookkeeping");
 
 struct DecArgs {
   GdnAttnArgs a;
@@ -144,8 +148,30 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(kb), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+// The next kernel of the stream may start once every CTA has said so; what it
+// reads of this one it waits for with pdl_wait.
+__device__ __forceinline__ void pdl_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void consumers_bar() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * DEC_WARPS) : "memory");
+}
+
+// First query head and number of query heads of item hs of a sequence.
+__device__ __forceinline__ int item_head(const DecArgs& p, int hs) {
+  return hs / p.subs * (p.a.h_q / p.a.h_kv) + hs % p.subs * ROWS;
+}
+__device__ __forceinline__ int item_rows(const DecArgs& p, int hs) {
+  return min(p.rows, p.a.h_q / p.a.h_kv - hs % p.subs * ROWS);
 }
 
 // The run [w, end) of units, item by item.
@@ -189,37 +215,42 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
   using C = DecCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   DecShared* sh = reinterpret_cast<DecShared*>(smem);
-  float* obuf = reinterpret_cast<float*>(smem + 4096);
+  const uint32_t q_smem = smem_u32(smem) + 1024;
+  float* obuf = reinterpret_cast<float*>(smem + 1024 + ROWS * C::Q_ROW);
   const GdnAttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t ring = smem_u32(smem) + 4096 + C::OBUF;
+  const uint32_t ring = smem_u32(smem) + C::HEAD;
   const int heads = a.h_kv * p.subs;
   const int n = (int)a.total_q;
 
-  // ---- this CTA's run of units ----
-  int64_t total = 0;
-  for (int base = 0; base < n; base += DEC_THREADS) {
-    const int b = base + tid;
-    int64_t before;
-    total += block_scan(b < n ? blocks_of(own_keys(p, b)) * heads : 0, sh->sum, DEC_WARPS + 1,
-                        before);
-  }
-  const int64_t runs = runs_of(p, total), c = blockIdx.x;
-  const int64_t w0 = c < runs ? total * c / runs : 0, w1 = c < runs ? total * (c + 1) / runs : 0;
+  pdl_launch();
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], DEC_WARPS);
     }
+    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, DEC_WARPS);
     fence_mbar_init();
   }
+  // ---- this CTA's run of units ----
+  int64_t total = 0, units = 0, before = 0;
+  for (int base = 0; base < n; base += DEC_THREADS) {
+    const int b = base + tid;
+    units = b < n ? blocks_of(own_keys(p, b)) * heads : 0;
+    total += block_scan(units, sh->sum, DEC_WARPS + 1, before);
+  }
+  const int64_t runs = runs_of(p, total), c = blockIdx.x;
+  const int64_t w0 = c < runs ? total * c / runs : 0, w1 = c < runs ? total * (c + 1) / runs : 0;
   int64_t seen = 0;
   for (int base = 0; base < n && w0 < w1; base += DEC_THREADS) {
     const int b = base + tid;
-    const int64_t u = b < n ? blocks_of(own_keys(p, b)) * heads : 0;
-    int64_t before;
-    const int64_t all = block_scan(u, sh->sum, DEC_WARPS + 1, before);
-    if (w0 >= seen + before && w0 < seen + before + u) {
+    int64_t all = total;
+    if (n > DEC_THREADS) {   // else the scan above has it all
+      units = b < n ? blocks_of(own_keys(p, b)) * heads : 0;
+      all = block_scan(units, sh->sum, DEC_WARPS + 1, before);
+    }
+    if (w0 >= seen + before && w0 < seen + before + units) {
       sh->found = b;
       sh->found_first = seen + before;
     }
@@ -238,7 +269,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
     walk.item_first = sh->found_first + walk.hs * walk.nt;
     Segment g;
     bool ok = true;
-    int j = 0;                       // blocks so far: the ring's position
+    int j = 0, items = 0;            // blocks and items so far: the rings' positions
     if (warp == DEC_WARPS) {
       // ---- loads: each lane one box of the block (K or V, rows, channels) ----
       const int per_kv = (KEYS / p.box_rows) * (D / 64);
@@ -248,6 +279,20 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
       while (ok && walk.next(p, heads, g)) {
         const int kvh = g.hs / p.subs;
         const int32_t* table = a.cache.block_table + (int64_t)g.b * a.cache.pages_per_seq;
+        // the item's queries, once the consumers have the last item's in registers
+        if (items > 0) ok = mbar_wait(&sh->q_empty, (items - 1) & 1, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++items;
+        const int h0 = item_head(p, g.hs);
+        const int rows = item_rows(p, g.hs);
+        if (lane == 0) mbar_expect_tx(&sh->q_full, (uint32_t)rows * D * 2);
+        __syncwarp();
+        if (lane < rows)
+          bulk_load(q_smem + (uint32_t)lane * C::Q_ROW,
+                    reinterpret_cast<const IO*>(a.q.data) + (int64_t)g.b * a.q.token_stride +
+                        (int64_t)(h0 + lane) * a.q.head_stride,
+                    D * 2, &sh->q_full);
         auto page_at = [&](int64_t t) {
           const int64_t pos = t * KEYS + r;
           return lane < 2 * per_kv && t < g.t1 && pos < g.keys
@@ -263,10 +308,10 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const int64_t left = g.keys - t * KEYS;
-          const int rows = (int)min((int64_t)KEYS, (left + p.box_rows - 1) / p.box_rows * p.box_rows);
-          if (lane == 0) mbar_expect_tx(&sh->full[s], (uint32_t)rows * D * 4);
+          const int there = (int)min((int64_t)KEYS, (left + p.box_rows - 1) / p.box_rows * p.box_rows);
+          if (lane == 0) mbar_expect_tx(&sh->full[s], (uint32_t)there * D * 4);
           __syncwarp();
-          if (lane < 2 * per_kv && r < rows) {
+          if (lane < 2 * per_kv && r < there) {
             if (page < 0 || page >= a.cache.num_pages) {
               set_status(a.d_status, GDN_DEV_BAD_PAGE);
               page = 0;
@@ -290,22 +335,20 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
       const int k_tok = warp * 16 + (mi >> 1) * 8 + mr, k_d = (mi & 1) * 8;
       const int v_tok = warp * 16 + (mi & 1) * 8 + mr, v_d = (mi >> 1) * 8;
       while (walk.next(p, heads, g)) {
-        const int kvh = g.hs / p.subs, sub = g.hs % p.subs;
-        const int group = a.h_q / a.h_kv;
-        const int h0 = kvh * group + sub * ROWS;
-        const int rows = min(p.rows, group - sub * ROWS);
-        const IO* q = reinterpret_cast<const IO*>(a.q.data) + (int64_t)g.b * a.q.token_stride +
-                      h0 * a.q.head_stride;
+        const int h0 = item_head(p, g.hs);
+        const int rows = item_rows(p, g.hs);
+        if (ok) ok = mbar_wait(&sh->q_full, items & 1, a.wait_ns);
+        __syncwarp();
+        ++items;
+        // rows past the item's heads hold anything: they stay in their own rows
         uint32_t qa[D / 16][4];
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = qrow + (e & 1) * 8, i = ks * 16 + qcol + (e >> 1) * 8;
-            qa[ks][e] = r < rows
-                            ? *reinterpret_cast<const uint32_t*>(q + r * a.q.head_stride + i)
-                            : 0u;
-          }
+          ldsm4(q_smem + (uint32_t)((mi & 1) * 8 + mr) * C::Q_ROW +
+                    (uint32_t)(ks * 32 + (mi >> 1) * 16),
+                qa[ks]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_empty);
         float o[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -424,19 +467,23 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
           for (int w = 0; w < DEC_WARPS; ++w) mm = fmaxf(mm, sh->m[w][qrow + 8 * r]);
           f[r] = mm == -INFINITY ? 0.f : fast_exp2((m[r] - mm) * c);
         }
-        // one quarter of the channels at a time, each warp at another one: every
-        // sum has a fixed order
+        // Up to four rows: each warp its own slab, summed on the way out.  More
+        // do not fit, and the warps add up in one slab, a quarter of the channels
+        // at a time, each at another one.  Either way every sum has a fixed order.
+        const int slabs = rows <= ROWS / DEC_WARPS ? DEC_WARPS : 1;
 #pragma unroll
         for (int st = 0; st < DEC_WARPS; ++st) {
+          if (slabs > 1 && st > 0) break;
           const int qt = (warp + st) % DEC_WARPS;
+          float* slab = obuf + (slabs > 1 ? warp * rows * D : 0);
 #pragma unroll
           for (int i = 0; i < D / 8; ++i) {
-            if (i / (D / 32) != qt) continue;
+            if (slabs == 1 && i / (D / 32) != qt) continue;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const int row = qrow + 8 * r;
               if (row >= rows) continue;
-              float2* dst = reinterpret_cast<float2*>(obuf + row * D + i * 8 + qcol);
+              float2* dst = reinterpret_cast<float2*>(slab + row * D + i * 8 + qcol);
               float2 v = make_float2(o[i][2 * r] * f[r], o[i][2 * r + 1] * f[r]);
               if (st > 0) {
                 const float2 w = *dst;
@@ -461,8 +508,14 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
 #pragma unroll
           for (int w = 0; w < DEC_WARPS; ++w)
             ll += mm == -INFINITY ? sh->l[w][row] : sh->l[w][row] * fast_exp2((sh->m[w][row] - mm) * c);
-          const float4 v0 = *reinterpret_cast<const float4*>(obuf + row * D + col);
-          const float4 v1 = *reinterpret_cast<const float4*>(obuf + row * D + col + 4);
+          float4 v0 = *reinterpret_cast<const float4*>(obuf + row * D + col);
+          float4 v1 = *reinterpret_cast<const float4*>(obuf + row * D + col + 4);
+          for (int w = 1; w < slabs; ++w) {
+            const float4 u0 = *reinterpret_cast<const float4*>(obuf + (w * rows + row) * D + col);
+            const float4 u1 = *reinterpret_cast<const float4*>(obuf + (w * rows + row) * D + col + 4);
+            v0.x += u0.x; v0.y += u0.y; v0.z += u0.z; v0.w += u0.w;
+            v1.x += u1.x; v1.y += u1.y; v1.z += u1.z; v1.w += u1.w;
+          }
           if (direct) {
             const float inv = 1.0f / ll;
             float y[8] = {v0.x * inv, v0.y * inv, v0.z * inv, v0.w * inv,
@@ -491,31 +544,41 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
     }
     if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
   }
+  // The merge waits for this kernel, and reads the prefix pass's partials too:
+  // this kernel may have started before that pass had ended.
+  pdl_wait();
 }
 
 // Joins the partial results of one item (sequence, key/value head, sub):
 //   M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// One CTA per item.  The partials' statistics are fetched side by side and
+// turned into one factor per partial and row first, so that the sums over the
+// partial outputs are independent loads (one after the other they would cost a
+// memory latency each).
 constexpr int MERGE_THREADS = 256;
+constexpr int MAX_PARTS = 2 * DEC_CTAS;   // of the prefix pass and of this one
 
 template <typename IO, int D>
 __global__ void __launch_bounds__(MERGE_THREADS)
     attn_merge_kernel(const __grid_constant__ DecArgs p) {
   __shared__ int64_t sums[MERGE_THREADS / 32];
+  __shared__ float2 ml[MAX_PARTS * ROWS];   // [part][row]: statistics, then (factor, -)
+  __shared__ int64_t first_row[MAX_PARTS];
+  __shared__ float inv_l[ROWS];
   const GdnAttnArgs& a = p.a;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int heads = a.h_kv * p.subs;
   const int n = (int)a.total_q;
   const int b = blockIdx.x / heads, hs = blockIdx.x % heads;
-  const int group = a.h_q / a.h_kv, kvh = hs / p.subs, sub = hs % p.subs;
-  const int h0 = kvh * group + sub * ROWS;
-  const int rows = min(p.rows, group - sub * ROWS);
+  const int h0 = item_head(p, hs);
+  const int rows = item_rows(p, hs);
   int64_t total = 0, mine = 0;
   for (int base = 0; base < n; base += MERGE_THREADS) {
     const int i = base + tid;
-    const int64_t u = i < n ? blocks_of(own_keys(p, i)) * heads : 0;
     int64_t before;
+    const int64_t u = i < n ? blocks_of(own_keys(p, i)) * heads : 0;
     total += block_scan(u, sums, MERGE_THREADS / 32, before);
-    mine += block_scan(i < b ? u : 0, sums, MERGE_THREADS / 32, before);
+    if (base <= b) mine += block_scan(i < b ? u : 0, sums, MERGE_THREADS / 32, before);
   }
   const int64_t nt = blocks_of(own_keys(p, b));
   const int64_t u0 = mine + hs * nt, u1 = u0 + nt;
@@ -527,47 +590,65 @@ __global__ void __launch_bounds__(MERGE_THREADS)
     c0 = ((u0 + 1) * runs - 1) / total;
     c1 = (u1 * runs - 1) / total;
     whole = c0 == c1;
-    if (whole && p.prefix == 0) return;   // written already
   }
-  const int own = nt > 0 ? (int)(c1 - c0 + 1) : 0;
-  auto row_of = [&](int i, int row) -> int64_t {   // partial i's row of the workspace
-    if (i < p.prefix) return ((int64_t)i * n + b) * a.h_q + h0 + row;
-    if (whole) return p.base_row + (2 * (int64_t)p.ctas + (int64_t)b * heads + hs) * p.rows + row;
-    const int64_t c = c0 + (i - p.prefix);
-    // a run that starts inside the item left its first partial, else its last
-    const int64_t slot = 2 * c + (total * c / runs > u0 ? 0 : 1);
-    return p.base_row + slot * p.rows + row;
-  };
-  const int parts = p.prefix + own;
+  const int parts = p.prefix + (int)(c1 - c0 + 1);
+  for (int i = tid; i < parts; i += MERGE_THREADS) {   // partial i's first row of the workspace
+    if (i < p.prefix) {
+      first_row[i] = ((int64_t)i * n + b) * a.h_q + h0;
+    } else if (whole) {
+      first_row[i] = p.base_row + (2 * (int64_t)p.ctas + (int64_t)b * heads + hs) * p.rows;
+    } else {
+      const int64_t c = c0 + (i - p.prefix);
+      // a run that starts inside the item left its first partial, else its last
+      first_row[i] = p.base_row + (2 * c + (total * c / runs > u0 ? 0 : 1)) * p.rows;
+    }
+  }
+  pdl_wait();
+  if (nt > 0 && whole && p.prefix == 0) return;   // written already
+  __syncthreads();
+  for (int i = tid; i < parts * rows; i += MERGE_THREADS)
+    ml[i] = a.part_ml[first_row[i / rows] + i % rows];
+  __syncthreads();
+  for (int row = warp; row < rows; row += MERGE_THREADS / 32) {
+    float mm = -INFINITY, ll = 0.f;
+    for (int i = lane; i < parts; i += 32)
+      if (ml[i * rows + row].y != 0.f) mm = fmaxf(mm, ml[i * rows + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    for (int i = lane; i < parts; i += 32) {
+      const float2 v = ml[i * rows + row];
+      // a partial that saw no key has factor 0, and its O was not written
+      const float f = v.y == 0.f ? 0.f : fast_exp2(v.x - mm);
+      ll += v.y == 0.f ? 0.f : f * v.y;
+      ml[i * rows + row].x = f;
+    }
+    ll = warp_sum(ll);
+    if (lane == 0) inv_l[row] = ll == 0.f ? 0.f : 1.0f / ll;
+  }
+  __syncthreads();
   for (int x = tid; x < rows * (D / 8); x += MERGE_THREADS) {
     const int row = x / (D / 8), col = x % (D / 8) * 8;
-    float mm = -INFINITY;
+    float y[8] = {};
+#pragma unroll 8
     for (int i = 0; i < parts; ++i) {
-      const float2 ml = a.part_ml[row_of(i, row)];
-      if (ml.y != 0.f) mm = fmaxf(mm, ml.x);
+      const float2 w = ml[i * rows + row];
+      const float4* src =
+          reinterpret_cast<const float4*>(a.part_o + (first_row[i] + row) * D + col);
+      const float4 v0 = src[0], v1 = src[1];
+      if (w.y != 0.f) {
+        y[0] = fmaf(w.x, v0.x, y[0]);
+        y[1] = fmaf(w.x, v0.y, y[1]);
+        y[2] = fmaf(w.x, v0.z, y[2]);
+        y[3] = fmaf(w.x, v0.w, y[3]);
+        y[4] = fmaf(w.x, v1.x, y[4]);
+        y[5] = fmaf(w.x, v1.y, y[5]);
+        y[6] = fmaf(w.x, v1.z, y[6]);
+        y[7] = fmaf(w.x, v1.w, y[7]);
+      }
     }
-    float ll = 0.f, y[8] = {};
-    for (int i = 0; i < parts; ++i) {
-      const int64_t r = row_of(i, row);
-      const float2 ml = a.part_ml[r];
-      if (ml.y == 0.f) continue;   // saw no key; its O was not written
-      const float f = fast_exp2(ml.x - mm);
-      ll += f * ml.y;
-      const float4 v0 = *reinterpret_cast<const float4*>(a.part_o + r * D + col);
-      const float4 v1 = *reinterpret_cast<const float4*>(a.part_o + r * D + col + 4);
-      y[0] = fmaf(f, v0.x, y[0]);
-      y[1] = fmaf(f, v0.y, y[1]);
-      y[2] = fmaf(f, v0.z, y[2]);
-      y[3] = fmaf(f, v0.w, y[3]);
-      y[4] = fmaf(f, v1.x, y[4]);
-      y[5] = fmaf(f, v1.y, y[5]);
-      y[6] = fmaf(f, v1.z, y[6]);
-      y[7] = fmaf(f, v1.w, y[7]);
-    }
-    const float inv = ll == 0.f ? 0.f : 1.0f / ll;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= inv;
-    if (a.gate.data && ll != 0.f) {
+    for (int e = 0; e < 8; ++e) y[e] *= inv_l[row];
+    if (a.gate.data && inv_l[row] != 0.f) {
       Vec8<IO> gv;
       gv.load(reinterpret_cast<const IO*>(a.gate.data) + (int64_t)b * a.gate.token_stride +
               (h0 + row) * a.gate.head_stride + col);
@@ -588,8 +669,6 @@ static int group_rows(int h_q, int h_kv) {
   const int g = h_q / h_kv;
   return g < ROWS ? g : ROWS;
 }
-
-constexpr int DEC_CTAS = 152;   // one per SM: the ring takes an SM's shared memory
 
 template <typename IO, int D>
 static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
@@ -631,11 +710,24 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
       return e;
     if (dev >= 0 && dev < 64) opted_in[dev] = 1;
   }
-  kernel<<<p.ctas, DEC_THREADS, C::SMEM, s>>>(p, kmap, vmap);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  attn_merge_kernel<IO, D>
-      <<<(unsigned)(a.total_q * a.h_kv * p.subs), MERGE_THREADS, 0, s>>>(p);
-  return cudaGetLastError();
+  // This pass needs nothing of the prefix pass and starts on SMs as they become
+  // free of it; the merge's search for its partials overlaps this pass's end.
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(DEC_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 0 ? 1 : 0;
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, p, kmap, vmap)) != cudaSuccess) return e;
+  cfg.gridDim = dim3((unsigned)(a.total_q * a.h_kv * p.subs));
+  cfg.blockDim = dim3(MERGE_THREADS);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_merge_kernel<IO, D>, p);
 }
 
 template <typename IO>

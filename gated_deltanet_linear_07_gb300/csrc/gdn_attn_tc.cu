@@ -235,6 +235,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[30]), "r"(v[31])
       : "memory");
 }
+// A whole 32-byte sector by one thread: rows are a thread each, so narrower
+// stores would reach L2 as parts of sectors.
+__device__ __forceinline__ void st_global_32b(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                              uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                   __cvta_generic_to_global(p)),
+               "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
+               : "memory");
+}
 __device__ __forceinline__ void pair_bar(int id) {   // the two warps that share 32 rows
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
@@ -336,6 +345,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const uint32_t rank = CG == 2 ? cta_rank() : 0u;
   const uint32_t q_smem = smem_u32(smem) + MISC_BYTES;
   const uint32_t ring = q_smem + C::Q_BYTES;
+
+  // the per-sequence pass of a decode needs nothing of this one but its SMs
+  if (PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- which rows and which keys ----
   const int gp = 1 << p.gp_shift;
@@ -653,11 +665,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tmem_ld32_nowait(tmem + lanes + C::TMEM_O + (uint32_t)col, o);
         tmem_wait_ld(o);
         if (live && l > 0.f) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + slot * D + col);
+          float* dst = a.part_o + slot * D + col;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          for (int k = 0; k < 32; k += 8)
+            st_global_32b(dst + k, o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5], o[k + 6],
+                          o[k + 7]);
         }
       }
     } else {
@@ -668,6 +680,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                                  h * a.gate.head_stride
                            : nullptr;
       IO* out = reinterpret_cast<IO*>(a.o) + (t * a.h_q + h) * D;
+      const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
 #pragma unroll 1
       for (int n = 0; n < D / 2; n += 32) {
         uint32_t o[32];
@@ -681,24 +694,31 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         if (live) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            float f[8];
+          for (int k = 0; k < 32; k += 16) {
+            Vec8<IO> ov[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[k + e]) * inv;
-            if (l == 0.f)
+            for (int v = 0; v < 2; ++v) {
+              float f[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = 0.f;
-            if (gate) {
-              Vec8<IO> gv;
-              gv.load(gate + col + k);
-              float g[8];
-              gv.get(g);
+              for (int e = 0; e < 8; ++e)
+                f[e] = l == 0.f ? 0.f : __uint_as_float(o[k + 8 * v + e]) * inv;
+              if (gate) {
+                Vec8<IO> gv;
+                gv.load(gate + col + k + 8 * v);
+                float g[8];
+                gv.get(g);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] *= gate_sigmoid(g[e]);
+                for (int e = 0; e < 8; ++e) f[e] *= gate_sigmoid(g[e]);
+              }
+              ov[v].set(f);
             }
-            Vec8<IO> ov;
-            ov.set(f);
-            ov.store(out + col + k);
+            if (wide) {
+              st_global_32b(out + col + k, ov[0].w.x, ov[0].w.y, ov[0].w.z, ov[0].w.w, ov[1].w.x,
+                            ov[1].w.y, ov[1].w.z, ov[1].w.w);
+            } else {
+              ov[0].store(out + col + k);
+              ov[1].store(out + col + k + 8);
+            }
           }
         }
       }

@@ -188,3 +188,16 @@ def test_on_another_stream_and_from_a_graph(gpu_lib):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, plain)
+
+
+def test_an_output_on_a_16_byte_boundary(gpu_lib):
+    g = torch.Generator().manual_seed(25)
+    n, d = 130, 128
+    q, k, v = (normal(g, n, 2, d).cuda() for _ in range(3))
+    dims, cu = gdn.make_attn_dims(2, 2, d), _ints([0, n])
+    plain = gdn.gdn_attn_prefill(dims, q, k, v, cu)
+    room = torch.zeros(n * 2 * d + 8, dtype=torch.bfloat16, device="cuda")
+    o = room[8:].view(n, 2, d)
+    assert o.data_ptr() % 32 == 16
+    gdn.gdn_attn_prefill(dims, q, k, v, cu, o=o)
+    assert torch.equal(o, plain) and (room[:8] == 0).all()
