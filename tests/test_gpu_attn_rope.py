@@ -39,6 +39,9 @@ CASES = [   # n, hq, hkv, d, rot, layout, io, start
     (64, 2, 1, 256, 0, "half", "bf16", 0),              # norms alone
     (2049, 8, 2, 64, 32, "interleaved", "fp16", 5),     # four tokens per CTA, a ragged last one
     (2050, 5, 1, 128, 128, "half", "bf16", 0),
+    (1024, 16, 4, 256, 64, "half", "bf16", 500_000),
+    (1100, 40, 8, 256, 256, "half", "fp32", 3),         # a token's rows in several parts
+    (1500, 96, 2, 128, 32, "interleaved", "bf16", 9),
 ]
 
 
@@ -83,6 +86,37 @@ def test_norm_of_zero_and_large_rows(gpu_lib):
     w = torch.ones(d, device="cuda")
     q, _ = gdn.gdn_qk_norm_rope(dims, x.cuda(), None, w, None, None, pos)
     assert (q[0] == 0).all() and (q[1] == 1).all()
+
+
+def test_append_of_many_rows_repeats_the_few(gpu_lib):
+    """The kernels for many and for few tokens give the same bits: a prompt
+    appended at once and the same prompt in pieces."""
+    n, hq, hkv, d, page = 1303, 4, 2, 256, 64
+    i = _inputs(31, n, hq, hkv, d, 64, "bf16", 0)
+    dims = gdn.make_attn_dims(hq, hkv, d, rot_dim=64, page_size=page)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    pos[700] = -1
+    seq = torch.zeros(n, dtype=torch.int32, device="cuda")
+    table = torch.arange(21, dtype=torch.int32, device="cuda").flip(0).view(1, 21).contiguous()
+    made = []
+    for cuts in ([0, n], [0, 1, 130, 1000, n]):
+        kc = torch.zeros(21, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+        vc, qs = torch.zeros_like(kc), []
+        for a, b in zip(cuts, cuts[1:]):
+            qs.append(gdn.gdn_kv_append(dims, i["qg"][a:b, :, :d], i["kv"][a:b, :hkv],
+                                        i["kv"][a:b, hkv:], i["wq"], i["wk"], i["freq"], pos[a:b], kc,
+                                        vc, table, row_seq=seq[a:b]))
+        made.append((torch.cat(qs), kc, vc))
+    for one, many in zip(*made):
+        assert torch.equal(one, many)
+    qg, kv, wq, wk, _, freq = i["cpu"]
+    live = torch.arange(n) != 700
+    p = pos.cpu()[live]
+    _check(made[0][0][live.cuda()], qg[live][:, :, :d], wq, p, freq, "half", torch.bfloat16, "q")
+    assert (made[0][0][700] == 0).all()
+    pg, off = 20 - p.long() // page, p.long() % page
+    _check(made[0][1].cpu()[pg, :, off], kv[live][:, :hkv], wk, p, freq, "half", torch.bfloat16, "k")
+    assert torch.equal(made[0][2].cpu()[pg, :, off], kv[live][:, hkv:])
 
 
 @pytest.mark.parametrize("io,d,page,layout", [("bf16", 256, 64, "half"), ("fp16", 128, 16, "half"),
