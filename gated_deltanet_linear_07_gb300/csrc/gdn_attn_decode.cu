@@ -387,18 +387,19 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
               mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
               mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2));
             }
-            // the reference maximum may lag by 2^8: see gdn_attn_tc.cu
-            bool far = false;
+            // The reference maximum may lag by 2^8: see gdn_attn_tc.cu.  A row's
+            // follows from the row alone, and rows without a head ask for nothing.
+            bool far[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              far |= mt[r] > m[r] && (m[r] == -INFINITY || (mt[r] - m[r]) * c > 8.0f);
-            if (__any_sync(0xffffffffu, far)) {
+              far[r] = qrow + 8 * r < rows && mt[r] > m[r] &&
+                       (m[r] == -INFINITY || (mt[r] - m[r]) * c > 8.0f);
+            if (__any_sync(0xffffffffu, far[0] || far[1])) {
               float f[2];
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
-                const float mn = fmaxf(m[r], mt[r]);
-                f[r] = fast_exp2((m[r] - (mn == -INFINITY ? 0.f : mn)) * c);
-                m[r] = mn;
+                f[r] = far[r] ? fast_exp2((m[r] - mt[r]) * c) : 1.f;
+                m[r] = far[r] ? mt[r] : m[r];
                 l[r] *= f[r];
               }
 #pragma unroll

@@ -53,12 +53,13 @@ struct TcCfg {
   static constexpr int FIT = (int)((232448u - MISC_BYTES - Q_BYTES) / STAGE);
   static constexpr int RING = FIT < MAX_RING ? FIT : MAX_RING;
   static constexpr uint32_t SMEM = MISC_BYTES + Q_BYTES + RING * STAGE;
-  static constexpr uint32_t TMEM_O = 256;   // after the two S buffers
+  static constexpr int NS = D == 256 ? 2 : 3;        // S buffers: 512 columns less O's
+  static constexpr uint32_t TMEM_O = NS * BN;
 };
 
 struct __align__(16) TcShared {
   uint64_t full[MAX_RING], empty[MAX_RING];
-  uint64_t q_full, s_full[2], p_ready[2], o_done, v_tail;
+  uint64_t q_full, s_full[3], p_ready[3], o_done[3], v_tail;
   uint32_t tmem;
   int32_t seq, tile, bad;
   int32_t scan[12];
@@ -82,41 +83,39 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+// Arrive on another CTA's mbarrier.  What the two CTAs hand over lies in tensor
+// memory, ordered by the tcgen05 fences, so a release at cluster scope (a memory
+// barrier: it was the softmax warps' longest stall, 2.2 of 7.5 cycles per issue)
+// is left to the one block whose V rows were cleared in shared memory.
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
 }
-template <int CG>
-__device__ __forceinline__ bool try_wait_scope(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  if (CG == 2) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  }
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
   return ok != 0;
 }
 // Bounded wait; once one has run out (ok false) the later ones return at once.
-template <int CG>
 __device__ __forceinline__ void wait_on(bool& ok, uint64_t* bar, uint32_t parity,
                                         uint64_t budget_ns) {
+  if (ok) ok = mbar_wait(bar, parity, budget_ns);
+}
+// The same for arrivals with a release at cluster scope.
+__device__ __forceinline__ void wait_on_cluster(bool& ok, uint64_t* bar, uint32_t parity,
+                                                uint64_t budget_ns) {
   if (!ok) return;
-  const uint32_t addr = smem_u32(bar);
-  if (try_wait_scope<CG>(addr, parity)) return;
   const uint64_t t0 = globaltimer_ns();
-  while (!try_wait_scope<CG>(addr, parity))
+  while (!try_wait_cluster(smem_u32(bar), parity))
     if (globaltimer_ns() - t0 > budget_ns) {
       ok = false;
       return;
@@ -392,11 +391,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       mbar_init(&sh->empty[s], 1);
     }
     mbar_init(&sh->q_full, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < C::NS; ++s) {
       mbar_init(&sh->s_full[s], 1);
       mbar_init(&sh->p_ready[s], 8 * CG);
+      mbar_init(&sh->o_done[s], 1);
     }
-    mbar_init(&sh->o_done, 1);
     mbar_init(&sh->v_tail, 1);
     fence_mbar_init();
   }
@@ -406,7 +405,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
-  bool ok = (smem_u32(smem) & 1023u) == 0 && blocks >= 0;
+  bool ok = (smem_u32(smem) & 1023u) == 0;
+  constexpr int NS = C::NS, AHEAD = NS - 1;   // S blocks formed ahead of the products with V
 
   if (warp == WARP_LOAD && lane == 0 && blocks > 0 && ok) {
     // ---- TMA loads; in a pair every copy reports to the first CTA's barrier ----
@@ -437,10 +437,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
     };
     int j = 0;
-    for (int i = 0; i <= blocks && ok; ++i) {
+    for (int i = 0; i < blocks + AHEAD && ok; ++i) {
       if (i < blocks) {   // K block i: this CTA's share of its rows
         const int s = j % C::RING;
-        if (j >= C::RING) wait_on<CG>(ok, &sh->empty[s], ((j / C::RING) - 1) & 1, a.wait_ns);
+        if (j >= C::RING) wait_on(ok, &sh->empty[s], ((j / C::RING) - 1) & 1, a.wait_ns);
         if (!ok) break;
         const int64_t t = (int64_t)(first_block + i) * BN;
         const int n = BN / CG;
@@ -453,13 +453,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                   D / 64, lead(&sh->full[s]));
         ++j;
       }
-      if (i > 0) {        // V block i - 1: this CTA's share of its channels
+      if (i >= AHEAD) {   // V block i - AHEAD: this CTA's share of its channels
         const int s = j % C::RING;
-        if (j >= C::RING) wait_on<CG>(ok, &sh->empty[s], ((j / C::RING) - 1) & 1, a.wait_ns);
+        if (j >= C::RING) wait_on(ok, &sh->empty[s], ((j / C::RING) - 1) & 1, a.wait_ns);
         if (!ok) break;
-        const int64_t t = (int64_t)(first_block + i - 1) * BN;
+        const int64_t t = (int64_t)(first_block + i - AHEAD) * BN;
         const uint32_t bytes = (uint32_t)rows_of(t, BN, p.v_rows) * (D / CG) * 2;
-        const bool own = tail && i == blocks;   // reports here: this CTA clears its rows past the end
+        const bool own = tail && i == blocks + AHEAD - 1;   // reports here: this CTA clears its rows past the end
         if (own)
           mbar_expect_tx(&sh->v_tail, bytes);
         else if (rank == 0)
@@ -478,36 +478,39 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     int j = 0;
     auto scores = [&](int i) {
       const int s = j % C::RING;
-      wait_on<CG>(ok, &sh->full[s], (j / C::RING) & 1, a.wait_ns);
+      wait_on(ok, &sh->full[s], (j / C::RING) & 1, a.wait_ns);
       ++j;
       if (!ok) return;
       tc_fence_after();
       const uint32_t kt = ring + (uint32_t)s * C::STAGE;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
-        mma_ss_cg<CG>(tmem + (uint32_t)(i & 1) * BN, sdesc_kmaj(q_smem, BM, ks),
+        mma_ss_cg<CG>(tmem + (uint32_t)(i % NS) * BN, sdesc_kmaj(q_smem, BM, ks),
                       sdesc_kmaj(kt, BN / CG, ks), id_s, ks > 0 ? 1u : 0u);
       commit_cg<CG>(&sh->empty[s]);
-      commit_cg<CG>(&sh->s_full[i & 1]);
+      commit_cg<CG>(&sh->s_full[i % NS]);
     };
-    wait_on<CG>(ok, &sh->q_full, 0, a.wait_ns);
-    if (ok) scores(0);
+    wait_on(ok, &sh->q_full, 0, a.wait_ns);
+    for (int i = 0; i < AHEAD && i < blocks && ok; ++i) scores(i);
     for (int i = 0; i < blocks && ok; ++i) {
-      if (i + 1 < blocks) scores(i + 1);
+      if (i + AHEAD < blocks) scores(i + AHEAD);
       const int s = j % C::RING;
-      if (!(tail && i == blocks - 1)) wait_on<CG>(ok, &sh->full[s], (j / C::RING) & 1, a.wait_ns);
+      if (!(tail && i == blocks - 1)) wait_on(ok, &sh->full[s], (j / C::RING) & 1, a.wait_ns);
       ++j;
-      wait_on<CG>(ok, &sh->p_ready[i & 1], (i >> 1) & 1, a.wait_ns);
+      if (tail && i == blocks - 1)
+        wait_on_cluster(ok, &sh->p_ready[i % NS], (i / NS) & 1, a.wait_ns);
+      else
+        wait_on(ok, &sh->p_ready[i % NS], (i / NS) & 1, a.wait_ns);
       if (!ok) break;
       tc_fence_after();
       const uint32_t vt = ring + (uint32_t)s * C::STAGE;
-      const uint32_t pt = tmem + (uint32_t)(i & 1) * BN;
+      const uint32_t pt = tmem + (uint32_t)(i % NS) * BN;
 #pragma unroll
       for (int ks = 0; ks < BN / 16; ++ks)
         mma_ts_cg<CG>(tmem + C::TMEM_O, pt + (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8),
                       sdesc_mnmaj(vt, BN, ks), id_o, (i > 0 || ks > 0) ? 1u : 0u);
       commit_cg<CG>(&sh->empty[s]);
-      commit_cg<CG>(&sh->o_done);
+      commit_cg<CG>(&sh->o_done[i % NS]);
     }
   } else if (warp < 8) {
     // ---- softmax: warps w and w + 4 share rows 32 (w % 4) .. + 31 ----
@@ -536,14 +539,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const float c = a.scale_log2;
     float m = -INFINITY;      // reference maximum of the raw scores
     float l = 0.f;            // this thread's half of the row sum
-    uint32_t ready[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-      ready[b] = CG == 2 ? map_cta(smem_u32(&sh->p_ready[b]), 0) : smem_u32(&sh->p_ready[b]);
+    const uint32_t ready = CG == 2 ? map_cta(smem_u32(&sh->p_ready[0]), 0) : 0u;
 
+    int b = -1;               // block i's S buffer, and the parity of its phase
+    uint32_t turn = 1;
     for (int i = 0; i < blocks; ++i) {
-      const int b = i & 1;
-      wait_on<CG>(ok, &sh->s_full[b], (i >> 1) & 1, a.wait_ns);
+      b = b == NS - 1 ? 0 : b + 1;
+      turn ^= b == 0;
+      wait_on(ok, &sh->s_full[b], turn, a.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) ok = false;
       tc_fence_after();
       const uint32_t st = tmem + lanes + (uint32_t)b * BN + (uint32_t)half * 64;
@@ -569,17 +572,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             fmaxf(mx[2 + k / 2 % 2], fmaxf(__uint_as_float(r1[k]), __uint_as_float(r1[k + 1])));
       }
       float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      sh->red[b][half][row] = mt;
+      sh->red[i & 1][half][row] = mt;
       pair_bar(1 + quarter);
-      mt = fmaxf(mt, sh->red[b][half ^ 1][row]);
+      mt = fmaxf(mt, sh->red[i & 1][half ^ 1][row]);
       // both warps of a row see the same maxima and so decide alike
-      const bool far = mt > m && (m == -INFINITY || (mt - m) * c > RESCALE_LOG2);
+      const bool far = live && mt > m && (m == -INFINITY || (mt - m) * c > RESCALE_LOG2);
       if (__any_sync(0xffffffffu, far)) {
-        const float mn = fmaxf(m, mt);
-        const float base = mn == -INFINITY ? 0.f : mn;
-        const float f = fast_exp2((m - base) * c);    // 0 for a first maximum
-        if (i > 0) {   // S(i) was formed after product i - 2: only i - 1 may be under way
-          wait_on<CG>(ok, &sh->o_done, (i - 1) & 1, a.wait_ns);
+        // a row's reference follows from the row alone: the others of the warp keep
+        // theirs (factor 1), and rows that are not there ask for nothing
+        const float f = far ? fast_exp2((m - mt) * c) : 1.f;    // 0 for a first maximum
+        m = far ? mt : m;
+        if (i > 0) {
+          // S(i) was formed after product i - NS, so of the products that report
+          // to one of the NS barriers at most one is under way
+          wait_on(ok, &sh->o_done[(i - 1) % NS], ((i - 1) / NS) & 1, a.wait_ns);
           if (!__all_sync(0xffffffffu, ok)) ok = false;
           tc_fence_after();
 #pragma unroll 1
@@ -594,7 +600,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
         }
         l *= f;
-        m = mn;
       }
       const float nm = m == -INFINITY ? 0.f : -m * c;
       uint32_t w[32];
@@ -618,7 +623,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       tmem_wait_st();
       if (tail && i == blocks - 1) {
         // the rows of V past the end are someone else's, or nothing: clear them
-        wait_on<CG>(ok, &sh->v_tail, 0, a.wait_ns);
+        wait_on(ok, &sh->v_tail, 0, a.wait_ns);
         const int s = (2 * blocks - 1) % C::RING;
         const int from = (int)(key_end - (int64_t)(first_block + i) * BN);
         const uint32_t vt2 = ring + (uint32_t)s * C::STAGE;
@@ -635,19 +640,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (CG == 2)
-          arrive_cluster(ready[b]);
-        else
+        if (CG == 1)
           mbar_arrive(&sh->p_ready[b]);
+        else if (tail && i == blocks - 1)
+          arrive_remote_release(ready + 8u * b);
+        else
+          arrive_remote(ready + 8u * b);
       }
     }
 
     // ---- the end: o = O / l ----
     if (blocks > 0) {
-      // S(blocks - 1) was formed after product blocks - 3: the last two may be
-      // under way, and a parity tells only one phase from the next
-      if (blocks > 1) wait_on<CG>(ok, &sh->o_done, (blocks - 2) & 1, a.wait_ns);
-      wait_on<CG>(ok, &sh->o_done, (blocks - 1) & 1, a.wait_ns);
+      wait_on(ok, &sh->o_done[(blocks - 1) % NS], ((blocks - 1) / NS) & 1, a.wait_ns);
       if (!__all_sync(0xffffffffu, ok)) ok = false;
       tc_fence_after();
     }

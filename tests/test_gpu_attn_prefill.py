@@ -201,3 +201,17 @@ def test_an_output_on_a_16_byte_boundary(gpu_lib):
     assert o.data_ptr() % 32 == 16
     gdn.gdn_attn_prefill(dims, q, k, v, cu, o=o)
     assert torch.equal(o, plain) and (room[:8] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_sequence_alone_and_in_a_batch_gives_the_same_bits(gpu_lib, d):
+    """Rows that share a warp with another sequence's, or with none, round alike."""
+    g = torch.Generator().manual_seed(26)
+    lens, hq, hkv = [37, 461, 90], 4, 2
+    cu = _cu(lens)
+    q, v = normal(g, cu[-1], hq, d).cuda(), normal(g, cu[-1], hkv, d).cuda()
+    k = (3 * normal(g, cu[-1], hkv, d)).cuda()
+    dims = gdn.make_attn_dims(hq, hkv, d)
+    o = _run(dims, q, k, v, cu)
+    for a, b in zip(cu, cu[1:]):
+        assert torch.equal(o[a:b], _run(dims, q[a:b], k[a:b], v[a:b], [0, b - a]))
