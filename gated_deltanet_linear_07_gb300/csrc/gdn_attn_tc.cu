@@ -110,6 +110,22 @@ __device__ __forceinline__ void wait_on(bool& ok, uint64_t* bar, uint32_t parity
                                         uint64_t budget_ns) {
   if (ok) ok = mbar_wait(bar, parity, budget_ns);
 }
+// The same without suspending the warp: for the MMA warp, whose next products
+// wait for nothing else.  All lanes together.
+__device__ __forceinline__ void spin_on(bool& ok, uint64_t* bar, uint32_t parity,
+                                        uint64_t budget_ns) {
+  if (ok) ok = mbar_spin(bar, parity, budget_ns);
+  ok = __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e)
+      :
+      : "memory");
+  return e != 0;
+}
 // The same for arrivals with a release at cluster scope.
 __device__ __forceinline__ void wait_on_cluster(bool& ok, uint64_t* bar, uint32_t parity,
                                                 uint64_t budget_ns) {
@@ -340,7 +356,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   TcShared* sh = reinterpret_cast<TcShared*>(smem);
   const GdnAttnArgs& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be the same in all lanes
   const uint32_t rank = CG == 2 ? cta_rank() : 0u;
   const uint32_t q_smem = smem_u32(smem) + MISC_BYTES;
   const uint32_t ring = q_smem + C::Q_BYTES;
@@ -471,46 +488,74 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         ++j;
       }
     }
-  } else if (warp == WARP_MMA && lane == 0 && rank == 0 && blocks > 0 && ok) {
+  } else if (warp == WARP_MMA && rank == 0 && blocks > 0 && ok) {
     // ---- MMAs, for both CTAs of a pair ----
+    // The whole warp walks through the loop and one elected lane issues: the
+    // descriptors are then uniform values.  From a branch of one lane each MMA
+    // took 60 to 100 cycles to issue, as long as it runs.
     constexpr uint32_t id_s = idesc_io<IO>(BM * CG, BN, false);
     constexpr uint32_t id_o = idesc_io<IO>(BM * CG, D, true);
-    int j = 0;
-    auto scores = [&](int i) {
-      const int s = j % C::RING;
-      wait_on(ok, &sh->full[s], (j / C::RING) & 1, a.wait_ns);
-      ++j;
+    const uint64_t q_desc = sdesc_kmaj(q_smem, BM, 0);
+    const uint64_t k_desc = sdesc_kmaj(ring, BN / CG, 0), v_desc = sdesc_mnmaj(ring, BN, 0);
+    int s = 0;                      // ring stage and the parity of its phase
+    uint32_t phase = 0;
+    auto next_stage = [&]() {
+      if (++s == C::RING) {
+        s = 0;
+        phase ^= 1;
+      }
+    };
+    int sb = 0;                     // S buffer of the next scores
+    auto scores = [&]() {
+      spin_on(ok, &sh->full[s], phase, a.wait_ns);
       if (!ok) return;
       tc_fence_after();
-      const uint32_t kt = ring + (uint32_t)s * C::STAGE;
+      const uint64_t kd = sdesc_add(k_desc, (uint32_t)s * C::STAGE);
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        mma_ss_cg<CG>(tmem + (uint32_t)(i % NS) * BN, sdesc_kmaj(q_smem, BM, ks),
-                      sdesc_kmaj(kt, BN / CG, ks), id_s, ks > 0 ? 1u : 0u);
-      commit_cg<CG>(&sh->empty[s]);
-      commit_cg<CG>(&sh->s_full[i % NS]);
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss_cg<CG>(tmem + (uint32_t)sb * BN,
+                        sdesc_add(q_desc, (uint32_t)((ks >> 2) * BM * 128 + (ks & 3) * 32)),
+                        sdesc_add(kd, (uint32_t)((ks >> 2) * (BN / CG) * 128 + (ks & 3) * 32)), id_s,
+                        ks > 0 ? 1u : 0u);
+        commit_cg<CG>(&sh->empty[s]);
+        commit_cg<CG>(&sh->s_full[sb]);
+      }
+      __syncwarp();
+      next_stage();
+      sb = sb == NS - 1 ? 0 : sb + 1;
     };
-    wait_on(ok, &sh->q_full, 0, a.wait_ns);
-    for (int i = 0; i < AHEAD && i < blocks && ok; ++i) scores(i);
+    spin_on(ok, &sh->q_full, 0, a.wait_ns);
+    for (int i = 0; i < AHEAD && i < blocks && ok; ++i) scores();
+    int pb = 0;                     // buffer of the next weights, and its phase
+    uint32_t turn = 0;
     for (int i = 0; i < blocks && ok; ++i) {
-      if (i + AHEAD < blocks) scores(i + AHEAD);
-      const int s = j % C::RING;
-      if (!(tail && i == blocks - 1)) wait_on(ok, &sh->full[s], (j / C::RING) & 1, a.wait_ns);
-      ++j;
-      if (tail && i == blocks - 1)
-        wait_on_cluster(ok, &sh->p_ready[i % NS], (i / NS) & 1, a.wait_ns);
+      if (i + AHEAD < blocks) scores();
+      const bool last = tail && i == blocks - 1;   // V's arrival is part of the weights' then
+      if (!last) spin_on(ok, &sh->full[s], phase, a.wait_ns);
+      if (last)
+        wait_on_cluster(ok, &sh->p_ready[pb], turn, a.wait_ns);
       else
-        wait_on(ok, &sh->p_ready[i % NS], (i / NS) & 1, a.wait_ns);
+        spin_on(ok, &sh->p_ready[pb], turn, a.wait_ns);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t vt = ring + (uint32_t)s * C::STAGE;
-      const uint32_t pt = tmem + (uint32_t)(i % NS) * BN;
+      const uint64_t vd = sdesc_add(v_desc, (uint32_t)s * C::STAGE);
+      const uint32_t pt = tmem + (uint32_t)pb * BN;
+      if (elect_one()) {
 #pragma unroll
-      for (int ks = 0; ks < BN / 16; ++ks)
-        mma_ts_cg<CG>(tmem + C::TMEM_O, pt + (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8),
-                      sdesc_mnmaj(vt, BN, ks), id_o, (i > 0 || ks > 0) ? 1u : 0u);
-      commit_cg<CG>(&sh->empty[s]);
-      commit_cg<CG>(&sh->o_done[i % NS]);
+        for (int ks = 0; ks < BN / 16; ++ks)
+          mma_ts_cg<CG>(tmem + C::TMEM_O, pt + (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8),
+                        sdesc_add(vd, (uint32_t)(ks * 16 * 128)), id_o,
+                        (i > 0 || ks > 0) ? 1u : 0u);
+        commit_cg<CG>(&sh->empty[s]);
+        commit_cg<CG>(&sh->o_done[pb]);
+      }
+      __syncwarp();
+      next_stage();
+      if (++pb == NS) {
+        pb = 0;
+        turn ^= 1;
+      }
     }
   } else if (warp < 8) {
     // ---- softmax: warps w and w + 4 share rows 32 (w % 4) .. + 31 ----
