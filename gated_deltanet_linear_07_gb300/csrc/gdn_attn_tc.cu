@@ -611,10 +611,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        mx[k / 2 % 2] = fmaxf(mx[k / 2 % 2], fmaxf(__uint_as_float(r0[k]), __uint_as_float(r0[k + 1])));
-        mx[2 + k / 2 % 2] =
-            fmaxf(mx[2 + k / 2 % 2], fmaxf(__uint_as_float(r1[k]), __uint_as_float(r1[k + 1])));
+      for (int k = 0; k < 32; k += 4) {
+        mx[0] = max3(mx[0], __uint_as_float(r0[k]), __uint_as_float(r0[k + 1]));
+        mx[1] = max3(mx[1], __uint_as_float(r0[k + 2]), __uint_as_float(r0[k + 3]));
+        mx[2] = max3(mx[2], __uint_as_float(r1[k]), __uint_as_float(r1[k + 1]));
+        mx[3] = max3(mx[3], __uint_as_float(r1[k + 2]), __uint_as_float(r1[k + 3]));
       }
       float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       sh->red[i & 1][half][row] = mt;
@@ -647,22 +648,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         l *= f;
       }
       const float nm = m == -INFINITY ? 0.f : -m * c;
+      const uint64_t c2 = pk(c, c), nm2 = pk(nm, nm);
       uint32_t w[32];
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
       for (int k = 0; k < 32; k += 2) {
-        const float e0 = fast_exp2(fmaf(__uint_as_float(r0[k]), c, nm));
-        const float e1 = fast_exp2(fmaf(__uint_as_float(r0[k + 1]), c, nm));
-        const float e2 = fast_exp2(fmaf(__uint_as_float(r1[k]), c, nm));
-        const float e3 = fast_exp2(fmaf(__uint_as_float(r1[k + 1]), c, nm));
-        sum[0] += e0;
-        sum[1] += e1;
-        sum[2] += e2;
-        sum[3] += e3;
+        float e0, e1, e2, e3;
+        unpk(fma2(pk(__uint_as_float(r0[k]), __uint_as_float(r0[k + 1])), c2, nm2), e0, e1);
+        unpk(fma2(pk(__uint_as_float(r1[k]), __uint_as_float(r1[k + 1])), c2, nm2), e2, e3);
+        e0 = fast_exp2(e0);
+        e1 = fast_exp2(e1);
+        e2 = fast_exp2(e2);
+        e3 = fast_exp2(e3);
+        sum[k / 2 % 2] = add2(sum[k / 2 % 2], pk(e0, e1));
+        sum[2 + k / 2 % 2] = add2(sum[2 + k / 2 % 2], pk(e2, e3));
         w[k / 2] = pack2<IO>(e0, e1);
         w[16 + k / 2] = pack2<IO>(e2, e3);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float la, lb;
+      unpk(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), la, lb);
+      l += la + lb;
       // over this half's own scores, which are in registers by now
       tmem_st32(st, w);
       tmem_wait_st();
