@@ -24,9 +24,16 @@
 // x 256 channels x 2 operands = 128 KB per 2048 cycles of products).
 //
 // Warps: 0-7 softmax (warps w and w + 4 share 32 rows, 64 of a block's 128
-// columns each), 8 the TMA loads, 9 the MMAs.  K and V blocks run through one
-// ring in the order K0 K1 V0 K2 V1 ..., which is the order the MMA warp
-// consumes: S(i+1) is formed while the softmax works on S(i).
+// columns each), 8 the TMA loads, 9 the MMAs, 10 the order of work.  K and V
+// blocks run through one ring in the order in which the MMA warp consumes them:
+// S is formed one or two blocks ahead of the product with V, so that the softmax
+// of one block and the products of the others overlap.
+//
+// Work items (a row block of one head group) are the clusters of the grid; a
+// running pair takes over items that have not been launched yet
+// (clusterlaunchcontrol), so that the loads and first scores of its next item run
+// under the last blocks and the output of this one.  Launched one by one, an item
+// cost 12 us beside its blocks.  The heaviest items come first.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -40,8 +47,8 @@ using namespace gdn::tc;
 
 constexpr int BM = 128;            // query rows per CTA (tensor-memory lanes)
 constexpr int BN = 128;            // keys per block
-constexpr int TC_THREADS = 320;
-constexpr int WARP_LOAD = 8, WARP_MMA = 9;
+constexpr int TC_THREADS = 352;
+constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ORDER = 10;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr uint32_t MISC_BYTES = 3072;
 constexpr int MAX_RING = 8;
@@ -57,12 +64,24 @@ struct TcCfg {
   static constexpr uint32_t TMEM_O = NS * BN;
 };
 
+// One work item, as the order warp hands it to the others.
+struct TcItem {
+  int64_t q0, len_q, k0, len_k;   // the sequence's queries and keys
+  int64_t tile;                   // row block of the pair within the sequence
+  int32_t head;                   // head group
+  int32_t split, first_block;     // prefix pass: which share of the keys
+  int32_t blocks;                 // key blocks; < 0: no more items
+};
+
 struct __align__(16) TcShared {
+  uint4 taken[2];        // answers of the launch control
   uint64_t full[MAX_RING], empty[MAX_RING];
-  uint64_t q_full, s_full[3], p_ready[3], o_done[3], v_tail;
+  uint64_t q_full, q_empty, s_full[3], p_ready[3], o_done[3], o_free, v_tail[2];
+  uint64_t item_full[2], item_empty[2], taken_full[2], taken_free;
+  TcItem item[2];
   uint32_t tmem;
-  int32_t seq, tile, bad;
-  int32_t scan[12];
+  int32_t bad;
+  int32_t tail_stage[2]; // ring stage of an item's last V block, where it passes the end
   float red[2][2][BM];   // row maxima of the two column halves, two turns
 };
 static_assert(sizeof(TcShared) <= MISC_BYTES, "shared bookkeeping");
@@ -88,7 +107,8 @@ __device__ __forceinline__ void cluster_sync_all() {
 // barrier: it was the softmax warps' longest stall, 2.2 of 7.5 cycles per issue)
 // is left to the one block whose V rows were cleared in shared memory.
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
 }
 __device__ __forceinline__ void arrive_remote_release(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
@@ -283,68 +303,94 @@ struct TcLaunch {
   int32_t k_rows, v_rows; // rows of one K / V box
 };
 
-// Which sequence and which of its row blocks is block j, counting from the
-// last one; by all threads.  False: there is none (or cu_seqlens is bad).
-__device__ __forceinline__ bool find_tile(const GdnAttnArgs& a, TcShared* sh, int64_t j, int tokens,
-                                          int64_t& q0, int64_t& len_q, int64_t& k0,
-                                          int64_t& len_k, int64_t& tile) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    sh->seq = -1;
-    sh->bad = 0;
+// Whether every sequence lies within the totals, in order; by all threads.
+__device__ __forceinline__ bool sequences_ok(const GdnAttnArgs& a, TcShared* sh) {
+  for (int b = threadIdx.x; b < a.num_seqs; b += TC_THREADS) {
+    const int64_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
+    const int64_t klo = a.cu_kv[b], khi = a.cu_kv[b + 1];
+    if (hi < lo || lo < 0 || hi > a.total_q || khi < klo || klo < 0 || khi > a.total_kv ||
+        (b == 0 && (lo != 0 || klo != 0)) ||
+        (b == a.num_seqs - 1 && (hi != a.total_q || khi != a.total_kv)))
+      sh->bad = 1;
   }
   __syncthreads();
-  // Last sequences and last blocks first: within a sequence the longest rows
-  // start first, so the tail of the grid is made of short ones.
-  int64_t before = 0;
-  for (int base = 0; base < a.num_seqs; base += TC_THREADS) {
-    const int i = base + tid;                   // sequence num_seqs - 1 - i
-    int64_t nt = 0;
-    if (i < a.num_seqs) {
-      const int b = a.num_seqs - 1 - i;
-      const int64_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
-      const int64_t klo = a.cu_kv[b], khi = a.cu_kv[b + 1];
-      if (hi < lo || lo < 0 || hi > a.total_q || khi < klo || klo < 0 || khi > a.total_kv ||
-          (b == 0 && (lo != 0 || klo != 0)) ||
-          (b == a.num_seqs - 1 && (hi != a.total_q || khi != a.total_kv)))
-        sh->bad = 1;
-      else
-        nt = (hi - lo + tokens - 1) / tokens;
-    }
-    int incl = (int)nt;
+  return sh->bad == 0;
+}
+
+// Which sequence and which of its row blocks is row block j of the grid, counting
+// from the last block of the last sequence: within a sequence the longest rows
+// come first.  By one warp, which keeps its place between calls.
+struct TileSearch {
+  int base = 0;            // 32 sequences from here (counted from the last one)
+  int64_t before = 0;      // row blocks of the sequences before them
+  int64_t nt = -1, incl = 0;   // this lane's sequence: its row blocks, and with those before it
+
+  __device__ void load(const GdnAttnArgs& a, int tokens) {
+    const int i = base + (threadIdx.x & 31), b = a.num_seqs - 1 - i;
+    nt = b >= 0 ? ((int64_t)a.cu_q[b + 1] - a.cu_q[b] + tokens - 1) / tokens : 0;
+    incl = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((threadIdx.x & 31) >= o) incl += v;
     }
-    if (lane == 31) sh->scan[warp] = incl;
-    __syncthreads();
-    int64_t off = before;
-    int64_t all = 0;
-    for (int w = 0; w < TC_THREADS / 32; ++w) {
-      if (w < warp) off += sh->scan[w];
-      all += sh->scan[w];
-    }
-    const int64_t first = off + incl - nt;
-    if (nt > 0 && j >= first && j < first + nt) {
-      sh->seq = a.num_seqs - 1 - i;
-      sh->tile = (int)(nt - 1 - (j - first));
-    }
-    before += all;
-    __syncthreads();
   }
-  if (sh->bad) {
-    if (tid == 0) set_status(a.d_status, GDN_DEV_BAD_CU_SEQLENS);
-    return false;
+  // False: there is no such block.
+  __device__ bool find(const GdnAttnArgs& a, int tokens, int64_t j, int& seq, int64_t& tile) {
+    if (nt < 0 || j < before) {
+      base = 0;
+      before = 0;
+      load(a, tokens);
+    }
+    for (;;) {
+      const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+      if (j < before + all) break;
+      before += all;
+      base += 32;
+      if (base >= a.num_seqs) {
+        nt = -1;   // start over next time
+        return false;
+      }
+      load(a, tokens);
+    }
+    const int64_t at = j - before;
+    const int src = __ffs(__ballot_sync(0xffffffffu, at < incl)) - 1;
+    const int64_t n = __shfl_sync(0xffffffffu, nt, src), end = __shfl_sync(0xffffffffu, incl, src);
+    seq = a.num_seqs - 1 - base - src;
+    tile = n - 1 - (at - (end - n));
+    return true;
   }
-  if (sh->seq < 0) return false;
-  const int b = sh->seq;
-  q0 = a.cu_q[b];
-  len_q = a.cu_q[b + 1] - q0;
-  k0 = a.cu_kv[b];
-  len_k = a.cu_kv[b + 1] - k0;
-  tile = sh->tile;
-  return true;
+};
+
+// Asks for a cluster that has not been launched yet; the answer goes to the same
+// place in both CTAs of a pair and reports to their barriers.
+template <int CG>
+__device__ __forceinline__ void take_cluster(uint32_t answer, uint32_t bar) {
+  if (CG == 2)
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes"
+        ".multicast::cluster::all.b128 [%0], [%1];" ::"r"(answer),
+        "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(answer),
+        "r"(bar)
+        : "memory");
+}
+// The taken cluster's first CTA, or -1.
+__device__ __forceinline__ int64_t taken_cluster(uint32_t answer) {
+  uint32_t x, got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\tmov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}\n"
+      : "=r"(x), "=r"(got)
+      : "r"(answer)
+      : "memory");
+  return got ? (int64_t)x : -1;
 }
 
 template <typename IO, int D, int CG, bool PREFIX>
@@ -361,134 +407,245 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const uint32_t rank = CG == 2 ? cta_rank() : 0u;
   const uint32_t q_smem = smem_u32(smem) + MISC_BYTES;
   const uint32_t ring = q_smem + C::Q_BYTES;
-
   // the per-sequence pass of a decode needs nothing of this one but its SMs
   if (PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // ---- which rows and which keys ----
   const int gp = 1 << p.gp_shift;
   const int cta_tokens = BM >> p.gp_shift;
-  const int64_t item = blockIdx.x / CG;
   const int heads = a.h_kv * p.subs;             // row groups that share a tile of tokens
-  const int head = (int)(item % heads);
-  const int kvh = head / p.subs;
-  const int h0 = kvh * (a.h_q / a.h_kv) + (head % p.subs) * gp;   // first packed query head
-  int64_t q0, len_q, k0, len_k, tile;
-  int split = 0, first_block = 0, blocks;
-  if (PREFIX) {
-    const int64_t rest = item / heads;
-    split = (int)(rest % a.splits);
-    tile = rest / a.splits;
-    q0 = 0;
-    len_q = a.total_q;
-    k0 = 0;
-    len_k = a.shared_len;
-    const int64_t all = (len_k + BN - 1) / BN;
-    first_block = (int)(all * split / a.splits);
-    blocks = (int)(all * (split + 1) / a.splits) - first_block;
-  } else {
-    if (!find_tile(a, sh, item / heads, cta_tokens * CG, q0, len_q, k0, len_k, tile)) return;
-    blocks = 0;
-  }
-  const int64_t tok0 = (tile * CG + rank) * cta_tokens;      // this CTA's first token
-  const int64_t off = len_k - len_q;                         // causal: token t sees t + off + 1
-  if (!PREFIX) {
-    // the keys that the last token of the pair's rows sees
-    const int64_t last = min(len_q, (tile + 1) * CG * cta_tokens) - 1;
-    const int64_t seen = last + off + 1;
-    blocks = seen > 0 ? (int)((seen + BN - 1) / BN) : 0;
-  }
-  // keys past `key_end` are another sequence's, or none
-  const int64_t key_end = len_k;
-  const bool tail = (int64_t)(first_block + blocks) * BN > key_end;
-
   if (tid == 0) {
     for (int s = 0; s < C::RING; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 1);
     }
     mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, 1);
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&sh->s_full[s], 1);
       mbar_init(&sh->p_ready[s], 8 * CG);
       mbar_init(&sh->o_done[s], 1);
     }
-    mbar_init(&sh->v_tail, 1);
+    mbar_init(&sh->o_free, 8 * CG);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh->v_tail[s], 1);
+      mbar_init(&sh->item_full[s], 1);
+      mbar_init(&sh->item_empty[s], 10);         // eight softmax warps, loads, MMAs
+      mbar_init(&sh->taken_full[s], 1);
+    }
+    mbar_init(&sh->taken_free, CG);
     fence_mbar_init();
+    sh->bad = 0;
   }
   if (warp == WARP_MMA) tmem_alloc_cg<CG>(&sh->tmem, 512);
   tc_fence_before();
   __syncthreads();
+  if (!PREFIX && !sequences_ok(a, sh)) {         // alike in every CTA
+    if (tid == 0) set_status(a.d_status, GDN_DEV_BAD_CU_SEQLENS);
+    if (CG == 2) cluster_sync_all();
+    if (warp == WARP_MMA) tmem_dealloc_cg<CG>(sh->tmem, 512);
+    return;
+  }
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
   bool ok = (smem_u32(smem) & 1023u) == 0;
   constexpr int NS = C::NS, AHEAD = NS - 1;   // S blocks formed ahead of the products with V
+  const uint64_t wait_ns = a.wait_ns;
 
-  if (warp == WARP_LOAD && lane == 0 && blocks > 0 && ok) {
+  // Items as the other warps see them, one after the other.
+  int turn_item = 0;
+  auto next_item = [&](TcItem& it) {
+    wait_on(ok, &sh->item_full[turn_item & 1], (turn_item >> 1) & 1, wait_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    it = sh->item[turn_item & 1];
+    return it.blocks >= 0;
+  };
+  auto item_over = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->item_empty[turn_item & 1]);
+    ++turn_item;
+  };
+  auto has_tail = [&](const TcItem& it) {        // the last block passes the keys' end
+    return (int64_t)(it.first_block + it.blocks) * BN > it.len_k;
+  };
+
+  if (warp == WARP_ORDER) {
+    // ---- the order of work: this cluster's own item, then taken ones ----
+    TileSearch search;
+    int64_t item = blockIdx.x / CG;
+    int asked = 0;
+    for (int k = 0; ok;) {
+      bool there = item >= 0;
+      TcItem it = {};
+      if (there) {
+        it.head = (int)(item % heads);
+        const int64_t rest = item / heads;
+        if (PREFIX) {
+          it.split = (int)(rest % a.splits);
+          it.tile = rest / a.splits;
+          it.len_q = a.total_q;
+          it.len_k = a.shared_len;
+          const int64_t all = (it.len_k + BN - 1) / BN;
+          it.first_block = (int)(all * it.split / a.splits);
+          it.blocks = (int)(all * (it.split + 1) / a.splits) - it.first_block;
+        } else {
+          int b;
+          there = search.find(a, cta_tokens * CG, rest, b, it.tile);
+          if (there) {
+            it.q0 = a.cu_q[b];
+            it.len_q = a.cu_q[b + 1] - it.q0;
+            it.k0 = a.cu_kv[b];
+            it.len_k = a.cu_kv[b + 1] - it.k0;
+            // the keys that the last token of the pair's rows sees
+            const int64_t last = min(it.len_q, (it.tile + 1) * CG * cta_tokens) - 1;
+            const int64_t seen = last + it.len_k - it.len_q + 1;
+            it.blocks = seen > 0 ? (int)((seen + BN - 1) / BN) : 0;
+          }
+        }
+      } else {
+        it.blocks = -1;
+      }
+      if (there || item < 0) {
+        // the first wait of each buffer is for nothing
+        if (k >= 2) wait_on(ok, &sh->item_empty[k & 1], ((k >> 1) - 1) & 1, wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          sh->item[k & 1] = it;
+          mbar_arrive(&sh->item_full[k & 1]);
+        }
+        ++k;
+        if (item < 0) break;
+      }
+      // The next one, once this item's buffer after next is free again: a pair
+      // holds no more than the item it works on and one more.
+      if (there && k >= 2) wait_on(ok, &sh->item_empty[k & 1], ((k >> 1) - 1) & 1, wait_ns);
+      const int s = asked & 1;
+      if (rank == 0) {
+        if (asked > 0) wait_on(ok, &sh->taken_free, (asked - 1) & 1, wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        mbar_expect_tx(&sh->taken_full[s], 16);
+        if (rank == 0) take_cluster<CG>(smem_u32(&sh->taken[s]), smem_u32(&sh->taken_full[s]));
+      }
+      __syncwarp();
+      wait_on(ok, &sh->taken_full[s], (asked >> 1) & 1, wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int64_t first = taken_cluster(smem_u32(&sh->taken[s]));
+      fence_async_smem();                       // read before the next answer lands there
+      __syncwarp();
+      if (lane == 0) {
+        if (CG == 2)
+          arrive_remote_release(map_cta(smem_u32(&sh->taken_free), 0));
+        else
+          mbar_arrive(&sh->taken_free);
+      }
+      ++asked;
+      item = first < 0 ? -1 : first / CG;
+    }
+  } else if (warp == WARP_LOAD) {
     // ---- TMA loads; in a pair every copy reports to the first CTA's barrier ----
     auto lead = [&](uint64_t* bar) {
       return CG == 2 ? map_cta(smem_u32(bar), 0) : smem_u32(bar);
     };
-    if (rank == 0) mbar_expect_tx(&sh->q_full, C::Q_BYTES * CG);
-    tma_load_4d<CG>(q_smem, &qmap, 0, h0, (int)(q0 + tok0), 0, lead(&sh->q_full));
-    // rows of [t, t + n) that exist, in whole boxes
-    auto rows_of = [&](int64_t t, int n, int box) -> int {
-      const int64_t left = PREFIX ? key_end - t : (int64_t)n;
-      return left <= 0 ? 0 : (int)min((int64_t)n, (left + box - 1) / box * box);
-    };
-    auto load_rows = [&](uint32_t dst, const CUtensorMap* map, int64_t t, int n, int box, int kb0,
-                         int kbs, uint32_t bar) {
-      if (!PREFIX) tma_load_4d<CG>(dst, map, 0, (int)(k0 + t), kb0, kvh, bar);
-      for (int r = 0; PREFIX && r < n && t + r < key_end; r += box) {
-        const int64_t pos = t + r;
-        int32_t page = __ldg(a.cache.block_table + (pos >> a.page_shift));
-        if (page < 0 || page >= a.cache.num_pages) {
-          set_status(a.d_status, GDN_DEV_BAD_PAGE);
-          page = 0;
+    int s = 0;                      // ring stage and the parity of its phase
+    uint32_t phase = 0;
+    int used = 0, tails = 0;        // items with keys, and with a tail, so far
+    TcItem it;
+    while (next_item(it)) {
+      if (it.blocks > 0 && lane == 0) {
+        const int kvh = it.head / p.subs;
+        const int h0 = kvh * (a.h_q / a.h_kv) + (it.head % p.subs) * gp;
+        const int64_t tok0 = (it.tile * CG + rank) * cta_tokens;
+        const bool tail = has_tail(it);
+        // rows of [t, t + n) that exist, in whole boxes
+        auto rows_of = [&](int64_t t, int n, int box) -> int {
+          const int64_t left = PREFIX ? it.len_k - t : (int64_t)n;
+          return left <= 0 ? 0 : (int)min((int64_t)n, (left + box - 1) / box * box);
+        };
+        auto load_rows = [&](uint32_t dst, const CUtensorMap* map, int64_t t, int n, int box,
+                             int kb0, int kbs, uint32_t bar) {
+          if (!PREFIX) tma_load_4d<CG>(dst, map, 0, (int)(it.k0 + t), kb0, kvh, bar);
+          for (int r = 0; PREFIX && r < n && t + r < it.len_k; r += box) {
+            const int64_t pos = t + r;
+            int32_t page = __ldg(a.cache.block_table + (pos >> a.page_shift));
+            if (page < 0 || page >= a.cache.num_pages) {
+              set_status(a.d_status, GDN_DEV_BAD_PAGE);
+              page = 0;
+            }
+            const int64_t row = (((int64_t)page * a.h_kv + kvh) << a.page_shift) +
+                                (pos & ((1 << a.page_shift) - 1));
+            for (int kb = 0; kb < kbs; ++kb)
+              tma_load_4d<CG>(dst + (uint32_t)(kb * n + r) * 128u, map, 0, (int)row, kb0 + kb, 0,
+                              bar);
+          }
+        };
+        auto room = [&]() {         // the stage's last user is through with it
+          wait_on(ok, &sh->empty[s], phase ^ 1, wait_ns);
+          return ok;
+        };
+        auto next_stage = [&]() {
+          if (++s == C::RING) {
+            s = 0;
+            phase ^= 1;
+          }
+        };
+        for (int i = 0; i < it.blocks + AHEAD && ok; ++i) {
+          if (i < it.blocks) {   // K block i: this CTA's share of its rows
+            if (!room()) break;
+            const int64_t t = (int64_t)(it.first_block + i) * BN;
+            const int n = BN / CG;
+            if (rank == 0) {
+              int rows = 0;
+              for (int c = 0; c < CG; ++c) rows += rows_of(t + c * n, n, p.k_rows);
+              mbar_expect_tx(&sh->full[s], (uint32_t)rows * D * 2);
+            }
+            load_rows(ring + (uint32_t)s * C::STAGE, &kmap, t + (int64_t)rank * n, n, p.k_rows, 0,
+                      D / 64, lead(&sh->full[s]));
+            next_stage();
+          }
+          if (i == 0) {          // Q, once the last item's scores are all formed
+            if (used > 0) wait_on(ok, &sh->q_empty, (used - 1) & 1, wait_ns);
+            if (!ok) break;
+            if (rank == 0) mbar_expect_tx(&sh->q_full, C::Q_BYTES * CG);
+            tma_load_4d<CG>(q_smem, &qmap, 0, h0, (int)(it.q0 + tok0), 0, lead(&sh->q_full));
+          }
+          if (i >= AHEAD) {      // V block i - AHEAD: this CTA's share of its channels
+            if (!room()) break;
+            const int64_t t = (int64_t)(it.first_block + i - AHEAD) * BN;
+            const uint32_t bytes = (uint32_t)rows_of(t, BN, p.v_rows) * (D / CG) * 2;
+            // a tail reports here: this CTA clears its rows past the end
+            const bool own = tail && i == it.blocks + AHEAD - 1;
+            uint64_t* const own_bar = &sh->v_tail[tails & 1];
+            if (own) {
+              sh->tail_stage[tails & 1] = s;
+              mbar_expect_tx(own_bar, bytes);
+            }
+            if (rank == 0) {
+              if (own)
+                mbar_arrive(&sh->full[s]);   // nobody waits for it; the phase has to pass
+              else
+                mbar_expect_tx(&sh->full[s], bytes * CG);
+            }
+            load_rows(ring + (uint32_t)s * C::STAGE, &vmap, t, BN, p.v_rows,
+                      (int)rank * (D / 64 / CG), D / 64 / CG,
+                      !own ? lead(&sh->full[s])
+                           : CG == 2 ? map_cta(smem_u32(own_bar), rank) : smem_u32(own_bar));
+            next_stage();
+          }
         }
-        const int64_t row = (((int64_t)page * a.h_kv + kvh) << a.page_shift) +
-                            (pos & ((1 << a.page_shift) - 1));
-        for (int kb = 0; kb < kbs; ++kb)
-          tma_load_4d<CG>(dst + (uint32_t)(kb * n + r) * 128u, map, 0, (int)row, kb0 + kb, 0, bar);
+        ++used;
+        if (tail) ++tails;
       }
-    };
-    int j = 0;
-    for (int i = 0; i < blocks + AHEAD && ok; ++i) {
-      if (i < blocks) {   // K block i: this CTA's share of its rows
-        const int s = j % C::RING;
-        if (j >= C::RING) wait_on(ok, &sh->empty[s], ((j / C::RING) - 1) & 1, a.wait_ns);
-        if (!ok) break;
-        const int64_t t = (int64_t)(first_block + i) * BN;
-        const int n = BN / CG;
-        if (rank == 0) {
-          int rows = 0;
-          for (int c = 0; c < CG; ++c) rows += rows_of(t + c * n, n, p.k_rows);
-          mbar_expect_tx(&sh->full[s], (uint32_t)rows * D * 2);
-        }
-        load_rows(ring + (uint32_t)s * C::STAGE, &kmap, t + (int64_t)rank * n, n, p.k_rows, 0,
-                  D / 64, lead(&sh->full[s]));
-        ++j;
-      }
-      if (i >= AHEAD) {   // V block i - AHEAD: this CTA's share of its channels
-        const int s = j % C::RING;
-        if (j >= C::RING) wait_on(ok, &sh->empty[s], ((j / C::RING) - 1) & 1, a.wait_ns);
-        if (!ok) break;
-        const int64_t t = (int64_t)(first_block + i - AHEAD) * BN;
-        const uint32_t bytes = (uint32_t)rows_of(t, BN, p.v_rows) * (D / CG) * 2;
-        const bool own = tail && i == blocks + AHEAD - 1;   // reports here: this CTA clears its rows past the end
-        if (own)
-          mbar_expect_tx(&sh->v_tail, bytes);
-        else if (rank == 0)
-          mbar_expect_tx(&sh->full[s], bytes * CG);
-        const uint32_t own_bar = CG == 2 ? map_cta(smem_u32(&sh->v_tail), rank)
-                                         : smem_u32(&sh->v_tail);
-        load_rows(ring + (uint32_t)s * C::STAGE, &vmap, t, BN, p.v_rows,
-                  (int)rank * (D / 64 / CG), D / 64 / CG, own ? own_bar : lead(&sh->full[s]));
-        ++j;
-      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      item_over();
     }
-  } else if (warp == WARP_MMA && rank == 0 && blocks > 0 && ok) {
+  } else if (warp == WARP_MMA) {
     // ---- MMAs, for both CTAs of a pair ----
     // The whole warp walks through the loop and one elected lane issues: the
     // descriptors are then uniform values.  From a branch of one lane each MMA
@@ -506,8 +663,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
     };
     int sb = 0;                     // S buffer of the next scores
-    auto scores = [&]() {
-      spin_on(ok, &sh->full[s], phase, a.wait_ns);
+    auto scores = [&](bool last) {
+      spin_on(ok, &sh->full[s], phase, wait_ns);
       if (!ok) return;
       tc_fence_after();
       const uint64_t kd = sdesc_add(k_desc, (uint32_t)s * C::STAGE);
@@ -520,233 +677,269 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         ks > 0 ? 1u : 0u);
         commit_cg<CG>(&sh->empty[s]);
         commit_cg<CG>(&sh->s_full[sb]);
+        if (last) commit_cg<CG>(&sh->q_empty);
       }
       __syncwarp();
       next_stage();
       sb = sb == NS - 1 ? 0 : sb + 1;
     };
-    spin_on(ok, &sh->q_full, 0, a.wait_ns);
-    for (int i = 0; i < AHEAD && i < blocks && ok; ++i) scores();
     int pb = 0;                     // buffer of the next weights, and its phase
     uint32_t turn = 0;
-    for (int i = 0; i < blocks && ok; ++i) {
-      if (i + AHEAD < blocks) scores();
-      const bool last = tail && i == blocks - 1;   // V's arrival is part of the weights' then
-      if (!last) spin_on(ok, &sh->full[s], phase, a.wait_ns);
-      if (last)
-        wait_on_cluster(ok, &sh->p_ready[pb], turn, a.wait_ns);
-      else
-        spin_on(ok, &sh->p_ready[pb], turn, a.wait_ns);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t vd = sdesc_add(v_desc, (uint32_t)s * C::STAGE);
-      const uint32_t pt = tmem + (uint32_t)pb * BN;
-      if (elect_one()) {
+    int used = 0;
+    TcItem it;
+    while (next_item(it)) {
+      if (it.blocks > 0 && rank == 0) {
+        const bool tail = has_tail(it);
+        spin_on(ok, &sh->q_full, used & 1, wait_ns);
+        for (int i = 0; i < AHEAD && i < it.blocks && ok; ++i) scores(i == it.blocks - 1);
+        for (int i = 0; i < it.blocks && ok; ++i) {
+          if (i + AHEAD < it.blocks) scores(i + AHEAD == it.blocks - 1);
+          const bool last = tail && i == it.blocks - 1;   // V's arrival is part of the weights' then
+          if (!last) spin_on(ok, &sh->full[s], phase, wait_ns);
+          // the last item's output has been read
+          if (i == 0 && used > 0) spin_on(ok, &sh->o_free, (used - 1) & 1, wait_ns);
+          if (last)
+            wait_on_cluster(ok, &sh->p_ready[pb], turn, wait_ns);
+          else
+            spin_on(ok, &sh->p_ready[pb], turn, wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = sdesc_add(v_desc, (uint32_t)s * C::STAGE);
+          const uint32_t pt = tmem + (uint32_t)pb * BN;
+          if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
-          mma_ts_cg<CG>(tmem + C::TMEM_O, pt + (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8),
-                        sdesc_add(vd, (uint32_t)(ks * 16 * 128)), id_o,
-                        (i > 0 || ks > 0) ? 1u : 0u);
-        commit_cg<CG>(&sh->empty[s]);
-        commit_cg<CG>(&sh->o_done[pb]);
+            for (int ks = 0; ks < BN / 16; ++ks)
+              mma_ts_cg<CG>(tmem + C::TMEM_O, pt + (uint32_t)((ks >> 2) * 64 + (ks & 3) * 8),
+                            sdesc_add(vd, (uint32_t)(ks * 16 * 128)), id_o,
+                            (i > 0 || ks > 0) ? 1u : 0u);
+            commit_cg<CG>(&sh->empty[s]);
+            commit_cg<CG>(&sh->o_done[pb]);
+          }
+          __syncwarp();
+          next_stage();
+          if (++pb == NS) {
+            pb = 0;
+            turn ^= 1;
+          }
+        }
+        ++used;
       }
-      __syncwarp();
-      next_stage();
-      if (++pb == NS) {
-        pb = 0;
-        turn ^= 1;
-      }
+      if (!ok) break;
+      item_over();
     }
-  } else if (warp < 8) {
+  } else {
     // ---- softmax: warps w and w + 4 share rows 32 (w % 4) .. + 31 ----
     const int quarter = warp & 3, half = warp >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const int64_t tok = tok0 + (row >> p.gp_shift);
-    const bool live = tok < len_q;
-    // how many keys this row sees; rows past the end follow the last one, so
-    // that they ask for no mask of their own
-    const int64_t vt = live ? tok : len_q - 1;
-    int64_t lim;
-    if (PREFIX) {
-      lim = min((int64_t)max(a.seq_lens[vt], 0), len_k);
-    } else {
-      lim = vt + off + 1;
-      lim = lim < 0 ? 0 : lim;
-    }
-    int64_t low = lim;   // the least of the warp's rows
-    if (PREFIX) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) low = min(low, (int64_t)__shfl_xor_sync(0xffffffffu, low, o));
-    } else {
-      low = __shfl_sync(0xffffffffu, lim, 0);
-    }
     const float c = a.scale_log2;
-    float m = -INFINITY;      // reference maximum of the raw scores
-    float l = 0.f;            // this thread's half of the row sum
     const uint32_t ready = CG == 2 ? map_cta(smem_u32(&sh->p_ready[0]), 0) : 0u;
-
-    int b = -1;               // block i's S buffer, and the parity of its phase
+    const uint32_t freed = CG == 2 ? map_cta(smem_u32(&sh->o_free), 0) : 0u;
+    // the first CTA's own arrivals stay in it
+    const bool local = CG == 1 || rank == 0;
+    int b = -1;               // this block's S buffer, and the parity of its phase
     uint32_t turn = 1;
-    for (int i = 0; i < blocks; ++i) {
-      b = b == NS - 1 ? 0 : b + 1;
-      turn ^= b == 0;
-      wait_on(ok, &sh->s_full[b], turn, a.wait_ns);
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
-      tc_fence_after();
-      const uint32_t st = tmem + lanes + (uint32_t)b * BN + (uint32_t)half * 64;
-      uint32_t r0[32], r1[32];
-      tmem_ld32_nowait(st, r0);
-      tmem_ld32_nowait(st + 32, r1);
-      tmem_wait_ld(r0);
-      tmem_wait_ld(r1);
-      const int64_t key = (int64_t)(first_block + i) * BN + half * 64;
-      if (low < key + 64) {
-        const int seen = (int)max((int64_t)-1, min((int64_t)64, lim - key));
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          if (k >= seen) r0[k] = 0xff800000u;
-          if (k + 32 >= seen) r1[k] = 0xff800000u;
-        }
+    int flip = 0, tails = 0;
+    TcItem it;
+    while (next_item(it)) {
+      const int blocks = it.blocks;
+      const bool tail = has_tail(it) && blocks > 0;
+      const int kvh = it.head / p.subs;
+      const int h = kvh * (a.h_q / a.h_kv) + (it.head % p.subs) * gp + (row & (gp - 1));
+      const int64_t tok = (it.tile * CG + rank) * cta_tokens + (row >> p.gp_shift);
+      const bool live = tok < it.len_q;
+      // how many keys this row sees; rows past the end follow the last one, so
+      // that they ask for no mask of their own
+      const int64_t vt = live ? tok : it.len_q - 1;
+      int64_t lim;
+      if (PREFIX) {
+        lim = min((int64_t)max(a.seq_lens[vt], 0), it.len_k);
+      } else {
+        lim = vt + it.len_k - it.len_q + 1;   // causal: the queries are the last of the keys
+        lim = lim < 0 ? 0 : lim;
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      int64_t low = lim;   // the least of the warp's rows
+      if (PREFIX) {
 #pragma unroll
-      for (int k = 0; k < 32; k += 4) {
-        mx[0] = max3(mx[0], __uint_as_float(r0[k]), __uint_as_float(r0[k + 1]));
-        mx[1] = max3(mx[1], __uint_as_float(r0[k + 2]), __uint_as_float(r0[k + 3]));
-        mx[2] = max3(mx[2], __uint_as_float(r1[k]), __uint_as_float(r1[k + 1]));
-        mx[3] = max3(mx[3], __uint_as_float(r1[k + 2]), __uint_as_float(r1[k + 3]));
+        for (int o = 16; o > 0; o >>= 1)
+          low = min(low, (int64_t)__shfl_xor_sync(0xffffffffu, low, o));
+      } else {
+        low = __shfl_sync(0xffffffffu, lim, 0);
       }
-      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      sh->red[i & 1][half][row] = mt;
-      pair_bar(1 + quarter);
-      mt = fmaxf(mt, sh->red[i & 1][half ^ 1][row]);
-      // both warps of a row see the same maxima and so decide alike
-      const bool far = live && mt > m && (m == -INFINITY || (mt - m) * c > RESCALE_LOG2);
-      if (__any_sync(0xffffffffu, far)) {
-        // a row's reference follows from the row alone: the others of the warp keep
-        // theirs (factor 1), and rows that are not there ask for nothing
-        const float f = far ? fast_exp2((m - mt) * c) : 1.f;    // 0 for a first maximum
-        m = far ? mt : m;
-        if (i > 0) {
-          // S(i) was formed after product i - NS, so of the products that report
-          // to one of the NS barriers at most one is under way
-          wait_on(ok, &sh->o_done[(i - 1) % NS], ((i - 1) / NS) & 1, a.wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) ok = false;
-          tc_fence_after();
-#pragma unroll 1
-          for (int n = 0; n < D / 2; n += 32) {
-            uint32_t o[32];
-            const uint32_t at = tmem + lanes + C::TMEM_O + (uint32_t)(half * (D / 2) + n);
-            tmem_ld32_nowait(at, o);
-            tmem_wait_ld(o);
+      float m = -INFINITY;      // reference maximum of the raw scores
+      float l = 0.f;            // this thread's half of the row sum
+
+      for (int i = 0; i < blocks; ++i) {
+        const int last_b = b;
+        const uint32_t last_turn = turn;
+        b = b == NS - 1 ? 0 : b + 1;
+        turn ^= b == 0;
+        wait_on(ok, &sh->s_full[b], turn, wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) ok = false;
+        tc_fence_after();
+        const uint32_t st = tmem + lanes + (uint32_t)b * BN + (uint32_t)half * 64;
+        uint32_t r0[32], r1[32];
+        tmem_ld32_nowait(st, r0);
+        tmem_ld32_nowait(st + 32, r1);
+        tmem_wait_ld(r0);
+        tmem_wait_ld(r1);
+        const int64_t key = (int64_t)(it.first_block + i) * BN + half * 64;
+        if (low < key + 64) {
+          const int seen = (int)max((int64_t)-1, min((int64_t)64, lim - key));
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(at, o);
+          for (int k = 0; k < 32; ++k) {
+            if (k >= seen) r0[k] = 0xff800000u;
+            if (k + 32 >= seen) r1[k] = 0xff800000u;
           }
         }
-        l *= f;
-      }
-      const float nm = m == -INFINITY ? 0.f : -m * c;
-      const uint64_t c2 = pk(c, c), nm2 = pk(nm, nm);
-      uint32_t w[32];
-      uint64_t sum[4] = {0, 0, 0, 0};
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        float e0, e1, e2, e3;
-        unpk(fma2(pk(__uint_as_float(r0[k]), __uint_as_float(r0[k + 1])), c2, nm2), e0, e1);
-        unpk(fma2(pk(__uint_as_float(r1[k]), __uint_as_float(r1[k + 1])), c2, nm2), e2, e3);
-        e0 = fast_exp2(e0);
-        e1 = fast_exp2(e1);
-        e2 = fast_exp2(e2);
-        e3 = fast_exp2(e3);
-        sum[k / 2 % 2] = add2(sum[k / 2 % 2], pk(e0, e1));
-        sum[2 + k / 2 % 2] = add2(sum[2 + k / 2 % 2], pk(e2, e3));
-        w[k / 2] = pack2<IO>(e0, e1);
-        w[16 + k / 2] = pack2<IO>(e2, e3);
-      }
-      float la, lb;
-      unpk(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), la, lb);
-      l += la + lb;
-      // over this half's own scores, which are in registers by now
-      tmem_st32(st, w);
-      tmem_wait_st();
-      if (tail && i == blocks - 1) {
-        // the rows of V past the end are someone else's, or nothing: clear them
-        wait_on(ok, &sh->v_tail, 0, a.wait_ns);
-        const int s = (2 * blocks - 1) % C::RING;
-        const int from = (int)(key_end - (int64_t)(first_block + i) * BN);
-        const uint32_t vt2 = ring + (uint32_t)s * C::STAGE;
-        constexpr int ATOMS = D / 64 / CG;
-        for (int x = from * 8 + tid; x < BN * 8; x += 256)
-#pragma unroll
-          for (int at = 0; at < ATOMS; ++at)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             vt2 + (uint32_t)(at * BN * 128 + x * 16)),
-                         "r"(0)
-                         : "memory");
-        fence_async_smem();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 1)
-          mbar_arrive(&sh->p_ready[b]);
-        else if (tail && i == blocks - 1)
-          arrive_remote_release(ready + 8u * b);
-        else
-          arrive_remote(ready + 8u * b);
-      }
-    }
-
-    // ---- the end: o = O / l ----
-    if (blocks > 0) {
-      wait_on(ok, &sh->o_done[(blocks - 1) % NS], ((blocks - 1) / NS) & 1, a.wait_ns);
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
-      tc_fence_after();
-    }
-    sh->red[blocks & 1][half][row] = l;
-    pair_bar(1 + quarter);
-    l += sh->red[blocks & 1][half ^ 1][row];
-    const int h = h0 + (row & (gp - 1));
-    if (PREFIX) {
-      const int64_t slot = ((int64_t)split * a.total_q + (live ? tok : 0)) * a.h_q + h;
-      if (live && half == 0) a.part_ml[slot] = make_float2(m * c, l);
+        for (int k = 0; k < 32; k += 4) {
+          mx[0] = max3(mx[0], __uint_as_float(r0[k]), __uint_as_float(r0[k + 1]));
+          mx[1] = max3(mx[1], __uint_as_float(r0[k + 2]), __uint_as_float(r0[k + 3]));
+          mx[2] = max3(mx[2], __uint_as_float(r1[k]), __uint_as_float(r1[k + 1]));
+          mx[3] = max3(mx[3], __uint_as_float(r1[k + 2]), __uint_as_float(r1[k + 3]));
+        }
+        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        flip ^= 1;
+        sh->red[flip][half][row] = mt;
+        pair_bar(1 + quarter);
+        mt = fmaxf(mt, sh->red[flip][half ^ 1][row]);
+        // both warps of a row see the same maxima and so decide alike
+        const bool far = live && mt > m && (m == -INFINITY || (mt - m) * c > RESCALE_LOG2);
+        if (__any_sync(0xffffffffu, far)) {
+          // a row's reference follows from the row alone: the others of the warp keep
+          // theirs (factor 1), and rows that are not there ask for nothing
+          const float f = far ? fast_exp2((m - mt) * c) : 1.f;    // 0 for a first maximum
+          m = far ? mt : m;
+          if (i > 0) {
+            // S(i) was formed after product i - NS, so of the products that report
+            // to one of the NS barriers at most one is under way
+            wait_on(ok, &sh->o_done[last_b], last_turn, wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) ok = false;
+            tc_fence_after();
 #pragma unroll 1
-      for (int n = 0; n < D / 2 && blocks > 0; n += 32) {
-        uint32_t o[32];
-        const int col = half * (D / 2) + n;
-        tmem_ld32_nowait(tmem + lanes + C::TMEM_O + (uint32_t)col, o);
-        tmem_wait_ld(o);
-        if (live && l > 0.f) {
-          float* dst = a.part_o + slot * D + col;
+            for (int n = 0; n < D / 2; n += 32) {
+              uint32_t o[32];
+              const uint32_t at = tmem + lanes + C::TMEM_O + (uint32_t)(half * (D / 2) + n);
+              tmem_ld32_nowait(at, o);
+              tmem_wait_ld(o);
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            st_global_32b(dst + k, o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5], o[k + 6],
-                          o[k + 7]);
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st32(at, o);
+            }
+          }
+          l *= f;
+        }
+        const float nm = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t c2 = pk(c, c), nm2 = pk(nm, nm);
+        uint32_t w[32];
+        uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float e0, e1, e2, e3;
+          unpk(fma2(pk(__uint_as_float(r0[k]), __uint_as_float(r0[k + 1])), c2, nm2), e0, e1);
+          unpk(fma2(pk(__uint_as_float(r1[k]), __uint_as_float(r1[k + 1])), c2, nm2), e2, e3);
+          e0 = fast_exp2(e0);
+          e1 = fast_exp2(e1);
+          e2 = fast_exp2(e2);
+          e3 = fast_exp2(e3);
+          sum[k / 2 % 2] = add2(sum[k / 2 % 2], pk(e0, e1));
+          sum[2 + k / 2 % 2] = add2(sum[2 + k / 2 % 2], pk(e2, e3));
+          w[k / 2] = pack2<IO>(e0, e1);
+          w[16 + k / 2] = pack2<IO>(e2, e3);
+        }
+        float la, lb;
+        unpk(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), la, lb);
+        l += la + lb;
+        // over this half's own scores, which are in registers by now
+        tmem_st32(st, w);
+        tmem_wait_st();
+        const bool last = tail && i == blocks - 1;
+        if (last) {
+          // the rows of V past the end are someone else's, or nothing: clear them
+          // (two barriers in turn: the loads may be one item ahead)
+          wait_on(ok, &sh->v_tail[tails & 1], (tails >> 1) & 1, wait_ns);
+          const int from = (int)(it.len_k - (int64_t)(it.first_block + i) * BN);
+          const uint32_t vt2 = ring + (uint32_t)sh->tail_stage[tails & 1] * C::STAGE;
+          constexpr int ATOMS = D / 64 / CG;
+          for (int x = from * 8 + tid; x < BN * 8; x += 256)
+#pragma unroll
+            for (int at = 0; at < ATOMS; ++at)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               vt2 + (uint32_t)(at * BN * 128 + x * 16)),
+                           "r"(0)
+                           : "memory");
+          fence_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (local)
+            mbar_arrive(&sh->p_ready[b]);
+          else if (last)
+            arrive_remote_release(ready + 8u * b);
+          else
+            arrive_remote(ready + 8u * b);
         }
       }
-    } else {
+      if (tail) ++tails;
+
+      // ---- the end: o = O / l ----
+      flip ^= 1;
+      sh->red[flip][half][row] = l;
+      pair_bar(1 + quarter);
+      l += sh->red[flip][half ^ 1][row];
+      if (blocks > 0) {
+        wait_on(ok, &sh->o_done[b], turn, wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) ok = false;
+        tc_fence_after();
+      }
       const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no key: zeros; NaN stays
-      const int64_t t = q0 + tok;
-      const IO* gate = a.gate.data && live
+      const int64_t t = it.q0 + tok;
+      const IO* gate = !PREFIX && a.gate.data && live
                            ? reinterpret_cast<const IO*>(a.gate.data) + t * a.gate.token_stride +
                                  h * a.gate.head_stride
                            : nullptr;
       IO* out = reinterpret_cast<IO*>(a.o) + (t * a.h_q + h) * D;
       const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+      const int64_t slot = PREFIX ? ((int64_t)it.split * a.total_q + (live ? tok : 0)) * a.h_q + h : 0;
+      if (PREFIX && live && half == 0) a.part_ml[slot] = make_float2(m * c, l);
 #pragma unroll 1
       for (int n = 0; n < D / 2; n += 32) {
         uint32_t o[32];
         const int col = half * (D / 2) + n;
+        Vec8<IO> gv[4];
+        if (gate) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) gv[v].load(gate + col + 8 * v);
+        }
         if (blocks > 0) {
           tmem_ld32_nowait(tmem + lanes + C::TMEM_O + (uint32_t)col, o);
           tmem_wait_ld(o);
+          if (n + 32 == D / 2) {        // all of O is in registers: the next item may write it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (local)
+                mbar_arrive(&sh->o_free);
+              else
+                arrive_remote(freed);
+            }
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
-        if (live) {
+        if (PREFIX) {
+          if (live && l != 0.f) {
+            float* dst = a.part_o + slot * D + col;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              st_global_32b(dst + k, o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5],
+                            o[k + 6], o[k + 7]);
+          }
+        } else if (live) {
 #pragma unroll
           for (int k = 0; k < 32; k += 16) {
             Vec8<IO> ov[2];
@@ -757,10 +950,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               for (int e = 0; e < 8; ++e)
                 f[e] = l == 0.f ? 0.f : __uint_as_float(o[k + 8 * v + e]) * inv;
               if (gate) {
-                Vec8<IO> gv;
-                gv.load(gate + col + k + 8 * v);
                 float g[8];
-                gv.get(g);
+                gv[k / 8 + v].get(g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= gate_sigmoid(g[e]);
               }
@@ -776,6 +967,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
         }
       }
+      if (!ok) break;
+      item_over();
     }
   }
   if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
