@@ -34,7 +34,6 @@ constexpr int ROWS = 16;              // query heads per item, at most
 constexpr int DEC_WARPS = 4;          // consumer warps, 16 keys of a block each
 constexpr int DEC_THREADS = 32 * (DEC_WARPS + 1);
 constexpr int DEC_MAX_STAGES = 8;
-constexpr int DEC_CTAS = 152;         // one per SM: the ring takes an SM's shared memory
 
 template <int D>
 struct DecCfg {
@@ -43,7 +42,11 @@ struct DecCfg {
   static constexpr uint32_t OBUF = ROWS * D * 4;           // joining the four warps' O
   static constexpr uint32_t Q_ROW = D * 2 + 16;            // padded: no bank conflicts in ldmatrix
   static constexpr uint32_t HEAD = (1024 + ROWS * Q_ROW + OBUF + 1023) / 1024 * 1024;
-  static constexpr int FIT = (int)((232448u - HEAD) / STAGE);
+  // Smaller heads want more warps to keep up with the loads; at 256 one warp's
+  // accumulator takes the registers of two.
+  static constexpr int PER_SM = D == 256 ? 1 : D == 128 ? 2 : 3;
+  static constexpr int CTAS = 152 * PER_SM;
+  static constexpr int FIT = (int)((233472u / PER_SM - 1024u - HEAD) / STAGE);
   static constexpr int STAGES = FIT < DEC_MAX_STAGES ? FIT : DEC_MAX_STAGES;
   static constexpr uint32_t SMEM = HEAD + STAGES * STAGE;
 };
@@ -209,7 +212,7 @@ struct Walk {
 };
 
 template <typename IO, int D>
-__global__ void __launch_bounds__(DEC_THREADS, 1)
+__global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
     attn_decode_kernel(const __grid_constant__ DecArgs p, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
   using C = DecCfg<D>;
@@ -557,32 +560,44 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
 // partial outputs are independent loads (one after the other they would cost a
 // memory latency each).
 constexpr int MERGE_THREADS = 256;
-constexpr int MAX_PARTS = 2 * DEC_CTAS;   // of the prefix pass and of this one
+
+// Partials of one item, at most: every head of a sequence has as many units, so
+// an item is at most 1 / heads of the line, and its ends cut two runs.
+static __host__ __device__ __forceinline__ int most_parts(const DecArgs& p) {
+  return p.prefix + p.ctas / (p.a.h_kv * p.subs) + 2;
+}
+
+// One item of 16 rows behind a prefix in 152 parts, runs of 456 CTAs: 83 KB.
+constexpr int MERGE_SMEM = 96 * 1024;
 
 template <typename IO, int D>
 __global__ void __launch_bounds__(MERGE_THREADS)
     attn_merge_kernel(const __grid_constant__ DecArgs p) {
-  __shared__ int64_t sums[MERGE_THREADS / 32];
-  __shared__ float2 ml[MAX_PARTS * ROWS];   // [part][row]: statistics, then (factor, -)
-  __shared__ int64_t first_row[MAX_PARTS];
+  extern __shared__ __align__(16) unsigned char merge_smem[];
+  __shared__ int64_t sums[MERGE_THREADS / 32], s_mine;
   __shared__ float inv_l[ROWS];
   const GdnAttnArgs& a = p.a;
+  int64_t* first_row = reinterpret_cast<int64_t*>(merge_smem);          // [part]
+  float2* ml = reinterpret_cast<float2*>(first_row + most_parts(p));    // [part][row]: statistics,
+                                                                        // then (factor, sum)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int heads = a.h_kv * p.subs;
   const int n = (int)a.total_q;
   const int b = blockIdx.x / heads, hs = blockIdx.x % heads;
   const int h0 = item_head(p, hs);
   const int rows = item_rows(p, hs);
-  int64_t total = 0, mine = 0;
+  int64_t total = 0;
   for (int base = 0; base < n; base += MERGE_THREADS) {
     const int i = base + tid;
     int64_t before;
     const int64_t u = i < n ? blocks_of(own_keys(p, i)) * heads : 0;
-    total += block_scan(u, sums, MERGE_THREADS / 32, before);
-    if (base <= b) mine += block_scan(i < b ? u : 0, sums, MERGE_THREADS / 32, before);
+    const int64_t all = block_scan(u, sums, MERGE_THREADS / 32, before);
+    if (i == b) s_mine = total + before;
+    total += all;
   }
+  __syncthreads();
   const int64_t nt = blocks_of(own_keys(p, b));
-  const int64_t u0 = mine + hs * nt, u1 = u0 + nt;
+  const int64_t u0 = s_mine + hs * nt, u1 = u0 + nt;
   // the CTAs whose runs meet [u0, u1)
   const int64_t runs = runs_of(p, total);
   int64_t c0 = 0, c1 = -1;
@@ -627,40 +642,34 @@ __global__ void __launch_bounds__(MERGE_THREADS)
     if (lane == 0) inv_l[row] = ll == 0.f ? 0.f : 1.0f / ll;
   }
   __syncthreads();
-  for (int x = tid; x < rows * (D / 8); x += MERGE_THREADS) {
-    const int row = x / (D / 8), col = x % (D / 8) * 8;
-    float y[8] = {};
+  for (int x = tid; x < rows * (D / 4); x += MERGE_THREADS) {
+    const int row = x / (D / 4), col = x % (D / 4) * 4;
+    float y[4] = {};
 #pragma unroll 8
     for (int i = 0; i < parts; ++i) {
       const float2 w = ml[i * rows + row];
-      const float4* src =
-          reinterpret_cast<const float4*>(a.part_o + (first_row[i] + row) * D + col);
-      const float4 v0 = src[0], v1 = src[1];
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + (first_row[i] + row) * D + col);
       if (w.y != 0.f) {
-        y[0] = fmaf(w.x, v0.x, y[0]);
-        y[1] = fmaf(w.x, v0.y, y[1]);
-        y[2] = fmaf(w.x, v0.z, y[2]);
-        y[3] = fmaf(w.x, v0.w, y[3]);
-        y[4] = fmaf(w.x, v1.x, y[4]);
-        y[5] = fmaf(w.x, v1.y, y[5]);
-        y[6] = fmaf(w.x, v1.z, y[6]);
-        y[7] = fmaf(w.x, v1.w, y[7]);
+        y[0] = fmaf(w.x, v.x, y[0]);
+        y[1] = fmaf(w.x, v.y, y[1]);
+        y[2] = fmaf(w.x, v.z, y[2]);
+        y[3] = fmaf(w.x, v.w, y[3]);
       }
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] *= inv_l[row];
+    for (int e = 0; e < 4; ++e) y[e] *= inv_l[row];
     if (a.gate.data && inv_l[row] != 0.f) {
-      Vec8<IO> gv;
-      gv.load(reinterpret_cast<const IO*>(a.gate.data) + (int64_t)b * a.gate.token_stride +
-              (h0 + row) * a.gate.head_stride + col);
-      float gf[8];
-      gv.get(gf);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= gate_sigmoid(gf[e]);
+      const uint2 g = *reinterpret_cast<const uint2*>(
+          reinterpret_cast<const IO*>(a.gate.data) + (int64_t)b * a.gate.token_stride +
+          (h0 + row) * a.gate.head_stride + col);
+      const float2 g0 = unpack2<IO>(g.x), g1 = unpack2<IO>(g.y);
+      y[0] *= gate_sigmoid(g0.x);
+      y[1] *= gate_sigmoid(g0.y);
+      y[2] *= gate_sigmoid(g1.x);
+      y[3] *= gate_sigmoid(g1.y);
     }
-    Vec8<IO> ov;
-    ov.set(y);
-    ov.store(reinterpret_cast<IO*>(a.o) + ((int64_t)b * a.h_q + h0 + row) * D + col);
+    *reinterpret_cast<uint2*>(reinterpret_cast<IO*>(a.o) + ((int64_t)b * a.h_q + h0 + row) * D +
+                              col) = make_uint2(pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3]));
   }
 }
 
@@ -683,7 +692,7 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
   p.prefix = a.splits;
   p.start = a.splits > 0 ? a.shared_len : 0;
   p.base_row = (int64_t)a.splits * a.total_q * a.h_q;
-  p.ctas = DEC_CTAS;
+  p.ctas = C::CTAS;
   const int page = 1 << a.page_shift;
   p.box_rows = page < KEYS ? page : KEYS;
   const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn_tensor_map_encoder());
@@ -709,6 +718,10 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)C::SMEM)) != cudaSuccess)
       return e;
+    if ((e = cudaFuncSetAttribute(attn_merge_kernel<IO, D>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  MERGE_SMEM)) != cudaSuccess)
+      return e;
     if (dev >= 0 && dev < 64) opted_in[dev] = 1;
   }
   // This pass needs nothing of the prefix pass and starts on SMs as they become
@@ -726,7 +739,7 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p, kmap, vmap)) != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)(a.total_q * a.h_kv * p.subs));
   cfg.blockDim = dim3(MERGE_THREADS);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = (size_t)most_parts(p) * (8 + 8 * p.rows);
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attn_merge_kernel<IO, D>, p);
 }
@@ -746,7 +759,8 @@ int64_t gdn_attn_decode_slots(int h_q, int h_kv, int d, int n, int64_t shared_le
   const int rows = group_rows(h_q, h_kv);
   const int64_t items = (int64_t)n * h_kv * ((h_q / h_kv + ROWS - 1) / ROWS);
   // prefix partials, two cut items per CTA, and with a prefix one per whole item
-  return splits * n * h_q + (2 * DEC_CTAS + (splits > 0 ? items : 0)) * rows;
+  const int ctas = d == 64 ? DecCfg<64>::CTAS : d == 128 ? DecCfg<128>::CTAS : DecCfg<256>::CTAS;
+  return splits * n * h_q + (2 * ctas + (splits > 0 ? items : 0)) * rows;
 }
 
 cudaError_t gdn_launch_attn_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {

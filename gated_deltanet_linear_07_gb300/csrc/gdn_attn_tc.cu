@@ -556,8 +556,30 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     uint32_t phase = 0;
     int used = 0, tails = 0;        // items with keys, and with a tail, so far
     TcItem it;
+    // A prefix's pages, 32 at a time, one to a lane: a lookup per box would be a
+    // memory latency each on the way of the loads.
+    struct Pages {
+      int64_t first = -32;
+      int32_t id = 0;
+    } k_pages, v_pages;
+    auto page_of = [&](Pages& c, int64_t pos) {
+      const int64_t pg = pos >> a.page_shift;
+      if (pg < c.first || pg >= c.first + 32) {
+        c.first = pg;
+        const int64_t mine = pg + lane;
+        c.id = 0;
+        if (mine << a.page_shift < a.shared_len) {
+          c.id = __ldg(a.cache.block_table + mine);
+          if (c.id < 0 || c.id >= a.cache.num_pages) {
+            set_status(a.d_status, GDN_DEV_BAD_PAGE);
+            c.id = 0;
+          }
+        }
+      }
+      return __shfl_sync(0xffffffffu, c.id, (int)(pg - c.first));
+    };
     while (next_item(it)) {
-      if (it.blocks > 0 && lane == 0) {
+      if (it.blocks > 0) {
         const int kvh = it.head / p.subs;
         const int h0 = kvh * (a.h_q / a.h_kv) + (it.head % p.subs) * gp;
         const int64_t tok0 = (it.tile * CG + rank) * cta_tokens;
@@ -567,25 +589,22 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           const int64_t left = PREFIX ? it.len_k - t : (int64_t)n;
           return left <= 0 ? 0 : (int)min((int64_t)n, (left + box - 1) / box * box);
         };
-        auto load_rows = [&](uint32_t dst, const CUtensorMap* map, int64_t t, int n, int box,
-                             int kb0, int kbs, uint32_t bar) {
-          if (!PREFIX) tma_load_4d<CG>(dst, map, 0, (int)(it.k0 + t), kb0, kvh, bar);
+        auto load_rows = [&](uint32_t dst, const CUtensorMap* map, Pages& pages, int64_t t, int n,
+                             int box, int kb0, int kbs, uint32_t bar) {
+          if (!PREFIX && lane == 0) tma_load_4d<CG>(dst, map, 0, (int)(it.k0 + t), kb0, kvh, bar);
           for (int r = 0; PREFIX && r < n && t + r < it.len_k; r += box) {
             const int64_t pos = t + r;
-            int32_t page = __ldg(a.cache.block_table + (pos >> a.page_shift));
-            if (page < 0 || page >= a.cache.num_pages) {
-              set_status(a.d_status, GDN_DEV_BAD_PAGE);
-              page = 0;
-            }
-            const int64_t row = (((int64_t)page * a.h_kv + kvh) << a.page_shift) +
+            const int64_t page = page_of(pages, pos);
+            const int64_t row = ((page * a.h_kv + kvh) << a.page_shift) +
                                 (pos & ((1 << a.page_shift) - 1));
-            for (int kb = 0; kb < kbs; ++kb)
-              tma_load_4d<CG>(dst + (uint32_t)(kb * n + r) * 128u, map, 0, (int)row, kb0 + kb, 0,
+            if (lane < kbs)
+              tma_load_4d<CG>(dst + (uint32_t)(lane * n + r) * 128u, map, 0, (int)row, kb0 + lane, 0,
                               bar);
           }
         };
         auto room = [&]() {         // the stage's last user is through with it
           wait_on(ok, &sh->empty[s], phase ^ 1, wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
           return ok;
         };
         auto next_stage = [&]() {
@@ -599,20 +618,24 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             if (!room()) break;
             const int64_t t = (int64_t)(it.first_block + i) * BN;
             const int n = BN / CG;
-            if (rank == 0) {
+            if (rank == 0 && lane == 0) {
               int rows = 0;
               for (int c = 0; c < CG; ++c) rows += rows_of(t + c * n, n, p.k_rows);
               mbar_expect_tx(&sh->full[s], (uint32_t)rows * D * 2);
             }
-            load_rows(ring + (uint32_t)s * C::STAGE, &kmap, t + (int64_t)rank * n, n, p.k_rows, 0,
-                      D / 64, lead(&sh->full[s]));
+            __syncwarp();
+            load_rows(ring + (uint32_t)s * C::STAGE, &kmap, k_pages, t + (int64_t)rank * n, n,
+                      p.k_rows, 0, D / 64, lead(&sh->full[s]));
             next_stage();
           }
           if (i == 0) {          // Q, once the last item's scores are all formed
             if (used > 0) wait_on(ok, &sh->q_empty, (used - 1) & 1, wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if (rank == 0) mbar_expect_tx(&sh->q_full, C::Q_BYTES * CG);
-            tma_load_4d<CG>(q_smem, &qmap, 0, h0, (int)(it.q0 + tok0), 0, lead(&sh->q_full));
+            if (lane == 0) {
+              if (rank == 0) mbar_expect_tx(&sh->q_full, C::Q_BYTES * CG);
+              tma_load_4d<CG>(q_smem, &qmap, 0, h0, (int)(it.q0 + tok0), 0, lead(&sh->q_full));
+            }
           }
           if (i >= AHEAD) {      // V block i - AHEAD: this CTA's share of its channels
             if (!room()) break;
@@ -621,17 +644,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             // a tail reports here: this CTA clears its rows past the end
             const bool own = tail && i == it.blocks + AHEAD - 1;
             uint64_t* const own_bar = &sh->v_tail[tails & 1];
-            if (own) {
-              sh->tail_stage[tails & 1] = s;
-              mbar_expect_tx(own_bar, bytes);
+            if (lane == 0) {
+              if (own) {
+                sh->tail_stage[tails & 1] = s;
+                mbar_expect_tx(own_bar, bytes);
+              }
+              if (rank == 0) {
+                if (own)
+                  mbar_arrive(&sh->full[s]);   // nobody waits for it; the phase has to pass
+                else
+                  mbar_expect_tx(&sh->full[s], bytes * CG);
+              }
             }
-            if (rank == 0) {
-              if (own)
-                mbar_arrive(&sh->full[s]);   // nobody waits for it; the phase has to pass
-              else
-                mbar_expect_tx(&sh->full[s], bytes * CG);
-            }
-            load_rows(ring + (uint32_t)s * C::STAGE, &vmap, t, BN, p.v_rows,
+            __syncwarp();
+            load_rows(ring + (uint32_t)s * C::STAGE, &vmap, v_pages, t, BN, p.v_rows,
                       (int)rank * (D / 64 / CG), D / 64 / CG,
                       !own ? lead(&sh->full[s])
                            : CG == 2 ? map_cta(smem_u32(own_bar), rank) : smem_u32(own_bar));
@@ -641,7 +667,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         ++used;
         if (tail) ++tails;
       }
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       item_over();
     }
