@@ -176,4 +176,6 @@ int64_t gdn_attn_decode_slots(int h_q, int h_kv, int d, int n, int64_t shared_le
 cudaError_t gdn_launch_attn_decode(const GdnAttnArgs& a, int io, cudaStream_t s);
 // How many CTA groups share the keys of the prefix pass (0: no pass).
 int gdn_attn_prefix_splits(int h_q, int h_kv, int d, int n, int64_t shared_len);
+// SMs that the prefix pass takes.
+int gdn_attn_prefix_ctas(int h_q, int h_kv, int d, int n, int64_t shared_len);
 cudaError_t gdn_launch_attn_prefix(const GdnAttnArgs& a, int io, cudaStream_t s);

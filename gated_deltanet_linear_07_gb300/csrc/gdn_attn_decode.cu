@@ -67,6 +67,8 @@ struct DecArgs {
   int32_t subs;          // items per (sequence, key/value head)
   int32_t box_rows;      // rows per TMA box
   int32_t ctas;          // CTAs that share the units
+  int32_t early, delay;  // of them, those that start beside the prefix pass, and how many units
+                         // of time before the others (0: no prefix pass)
   int32_t prefix;        // prefix partials per row (0: none)
 };
 
@@ -82,11 +84,45 @@ __device__ __forceinline__ int64_t own_keys(const DecArgs& p, int b) {
 }
 __device__ __forceinline__ int64_t blocks_of(int64_t keys) { return (keys + KEYS - 1) / KEYS; }
 
-// The units are shared by this many CTAs, in runs [units i / runs, units (i + 1) / runs):
-// none of them is empty.
-__device__ __forceinline__ int64_t runs_of(const DecArgs& p, int64_t units) {
-  return units < p.ctas ? units : (int64_t)p.ctas;
-}
+// Which units each CTA takes: run c is [start(c), start(c + 1)).  Without a prefix
+// pass the runs are equal.  Behind one, the first `early` CTAs start on the SMs
+// that the prefix pass leaves free and the others when it ends, `delay` units of
+// time later: the line is stretched by that much for each of those, and their
+// runs leave the stretch out.  (Where the early ones can do all of it before, they
+// do.)  Behind a long prefix some runs may be empty.
+struct Line {
+  int64_t units, stretched;
+  int ctas, early, delay;
+  __device__ __forceinline__ Line(const DecArgs& p, int64_t n) : units(n), stretched(n), delay(p.delay) {
+    const bool alone = p.early > 0 && n < (int64_t)p.delay * p.early;
+    if (p.early == 0 || alone) {
+      const int most = alone ? p.early : p.ctas;
+      ctas = n < most ? (int)n : most;
+      early = ctas;
+    } else {
+      ctas = p.ctas;
+      early = p.early;
+      stretched += (int64_t)delay * (ctas - early);
+    }
+  }
+  __device__ __forceinline__ int64_t start(int c) const {
+    return stretched * c / ctas - (c > early ? (int64_t)delay * (c - early) : 0);
+  }
+  // The CTA whose run holds unit u: the last whose run starts at or before it.
+  __device__ __forceinline__ int owner(int64_t u) const {
+    if (early == ctas) return (int)(((u + 1) * ctas - 1) / stretched);
+    int lo = 0, hi = ctas;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      const int64_t out = mid > early ? (int64_t)delay * (mid - early) : 0;
+      if (stretched * mid < (u + out + 1) * ctas)   // start(mid) <= u
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  }
+};
 
 // Sum of v over the CTA's threads (in every thread) and, in `before`, over the
 // threads below this one.
@@ -243,8 +279,9 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
     units = b < n ? blocks_of(own_keys(p, b)) * heads : 0;
     total += block_scan(units, sh->sum, DEC_WARPS + 1, before);
   }
-  const int64_t runs = runs_of(p, total), c = blockIdx.x;
-  const int64_t w0 = c < runs ? total * c / runs : 0, w1 = c < runs ? total * (c + 1) / runs : 0;
+  const Line line(p, total);
+  const int c = (int)blockIdx.x;
+  const int64_t w0 = c < line.ctas ? line.start(c) : 0, w1 = c < line.ctas ? line.start(c + 1) : 0;
   int64_t seen = 0;
   for (int base = 0; base < n && w0 < w1; base += DEC_THREADS) {
     const int b = base + tid;
@@ -561,10 +598,11 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
 // memory latency each).
 constexpr int MERGE_THREADS = 256;
 
-// Partials of one item, at most: every head of a sequence has as many units, so
-// an item is at most 1 / heads of the line, and its ends cut two runs.
+// Partials of one item, at most.  With equal runs every head of a sequence has as
+// many units, so an item is at most 1 / heads of the line, and its ends cut two
+// runs; the short runs behind a prefix pass may all meet one item.
 static __host__ __device__ __forceinline__ int most_parts(const DecArgs& p) {
-  return p.prefix + p.ctas / (p.a.h_kv * p.subs) + 2;
+  return p.prefix + (p.early > 0 ? p.ctas : p.ctas / (p.a.h_kv * p.subs) + 2);
 }
 
 // One item of 16 rows behind a prefix in 152 parts, runs of 456 CTAs: 83 KB.
@@ -599,31 +637,33 @@ __global__ void __launch_bounds__(MERGE_THREADS)
   const int64_t nt = blocks_of(own_keys(p, b));
   const int64_t u0 = s_mine + hs * nt, u1 = u0 + nt;
   // the CTAs whose runs meet [u0, u1)
-  const int64_t runs = runs_of(p, total);
-  int64_t c0 = 0, c1 = -1;
+  const Line line(p, total);
+  int c0 = 0, c1 = -1;
   bool whole = false;
   if (nt > 0) {
-    c0 = ((u0 + 1) * runs - 1) / total;
-    c1 = (u1 * runs - 1) / total;
+    c0 = line.owner(u0);
+    c1 = line.owner(u1 - 1);
     whole = c0 == c1;
   }
-  const int parts = p.prefix + (int)(c1 - c0 + 1);
+  const int parts = p.prefix + c1 - c0 + 1;
   for (int i = tid; i < parts; i += MERGE_THREADS) {   // partial i's first row of the workspace
     if (i < p.prefix) {
       first_row[i] = ((int64_t)i * n + b) * a.h_q + h0;
     } else if (whole) {
       first_row[i] = p.base_row + (2 * (int64_t)p.ctas + (int64_t)b * heads + hs) * p.rows;
     } else {
-      const int64_t c = c0 + (i - p.prefix);
+      const int c = c0 + (i - p.prefix);
       // a run that starts inside the item left its first partial, else its last
-      first_row[i] = p.base_row + (2 * c + (total * c / runs > u0 ? 0 : 1)) * p.rows;
+      const int64_t at = line.start(c);
+      first_row[i] = at == line.start(c + 1) ? -1 : p.base_row + (2 * c + (at > u0 ? 0 : 1)) * p.rows;
     }
   }
   pdl_wait();
   if (nt > 0 && whole && p.prefix == 0) return;   // written already
   __syncthreads();
   for (int i = tid; i < parts * rows; i += MERGE_THREADS)
-    ml[i] = a.part_ml[first_row[i / rows] + i % rows];
+    ml[i] = first_row[i / rows] < 0 ? make_float2(0.f, 0.f)   // an empty run
+                                    : a.part_ml[first_row[i / rows] + i % rows];
   __syncthreads();
   for (int row = warp; row < rows; row += MERGE_THREADS / 32) {
     float mm = -INFINITY, ll = 0.f;
@@ -648,7 +688,9 @@ __global__ void __launch_bounds__(MERGE_THREADS)
 #pragma unroll 8
     for (int i = 0; i < parts; ++i) {
       const float2 w = ml[i * rows + row];
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + (first_row[i] + row) * D + col);
+      // (of an empty run, anything that is there: its factor is 0)
+      const float4 v = *reinterpret_cast<const float4*>(
+          a.part_o + (max(first_row[i], (int64_t)0) + row) * D + col);
       if (w.y != 0.f) {
         y[0] = fmaf(w.x, v.x, y[0]);
         y[1] = fmaf(w.x, v.y, y[1]);
@@ -693,6 +735,18 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
   p.start = a.splits > 0 ? a.shared_len : 0;
   p.base_row = (int64_t)a.splits * a.total_q * a.h_q;
   p.ctas = C::CTAS;
+  p.early = p.delay = 0;
+  if (a.splits > 0) {
+    // The SMs that the prefix pass leaves free, and its length in units of 64 keys:
+    // 128 keys of it take about as long as 0.8 units, or 0.6 below head dim 256
+    // where the units are smaller, and it starts and ends in about 5.
+    const int left = 152 - gdn_attn_prefix_ctas(a.h_q, a.h_kv, D, (int)a.total_q, a.shared_len);
+    if (left > 0) {
+      const int64_t blocks = ((a.shared_len + 127) / 128 + a.splits - 1) / a.splits;
+      p.early = left * C::PER_SM;
+      p.delay = (int)(blocks * (D == 256 ? 8 : 6) / 10 + 5);
+    }
+  }
   const int page = 1 << a.page_shift;
   p.box_rows = page < KEYS ? page : KEYS;
   const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn_tensor_map_encoder());

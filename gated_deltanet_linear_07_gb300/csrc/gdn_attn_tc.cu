@@ -422,7 +422,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     mbar_init(&sh->q_empty, 1);
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&sh->s_full[s], 1);
-      mbar_init(&sh->p_ready[s], 8 * CG);
+      // its own eight warps, and in a pair's first CTA the other one's together
+      mbar_init(&sh->p_ready[s], CG == 2 && rank == 0 ? 9 : 8);
       mbar_init(&sh->o_done[s], 1);
     }
     mbar_init(&sh->o_free, 8 * CG);
@@ -556,52 +557,39 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     uint32_t phase = 0;
     int used = 0, tails = 0;        // items with keys, and with a tail, so far
     TcItem it;
-    // A prefix's pages, 32 at a time, one to a lane: a lookup per box would be a
-    // memory latency each on the way of the loads.
-    struct Pages {
-      int64_t first = -32;
-      int32_t id = 0;
-    } k_pages, v_pages;
-    auto page_of = [&](Pages& c, int64_t pos) {
-      const int64_t pg = pos >> a.page_shift;
-      if (pg < c.first || pg >= c.first + 32) {
-        c.first = pg;
-        const int64_t mine = pg + lane;
-        c.id = 0;
-        if (mine << a.page_shift < a.shared_len) {
-          c.id = __ldg(a.cache.block_table + mine);
-          if (c.id < 0 || c.id >= a.cache.num_pages) {
-            set_status(a.d_status, GDN_DEV_BAD_PAGE);
-            c.id = 0;
-          }
-        }
-      }
-      return __shfl_sync(0xffffffffu, c.id, (int)(pg - c.first));
-    };
+    // In the cache a block's rows lie in pages: each lane brings one box of the block
+    // (rows of one page, 64 channels) and looks its page up a block ahead.  (One
+    // lane after the other with a lookup each held a pair to 45 GB/s per SM.)
+    const int k_box = lane % (D / 64), k_row = lane / (D / 64) * p.k_rows;
+    const int v_box = lane % (D / 64 / CG), v_row = lane / (D / 64 / CG) * p.v_rows;
     while (next_item(it)) {
       if (it.blocks > 0) {
         const int kvh = it.head / p.subs;
         const int h0 = kvh * (a.h_q / a.h_kv) + (it.head % p.subs) * gp;
         const int64_t tok0 = (it.tile * CG + rank) * cta_tokens;
         const bool tail = has_tail(it);
-        // rows of [t, t + n) that exist, in whole boxes
-        auto rows_of = [&](int64_t t, int n, int box) -> int {
-          const int64_t left = PREFIX ? it.len_k - t : (int64_t)n;
-          return left <= 0 ? 0 : (int)min((int64_t)n, (left + box - 1) / box * box);
-        };
-        auto load_rows = [&](uint32_t dst, const CUtensorMap* map, Pages& pages, int64_t t, int n,
-                             int box, int kb0, int kbs, uint32_t bar) {
-          if (!PREFIX && lane == 0) tma_load_4d<CG>(dst, map, 0, (int)(it.k0 + t), kb0, kvh, bar);
-          for (int r = 0; PREFIX && r < n && t + r < it.len_k; r += box) {
-            const int64_t pos = t + r;
-            const int64_t page = page_of(pages, pos);
-            const int64_t row = ((page * a.h_kv + kvh) << a.page_shift) +
-                                (pos & ((1 << a.page_shift) - 1));
-            if (lane < kbs)
-              tma_load_4d<CG>(dst + (uint32_t)(lane * n + r) * 128u, map, 0, (int)row, kb0 + lane, 0,
-                              bar);
+        const int keys = PREFIX ? (int)it.len_k : 0;
+        auto page_at = [&](int pos) {
+          int32_t page = PREFIX && pos < keys ? __ldg(a.cache.block_table + (pos >> a.page_shift)) : 0;
+          if (PREFIX && (page < 0 || page >= a.cache.num_pages)) {
+            set_status(a.d_status, GDN_DEV_BAD_PAGE);
+            page = 0;
           }
+          return page;
         };
+        auto row_at = [&](int32_t page, int pos) {
+          return (int)((((int64_t)page * a.h_kv + kvh) << a.page_shift) +
+                       (pos & ((1 << a.page_shift) - 1)));
+        };
+        // rows of [t, t + n) that exist, in whole boxes
+        auto rows_of = [&](int t, int n, int box_mask) {
+          return !PREFIX || t + n <= keys ? n : max(0, keys - t + box_mask) & ~box_mask;
+        };
+        const int k_pos = it.first_block * BN + (int)rank * (BN / CG) + k_row;
+        const int v_pos = it.first_block * BN + v_row;
+        int32_t k_page = 0, v_page = 0;
+        if (PREFIX && k_row < BN / CG) k_page = page_at(k_pos);
+        if (PREFIX && v_row < BN) v_page = page_at(v_pos);
         auto room = [&]() {         // the stage's last user is through with it
           wait_on(ok, &sh->empty[s], phase ^ 1, wait_ns);
           ok = __all_sync(0xffffffffu, ok);
@@ -616,16 +604,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         for (int i = 0; i < it.blocks + AHEAD && ok; ++i) {
           if (i < it.blocks) {   // K block i: this CTA's share of its rows
             if (!room()) break;
-            const int64_t t = (int64_t)(it.first_block + i) * BN;
-            const int n = BN / CG;
+            const int t = (it.first_block + i) * BN;
+            constexpr int n = BN / CG;
+            const uint32_t dst = ring + (uint32_t)s * C::STAGE;
+            const uint32_t bar = lead(&sh->full[s]);
             if (rank == 0 && lane == 0) {
               int rows = 0;
-              for (int c = 0; c < CG; ++c) rows += rows_of(t + c * n, n, p.k_rows);
+              for (int c = 0; c < CG; ++c) rows += rows_of(t + c * n, n, p.k_rows - 1);
               mbar_expect_tx(&sh->full[s], (uint32_t)rows * D * 2);
             }
             __syncwarp();
-            load_rows(ring + (uint32_t)s * C::STAGE, &kmap, k_pages, t + (int64_t)rank * n, n,
-                      p.k_rows, 0, D / 64, lead(&sh->full[s]));
+            if (!PREFIX) {
+              if (lane == 0)
+                tma_load_4d<CG>(dst, &kmap, 0, (int)(it.k0 + t + (int)rank * n), 0, kvh, bar);
+            } else if (k_row < n) {
+              const int pos = k_pos + i * BN;
+              if (pos < keys)
+                tma_load_4d<CG>(dst + (uint32_t)(k_box * n + k_row) * 128u, &kmap, 0,
+                                row_at(k_page, pos), k_box, 0, bar);
+              k_page = page_at(i + 1 < it.blocks ? pos + BN : keys);
+            }
             next_stage();
           }
           if (i == 0) {          // Q, once the last item's scores are all formed
@@ -639,11 +637,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           if (i >= AHEAD) {      // V block i - AHEAD: this CTA's share of its channels
             if (!room()) break;
-            const int64_t t = (int64_t)(it.first_block + i - AHEAD) * BN;
-            const uint32_t bytes = (uint32_t)rows_of(t, BN, p.v_rows) * (D / CG) * 2;
+            const int t = (it.first_block + i - AHEAD) * BN;
+            const uint32_t bytes = (uint32_t)rows_of(t, BN, p.v_rows - 1) * (D / CG) * 2;
             // a tail reports here: this CTA clears its rows past the end
             const bool own = tail && i == it.blocks + AHEAD - 1;
             uint64_t* const own_bar = &sh->v_tail[tails & 1];
+            const uint32_t dst = ring + (uint32_t)s * C::STAGE;
+            const uint32_t bar = !own ? lead(&sh->full[s])
+                                      : CG == 2 ? map_cta(smem_u32(own_bar), rank) : smem_u32(own_bar);
             if (lane == 0) {
               if (own) {
                 sh->tail_stage[tails & 1] = s;
@@ -657,10 +658,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
               }
             }
             __syncwarp();
-            load_rows(ring + (uint32_t)s * C::STAGE, &vmap, v_pages, t, BN, p.v_rows,
-                      (int)rank * (D / 64 / CG), D / 64 / CG,
-                      !own ? lead(&sh->full[s])
-                           : CG == 2 ? map_cta(smem_u32(own_bar), rank) : smem_u32(own_bar));
+            constexpr int kbs = D / 64 / CG;
+            if (!PREFIX) {
+              if (lane == 0)
+                tma_load_4d<CG>(dst, &vmap, 0, (int)(it.k0 + t), (int)rank * kbs, kvh, bar);
+            } else if (v_row < BN) {
+              const int pos = v_pos + (i - AHEAD) * BN;
+              if (pos < keys)
+                tma_load_4d<CG>(dst + (uint32_t)(v_box * BN + v_row) * 128u, &vmap, 0,
+                                row_at(v_page, pos), (int)rank * kbs + v_box, 0, bar);
+              v_page = page_at(i - AHEAD + 1 < it.blocks ? pos + BN : keys);
+            }
             next_stage();
           }
         }
@@ -749,6 +757,27 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         ++used;
       }
+      if (CG == 2 && rank == 1) {
+        // The second CTA's weights are reported by this warp, which has nothing else to
+        // do: an arrival at the other CTA took each softmax warp 140 cycles.
+        const uint32_t ready = map_cta(smem_u32(&sh->p_ready[0]), 0);
+        const bool tail = has_tail(it);
+        for (int i = 0; i < it.blocks && ok; ++i) {
+          spin_on(ok, &sh->p_ready[pb], turn, wait_ns);
+          if (!ok) break;
+          if (lane == 0) {
+            if (tail && i == it.blocks - 1)
+              arrive_remote_release(ready + 8u * pb);
+            else
+              arrive_remote(ready + 8u * pb);
+          }
+          __syncwarp();
+          if (++pb == NS) {
+            pb = 0;
+            turn ^= 1;
+          }
+        }
+      }
       if (!ok) break;
       item_over();
     }
@@ -758,7 +787,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const float c = a.scale_log2;
-    const uint32_t ready = CG == 2 ? map_cta(smem_u32(&sh->p_ready[0]), 0) : 0u;
     const uint32_t freed = CG == 2 ? map_cta(smem_u32(&sh->o_free), 0) : 0u;
     // the first CTA's own arrivals stay in it
     const bool local = CG == 1 || rank == 0;
@@ -899,14 +927,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (local)
-            mbar_arrive(&sh->p_ready[b]);
-          else if (last)
-            arrive_remote_release(ready + 8u * b);
-          else
-            arrive_remote(ready + 8u * b);
-        }
+        if (lane == 0) mbar_arrive(&sh->p_ready[b]);
       }
       if (tail) ++tails;
 
@@ -1121,21 +1142,37 @@ cudaError_t gdn_launch_attn_prefill(const GdnAttnArgs& a, int io, cudaStream_t s
                         : launch_tc_d<__half, false>(a, io, s);
 }
 
-// Enough CTA groups to give every SM (pair) one, each with at least two key
-// blocks: a partial output costs h_q d floats per row to write and to merge.
+// Row blocks x head groups of the prefix pass, and the CTAs of each.
+static int64_t prefix_items(int h_q, int h_kv, int d, int n, int& cg) {
+  cg = d == 64 ? 1 : 2;
+  int gp = 1;
+  while ((h_q / h_kv) % (2 * gp) == 0 && gp < 128) gp *= 2;
+  const int64_t tokens = (int64_t)gdn::attn::BM / gp * cg;
+  return ((n + tokens - 1) / tokens) * (h_q / gp);
+}
+
+// The keys of the prefix are cut so that two thirds of the SMs have a share, each
+// of at least two blocks: the pass over the sequences' own keys starts on the
+// other third at once.  (All SMs for the one, then all for the other: 75 us instead
+// of PREFIX_US for 64 rows behind 32768 tokens with up to 1024 of their own, and a
+// partial output costs h_q d floats per row to write and to merge.)
 int gdn_attn_prefix_splits(int h_q, int h_kv, int d, int n, int64_t shared_len) {
   // one row alone shares nothing: its own pass covers the prefix too
   if (shared_len <= 0 || n <= 1) return 0;
-  const int cg = d == 64 ? 1 : 2;
-  int gp = 1;
-  while ((h_q / h_kv) % (2 * gp) == 0 && gp < 128) gp *= 2;
-  const int64_t rows = (int64_t)gdn::attn::BM / gp * cg;
-  const int64_t items = ((n + rows - 1) / rows) * (h_q / gp);
+  int cg;
+  const int64_t items = prefix_items(h_q, h_kv, d, n, cg);
   const int64_t blocks = (shared_len + gdn::attn::BN - 1) / gdn::attn::BN;
-  int64_t splits = (152 / cg) / items;
+  int64_t splits = (96 / cg) / items;
   if (splits > (blocks + 1) / 2) splits = (blocks + 1) / 2;
   if (splits < 1) splits = 1;
   return (int)splits;
+}
+
+int gdn_attn_prefix_ctas(int h_q, int h_kv, int d, int n, int64_t shared_len) {
+  int cg;
+  const int64_t items = prefix_items(h_q, h_kv, d, n, cg);
+  const int64_t ctas = items * gdn_attn_prefix_splits(h_q, h_kv, d, n, shared_len) * cg;
+  return ctas < 152 ? (int)ctas : 152;
 }
 
 cudaError_t gdn_launch_attn_prefix(const GdnAttnArgs& a, int io, cudaStream_t s) {
