@@ -80,7 +80,6 @@ struct __align__(16) TcShared {
   uint64_t item_full[2], item_empty[2], taken_full[2], taken_free;
   TcItem item[2];
   uint32_t tmem;
-  int32_t bad;
   int32_t tail_stage[2]; // ring stage of an item's last V block, where it passes the end
   float red[2][2][BM];   // row maxima of the two column halves, two turns
 };
@@ -303,61 +302,73 @@ struct TcLaunch {
   int32_t k_rows, v_rows; // rows of one K / V box
 };
 
-// Whether every sequence lies within the totals, in order; by all threads.
-__device__ __forceinline__ bool sequences_ok(const GdnAttnArgs& a, TcShared* sh) {
-  for (int b = threadIdx.x; b < a.num_seqs; b += TC_THREADS) {
-    const int64_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
-    const int64_t klo = a.cu_kv[b], khi = a.cu_kv[b + 1];
-    if (hi < lo || lo < 0 || hi > a.total_q || khi < klo || klo < 0 || khi > a.total_kv ||
-        (b == 0 && (lo != 0 || klo != 0)) ||
-        (b == a.num_seqs - 1 && (hi != a.total_q || khi != a.total_kv)))
-      sh->bad = 1;
-  }
-  __syncthreads();
-  return sh->bad == 0;
-}
-
 // Which sequence and which of its row blocks is row block j of the grid, counting
 // from the last block of the last sequence: within a sequence the longest rows
 // come first.  By one warp, which keeps its place between calls.
 struct TileSearch {
-  int base = 0;            // 32 sequences from here (counted from the last one)
+  int base = -1;           // 32 sequences from here (counted from the last one), one to a lane
   int64_t before = 0;      // row blocks of the sequences before them
-  int64_t nt = -1, incl = 0;   // this lane's sequence: its row blocks, and with those before it
+  int64_t q0, len_q, k0, len_k;   // this lane's sequence
+  int64_t nt, incl;               // its row blocks, and with those before it
 
-  __device__ void load(const GdnAttnArgs& a, int tokens) {
-    const int i = base + (threadIdx.x & 31), b = a.num_seqs - 1 - i;
-    nt = b >= 0 ? ((int64_t)a.cu_q[b + 1] - a.cu_q[b] + tokens - 1) / tokens : 0;
+  static __device__ __forceinline__ bool fits(const GdnAttnArgs& a, int b, int64_t lo, int64_t hi,
+                                              int64_t klo, int64_t khi) {
+    return hi >= lo && lo >= 0 && hi <= a.total_q && khi >= klo && klo >= 0 && khi <= a.total_kv &&
+           (b > 0 || (lo == 0 && klo == 0)) &&
+           (b < a.num_seqs - 1 || (hi == a.total_q && khi == a.total_kv));
+  }
+  // False in a lane whose sequence is not within the totals, in its order.
+  __device__ bool load(const GdnAttnArgs& a, int tokens, int first) {
+    const int lane = threadIdx.x & 31, b = a.num_seqs - 1 - first - lane;
+    base = first;
+    q0 = len_q = k0 = len_k = nt = 0;
+    bool fine = true;
+    if (b >= 0) {
+      const int64_t q1 = a.cu_q[b + 1], k1 = a.cu_kv[b + 1];
+      q0 = a.cu_q[b];
+      k0 = a.cu_kv[b];
+      len_q = q1 - q0;
+      len_k = k1 - k0;
+      nt = (len_q + tokens - 1) / tokens;
+      fine = fits(a, b, q0, q1, k0, k1);
+    }
     incl = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if ((threadIdx.x & 31) >= o) incl += v;
+      if (lane >= o) incl += v;
     }
+    return fine;
+  }
+  // Whether all sequences are; leaves the search at the first ones.
+  __device__ bool check(const GdnAttnArgs& a, int tokens) {
+    bool fine = load(a, tokens, 0);
+#pragma unroll 8
+    for (int b = a.num_seqs - 33 - (int)(threadIdx.x & 31); b >= 0; b -= 32)
+      fine = fits(a, b, a.cu_q[b], a.cu_q[b + 1], a.cu_kv[b], a.cu_kv[b + 1]) && fine;
+    return __all_sync(0xffffffffu, fine);
   }
   // False: there is no such block.
-  __device__ bool find(const GdnAttnArgs& a, int tokens, int64_t j, int& seq, int64_t& tile) {
-    if (nt < 0 || j < before) {
-      base = 0;
+  __device__ bool find(const GdnAttnArgs& a, int tokens, int64_t j, TcItem& it) {
+    if (j < before) {
       before = 0;
-      load(a, tokens);
+      load(a, tokens, 0);
     }
     for (;;) {
       const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
       if (j < before + all) break;
+      if (base + 32 >= a.num_seqs) return false;
       before += all;
-      base += 32;
-      if (base >= a.num_seqs) {
-        nt = -1;   // start over next time
-        return false;
-      }
-      load(a, tokens);
+      load(a, tokens, base + 32);
     }
     const int64_t at = j - before;
     const int src = __ffs(__ballot_sync(0xffffffffu, at < incl)) - 1;
     const int64_t n = __shfl_sync(0xffffffffu, nt, src), end = __shfl_sync(0xffffffffu, incl, src);
-    seq = a.num_seqs - 1 - base - src;
-    tile = n - 1 - (at - (end - n));
+    it.tile = n - 1 - (at - (end - n));
+    it.q0 = __shfl_sync(0xffffffffu, q0, src);
+    it.len_q = __shfl_sync(0xffffffffu, len_q, src);
+    it.k0 = __shfl_sync(0xffffffffu, k0, src);
+    it.len_k = __shfl_sync(0xffffffffu, len_k, src);
     return true;
   }
 };
@@ -435,17 +446,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
     mbar_init(&sh->taken_free, CG);
     fence_mbar_init();
-    sh->bad = 0;
   }
   if (warp == WARP_MMA) tmem_alloc_cg<CG>(&sh->tmem, 512);
+  if (warp == WARP_LOAD && lane < 3)
+    asm volatile("prefetch.tensormap [%0];" ::"l"(
+                     reinterpret_cast<uint64_t>(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap))
+                 : "memory");
   tc_fence_before();
   __syncthreads();
-  if (!PREFIX && !sequences_ok(a, sh)) {         // alike in every CTA
-    if (tid == 0) set_status(a.d_status, GDN_DEV_BAD_CU_SEQLENS);
-    if (CG == 2) cluster_sync_all();
-    if (warp == WARP_MMA) tmem_dealloc_cg<CG>(sh->tmem, 512);
-    return;
-  }
   if (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
@@ -475,6 +483,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     // ---- the order of work: this cluster's own item, then taken ones ----
     TileSearch search;
     int64_t item = blockIdx.x / CG;
+    // (alike in every CTA, and before any of them has been given an item)
+    if (!PREFIX && !search.check(a, cta_tokens * CG)) {
+      if (lane == 0) set_status(a.d_status, GDN_DEV_BAD_CU_SEQLENS);
+      item = -1;
+    }
     int asked = 0;
     for (int k = 0; ok;) {
       bool there = item >= 0;
@@ -491,13 +504,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           it.first_block = (int)(all * it.split / a.splits);
           it.blocks = (int)(all * (it.split + 1) / a.splits) - it.first_block;
         } else {
-          int b;
-          there = search.find(a, cta_tokens * CG, rest, b, it.tile);
+          there = search.find(a, cta_tokens * CG, rest, it);
           if (there) {
-            it.q0 = a.cu_q[b];
-            it.len_q = a.cu_q[b + 1] - it.q0;
-            it.k0 = a.cu_kv[b];
-            it.len_k = a.cu_kv[b + 1] - it.k0;
             // the keys that the last token of the pair's rows sees
             const int64_t last = min(it.len_q, (it.tile + 1) * CG * cta_tokens) - 1;
             const int64_t seen = last + it.len_k - it.len_q + 1;
@@ -932,6 +940,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       if (tail) ++tails;
 
       // ---- the end: o = O / l ----
+      // the gate's row comes in under the last product
+      const int64_t t = it.q0 + tok;
+      Vec8<IO> gv[PREFIX ? 1 : D / 16];
+      const bool gated = !PREFIX && a.gate.data && live;
+      if (gated) {
+        const IO* gate = reinterpret_cast<const IO*>(a.gate.data) + t * a.gate.token_stride +
+                         h * a.gate.head_stride + half * (D / 2);
+#pragma unroll
+        for (int v = 0; v < (PREFIX ? 1 : D / 16); ++v) gv[v].load(gate + 8 * v);
+      }
       flip ^= 1;
       sh->red[flip][half][row] = l;
       pair_bar(1 + quarter);
@@ -942,24 +960,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tc_fence_after();
       }
       const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no key: zeros; NaN stays
-      const int64_t t = it.q0 + tok;
-      const IO* gate = !PREFIX && a.gate.data && live
-                           ? reinterpret_cast<const IO*>(a.gate.data) + t * a.gate.token_stride +
-                                 h * a.gate.head_stride
-                           : nullptr;
       IO* out = reinterpret_cast<IO*>(a.o) + (t * a.h_q + h) * D;
       const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
       const int64_t slot = PREFIX ? ((int64_t)it.split * a.total_q + (live ? tok : 0)) * a.h_q + h : 0;
       if (PREFIX && live && half == 0) a.part_ml[slot] = make_float2(m * c, l);
-#pragma unroll 1
+#pragma unroll
       for (int n = 0; n < D / 2; n += 32) {
         uint32_t o[32];
         const int col = half * (D / 2) + n;
-        Vec8<IO> gv[4];
-        if (gate) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) gv[v].load(gate + col + 8 * v);
-        }
         if (blocks > 0) {
           tmem_ld32_nowait(tmem + lanes + C::TMEM_O + (uint32_t)col, o);
           tmem_wait_ld(o);
@@ -995,9 +1003,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 f[e] = l == 0.f ? 0.f : __uint_as_float(o[k + 8 * v + e]) * inv;
-              if (gate) {
+              if (gated) {
                 float g[8];
-                gv[k / 8 + v].get(g);
+                gv[PREFIX ? 0 : (n + k) / 8 + v].get(g);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] *= gate_sigmoid(g[e]);
               }
