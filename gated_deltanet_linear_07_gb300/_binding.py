@@ -136,7 +136,7 @@ def load() -> ctypes.CDLL:
     RP, KV = ctypes.POINTER(gdn_rope_params), ctypes.POINTER(gdn_kv_cache)
     lib.gdn_qk_norm_rope.argtypes = [A, RP, V, V, P, I64, P, P, P]
     lib.gdn_qk_norm_rope.restype = ctypes.c_int
-    lib.gdn_kv_append.argtypes = [A, RP, V, V, V, P, P, I64, KV, P, P, P]
+    lib.gdn_kv_append.argtypes = [A, RP, V, V, V, P, P, I64, KV, P, P, P, P]
     lib.gdn_kv_append.restype = ctypes.c_int
     lib.gdn_attn_prefill.argtypes = [A, V, V, V, P, P, I32, I64, I64, V, P, P, P]
     lib.gdn_attn_prefill.restype = ctypes.c_int
@@ -653,11 +653,12 @@ def gdn_qk_norm_rope(dims, q, k, q_norm, k_norm, inv_freq, positions, q_out=None
 
 
 def gdn_kv_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions, k_cache, v_cache, block_table,
-                  row_seq=None, q_out=None, rope_scale=1.0, d_status=None, stream=None):
+                  row_seq=None, q_out=None, k_out=None, rope_scale=1.0, d_status=None, stream=None):
     """gdn_qk_norm_rope with the keys, and the values, going into the paged
     cache (see gdn_kv_append in include/gdn.h): caches [num_pages, h_kv,
     page_size, d], block_table [num_seqs, pages_per_seq] int32, row_seq [n]
-    int32 (None: row t is sequence t).  Returns q_out (None when q is None)."""
+    int32 (None: row t is sequence t), k_out [n, h_kv, d] or None (packed keys
+    too, for a prompt's attention).  Returns q_out (None when q is None)."""
     lib = _attn_lib()
     n, dt, d, hkv = positions.numel(), _io_of(dims), dims.d, dims.h_kv
     i32 = _torch.int32
@@ -674,6 +675,7 @@ def gdn_kv_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions, k_cache, v
         ctypes.byref(dims), ctypes.byref(p), _ref(qv), ctypes.byref(kv), ctypes.byref(vv),
         _flat(positions, "positions", i32, n),
         None if row_seq is None else _flat(row_seq, "row_seq", i32, n), n, ctypes.byref(c), qp,
+        None if k_out is None else _flat(k_out, "k_out", dt, n * hkv * d),
         None if d_status is None else _flat(d_status, "d_status", i32, 1),
         _attn_stream(stream, positions))
     if rc:

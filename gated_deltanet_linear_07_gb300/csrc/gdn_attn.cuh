@@ -135,7 +135,7 @@ __device__ __forceinline__ float gate_sigmoid(float x) {
 struct GdnRopeArgs {
   gdn_view q, k, v;            // null data: left out (v: no append)
   void* q_out;
-  void* k_out;                 // null with an append: k goes to the cache
+  void* k_out;                 // may be null with an append: k goes to the cache
   const float* q_norm;
   const float* k_norm;
   const double* inv_freq;

@@ -121,8 +121,8 @@ GDN_EXPORT int gdn_qk_norm_rope(const gdn_attn_dims* dims, const gdn_rope_params
 GDN_EXPORT int gdn_kv_append(const gdn_attn_dims* dims, const gdn_rope_params* params,
                              const gdn_view* q, const gdn_view* k, const gdn_view* v,
                              const int32_t* positions, const int32_t* row_seq, int64_t n,
-                             const gdn_kv_cache* cache, void* q_out, int32_t* d_status,
-                             gdn_stream_t stream) {
+                             const gdn_kv_cache* cache, void* q_out, void* k_out,
+                             int32_t* d_status, gdn_stream_t stream) {
   int rc = check_dims(dims, true);
   if (rc != GDN_OK) return rc;
   if (!params || n < 0) return GDN_EINVAL;
@@ -131,7 +131,7 @@ GDN_EXPORT int gdn_kv_append(const gdn_attn_dims* dims, const gdn_rope_params* p
   if (n == 0) return GDN_OK;
   const gdn_view qv = view_or_none(q), kv = view_or_none(k), vv = view_or_none(v);
   if (!kv.data || !vv.data) return GDN_EINVAL;
-  return rope_impl(dims, params, qv, kv, vv, positions, row_seq, n, cache, q_out, nullptr, d_status,
+  return rope_impl(dims, params, qv, kv, vv, positions, row_seq, n, cache, q_out, k_out, d_status,
                    stream);
 }
 

@@ -232,21 +232,22 @@ __device__ __forceinline__ int64_t cache_row(const GdnRopeArgs& a, int64_t t, in
   return (((int64_t)page * a.h_kv) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
-// The finished row to q_out, k_out or the cache (dst: cache_row).
+// The finished row to q_out, k_out or the cache (dst: cache_row); a padding row of
+// an append is zeros.
 template <typename IO, int D>
 __device__ __forceinline__ void put_row(const GdnRopeArgs& a, Row w, int64_t t, int32_t pos,
                                         int64_t dst, int part, Vec8<IO>& x) {
-  if (w.kind == ROW_Q || !a.v.data) {
-    if (a.v.data && pos < 0) {   // padding row of an append
-      const float zero[8] = {};
-      x.set(zero);
-    }
-    IO* out = reinterpret_cast<IO*>(w.kind == ROW_Q ? a.q_out : a.k_out);
-    x.store(out + (t * (w.kind == ROW_Q ? a.h_q : a.h_kv) + w.head) * D + 8 * part);
-  } else if (dst >= 0) {
+  const bool append = a.v.data != nullptr;
+  if (append && pos < 0) {
+    const float zero[8] = {};
+    x.set(zero);
+  }
+  if (append && w.kind != ROW_Q && dst >= 0) {
     const int64_t row = dst + ((int64_t)w.head << a.page_shift);
     x.store(reinterpret_cast<IO*>(w.kind == ROW_V ? a.cache.v : a.cache.k) + row * D + 8 * part);
   }
+  IO* out = reinterpret_cast<IO*>(w.kind == ROW_Q ? a.q_out : w.kind == ROW_K ? a.k_out : nullptr);
+  if (out) x.store(out + (t * (w.kind == ROW_Q ? a.h_q : a.h_kv) + w.head) * D + 8 * part);
 }
 
 // ---- few tokens: one CTA per token, or several with a share of its rows -----
@@ -438,8 +439,9 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
     const int64_t n = a.n;
     const int h_q = a.h_q, h_kv = a.h_kv, page_shift = a.page_shift;
     IO* const q_out = reinterpret_cast<IO*>(a.q_out) + 8 * at.part;
-    IO* const k_out = reinterpret_cast<IO*>(append ? a.cache.k : a.k_out) + 8 * at.part;
-    IO* const v_out = reinterpret_cast<IO*>(a.cache.v) + 8 * at.part;
+    IO* const k_out = a.k_out ? reinterpret_cast<IO*>(a.k_out) + 8 * at.part : nullptr;
+    IO* const k_cache = reinterpret_cast<IO*>(a.cache.k) + 8 * at.part;
+    IO* const v_cache = reinterpret_cast<IO*>(a.cache.v) + 8 * at.part;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x, advance()) {
       const int64_t g = parts == 1 ? u : u / parts;
       const int part = parts == 1 ? 0 : (int)(u - g * parts);
@@ -467,24 +469,28 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
           norm_rotate<IO, D, N>(at, toks, is_q ? q_normed : k_normed, interleaved, rotate, eps, wt,
                                 cs, x);
         }
-        if (is_q || !append) {
-          const int heads = is_q ? h_q : h_kv;
-          IO* out = (is_q ? q_out : k_out) + (g * N * heads + head) * D;
+        if (append) {
 #pragma unroll
-          for (int tt = 0; tt < N; ++tt) {
-            if (append && sh.pos[s][tt] < 0) {   // padding row
+          for (int tt = 0; tt < N; ++tt)
+            if (sh.pos[s][tt] < 0) {   // padding row
               const float zero[8] = {};
               x[tt].set(zero);
             }
-            if (tt < toks) x[tt].store(out + (int64_t)tt * heads * D);
-          }
-        } else {
-          IO* out = (is_v ? v_out : k_out) + ((int64_t)head << page_shift) * D;
+        }
+        if (append && !is_q) {
+          IO* out = (is_v ? v_cache : k_cache) + ((int64_t)head << page_shift) * D;
 #pragma unroll
           for (int tt = 0; tt < N; ++tt) {
             const int64_t dst = sh.dst[s][tt];
             if (tt < toks && dst >= 0) x[tt].store(out + dst * D);
           }
+        }
+        if (is_q || (!is_v && k_out)) {
+          const int heads = is_q ? h_q : h_kv;
+          IO* out = (is_q ? q_out : k_out) + (g * N * heads + head) * D;
+#pragma unroll
+          for (int tt = 0; tt < N; ++tt)
+            if (tt < toks) x[tt].store(out + (int64_t)tt * heads * D);
         }
       }
       __syncwarp();

@@ -526,22 +526,23 @@ int gdn_qk_norm_rope(const gdn_attn_dims* dims, const gdn_rope_params* params, c
  * gdn_kv_append -- the new tokens' keys and values go into the paged cache,
  * the keys normed and rotated on the way as gdn_qk_norm_rope defines it; the
  * queries too, into q_out, when q is given: one launch for a decode step or
- * a prompt.
+ * a prompt.  A prompt's attention reads its keys packed: k_out, when given,
+ * receives them as gdn_qk_norm_rope would leave them.
  *   q, k, v    views [n][h_q or h_kv][d] IO (q with null data: left out)
  *   positions  [n] int32 (device): position of row t in its sequence, which is
  *              also its place in the cache; < 0 marks a padding row (q_out
- *              zeroed, nothing stored)
+ *              and k_out zeroed, nothing stored)
  *   row_seq    [n] int32 (device): the row's sequence; NULL: row t is
  *              sequence t (then n <= cache->num_seqs, else GDN_EINVAL)
  * A row whose sequence is outside [0, num_seqs) or whose position its block
  * table row cannot hold sets GDN_DEV_BAD_LENGTH; one whose page is outside
  * [0, num_pages) sets GDN_DEV_BAD_PAGE.  Such a row is not stored (its q_out
- * is written).  Two rows of one call must not have the same place.
+ * and k_out are written).  Two rows of one call must not have the same place.
  */
 int gdn_kv_append(const gdn_attn_dims* dims, const gdn_rope_params* params, const gdn_view* q,
                   const gdn_view* k, const gdn_view* v, const int32_t* positions,
                   const int32_t* row_seq, int64_t n, const gdn_kv_cache* cache, void* q_out,
-                  int32_t* d_status, gdn_stream_t stream);
+                  void* k_out, int32_t* d_status, gdn_stream_t stream);
 
 /*
  * gdn_attn_prefill -- causal attention over packed prompts with grouped heads.

@@ -70,12 +70,13 @@ BAD_CACHES = [(dict(k=None), -1), (dict(v=None), -1), (dict(table=None), -1), (d
               (dict(pages=1 << 31), -2), (dict(per=1 << 30), -2)]
 
 
-def append(lib, dims=None, k=view(), v=view(), c=None, n=4, row_seq=FAKE, q_out=FAKE, q=view()):
+def append(lib, dims=None, k=view(), v=view(), c=None, n=4, row_seq=FAKE, q_out=FAKE, q=view(),
+           k_out=None):
     p = gdn.gdn_rope_params(FAKE, FAKE, FAKE, 1.0)
     d = dims or gdn.make_attn_dims(**A)
     return lib.gdn_kv_append(ctypes.byref(d), ctypes.byref(p), _binding._ref(q), _binding._ref(k),
                              _binding._ref(v), FAKE, row_seq, n, _binding._ref(c or cache()), q_out,
-                             None, None)
+                             k_out, None, None)
 
 
 def test_append_refusals(lib):
@@ -89,6 +90,7 @@ def test_append_refusals(lib):
     assert append(lib, v=None) == -1
     assert append(lib, q_out=None) == -1
     assert append(lib, v=view(FAKE + 4)) == -5
+    assert append(lib, k_out=FAKE + 8) == -5
 
 
 def prefill(lib, dims=None, q=view(), k=view(), v=view(), cu=FAKE, cu_kv=None, B=2, tq=64, tk=64,

@@ -193,3 +193,27 @@ def test_append_without_queries_and_one_row_per_sequence(gpu_lib):
     pg = table[torch.arange(n), pos.long() // page].long()
     _check(kc.cpu()[pg, :, pos.long() % page], kv[:, :hkv], wk, pos, freq, "half", torch.bfloat16, "k")
     assert torch.equal(vc.cpu()[pg, :, pos.long() % page], kv[:, hkv:])
+
+
+@pytest.mark.parametrize("n", [50, 700])
+def test_append_with_packed_keys_is_the_norm_and_rotation_and_the_append(gpu_lib, n):
+    hq, hkv, d, page = 4, 2, 128, 16
+    i = _inputs(41, n, hq, hkv, d, 128, "bf16", 0)
+    dims = gdn.make_attn_dims(hq, hkv, d, rot_dim=128, page_size=page)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    pos[9] = -1
+    q, k, v = i["qg"][:, :, :d], i["kv"][:, :hkv], i["kv"][:, hkv:]
+    w = (i["wq"], i["wk"], i["freq"], pos)
+    qn, kn = gdn.gdn_qk_norm_rope(dims, q, k, *w)
+    pages = (n + page - 1) // page
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages)
+    seq = torch.zeros(n, dtype=torch.int32, device="cuda")
+    kc = torch.zeros(pages, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    vc, packed = torch.zeros_like(kc), torch.full((n, hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    qa = gdn.gdn_kv_append(dims, q, k, v, *w, kc, vc, table, row_seq=seq, k_out=packed)
+    live = torch.arange(n, device="cuda") != 9
+    assert torch.equal(qa[live], qn[live]) and torch.equal(packed[live], kn[live])
+    assert (qa[9] == 0).all() and (packed[9] == 0).all()
+    rows = kc.transpose(1, 2).reshape(-1, hkv, d)[:n]
+    assert torch.equal(rows[live], kn[live]) and (rows[9] == 0).all()
+    assert torch.equal(vc.transpose(1, 2).reshape(-1, hkv, d)[:n][live], v[live])
