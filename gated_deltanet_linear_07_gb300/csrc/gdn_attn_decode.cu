@@ -16,6 +16,11 @@
 // with their own m, l and O (the 16 x D accumulator of mma.sync m16n8k16, its
 // 16 rows being the item's query heads): no barrier between them inside a run.
 //
+// Few keys in all (at most FEW_BLOCKS blocks per CTA with a cluster of CTAs to an
+// item and no more CTAs than fit at once): the same kernel with the items cut over
+// the clusters, which join their partials through distributed shared memory.  No
+// search for the run, no second launch: 700 keys of 4 heads, FEW_US us instead of 10.
+//
 // Behind a shared prefix (gdn_attn_tc.cu computes it once for all rows) the
 // items start at shared_len and the merge adds the prefix's partials.
 #include <cuda.h>
@@ -34,6 +39,7 @@ constexpr int ROWS = 16;              // query heads per item, at most
 constexpr int DEC_WARPS = 4;          // consumer warps, 16 keys of a block each
 constexpr int DEC_THREADS = 32 * (DEC_WARPS + 1);
 constexpr int DEC_MAX_STAGES = 8;
+constexpr int FEW_BLOCKS = 4;
 
 template <int D>
 struct DecCfg {
@@ -54,6 +60,7 @@ struct DecCfg {
 struct __align__(16) DecShared {
   uint64_t full[DEC_MAX_STAGES], empty[DEC_MAX_STAGES], q_full, q_empty;
   float m[DEC_WARPS][ROWS], l[DEC_WARPS][ROWS];
+  float2 ml[ROWS];       // of the whole CTA, for its cluster
   int64_t sum[DEC_WARPS + 1], found_first;
   int32_t found;
 };
@@ -70,6 +77,7 @@ struct DecArgs {
   int32_t early, delay;  // of them, those that start beside the prefix pass, and how many units
                          // of time before the others (0: no prefix pass)
   int32_t prefix;        // prefix partials per row (0: none)
+  int32_t cluster;       // CTAs per item (the form for few keys; 0: runs of units)
 };
 
 // Keys of sequence b that this pass sees.
@@ -213,6 +221,27 @@ __device__ __forceinline__ int item_rows(const DecArgs& p, int hs) {
   return min(p.rows, p.a.h_q / p.a.h_kv - hs % p.subs * ROWS);
 }
 
+// Four channels of a finished output: y / l, gated (zeros where no key was seen).
+template <typename IO, int D>
+__device__ __forceinline__ void put_four(const GdnAttnArgs& a, int b, int h, int col, float l,
+                                         float (&y)[4]) {
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] *= inv;
+  if (a.gate.data && l != 0.f) {
+    const uint2 g = *reinterpret_cast<const uint2*>(reinterpret_cast<const IO*>(a.gate.data) +
+                                                    (int64_t)b * a.gate.token_stride +
+                                                    h * a.gate.head_stride + col);
+    const float2 g0 = unpack2<IO>(g.x), g1 = unpack2<IO>(g.y);
+    y[0] *= gate_sigmoid(g0.x);
+    y[1] *= gate_sigmoid(g0.y);
+    y[2] *= gate_sigmoid(g1.x);
+    y[3] *= gate_sigmoid(g1.y);
+  }
+  *reinterpret_cast<uint2*>(reinterpret_cast<IO*>(a.o) + ((int64_t)b * a.h_q + h) * D + col) =
+      make_uint2(pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3]));
+}
+
 // The run [w, end) of units, item by item.
 struct Segment {
   int b, hs;             // sequence, and key/value head * subs + sub
@@ -247,7 +276,31 @@ struct Walk {
   }
 };
 
-template <typename IO, int D>
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 ld_peer_16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer_8(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+template <typename IO, int D, bool FEW>
 __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
     attn_decode_kernel(const __grid_constant__ DecArgs p, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
@@ -272,41 +325,59 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
     mbar_init(&sh->q_empty, DEC_WARPS);
     fence_mbar_init();
   }
-  // ---- this CTA's run of units ----
-  int64_t total = 0, units = 0, before = 0;
-  for (int base = 0; base < n; base += DEC_THREADS) {
-    const int b = base + tid;
-    units = b < n ? blocks_of(own_keys(p, b)) * heads : 0;
-    total += block_scan(units, sh->sum, DEC_WARPS + 1, before);
-  }
-  const Line line(p, total);
-  const int c = (int)blockIdx.x;
-  const int64_t w0 = c < line.ctas ? line.start(c) : 0, w1 = c < line.ctas ? line.start(c + 1) : 0;
-  int64_t seen = 0;
-  for (int base = 0; base < n && w0 < w1; base += DEC_THREADS) {
-    const int b = base + tid;
-    int64_t all = total;
-    if (n > DEC_THREADS) {   // else the scan above has it all
-      units = b < n ? blocks_of(own_keys(p, b)) * heads : 0;
-      all = block_scan(units, sh->sum, DEC_WARPS + 1, before);
-    }
-    if (w0 >= seen + before && w0 < seen + before + units) {
-      sh->found = b;
-      sh->found_first = seen + before;
-    }
-    seen += all;
-  }
-  __syncthreads();
-
-  if (w0 < w1) {
-    Walk walk;
-    walk.w = w0;
-    walk.end = w1;
-    walk.b = sh->found;
+  Walk walk;
+  int64_t w0, w1;
+  if (FEW) {
+    // ---- this CTA's share of its cluster's item ----
+    const int item = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+    walk.b = item / heads;
+    walk.hs = item % heads;
     walk.keys = own_keys(p, walk.b);
     walk.nt = blocks_of(walk.keys);
-    walk.hs = (int)((w0 - sh->found_first) / walk.nt);
-    walk.item_first = sh->found_first + walk.hs * walk.nt;
+    walk.item_first = 0;
+    w0 = walk.nt * rank / p.cluster;
+    w1 = walk.nt * (rank + 1) / p.cluster;
+    if (tid < ROWS) sh->ml[tid] = make_float2(-INFINITY, 0.f);
+    __syncthreads();
+  } else {
+    // ---- this CTA's run of units ----
+    int64_t total = 0, units = 0, before = 0;
+    for (int base = 0; base < n; base += DEC_THREADS) {
+      const int b = base + tid;
+      units = b < n ? blocks_of(own_keys(p, b)) * heads : 0;
+      total += block_scan(units, sh->sum, DEC_WARPS + 1, before);
+    }
+    const Line line(p, total);
+    const int c = (int)blockIdx.x;
+    w0 = c < line.ctas ? line.start(c) : 0;
+    w1 = c < line.ctas ? line.start(c + 1) : 0;
+    int64_t seen = 0;
+    for (int base = 0; base < n && w0 < w1; base += DEC_THREADS) {
+      const int b = base + tid;
+      int64_t all = total;
+      if (n > DEC_THREADS) {   // else the scan above has it all
+        units = b < n ? blocks_of(own_keys(p, b)) * heads : 0;
+        all = block_scan(units, sh->sum, DEC_WARPS + 1, before);
+      }
+      if (w0 >= seen + before && w0 < seen + before + units) {
+        sh->found = b;
+        sh->found_first = seen + before;
+      }
+      seen += all;
+    }
+    __syncthreads();
+  }
+
+  if (w0 < w1) {
+    walk.w = w0;
+    walk.end = w1;
+    if (!FEW) {
+      walk.b = sh->found;
+      walk.keys = own_keys(p, walk.b);
+      walk.nt = blocks_of(walk.keys);
+      walk.hs = (int)((w0 - sh->found_first) / walk.nt);
+      walk.item_first = sh->found_first + walk.hs * walk.nt;
+    }
     Segment g;
     bool ok = true;
     int j = 0, items = 0;            // blocks and items so far: the rings' positions
@@ -537,7 +608,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
           consumers_bar();
         }
         // ---- out: the output itself, or a partial result ----
-        const bool direct = g.whole && p.prefix == 0;
+        const bool direct = !FEW && g.whole && p.prefix == 0;
         const int64_t slot = g.whole ? 2 * (int64_t)p.ctas + (int64_t)g.b * heads + g.hs
                                      : 2 * (int64_t)blockIdx.x + (g.t0 > 0 ? 0 : 1);
         const int64_t part = p.base_row + slot * p.rows;
@@ -557,7 +628,12 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
             v0.x += u0.x; v0.y += u0.y; v0.z += u0.z; v0.w += u0.w;
             v1.x += u1.x; v1.y += u1.y; v1.z += u1.z; v1.w += u1.w;
           }
-          if (direct) {
+          if (FEW) {
+            float4* dst = reinterpret_cast<float4*>(obuf + row * D + col);
+            dst[0] = v0;
+            dst[1] = v1;
+            if (col == 0) sh->ml[row] = make_float2(mm, ll);
+          } else if (direct) {
             const float inv = 1.0f / ll;
             float y[8] = {v0.x * inv, v0.y * inv, v0.z * inv, v0.w * inv,
                           v1.x * inv, v1.y * inv, v1.z * inv, v1.w * inv};
@@ -584,6 +660,34 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
       }
     }
     if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
+  }
+  if (FEW) {
+    // ---- the cluster's partials joined, a share of the channels by each CTA ----
+    __syncwarp();
+    cluster_barrier();
+    const int rank = blockIdx.x % p.cluster;
+    const int rows = item_rows(p, walk.hs), h0 = item_head(p, walk.hs);
+    const uint32_t ml_at = smem_u32(sh->ml), o_at = smem_u32(obuf);
+    for (int x = rank * DEC_THREADS + tid; x < rows * (D / 4); x += p.cluster * DEC_THREADS) {
+      const int row = x / (D / 4), col = x % (D / 4) * 4;
+      float mm = -INFINITY, ll = 0.f;
+      for (int r = 0; r < p.cluster; ++r)
+        mm = fmaxf(mm, ld_peer_8(peer_addr(ml_at + 8u * row, r)).x);
+      float y[4] = {};
+      for (int r = 0; r < p.cluster; ++r) {
+        const float2 v = ld_peer_8(peer_addr(ml_at + 8u * row, r));
+        if (v.y == 0.f) continue;   // saw no key
+        const float f = fast_exp2((v.x - mm) * a.scale_log2);
+        const float4 o = ld_peer_16(peer_addr(o_at + (uint32_t)(row * D + col) * 4u, r));
+        ll += f * v.y;
+        y[0] = fmaf(f, o.x, y[0]);
+        y[1] = fmaf(f, o.y, y[1]);
+        y[2] = fmaf(f, o.z, y[2]);
+        y[3] = fmaf(f, o.w, y[3]);
+      }
+      put_four<IO, D>(a, walk.b, h0 + row, col, ll, y);
+    }
+    cluster_barrier();   // the others may still read this CTA's
   }
   // The merge waits for this kernel, and reads the prefix pass's partials too:
   // this kernel may have started before that pass had ended.
@@ -613,7 +717,7 @@ __global__ void __launch_bounds__(MERGE_THREADS)
     attn_merge_kernel(const __grid_constant__ DecArgs p) {
   extern __shared__ __align__(16) unsigned char merge_smem[];
   __shared__ int64_t sums[MERGE_THREADS / 32], s_mine;
-  __shared__ float inv_l[ROWS];
+  __shared__ float sum_l[ROWS];
   const GdnAttnArgs& a = p.a;
   int64_t* first_row = reinterpret_cast<int64_t*>(merge_smem);          // [part]
   float2* ml = reinterpret_cast<float2*>(first_row + most_parts(p));    // [part][row]: statistics,
@@ -679,7 +783,7 @@ __global__ void __launch_bounds__(MERGE_THREADS)
       ml[i * rows + row].x = f;
     }
     ll = warp_sum(ll);
-    if (lane == 0) inv_l[row] = ll == 0.f ? 0.f : 1.0f / ll;
+    if (lane == 0) sum_l[row] = ll;
   }
   __syncthreads();
   for (int x = tid; x < rows * (D / 4); x += MERGE_THREADS) {
@@ -698,20 +802,7 @@ __global__ void __launch_bounds__(MERGE_THREADS)
         y[3] = fmaf(w.x, v.w, y[3]);
       }
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) y[e] *= inv_l[row];
-    if (a.gate.data && inv_l[row] != 0.f) {
-      const uint2 g = *reinterpret_cast<const uint2*>(
-          reinterpret_cast<const IO*>(a.gate.data) + (int64_t)b * a.gate.token_stride +
-          (h0 + row) * a.gate.head_stride + col);
-      const float2 g0 = unpack2<IO>(g.x), g1 = unpack2<IO>(g.y);
-      y[0] *= gate_sigmoid(g0.x);
-      y[1] *= gate_sigmoid(g0.y);
-      y[2] *= gate_sigmoid(g1.x);
-      y[3] *= gate_sigmoid(g1.y);
-    }
-    *reinterpret_cast<uint2*>(reinterpret_cast<IO*>(a.o) + ((int64_t)b * a.h_q + h0 + row) * D +
-                              col) = make_uint2(pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3]));
+    put_four<IO, D>(a, b, h0 + row, col, sum_l[row], y);
   }
 }
 
@@ -764,12 +855,16 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  auto kernel = attn_decode_kernel<IO, D>;
+  auto kernel = attn_decode_kernel<IO, D, false>;
+  auto few = attn_decode_kernel<IO, D, true>;
   static int opted_in[64] = {};
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !opted_in[dev]) {
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)C::SMEM)) != cudaSuccess)
+      return e;
+    if ((e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)C::SMEM)) != cudaSuccess)
       return e;
     if ((e = cudaFuncSetAttribute(attn_merge_kernel<IO, D>,
@@ -778,16 +873,33 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
       return e;
     if (dev >= 0 && dev < 64) opted_in[dev] = 1;
   }
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(DEC_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  // Few keys: the block table bounds the sequences' lengths, which are not known here.
+  p.cluster = 1;
+  const int64_t items = a.total_q * a.h_kv * p.subs;
+  const int64_t blocks = (((int64_t)a.cache.pages_per_seq << a.page_shift) + KEYS - 1) / KEYS;
+  while (p.cluster < 8 && items * p.cluster * 2 <= C::CTAS && p.cluster < blocks) p.cluster *= 2;
+  if (a.splits == 0 && items * p.cluster <= C::CTAS && blocks <= (int64_t)FEW_BLOCKS * p.cluster) {
+    cudaLaunchAttribute cluster[1];
+    cluster[0].id = cudaLaunchAttributeClusterDimension;
+    cluster[0].val.clusterDim.x = (unsigned)p.cluster;
+    cluster[0].val.clusterDim.y = 1;
+    cluster[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(items * p.cluster));
+    cfg.attrs = cluster;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, few, p, kmap, vmap);
+  }
+  p.cluster = 0;
   // This pass needs nothing of the prefix pass and starts on SMs as they become
   // free of it; the merge's search for its partials overlaps this pass's end.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.ctas);
-  cfg.blockDim = dim3(DEC_THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 0 ? 1 : 0;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p, kmap, vmap)) != cudaSuccess) return e;

@@ -56,15 +56,20 @@ def test_decode(gpu_lib, lens, hq, hkv, d, page, io, gate, shared):
     qg = normal(g, n, hq, 2 * d, dtype=dt)
     dims = gdn.make_attn_dims(hq, hkv, d, io=io, page_size=page)
     qgd, status = qg.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda")
-    o = gdn.gdn_attn_decode(dims, qgd[..., :d], kc.cuda(), vc.cuda(), table.cuda(), _ints(lens),
-                            _workspace(dims, n, shared), shared_len=shared,
-                            gate=qgd[..., d:] if gate else None, d_status=status)
-    torch.cuda.synchronize()
-    assert status.item() == 0
     # rows that end inside the prefix see its first tokens
     ref, slack = _attn.decode(qg[..., :d], kc, vc, table, lens, qg[..., d:] if gate else None,
                               _attn.scale_of(d), dt)
-    _attn.check(o, ref, slack, dt, "o")
+    # a block table that could hold long sequences, its other entries no pages at all:
+    # the form for few keys does not apply
+    wide = torch.full((n, max(table.shape[1], 16384 // page)), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    for what, tb in (("o", table), ("o (wide table)", wide)):
+        o = gdn.gdn_attn_decode(dims, qgd[..., :d], kc.cuda(), vc.cuda(), tb.cuda(), _ints(lens),
+                                _workspace(dims, n, shared), shared_len=shared,
+                                gate=qgd[..., d:] if gate else None, d_status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        _attn.check(o, ref, slack, dt, what)
 
 
 def test_growing_scores_and_scale(gpu_lib):
@@ -204,3 +209,34 @@ def test_appending_and_decoding_token_by_token_equals_the_prefill(gpu_lib):
         o = gdn.gdn_attn_decode(dims, qt, kc, vc, table, _ints([t + 1]), ws, gate=gate[one])
         err = (o.float() - full[one].float()).abs().max()
         assert float(err) <= 4 * 2.0 ** -8 * float(v.float().abs().max()), t
+
+
+def test_a_cache_past_32_bit_offsets(gpu_lib):
+    """Rows beyond 2^31 elements of the pool: appended, then read back by decode,
+    alone (few keys) and behind a shared prefix."""
+    g = torch.Generator().manual_seed(44)
+    hq, hkv, d, page = 2, 1, 256, 128
+    pool = 2 ** 31 // (hkv * page * d) + 40
+    kc = torch.empty(pool, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.empty_like(kc)
+    lens = [300, 290]
+    rows = sum(lens)
+    assert (pool - 8) * hkv * page * d > 2 ** 31
+    table = torch.tensor([[pool - 1, pool - 5, pool - 2], [pool - 1, pool - 3, pool - 4]],
+                         dtype=torch.int32)
+    k, v = normal(g, rows, hkv, d), normal(g, rows, hkv, d)
+    k[300:428], v[300:428] = k[:128], v[:128]           # the first page is common
+    pos = torch.cat([torch.arange(n) for n in lens]).to(torch.int32)
+    seq = torch.tensor([0] * 300 + [1] * 290, dtype=torch.int32)
+    pos[300:428] = -1                                    # and written once
+    dims = gdn.make_attn_dims(hq, hkv, d, page_size=page)
+    gdn.gdn_kv_append(dims, None, k.cuda(), v.cuda(), None, None, None, pos.cuda(), kc, vc,
+                      table.cuda(), row_seq=seq.cuda())
+    q = normal(g, 2, hq, d)
+    last = kc[pool - 8:].cpu(), vc[pool - 8:].cpu()
+    ref, slack = _attn.decode(q, *last, table - (pool - 8), lens, None, _attn.scale_of(d),
+                              torch.bfloat16)
+    for shared in (0, 128):
+        o = gdn.gdn_attn_decode(dims, q.cuda(), kc, vc, table.cuda(), _ints(lens),
+                                _workspace(dims, 2, shared), shared_len=shared)
+        _attn.check(o, ref, slack, torch.bfloat16, f"shared {shared}")
