@@ -534,94 +534,33 @@ def rope_frequencies(rot_dim, theta=1e4, scaling=None, factor=1.0, original_len=
     return freq.to(device), rope_scale
 
 
-# The attention calls are short (a decode step's kernels take microseconds), so
-# their marshalling is kept to plain integers: one check per tensor, pointers as
-# numbers, no helper objects beyond the structs that the C ABI takes.
-_torch = None
-_DTYPES = ()
+_calls = None
 
 
-def _attn_lib():
-    """The library, with torch and the dtypes of gdn_attn_dims.io at hand."""
-    global _torch, _DTYPES
-    if _torch is None:
+def _attn_calls():
+    """The marshalling module of the attention calls, handed the library's entry
+    points (its shape, type and layout checks raise as this module's do)."""
+    global _calls
+    if _calls is None:
         import torch
-        _DTYPES = (torch.float32, torch.bfloat16, torch.float16)
-        _torch = torch
-    return _lib if _lib is not None else load()
-
-
-def _attn_stream(stream, t):
-    if stream is not None:
-        return int(stream)
-    # the raw handle of the current stream; current_stream() builds an object first
-    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None and t.is_cuda:
-        return raw(t.device.index)
-    return _torch.cuda.current_stream().cuda_stream
-
-
-def _io_of(dims):
-    io = dims.io
-    return _DTYPES[io] if 0 <= io < 3 else _DTYPES[0]
-
-
-def _view(t, name, dtype, heads, d, n):
-    """gdn_view of a [n, heads, d] tensor whose channels are contiguous."""
-    if t.shape != (n, heads, d):
-        raise ValueError(f"{name} must be [{n}, {heads}, {d}], got {list(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    ts, hs, cs = t.stride()
-    if cs != 1:
-        raise ValueError(f"{name}'s channels must be contiguous")
-    return gdn_view(t.data_ptr(), ts, hs)
-
-
-def _flat(t, name, dtype, numel):
-    """Address of a contiguous tensor of this type and size."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() != numel:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _out(t, name, dtype, n, heads, d, like):
-    """(tensor, address) of an output, allocated when not given."""
-    if t is None:
-        t = _torch.empty((n, heads, d), dtype=dtype, device=like.device)
-        return t, t.data_ptr()
-    return t, _flat(t, name, dtype, n * heads * d)
+        lib = load()
+        path = os.path.join(PKG, "_attn_calls.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it first "
+                              "(python -c 'import __graft_entry__ as g; g.build()')")
+        from . import _attn_calls as calls
+        fns = (lib.gdn_qk_norm_rope, lib.gdn_kv_append, lib.gdn_attn_prefill, lib.gdn_attn_decode)
+        # the raw handle of a device's current stream; current_stream() builds an object first
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        calls.setup((torch.float32, torch.bfloat16, torch.float16), torch.int32, torch.float64,
+                    torch.empty, raw, lambda: torch.cuda.current_stream().cuda_stream, GdnError,
+                    tuple(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
+        _calls = calls
+    return _calls
 
 
 def _ref(v):
     return None if v is None else ctypes.byref(v)
-
-
-def _cache(d, dtype, k_cache, v_cache, block_table):
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[1:] != (d.h_kv, d.page_size, d.d):
-        raise ValueError(f"k_cache must be [num_pages, {d.h_kv}, {d.page_size}, {d.d}], got "
-                         f"{list(shape)}")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [num_seqs, pages_per_seq]")
-    n = k_cache.numel()
-    seqs, per = block_table.shape
-    return gdn_kv_cache(_flat(k_cache, "k_cache", dtype, n), _flat(v_cache, "v_cache", dtype, n),
-                        _flat(block_table, "block_table", _torch.int32, seqs * per), shape[0], seqs,
-                        per)
-
-
-def _rope_params(d, q_norm, k_norm, inv_freq, rope_scale):
-    f32 = _DTYPES[0]
-    return gdn_rope_params(
-        None if q_norm is None else _flat(q_norm, "q_norm", f32, d.d),
-        None if k_norm is None else _flat(k_norm, "k_norm", f32, d.d),
-        None if inv_freq is None else _flat(inv_freq, "inv_freq", _torch.float64, d.rot_dim // 2),
-        rope_scale)
 
 
 def gdn_qk_norm_rope(dims, q, k, q_norm, k_norm, inv_freq, positions, q_out=None, k_out=None,
@@ -630,26 +569,8 @@ def gdn_qk_norm_rope(dims, q, k, q_norm, k_norm, inv_freq, positions, q_out=None
     include/gdn.h): q [n, h_q, d], k [n, h_kv, d] (either may be None), norm
     weights [d] fp32 or None, inv_freq [rot_dim / 2] fp64, positions [n] int32.
     Outputs are allocated when not given.  Returns (q_out, k_out)."""
-    lib = _attn_lib()
-    n, dt, d = positions.numel(), _io_of(dims), dims.d
-    qv = kv = qp = kp = None
-    if q is not None:
-        qv = _view(q, "q", dt, dims.h_q, d, n)
-        q_out, qp = _out(q_out, "q_out", dt, n, dims.h_q, d, q)
-    else:
-        q_out = None
-    if k is not None:
-        kv = _view(k, "k", dt, dims.h_kv, d, n)
-        k_out, kp = _out(k_out, "k_out", dt, n, dims.h_kv, d, k)
-    else:
-        k_out = None
-    p = _rope_params(dims, q_norm, k_norm, inv_freq, rope_scale)
-    rc = lib.gdn_qk_norm_rope(ctypes.byref(dims), ctypes.byref(p), _ref(qv), _ref(kv),
-                              _flat(positions, "positions", _torch.int32, n), n, qp, kp,
-                              _attn_stream(stream, positions))
-    if rc:
-        raise GdnError("gdn_qk_norm_rope", rc)
-    return q_out, k_out
+    return (_calls or _attn_calls()).qk_norm_rope(dims, q, k, q_norm, k_norm, inv_freq, positions,
+                                                  q_out, k_out, rope_scale, stream)
 
 
 def gdn_kv_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions, k_cache, v_cache, block_table,
@@ -659,28 +580,9 @@ def gdn_kv_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions, k_cache, v
     page_size, d], block_table [num_seqs, pages_per_seq] int32, row_seq [n]
     int32 (None: row t is sequence t), k_out [n, h_kv, d] or None (packed keys
     too, for a prompt's attention).  Returns q_out (None when q is None)."""
-    lib = _attn_lib()
-    n, dt, d, hkv = positions.numel(), _io_of(dims), dims.d, dims.h_kv
-    i32 = _torch.int32
-    qv = qp = None
-    if q is not None:
-        qv = _view(q, "q", dt, dims.h_q, d, n)
-        q_out, qp = _out(q_out, "q_out", dt, n, dims.h_q, d, q)
-    else:
-        q_out = None
-    kv, vv = _view(k, "k", dt, hkv, d, n), _view(v, "v", dt, hkv, d, n)
-    p = _rope_params(dims, q_norm, k_norm, inv_freq, rope_scale)
-    c = _cache(dims, dt, k_cache, v_cache, block_table)
-    rc = lib.gdn_kv_append(
-        ctypes.byref(dims), ctypes.byref(p), _ref(qv), ctypes.byref(kv), ctypes.byref(vv),
-        _flat(positions, "positions", i32, n),
-        None if row_seq is None else _flat(row_seq, "row_seq", i32, n), n, ctypes.byref(c), qp,
-        None if k_out is None else _flat(k_out, "k_out", dt, n * hkv * d),
-        None if d_status is None else _flat(d_status, "d_status", i32, 1),
-        _attn_stream(stream, positions))
-    if rc:
-        raise GdnError("gdn_kv_append", rc)
-    return q_out
+    return (_calls or _attn_calls()).kv_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions,
+                                               k_cache, v_cache, block_table, row_seq, q_out, k_out,
+                                               rope_scale, d_status, stream)
 
 
 def gdn_attn_prefill(dims, q, k, v, cu_seqlens, cu_seqlens_kv=None, gate=None, o=None,
@@ -689,22 +591,8 @@ def gdn_attn_prefill(dims, q, k, v, cu_seqlens, cu_seqlens_kv=None, gate=None, o
     include/gdn.h): q [total_q, h_q, d], k, v [total_kv, h_kv, d], cu_seqlens
     [num_seqs + 1] int32 (cu_seqlens_kv None: the same for the keys), gate
     [total_q, h_q, d] or None.  o is allocated when not given.  Returns o."""
-    lib = _attn_lib()
-    dt, d, hq, hkv, i32 = _io_of(dims), dims.d, dims.h_q, dims.h_kv, _torch.int32
-    tq, tk, seqs = q.shape[0], k.shape[0], cu_seqlens.numel() - 1
-    qv = _view(q, "q", dt, hq, d, tq)
-    kv, vv = _view(k, "k", dt, hkv, d, tk), _view(v, "v", dt, hkv, d, tk)
-    gv = None if gate is None else _view(gate, "gate", dt, hq, d, tq)
-    o, op = _out(o, "o", dt, tq, hq, d, q)
-    rc = lib.gdn_attn_prefill(
-        ctypes.byref(dims), ctypes.byref(qv), ctypes.byref(kv), ctypes.byref(vv),
-        _flat(cu_seqlens, "cu_seqlens", i32, seqs + 1),
-        None if cu_seqlens_kv is None else _flat(cu_seqlens_kv, "cu_seqlens_kv", i32, seqs + 1),
-        seqs, tq, tk, _ref(gv), op,
-        None if d_status is None else _flat(d_status, "d_status", i32, 1), _attn_stream(stream, q))
-    if rc:
-        raise GdnError("gdn_attn_prefill", rc)
-    return o
+    return (_calls or _attn_calls()).attn_prefill(dims, q, k, v, cu_seqlens, cu_seqlens_kv, gate, o,
+                                                  d_status, stream)
 
 
 def gdn_attn_decode_workspace_size(dims, n: int, shared_len: int = 0) -> int:
@@ -718,22 +606,6 @@ def gdn_attn_decode(dims, q, k_cache, v_cache, block_table, seq_lens, workspace,
     page_size, d], block_table [num_seqs, pages_per_seq] int32, seq_lens [n]
     int32; the first shared_len tokens (whole pages) are common to all rows.
     o is allocated when not given.  Returns o."""
-    lib = _attn_lib()
-    dt, d, hq, i32 = _io_of(dims), dims.d, dims.h_q, _torch.int32
-    n = q.shape[0]
-    qv = _view(q, "q", dt, hq, d, n)
-    gv = None if gate is None else _view(gate, "gate", dt, hq, d, n)
-    c = _cache(dims, dt, k_cache, v_cache, block_table)
-    o, op = _out(o, "o", dt, n, hq, d, q)
-    ws = ws_bytes = 0
-    if workspace is not None:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    rc = lib.gdn_attn_decode(
-        ctypes.byref(dims), ctypes.byref(qv), ctypes.byref(c), _flat(seq_lens, "seq_lens", i32, n), n,
-        int(shared_len), _ref(gv), op, ws, ws_bytes,
-        None if d_status is None else _flat(d_status, "d_status", i32, 1), _attn_stream(stream, q))
-    if rc:
-        raise GdnError("gdn_attn_decode", rc)
-    return o
+    return (_calls or _attn_calls()).attn_decode(dims, q, k_cache, v_cache, block_table, seq_lens,
+                                                 workspace, int(shared_len), gate, o, d_status,
+                                                 stream)

@@ -1,17 +1,21 @@
 """Builds libgdn_gb300.so in-tree with nvcc for sm_103a (one translation unit
 per .cu file, compiled in parallel, linked with -shared).  No cmake, no torch
-extension machinery: the library is a plain C ABI over the CUDA runtime."""
+extension machinery: the library is a plain C ABI over the CUDA runtime.  Beside
+it goes a small CPython module that marshals the attention calls (gcc)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgdn_gb300.so")
+CALLS_SRC = os.path.join(CSRC, "attn_calls.c")       # the attention calls' marshalling
+CALLS = os.path.join(PKG, "_attn_calls.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -31,15 +35,15 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    out = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
+    out = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".c"))]
     out.append(os.path.join(ROOT, "include", "gdn.h"))
     return out
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _deps() + [__file__])
 
 
@@ -70,6 +74,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    r = subprocess.run(["gcc", "-O2", "-std=c99", "-Wall", "-Werror", "-shared", "-fPIC",
+                        "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"],
+                        "-I", os.path.join(ROOT, "include"), CALLS_SRC, "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {os.path.basename(CALLS_SRC)}:\n{r.stderr[-4000:]}")
+    os.replace(tmp, CALLS)
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -186,6 +186,21 @@ def test_binding_checks_its_tensors():
         gdn.gdn_attn_decode(d, q, kc, kc, table, pos[:2], torch.zeros(1))
 
 
+def test_binding_refuses_host_tensors():
+    d = gdn.make_attn_dims(4, 2, 64, rot_dim=0, page_size=16)
+    q, k = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(3, dtype=torch.int32)
+    kc, table = torch.zeros(5, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(3, 2, dtype=torch.int32)
+    for call in (lambda: gdn.gdn_qk_norm_rope(d, q, k, None, None, None, i),
+                 lambda: gdn.gdn_kv_append(d, q, k, k, None, None, None, i, kc, kc.clone(), table),
+                 lambda: gdn.gdn_attn_prefill(d, q, k, k, i[:2]),
+                 lambda: gdn.gdn_attn_decode(d, q, kc, kc, table, i, torch.zeros(1 << 20))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(TypeError):
+        gdn.gdn_attn_prefill(gdn.make_dims(16, 32, 128, 128), q, k, k, i[:2])
+
+
 def test_rope_frequencies():
     f, s = gdn.rope_frequencies(64, 1e6)
     assert s == 1.0 and f.dtype == torch.float64 and f[0] == 1.0
