@@ -53,12 +53,17 @@ constexpr float RESCALE_LOG2 = 8.0f;
 constexpr uint32_t MISC_BYTES = 3072;
 constexpr int MAX_RING = 8;
 
-template <int D, int CG>
+// The ring takes what shared memory is left, except that packed keys of head dim 256
+// do better with four stages than with five (they come from L2, and a load that runs
+// further ahead holds the next item's queries back: 4096 tokens 94 and 99 us); a
+// prefix comes from HBM and wants them all.
+template <int D, int CG, bool PREFIX>
 struct TcCfg {
   static constexpr uint32_t Q_BYTES = BM * D * 2;
   static constexpr uint32_t STAGE = BN * D * 2 / CG;
   static constexpr int FIT = (int)((232448u - MISC_BYTES - Q_BYTES) / STAGE);
-  static constexpr int RING = FIT < MAX_RING ? FIT : MAX_RING;
+  static constexpr int MOST = D == 256 && !PREFIX ? 4 : MAX_RING;
+  static constexpr int RING = FIT < MOST ? FIT : MOST;
   static constexpr uint32_t SMEM = MISC_BYTES + Q_BYTES + RING * STAGE;
   static constexpr int NS = D == 256 ? 2 : 3;        // S buffers: 512 columns less O's
   static constexpr uint32_t TMEM_O = NS * BN;
@@ -68,7 +73,7 @@ struct TcCfg {
 struct TcItem {
   int64_t q0, len_q, k0, len_k;   // the sequence's queries and keys
   int64_t tile;                   // row block of the pair within the sequence
-  int32_t head;                   // head group
+  int32_t kvh, h0;                // key/value head, first packed query head
   int32_t split, first_block;     // prefix pass: which share of the keys
   int32_t blocks;                 // key blocks; < 0: no more items
 };
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     attn_tc_kernel(const __grid_constant__ TcLaunch p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
-  using C = TcCfg<D, CG>;
+  using C = TcCfg<D, CG, PREFIX>;
   extern __shared__ __align__(1024) unsigned char smem[];
   TcShared* sh = reinterpret_cast<TcShared*>(smem);
   const GdnAttnArgs& a = p.a;
@@ -493,8 +498,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       bool there = item >= 0;
       TcItem it = {};
       if (there) {
-        it.head = (int)(item % heads);
+        const int head = (int)(item % heads);
         const int64_t rest = item / heads;
+        it.kvh = head / p.subs;
+        it.h0 = it.kvh * (a.h_q / a.h_kv) + (head % p.subs) * gp;
         if (PREFIX) {
           it.split = (int)(rest % a.splits);
           it.tile = rest / a.splits;
@@ -572,8 +579,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const int v_box = lane % (D / 64 / CG), v_row = lane / (D / 64 / CG) * p.v_rows;
     while (next_item(it)) {
       if (it.blocks > 0) {
-        const int kvh = it.head / p.subs;
-        const int h0 = kvh * (a.h_q / a.h_kv) + (it.head % p.subs) * gp;
+        const int kvh = it.kvh, h0 = it.h0;
         const int64_t tok0 = (it.tile * CG + rank) * cta_tokens;
         const bool tail = has_tail(it);
         const int keys = PREFIX ? (int)it.len_k : 0;
@@ -805,8 +811,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     while (next_item(it)) {
       const int blocks = it.blocks;
       const bool tail = has_tail(it) && blocks > 0;
-      const int kvh = it.head / p.subs;
-      const int h = kvh * (a.h_q / a.h_kv) + (it.head % p.subs) * gp + (row & (gp - 1));
+      const int h = it.h0 + (row & (gp - 1));
       const int64_t tok = (it.tile * CG + rank) * cta_tokens + (row >> p.gp_shift);
       const bool live = tok < it.len_q;
       // how many keys this row sees; rows past the end follow the last one, so
@@ -1057,7 +1062,7 @@ static cuuint64_t stride_bytes(int64_t elements, int64_t extent) {
 
 template <typename IO, int D, int CG, bool PREFIX>
 static cudaError_t launch_tc(const GdnAttnArgs& a, int io, cudaStream_t s) {
-  using C = TcCfg<D, CG>;
+  using C = TcCfg<D, CG, PREFIX>;
   cudaError_t e = cudaSuccess;
   TcLaunch p;
   p.a = a;
