@@ -19,7 +19,7 @@
 // Few keys in all (at most FEW_BLOCKS blocks per CTA with a cluster of CTAs to an
 // item and no more CTAs than fit at once): the same kernel with the items cut over
 // the clusters, which join their partials through distributed shared memory.  No
-// search for the run, no second launch: 700 keys of 4 heads, FEW_US us instead of 10.
+// search for the run, no second launch: 700 keys of 4 heads, 8 us instead of 10.
 //
 // Behind a shared prefix (gdn_attn_tc.cu computes it once for all rows) the
 // items start at shared_len and the merge adds the prefix's partials.

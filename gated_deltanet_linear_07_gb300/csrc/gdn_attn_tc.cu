@@ -1167,7 +1167,7 @@ static int64_t prefix_items(int h_q, int h_kv, int d, int n, int& cg) {
 // The keys of the prefix are cut so that two thirds of the SMs have a share, each
 // of at least two blocks: the pass over the sequences' own keys starts on the
 // other third at once.  (All SMs for the one, then all for the other: 75 us instead
-// of PREFIX_US for 64 rows behind 32768 tokens with up to 1024 of their own, and a
+// of 65 for 64 rows behind 32768 tokens with up to 1024 of their own, and a
 // partial output costs h_q d floats per row to write and to merge.)
 int gdn_attn_prefix_splits(int h_q, int h_kv, int d, int n, int64_t shared_len) {
   // one row alone shares nothing: its own pass covers the prefix too
