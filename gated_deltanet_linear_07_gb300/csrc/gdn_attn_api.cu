@@ -11,6 +11,7 @@
 namespace {
 
 constexpr size_t kAlign = 256;
+constexpr int64_t kMostTokens = 0x7fff0000;   // the kernels' block ends stay below 2^31
 constexpr uint64_t kWaitNs = 4000000000ull, kTestWaitNs = 2000000ull;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -58,7 +59,7 @@ int check_cache(const gdn_attn_dims* d, const gdn_kv_cache* c) {
   if (!page_ok(d->page_size)) return GDN_EUNSUPPORTED;
   // rows of the pool are 32-bit coordinates of a tensor map
   if (c->num_pages > 0x7fffffffLL / ((int64_t)d->h_kv * d->page_size)) return GDN_EUNSUPPORTED;
-  if ((int64_t)c->pages_per_seq * d->page_size > 0x7fffffffLL) return GDN_EUNSUPPORTED;
+  if ((int64_t)c->pages_per_seq * d->page_size > kMostTokens) return GDN_EUNSUPPORTED;
   if (!aligned16(c->k) || !aligned16(c->v)) return GDN_EALIGN;
   return GDN_OK;
 }
@@ -150,7 +151,7 @@ GDN_EXPORT int gdn_attn_prefill(const gdn_attn_dims* dims, const gdn_view* q, co
   if (!q || !k || !v || !q->data || !o || !cu_seqlens_q) return GDN_EINVAL;
   if (total_kv > 0 && (!k->data || !v->data)) return GDN_EINVAL;
   if (o == q->data || o == k->data || o == v->data || o == gv.data) return GDN_EINVAL;
-  if (total_q > 0x7fffffffLL || total_kv > 0x7fffffffLL) return GDN_EUNSUPPORTED;
+  if (total_q > kMostTokens || total_kv > kMostTokens) return GDN_EUNSUPPORTED;
   if (!aligned16(o)) return GDN_EALIGN;
   if ((rc = check_view(dims, q)) != GDN_OK) return rc;
   if (total_kv > 0 && ((rc = check_view(dims, k)) != GDN_OK || (rc = check_view(dims, v)) != GDN_OK))

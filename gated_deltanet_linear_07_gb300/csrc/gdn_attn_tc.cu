@@ -71,8 +71,9 @@ struct TcCfg {
 
 // One work item, as the order warp hands it to the others.
 struct TcItem {
-  int64_t q0, len_q, k0, len_k;   // the sequence's queries and keys
-  int64_t tile;                   // row block of the pair within the sequence
+  int32_t q0, len_q, k0, len_k;   // the sequence's queries and keys (totals stay 2^16
+                                  // below 2^31, so that block ends fit too)
+  int32_t tile;                   // row block of the pair within the sequence
   int32_t kvh, h0;                // key/value head, first packed query head
   int32_t split, first_block;     // prefix pass: which share of the keys
   int32_t blocks;                 // key blocks; < 0: no more items
@@ -283,6 +284,12 @@ __device__ __forceinline__ void st_global_32b(void* p, uint32_t a, uint32_t b, u
                "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
                : "memory");
 }
+__device__ __forceinline__ void ld_global_32b(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
+                 "=r"(b.w)
+               : "l"(__cvta_generic_to_global(p)));
+}
 __device__ __forceinline__ void pair_bar(int id) {   // the two warps that share 32 rows
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
@@ -369,11 +376,11 @@ struct TileSearch {
     const int64_t at = j - before;
     const int src = __ffs(__ballot_sync(0xffffffffu, at < incl)) - 1;
     const int64_t n = __shfl_sync(0xffffffffu, nt, src), end = __shfl_sync(0xffffffffu, incl, src);
-    it.tile = n - 1 - (at - (end - n));
-    it.q0 = __shfl_sync(0xffffffffu, q0, src);
-    it.len_q = __shfl_sync(0xffffffffu, len_q, src);
-    it.k0 = __shfl_sync(0xffffffffu, k0, src);
-    it.len_k = __shfl_sync(0xffffffffu, len_k, src);
+    it.tile = (int32_t)(n - 1 - (at - (end - n)));
+    it.q0 = __shfl_sync(0xffffffffu, (int32_t)q0, src);
+    it.len_q = __shfl_sync(0xffffffffu, (int32_t)len_q, src);
+    it.k0 = __shfl_sync(0xffffffffu, (int32_t)k0, src);
+    it.len_k = __shfl_sync(0xffffffffu, (int32_t)len_k, src);
     return true;
   }
 };
@@ -481,7 +488,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     ++turn_item;
   };
   auto has_tail = [&](const TcItem& it) {        // the last block passes the keys' end
-    return (int64_t)(it.first_block + it.blocks) * BN > it.len_k;
+    return (it.first_block + it.blocks) * BN > it.len_k;
   };
 
   if (warp == WARP_ORDER) {
@@ -504,19 +511,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         it.h0 = it.kvh * (a.h_q / a.h_kv) + (head % p.subs) * gp;
         if (PREFIX) {
           it.split = (int)(rest % a.splits);
-          it.tile = rest / a.splits;
-          it.len_q = a.total_q;
-          it.len_k = a.shared_len;
-          const int64_t all = (it.len_k + BN - 1) / BN;
+          it.tile = (int32_t)(rest / a.splits);
+          it.len_q = (int32_t)a.total_q;
+          it.len_k = (int32_t)a.shared_len;
+          const int64_t all = (a.shared_len + BN - 1) / BN;
           it.first_block = (int)(all * it.split / a.splits);
           it.blocks = (int)(all * (it.split + 1) / a.splits) - it.first_block;
         } else {
           there = search.find(a, cta_tokens * CG, rest, it);
           if (there) {
             // the keys that the last token of the pair's rows sees
-            const int64_t last = min(it.len_q, (it.tile + 1) * CG * cta_tokens) - 1;
-            const int64_t seen = last + it.len_k - it.len_q + 1;
-            it.blocks = seen > 0 ? (int)((seen + BN - 1) / BN) : 0;
+            const int last = min(it.len_q, (it.tile + 1) * CG * cta_tokens) - 1;
+            const int seen = last + it.len_k - it.len_q + 1;
+            it.blocks = seen > 0 ? (seen + BN - 1) / BN : 0;
           }
         }
       } else {
@@ -580,9 +587,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     while (next_item(it)) {
       if (it.blocks > 0) {
         const int kvh = it.kvh, h0 = it.h0;
-        const int64_t tok0 = (it.tile * CG + rank) * cta_tokens;
+        const int tok0 = (it.tile * CG + (int)rank) * cta_tokens;
         const bool tail = has_tail(it);
-        const int keys = PREFIX ? (int)it.len_k : 0;
+        const int keys = PREFIX ? it.len_k : 0;
         auto page_at = [&](int pos) {
           int32_t page = PREFIX && pos < keys ? __ldg(a.cache.block_table + (pos >> a.page_shift)) : 0;
           if (PREFIX && (page < 0 || page >= a.cache.num_pages)) {
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             __syncwarp();
             if (!PREFIX) {
               if (lane == 0)
-                tma_load_4d<CG>(dst, &kmap, 0, (int)(it.k0 + t + (int)rank * n), 0, kvh, bar);
+                tma_load_4d<CG>(dst, &kmap, 0, it.k0 + t + (int)rank * n, 0, kvh, bar);
             } else if (k_row < n) {
               const int pos = k_pos + i * BN;
               if (pos < keys)
@@ -646,7 +653,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             if (!ok) break;
             if (lane == 0) {
               if (rank == 0) mbar_expect_tx(&sh->q_full, C::Q_BYTES * CG);
-              tma_load_4d<CG>(q_smem, &qmap, 0, h0, (int)(it.q0 + tok0), 0, lead(&sh->q_full));
+              tma_load_4d<CG>(q_smem, &qmap, 0, h0, it.q0 + tok0, 0, lead(&sh->q_full));
             }
           }
           if (i >= AHEAD) {      // V block i - AHEAD: this CTA's share of its channels
@@ -675,7 +682,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             constexpr int kbs = D / 64 / CG;
             if (!PREFIX) {
               if (lane == 0)
-                tma_load_4d<CG>(dst, &vmap, 0, (int)(it.k0 + t), (int)rank * kbs, kvh, bar);
+                tma_load_4d<CG>(dst, &vmap, 0, it.k0 + t, (int)rank * kbs, kvh, bar);
             } else if (v_row < BN) {
               const int pos = v_pos + (i - AHEAD) * BN;
               if (pos < keys)
@@ -812,23 +819,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       const int blocks = it.blocks;
       const bool tail = has_tail(it) && blocks > 0;
       const int h = it.h0 + (row & (gp - 1));
-      const int64_t tok = (it.tile * CG + rank) * cta_tokens + (row >> p.gp_shift);
+      const int tok = (it.tile * CG + (int)rank) * cta_tokens + (row >> p.gp_shift);
       const bool live = tok < it.len_q;
       // how many keys this row sees; rows past the end follow the last one, so
       // that they ask for no mask of their own
-      const int64_t vt = live ? tok : it.len_q - 1;
-      int64_t lim;
+      const int vt = live ? tok : it.len_q - 1;
+      int lim;
       if (PREFIX) {
-        lim = min((int64_t)max(a.seq_lens[vt], 0), it.len_k);
+        lim = min(max(a.seq_lens[vt], 0), it.len_k);
       } else {
         lim = vt + it.len_k - it.len_q + 1;   // causal: the queries are the last of the keys
         lim = lim < 0 ? 0 : lim;
       }
-      int64_t low = lim;   // the least of the warp's rows
+      int low = lim;   // the least of the warp's rows
       if (PREFIX) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-          low = min(low, (int64_t)__shfl_xor_sync(0xffffffffu, low, o));
+          low = min(low, __shfl_xor_sync(0xffffffffu, low, o));
       } else {
         low = __shfl_sync(0xffffffffu, lim, 0);
       }
@@ -849,9 +856,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tmem_ld32_nowait(st + 32, r1);
         tmem_wait_ld(r0);
         tmem_wait_ld(r1);
-        const int64_t key = (int64_t)(it.first_block + i) * BN + half * 64;
+        const int key = (it.first_block + i) * BN + half * 64;
         if (low < key + 64) {
-          const int seen = (int)max((int64_t)-1, min((int64_t)64, lim - key));
+          const int seen = lim - key;
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             if (k >= seen) r0[k] = 0xff800000u;
@@ -926,7 +933,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           // the rows of V past the end are someone else's, or nothing: clear them
           // (two barriers in turn: the loads may be one item ahead)
           wait_on(ok, &sh->v_tail[tails & 1], (tails >> 1) & 1, wait_ns);
-          const int from = (int)(it.len_k - (int64_t)(it.first_block + i) * BN);
+          const int from = it.len_k - (it.first_block + i) * BN;
           const uint32_t vt2 = ring + (uint32_t)sh->tail_stage[tails & 1] * C::STAGE;
           constexpr int ATOMS = D / 64 / CG;
           for (int x = from * 8 + tid; x < BN * 8; x += 256)
@@ -946,14 +953,24 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 
       // ---- the end: o = O / l ----
       // the gate's row comes in under the last product
-      const int64_t t = it.q0 + tok;
-      Vec8<IO> gv[PREFIX ? 1 : D / 16];
+      const int64_t t = (int64_t)it.q0 + tok;
+      Vec8<IO> gv[PREFIX ? 2 : D / 16];
       const bool gated = !PREFIX && a.gate.data && live;
       if (gated) {
         const IO* gate = reinterpret_cast<const IO*>(a.gate.data) + t * a.gate.token_stride +
                          h * a.gate.head_stride + half * (D / 2);
+        // Rows are a thread each, so an access of a warp touches 32 lines whatever its
+        // width, and the load/store unit takes one a cycle: 32 bytes at a time.
+        const bool sectors = (reinterpret_cast<uintptr_t>(gate) & 31u) == 0;
 #pragma unroll
-        for (int v = 0; v < (PREFIX ? 1 : D / 16); ++v) gv[v].load(gate + 8 * v);
+        for (int v = 0; v < (PREFIX ? 2 : D / 16); v += 2) {
+          if (sectors) {
+            ld_global_32b(gate + 8 * v, gv[v].w, gv[v + 1].w);
+          } else {
+            gv[v].load(gate + 8 * v);
+            gv[v + 1].load(gate + 8 * v + 8);
+          }
+        }
       }
       flip ^= 1;
       sh->red[flip][half][row] = l;

@@ -461,7 +461,8 @@ int gdn_decode_step_gated_norm(const gdn_dims* dims, const gdn_params* params,
  *   paged cache  k, v [num_pages][h_kv][page_size][d] IO: the rows of one page
  *                and head are contiguous.  Token p of sequence b is row
  *                p % page_size of page block_table[b][p / page_size].
- * The norm weights are applied as stored, in fp32.  Ownership, streams, graph
+ * The norm weights are applied as stored, in fp32.  A call's tokens, and those a
+ * block table row can hold, are at most 2^31 - 2^16 (GDN_EUNSUPPORTED).  Ownership, streams, graph
  * capture and errors follow the rules at the top of this file.
  * ------------------------------------------------------------------------- */
 #define GDN_ROPE_HALF 0         /* channel i turns with channel i + rot_dim / 2 */
