@@ -12,7 +12,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMostTokens = 0x7fff0000;   // the kernels' block ends stay below 2^31
-constexpr uint64_t kWaitNs = 4000000000ull, kTestWaitNs = 2000000ull;
+constexpr uint64_t kWaitNs = 4000000000ull;
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
@@ -23,7 +23,7 @@ int elem(const gdn_attn_dims* d) { return d->io == GDN_FP32 ? 4 : 2; }
 int check_dims(const gdn_attn_dims* d, bool fp32) {
   if (!d) return GDN_EINVAL;
   if (d->h_q <= 0 || d->h_kv <= 0 || d->h_q % d->h_kv != 0) return GDN_EINVAL;
-  if (d->flags & ~GDN_TEST_WAIT_TIMEOUT) return GDN_EINVAL;
+  if (d->flags != 0) return GDN_EINVAL;
   if (!(d->norm_eps >= 0.f) || d->norm_eps > 1e30f) return GDN_EINVAL;   // also rejects NaN
   if (!(d->scale >= 0.f) || d->scale > 1e30f) return GDN_EINVAL;
   if (d->rope != GDN_ROPE_HALF && d->rope != GDN_ROPE_INTERLEAVED) return GDN_EINVAL;
@@ -38,12 +38,15 @@ int check_dims(const gdn_attn_dims* d, bool fp32) {
 bool page_ok(int32_t p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 int page_shift(int32_t p) { return p == 16 ? 4 : p == 32 ? 5 : p == 64 ? 6 : 7; }
 
-// A view with data: its address and strides keep every row 16-byte aligned,
-// and its rows lie within what a tensor map and 64-bit offsets can address.
-int check_view(const gdn_attn_dims* d, const gdn_view* v) {
+// A view [tokens][heads][d] with data: its address and strides keep every row
+// 16-byte aligned, no two rows of it are the same (a tensor map has no stride of
+// zero), and its rows lie within what a tensor map and 64-bit offsets can address.
+int check_view(const gdn_attn_dims* d, const gdn_view* v, int64_t tokens, int64_t heads) {
   if (!aligned16(v->data)) return GDN_EALIGN;
   if (v->token_stride < 0 || v->head_stride < 0) return GDN_EINVAL;
   if (v->token_stride * elem(d) % 16 != 0 || v->head_stride * elem(d) % 16 != 0) return GDN_EALIGN;
+  if ((tokens > 1 && v->token_stride == 0) || (heads > 1 && v->head_stride == 0))
+    return GDN_EUNSUPPORTED;
   if (v->token_stride >= (1LL << 36) || v->head_stride >= (1LL << 36)) return GDN_EUNSUPPORTED;
   return GDN_OK;
 }
@@ -78,7 +81,7 @@ int rope_impl(const gdn_attn_dims* d, const gdn_rope_params* pr, const gdn_view&
     return GDN_EALIGN;
   for (const gdn_view* w : {&q, &k, &v})
     if (w->data) {
-      const int rc = check_view(d, w);
+      const int rc = check_view(d, w, n, w == &q ? d->h_q : d->h_kv);
       if (rc != GDN_OK) return rc;
     }
   GdnRopeArgs a;
@@ -153,10 +156,11 @@ GDN_EXPORT int gdn_attn_prefill(const gdn_attn_dims* dims, const gdn_view* q, co
   if (o == q->data || o == k->data || o == v->data || o == gv.data) return GDN_EINVAL;
   if (total_q > kMostTokens || total_kv > kMostTokens) return GDN_EUNSUPPORTED;
   if (!aligned16(o)) return GDN_EALIGN;
-  if ((rc = check_view(dims, q)) != GDN_OK) return rc;
-  if (total_kv > 0 && ((rc = check_view(dims, k)) != GDN_OK || (rc = check_view(dims, v)) != GDN_OK))
+  if ((rc = check_view(dims, q, total_q, dims->h_q)) != GDN_OK) return rc;
+  if (total_kv > 0 && ((rc = check_view(dims, k, total_kv, dims->h_kv)) != GDN_OK ||
+                       (rc = check_view(dims, v, total_kv, dims->h_kv)) != GDN_OK))
     return rc;
-  if (gv.data && (rc = check_view(dims, &gv)) != GDN_OK) return rc;
+  if (gv.data && (rc = check_view(dims, &gv, total_q, dims->h_q)) != GDN_OK) return rc;
   GdnAttnArgs a;
   memset(&a, 0, sizeof(a));
   a.q = *q; a.k = *k; a.v = *v; a.gate = gv;
@@ -167,7 +171,7 @@ GDN_EXPORT int gdn_attn_prefill(const gdn_attn_dims* dims, const gdn_view* q, co
   a.num_seqs = num_seqs;
   a.total_q = total_q; a.total_kv = total_kv;
   a.d_status = d_status;
-  a.wait_ns = (dims->flags & GDN_TEST_WAIT_TIMEOUT) ? kTestWaitNs : kWaitNs;
+  a.wait_ns = kWaitNs;
   a.scale_log2 = scale_log2_of(dims);
   a.h_q = dims->h_q; a.h_kv = dims->h_kv; a.d = dims->d;
   return cuda_rc(gdn_launch_attn_prefill(a, dims->io, reinterpret_cast<cudaStream_t>(stream)));
@@ -201,8 +205,8 @@ GDN_EXPORT int gdn_attn_decode(const gdn_attn_dims* dims, const gdn_view* q,
     return GDN_EWORKSPACE;
   if (!aligned16(o) || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
     return GDN_EALIGN;
-  if ((rc = check_view(dims, q)) != GDN_OK) return rc;
-  if (gv.data && (rc = check_view(dims, &gv)) != GDN_OK) return rc;
+  if ((rc = check_view(dims, q, n, dims->h_q)) != GDN_OK) return rc;
+  if (gv.data && (rc = check_view(dims, &gv, n, dims->h_q)) != GDN_OK) return rc;
   GdnAttnArgs a;
   memset(&a, 0, sizeof(a));
   a.q = *q; a.gate = gv;
@@ -218,7 +222,7 @@ GDN_EXPORT int gdn_attn_decode(const gdn_attn_dims* dims, const gdn_view* q,
   a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(workspace) +
                                         align_up((size_t)slots * dims->d * 4));
   a.d_status = d_status;
-  a.wait_ns = (dims->flags & GDN_TEST_WAIT_TIMEOUT) ? kTestWaitNs : kWaitNs;
+  a.wait_ns = kWaitNs;
   a.scale_log2 = scale_log2_of(dims);
   a.h_q = dims->h_q; a.h_kv = dims->h_kv; a.d = dims->d;
   return cuda_rc(gdn_launch_attn_decode(a, dims->io, reinterpret_cast<cudaStream_t>(stream)));

@@ -457,7 +457,8 @@ int gdn_decode_step_gated_norm(const gdn_dims* dims, const gdn_params* params,
  *                contiguous: element (t, h, i) at data + t * token_stride +
  *                h * head_stride + i, strides in elements, so that q, k, v and
  *                the gate may be slices of one projection's output.  Address
- *                and strides must be multiples of 16 bytes (GDN_EALIGN).
+ *                and strides must be multiples of 16 bytes (GDN_EALIGN), the
+ *                strides of axes longer than one above zero (GDN_EUNSUPPORTED).
  *   paged cache  k, v [num_pages][h_kv][page_size][d] IO: the rows of one page
  *                and head are contiguous.  Token p of sequence b is row
  *                p % page_size of page block_table[b][p / page_size].
@@ -479,8 +480,7 @@ typedef struct {
   int32_t page_size; /* tokens per cache page: 16, 32, 64 or 128 */
   float norm_eps;    /* added to the mean of squares inside the root, >= 0 */
   float scale;       /* softmax scale, > 0; 0 means 1 / sqrt(d) */
-  int32_t flags;     /* 0 or GDN_TEST_WAIT_TIMEOUT (the waits of the attention kernels give up
-                        after 2 ms instead of 4 s); other bits: GDN_EINVAL */
+  int32_t flags;     /* 0, else GDN_EINVAL */
 } gdn_attn_dims;
 
 typedef struct {

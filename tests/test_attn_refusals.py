@@ -55,6 +55,8 @@ def test_norm_rope_refusals(lib):
     assert norm_rope(lib, q=view(ts=4100)) == -5      # rows not 16-byte aligned
     assert norm_rope(lib, k=view(hs=260)) == -5
     assert norm_rope(lib, k=view(hs=-256)) == -1
+    assert norm_rope(lib, k=view(hs=0)) == -2          # a broadcast head
+    assert norm_rope(lib, q=view(ts=0)) == -2
     assert norm_rope(lib, qn=FAKE + 4) == -5
     assert norm_rope(lib, k_out=FAKE + 8) == -5
     assert lib.gdn_qk_norm_rope(ctypes.byref(gdn.make_attn_dims(**A)), None, None, None, FAKE, 4,
@@ -119,6 +121,8 @@ def test_prefill_refusals(lib):
     assert prefill(lib, k=view(ts=1028)) == -5
     assert prefill(lib, gate=view(FAKE + 2)) == -5
     assert prefill(lib, tq=1 << 31, tk=1 << 31) == -2
+    assert prefill(lib, tq=(1 << 31) - 1, tk=(1 << 31) - 1) == -2   # block ends past 2^31
+    assert prefill(lib, v=view(ts=0)) == -2
 
 
 def decode(lib, dims=None, q=view(), c=None, lens=FAKE, n=4, shared=0, gate=None, o=FAKE + 4096,
