@@ -319,12 +319,12 @@ struct TcLaunch {
 // come first.  By one warp, which keeps its place between calls.
 struct TileSearch {
   int base = -1;           // 32 sequences from here (counted from the last one), one to a lane
-  int64_t before = 0;      // row blocks of the sequences before them
-  int64_t q0, len_q, k0, len_k;   // this lane's sequence
-  int64_t nt, incl;               // its row blocks, and with those before it
+  int before = 0;          // row blocks of the sequences before them
+  int q0, len_q, k0, len_k;   // this lane's sequence
+  int nt, incl;               // its row blocks, and with those before it
 
-  static __device__ __forceinline__ bool fits(const GdnAttnArgs& a, int b, int64_t lo, int64_t hi,
-                                              int64_t klo, int64_t khi) {
+  static __device__ __forceinline__ bool fits(const GdnAttnArgs& a, int b, int lo, int hi, int klo,
+                                              int khi) {
     return hi >= lo && lo >= 0 && hi <= a.total_q && khi >= klo && klo >= 0 && khi <= a.total_kv &&
            (b > 0 || (lo == 0 && klo == 0)) &&
            (b < a.num_seqs - 1 || (hi == a.total_q && khi == a.total_kv));
@@ -336,18 +336,20 @@ struct TileSearch {
     q0 = len_q = k0 = len_k = nt = 0;
     bool fine = true;
     if (b >= 0) {
-      const int64_t q1 = a.cu_q[b + 1], k1 = a.cu_kv[b + 1];
+      const int q1 = a.cu_q[b + 1], k1 = a.cu_kv[b + 1];
       q0 = a.cu_q[b];
       k0 = a.cu_kv[b];
-      len_q = q1 - q0;
-      len_k = k1 - k0;
-      nt = (len_q + tokens - 1) / tokens;
       fine = fits(a, b, q0, q1, k0, k1);
+      if (fine) {
+        len_q = q1 - q0;
+        len_k = k1 - k0;
+        nt = (len_q + tokens - 1) / tokens;
+      }
     }
     incl = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
     return fine;
@@ -361,26 +363,26 @@ struct TileSearch {
     return __all_sync(0xffffffffu, fine);
   }
   // False: there is no such block.
-  __device__ bool find(const GdnAttnArgs& a, int tokens, int64_t j, TcItem& it) {
+  __device__ bool find(const GdnAttnArgs& a, int tokens, int j, TcItem& it) {
     if (j < before) {
       before = 0;
       load(a, tokens, 0);
     }
     for (;;) {
-      const int64_t all = __shfl_sync(0xffffffffu, incl, 31);
+      const int all = __shfl_sync(0xffffffffu, incl, 31);
       if (j < before + all) break;
       if (base + 32 >= a.num_seqs) return false;
       before += all;
       load(a, tokens, base + 32);
     }
-    const int64_t at = j - before;
+    const int at = j - before;
     const int src = __ffs(__ballot_sync(0xffffffffu, at < incl)) - 1;
-    const int64_t n = __shfl_sync(0xffffffffu, nt, src), end = __shfl_sync(0xffffffffu, incl, src);
-    it.tile = (int32_t)(n - 1 - (at - (end - n)));
-    it.q0 = __shfl_sync(0xffffffffu, (int32_t)q0, src);
-    it.len_q = __shfl_sync(0xffffffffu, (int32_t)len_q, src);
-    it.k0 = __shfl_sync(0xffffffffu, (int32_t)k0, src);
-    it.len_k = __shfl_sync(0xffffffffu, (int32_t)len_k, src);
+    const int n = __shfl_sync(0xffffffffu, nt, src), end = __shfl_sync(0xffffffffu, incl, src);
+    it.tile = n - 1 - (at - (end - n));
+    it.q0 = __shfl_sync(0xffffffffu, q0, src);
+    it.len_q = __shfl_sync(0xffffffffu, len_q, src);
+    it.k0 = __shfl_sync(0xffffffffu, k0, src);
+    it.len_k = __shfl_sync(0xffffffffu, len_k, src);
     return true;
   }
 };
@@ -403,7 +405,7 @@ __device__ __forceinline__ void take_cluster(uint32_t answer, uint32_t bar) {
         : "memory");
 }
 // The taken cluster's first CTA, or -1.
-__device__ __forceinline__ int64_t taken_cluster(uint32_t answer) {
+__device__ __forceinline__ int taken_cluster(uint32_t answer) {
   uint32_t x, got;
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
@@ -413,7 +415,7 @@ __device__ __forceinline__ int64_t taken_cluster(uint32_t answer) {
       : "=r"(x), "=r"(got)
       : "r"(answer)
       : "memory");
-  return got ? (int64_t)x : -1;
+  return got ? (int)x : -1;
 }
 
 template <typename IO, int D, int CG, bool PREFIX>
@@ -460,6 +462,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     fence_mbar_init();
   }
   if (warp == WARP_MMA) tmem_alloc_cg<CG>(&sh->tmem, 512);
+  // the sequences' places are looked up while the pair sets itself up (512 tokens of
+  // 16 + 4 heads of 256: 13.3 us, looked up after it 14.8)
+  TileSearch search;
+  bool sequences_fit = true;
+  if (!PREFIX && warp == WARP_ORDER) sequences_fit = search.check(a, cta_tokens * CG);
   if (warp == WARP_LOAD && lane < 3)
     asm volatile("prefetch.tensormap [%0];" ::"l"(
                      reinterpret_cast<uint64_t>(lane == 0 ? &qmap : lane == 1 ? &kmap : &vmap))
@@ -493,10 +500,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 
   if (warp == WARP_ORDER) {
     // ---- the order of work: this cluster's own item, then taken ones ----
-    TileSearch search;
-    int64_t item = blockIdx.x / CG;
+    int item = blockIdx.x / CG;
     // (alike in every CTA, and before any of them has been given an item)
-    if (!PREFIX && !search.check(a, cta_tokens * CG)) {
+    if (!sequences_fit) {
       if (lane == 0) set_status(a.d_status, GDN_DEV_BAD_CU_SEQLENS);
       item = -1;
     }
@@ -505,13 +511,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       bool there = item >= 0;
       TcItem it = {};
       if (there) {
-        const int head = (int)(item % heads);
-        const int64_t rest = item / heads;
+        const int rest = item / heads, head = item - rest * heads;
         it.kvh = head / p.subs;
         it.h0 = it.kvh * (a.h_q / a.h_kv) + (head % p.subs) * gp;
         if (PREFIX) {
-          it.split = (int)(rest % a.splits);
-          it.tile = (int32_t)(rest / a.splits);
+          it.tile = rest / a.splits;
+          it.split = rest - it.tile * a.splits;
           it.len_q = (int32_t)a.total_q;
           it.len_k = (int32_t)a.shared_len;
           const int64_t all = (a.shared_len + BN - 1) / BN;
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       wait_on(ok, &sh->taken_full[s], (asked >> 1) & 1, wait_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int64_t first = taken_cluster(smem_u32(&sh->taken[s]));
+      const int first = taken_cluster(smem_u32(&sh->taken[s]));
       fence_async_smem();                       // read before the next answer lands there
       __syncwarp();
       if (lane == 0) {
