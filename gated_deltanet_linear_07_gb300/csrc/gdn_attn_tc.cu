@@ -24,7 +24,8 @@
 // x 256 channels x 2 operands = 128 KB per 2048 cycles of products).
 //
 // Warps: 0-7 softmax (warps w and w + 4 share 32 rows, 64 of a block's 128
-// columns each), 8 the TMA loads, 9 the MMAs, 10 the order of work.  K and V
+// columns each), 8 the TMA loads, 9 the MMAs, 10 the order of work, 11-14 the output
+// of packed prompts below head dim 256 (else the softmax warps').  K and V
 // blocks run through one ring in the order in which the MMA warp consumes them:
 // S is formed one or two blocks ahead of the product with V, so that the softmax
 // of one block and the products of the others overlap.
@@ -47,8 +48,7 @@ using namespace gdn::tc;
 
 constexpr int BM = 128;            // query rows per CTA (tensor-memory lanes)
 constexpr int BN = 128;            // keys per block
-constexpr int TC_THREADS = 352;
-constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ORDER = 10;
+constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ORDER = 10, WARP_OUT = 11;
 constexpr float RESCALE_LOG2 = 8.0f;
 constexpr uint32_t MISC_BYTES = 3072;
 constexpr int MAX_RING = 8;
@@ -59,12 +59,21 @@ constexpr int MAX_RING = 8;
 // prefix comes from HBM and wants them all.
 template <int D, int CG, bool PREFIX>
 struct TcCfg {
+  // Output by warps of its own, while the next item's softmax begins: packed prompts of
+  // 16 sequences with 32 + 8 heads of 128 372 -> 339 us, 40 of 125 tokens 50 -> 45.  At
+  // head dim 256 four more warps of registers are all there is, and their output takes
+  // longer than the softmax of a first block: 4096 gated tokens 90 us by the softmax
+  // warps, 97 by these.
+  static constexpr bool OUT_WARPS = !PREFIX && D < 256;
+  static constexpr int THREADS = OUT_WARPS ? 480 : 352;
+  static constexpr int ITEMS = OUT_WARPS ? 3 : 2;     // under way at a time
+  static constexpr uint32_t SUMS = OUT_WARPS ? ITEMS * 2 * BM * 4 : 0;   // their row sums
   static constexpr uint32_t Q_BYTES = BM * D * 2;
   static constexpr uint32_t STAGE = BN * D * 2 / CG;
-  static constexpr int FIT = (int)((232448u - MISC_BYTES - Q_BYTES) / STAGE);
+  static constexpr int FIT = (int)((232448u - MISC_BYTES - SUMS - Q_BYTES) / STAGE);
   static constexpr int MOST = D == 256 && !PREFIX ? 4 : MAX_RING;
   static constexpr int RING = FIT < MOST ? FIT : MOST;
-  static constexpr uint32_t SMEM = MISC_BYTES + Q_BYTES + RING * STAGE;
+  static constexpr uint32_t SMEM = MISC_BYTES + SUMS + Q_BYTES + RING * STAGE;
   static constexpr int NS = D == 256 ? 2 : 3;        // S buffers: 512 columns less O's
   static constexpr uint32_t TMEM_O = NS * BN;
 };
@@ -82,11 +91,11 @@ struct TcItem {
 struct __align__(16) TcShared {
   uint4 taken[2];        // answers of the launch control
   uint64_t full[MAX_RING], empty[MAX_RING];
-  uint64_t q_full, q_empty, s_full[3], p_ready[3], o_done[3], o_free, v_tail[2];
-  uint64_t item_full[2], item_empty[2], taken_full[2], taken_free;
-  TcItem item[2];
+  uint64_t q_full, q_empty, s_full[3], p_ready[3], o_done[3], o_free, v_tail[3], l_full[3];
+  uint64_t item_full[3], item_empty[3], taken_full[2], taken_free;
+  TcItem item[3];
   uint32_t tmem;
-  int32_t tail_stage[2]; // ring stage of an item's last V block, where it passes the end
+  int32_t tail_stage[3]; // ring stage of an item's last V block, where it passes the end
   float red[2][2][BM];   // row maxima of the two column halves, two turns
 };
 static_assert(sizeof(TcShared) <= MISC_BYTES, "shared bookkeeping");
@@ -305,6 +314,51 @@ __host__ __device__ constexpr uint32_t idesc_io<__half>(int M, int N, bool b_mn)
   return idesc_f16(M, N, false, b_mn);
 }
 
+// 32 columns of O of this thread's row on their way out: divided by l, gated.
+template <typename IO>
+__device__ __forceinline__ void put_32(IO* out, bool wide, const uint32_t (&o)[32], float l,
+                                       float inv, bool gated, const Vec8<IO>* g8) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 16) {
+    Vec8<IO> ov[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = l == 0.f ? 0.f : __uint_as_float(o[k + 8 * v + e]) * inv;
+      if (gated) {
+        float g[8];
+        g8[k / 8 + v].get(g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= gate_sigmoid(g[e]);
+      }
+      ov[v].set(f);
+    }
+    if (wide) {
+      st_global_32b(out + k, ov[0].w.x, ov[0].w.y, ov[0].w.z, ov[0].w.w, ov[1].w.x, ov[1].w.y,
+                    ov[1].w.z, ov[1].w.w);
+    } else {
+      ov[0].store(out + k);
+      ov[1].store(out + k + 8);
+    }
+  }
+}
+// The same columns of the gate.  Rows are a thread each, so an access of a warp touches
+// 32 lines whatever its width, and the load/store unit takes one a cycle: 32 bytes at a
+// time where they are aligned.
+template <typename IO>
+__device__ __forceinline__ void get_32(const IO* gate, bool sectors, Vec8<IO>* g8) {
+#pragma unroll
+  for (int v = 0; v < 4; v += 2) {
+    if (sectors) {
+      ld_global_32b(gate + 8 * v, g8[v].w, g8[v + 1].w);
+    } else {
+      g8[v].load(gate + 8 * v);
+      g8[v + 1].load(gate + 8 * v + 8);
+    }
+  }
+}
+
 // ---- the kernel ---------------------------------------------------------------
 
 struct TcLaunch {
@@ -419,7 +473,7 @@ __device__ __forceinline__ int taken_cluster(uint32_t answer) {
 }
 
 template <typename IO, int D, int CG, bool PREFIX>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+__global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
     attn_tc_kernel(const __grid_constant__ TcLaunch p, const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
@@ -430,7 +484,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // known to be the same in all lanes
   const uint32_t rank = CG == 2 ? cta_rank() : 0u;
-  const uint32_t q_smem = smem_u32(smem) + MISC_BYTES;
+  // [item in turn][column half][row]
+  float(*sums)[2][BM] = reinterpret_cast<float(*)[2][BM]>(smem + MISC_BYTES);
+  const uint32_t q_smem = smem_u32(smem) + MISC_BYTES + C::SUMS;
   const uint32_t ring = q_smem + C::Q_BYTES;
   // the per-sequence pass of a decode needs nothing of this one but its SMs
   if (PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -451,13 +507,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       mbar_init(&sh->p_ready[s], CG == 2 && rank == 0 ? 9 : 8);
       mbar_init(&sh->o_done[s], 1);
     }
-    mbar_init(&sh->o_free, 8 * CG);
-    for (int s = 0; s < 2; ++s) {
+    mbar_init(&sh->o_free, (C::OUT_WARPS ? 4 : 8) * CG);
+    for (int s = 0; s < C::ITEMS; ++s) {
       mbar_init(&sh->v_tail[s], 1);
       mbar_init(&sh->item_full[s], 1);
-      mbar_init(&sh->item_empty[s], 10);         // eight softmax warps, loads, MMAs
-      mbar_init(&sh->taken_full[s], 1);
+      mbar_init(&sh->item_empty[s], C::OUT_WARPS ? 14 : 10);   // softmax, loads, MMAs, output
+      mbar_init(&sh->l_full[s], 8);
     }
+    mbar_init(&sh->taken_full[0], 1);
+    mbar_init(&sh->taken_full[1], 1);
     mbar_init(&sh->taken_free, CG);
     fence_mbar_init();
   }
@@ -481,18 +539,25 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const uint64_t wait_ns = a.wait_ns;
 
   // Items as the other warps see them, one after the other.
-  int turn_item = 0;
+  int at_item = 0;                  // buffer of the item, and the parity of its phase
+  uint32_t item_turn = 0;
+  auto step_item = [&]() {
+    if (++at_item == C::ITEMS) {
+      at_item = 0;
+      item_turn ^= 1;
+    }
+  };
   auto next_item = [&](TcItem& it) {
-    wait_on(ok, &sh->item_full[turn_item & 1], (turn_item >> 1) & 1, wait_ns);
+    wait_on(ok, &sh->item_full[at_item], item_turn, wait_ns);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) return false;
-    it = sh->item[turn_item & 1];
+    it = sh->item[at_item];
     return it.blocks >= 0;
   };
   auto item_over = [&]() {
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->item_empty[turn_item & 1]);
-    ++turn_item;
+    if (lane == 0) mbar_arrive(&sh->item_empty[at_item]);
+    step_item();
   };
   auto has_tail = [&](const TcItem& it) {        // the last block passes the keys' end
     return (it.first_block + it.blocks) * BN > it.len_k;
@@ -536,19 +601,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       if (there || item < 0) {
         // the first wait of each buffer is for nothing
-        if (k >= 2) wait_on(ok, &sh->item_empty[k & 1], ((k >> 1) - 1) & 1, wait_ns);
+        if (k >= C::ITEMS) wait_on(ok, &sh->item_empty[at_item], item_turn ^ 1, wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
-          sh->item[k & 1] = it;
-          mbar_arrive(&sh->item_full[k & 1]);
+          sh->item[at_item] = it;
+          mbar_arrive(&sh->item_full[at_item]);
         }
         ++k;
+        step_item();
         if (item < 0) break;
       }
       // The next one, once this item's buffer after next is free again: a pair
       // holds no more than the item it works on and one more.
-      if (there && k >= 2) wait_on(ok, &sh->item_empty[k & 1], ((k >> 1) - 1) & 1, wait_ns);
+      if (there && k >= C::ITEMS)
+        wait_on(ok, &sh->item_empty[at_item], item_turn ^ 1, wait_ns);
       const int s = asked & 1;
       if (rank == 0) {
         if (asked > 0) wait_on(ok, &sh->taken_free, (asked - 1) & 1, wait_ns);
@@ -582,7 +649,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     };
     int s = 0;                      // ring stage and the parity of its phase
     uint32_t phase = 0;
-    int used = 0, tails = 0;        // items with keys, and with a tail, so far
+    int used = 0;                   // items with keys so far
+    int tail_at = 0;                // where the next tail reports
     TcItem it;
     // In the cache a block's rows lie in pages: each lane brings one box of the block
     // (rows of one page, 64 channels) and looks its page up a block ahead.  (One
@@ -667,13 +735,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const uint32_t bytes = (uint32_t)rows_of(t, BN, p.v_rows - 1) * (D / CG) * 2;
             // a tail reports here: this CTA clears its rows past the end
             const bool own = tail && i == it.blocks + AHEAD - 1;
-            uint64_t* const own_bar = &sh->v_tail[tails & 1];
+            uint64_t* const own_bar = &sh->v_tail[tail_at];
             const uint32_t dst = ring + (uint32_t)s * C::STAGE;
             const uint32_t bar = !own ? lead(&sh->full[s])
                                       : CG == 2 ? map_cta(smem_u32(own_bar), rank) : smem_u32(own_bar);
             if (lane == 0) {
               if (own) {
-                sh->tail_stage[tails & 1] = s;
+                sh->tail_stage[tail_at] = s;
                 mbar_expect_tx(own_bar, bytes);
               }
               if (rank == 0) {
@@ -699,7 +767,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
         }
         ++used;
-        if (tail) ++tails;
+        if (tail && ++tail_at == C::ITEMS) tail_at = 0;
       }
       if (!ok) break;
       item_over();
@@ -807,6 +875,70 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       if (!ok) break;
       item_over();
     }
+  } else if (C::OUT_WARPS && warp >= WARP_OUT) {
+    // ---- output: o = O / l, gated; a warp has 32 rows, a thread one of them ----
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t o_at = tmem + ((uint32_t)(quarter * 32) << 16) + C::TMEM_O;
+    const uint32_t freed = CG == 2 ? map_cta(smem_u32(&sh->o_free), 0) : 0u;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+    int nb = 0;               // S buffer of the item's first block, and the parity of its phase
+    uint32_t turn = 0;
+    TcItem it;
+    while (next_item(it)) {
+      const int h = it.h0 + (row & (gp - 1));
+      const int tok = (it.tile * CG + (int)rank) * cta_tokens + (row >> p.gp_shift);
+      const bool live = tok < it.len_q;
+      const int64_t t = (int64_t)it.q0 + tok;
+      const bool gated = a.gate.data && live;
+      Vec8<IO> gv[C::OUT_WARPS ? D / 8 : 1];     // the gate's row comes in under the products
+      if (gated) {
+        const IO* gate = reinterpret_cast<const IO*>(a.gate.data) + t * a.gate.token_stride +
+                         h * a.gate.head_stride;
+        const bool sectors = (reinterpret_cast<uintptr_t>(gate) & 31u) == 0;
+#pragma unroll
+        for (int n = 0; n < (C::OUT_WARPS ? D : 0); n += 32) get_32(gate + n, sectors, gv + n / 8);
+      }
+      wait_on(ok, &sh->l_full[at_item], item_turn, wait_ns);
+      if (!__all_sync(0xffffffffu, ok)) ok = false;
+      const float l = sums[at_item][0][row] + sums[at_item][1][row];
+      if (it.blocks > 0) {
+        // The last scores were formed after the product NS before them, so of the
+        // products that report to one of the NS barriers only the last can be under way.
+        const int last = nb + it.blocks - 1;
+        wait_on(ok, &sh->o_done[last % NS], turn ^ ((last / NS) & 1), wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) ok = false;
+        turn ^= ((last + 1) / NS) & 1;
+        nb = (last + 1) % NS;
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no key: zeros; NaN stays
+      IO* out = reinterpret_cast<IO*>(a.o) + (t * a.h_q + h) * D;
+#pragma unroll
+      for (int n = 0; n < (C::OUT_WARPS ? D : 0); n += 32) {
+        uint32_t o[32];
+        if (it.blocks > 0) {
+          tmem_ld32_nowait(o_at + n, o);
+          tmem_wait_ld(o);
+          if (n + 32 == D) {            // all of O is in registers: the next item may write it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 1 || rank == 0)   // the first CTA's own arrivals stay in it
+                mbar_arrive(&sh->o_free);
+              else
+                arrive_remote(freed);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (live) put_32(out + n, wide, o, l, inv, gated, gv + n / 8);
+      }
+      if (!ok) break;
+      item_over();
+    }
   } else {
     // ---- softmax: warps w and w + 4 share rows 32 (w % 4) .. + 31 ----
     const int quarter = warp & 3, half = warp >> 2;
@@ -818,7 +950,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const bool local = CG == 1 || rank == 0;
     int b = -1;               // this block's S buffer, and the parity of its phase
     uint32_t turn = 1;
-    int flip = 0, tails = 0;
+    int flip = 0;
+    int tail_at = 0;          // where the next tail reports, and the parity of its phase
+    uint32_t tail_turn = 0;
     TcItem it;
     while (next_item(it)) {
       const int blocks = it.blocks;
@@ -936,10 +1070,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         const bool last = tail && i == blocks - 1;
         if (last) {
           // the rows of V past the end are someone else's, or nothing: clear them
-          // (two barriers in turn: the loads may be one item ahead)
-          wait_on(ok, &sh->v_tail[tails & 1], (tails >> 1) & 1, wait_ns);
+          // (a barrier per item under way: the loads may be that far ahead)
+          wait_on(ok, &sh->v_tail[tail_at], tail_turn, wait_ns);
           const int from = it.len_k - (it.first_block + i) * BN;
-          const uint32_t vt2 = ring + (uint32_t)sh->tail_stage[tails & 1] * C::STAGE;
+          const uint32_t vt2 = ring + (uint32_t)sh->tail_stage[tail_at] * C::STAGE;
           constexpr int ATOMS = D / 64 / CG;
           for (int x = from * 8 + tid; x < BN * 8; x += 256)
 #pragma unroll
@@ -954,97 +1088,75 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->p_ready[b]);
       }
-      if (tail) ++tails;
+      if (tail && ++tail_at == C::ITEMS) {
+        tail_at = 0;
+        tail_turn ^= 1;
+      }
 
-      // ---- the end: o = O / l ----
-      // the gate's row comes in under the last product
-      const int64_t t = (int64_t)it.q0 + tok;
-      Vec8<IO> gv[PREFIX ? 2 : D / 16];
-      const bool gated = !PREFIX && a.gate.data && live;
-      if (gated) {
-        const IO* gate = reinterpret_cast<const IO*>(a.gate.data) + t * a.gate.token_stride +
-                         h * a.gate.head_stride + half * (D / 2);
-        // Rows are a thread each, so an access of a warp touches 32 lines whatever its
-        // width, and the load/store unit takes one a cycle: 32 bytes at a time.
-        const bool sectors = (reinterpret_cast<uintptr_t>(gate) & 31u) == 0;
+      if (C::OUT_WARPS) {       // the output warps do the rest
+        sums[at_item][half][row] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->l_full[at_item]);
+      } else {
+        // ---- the end: o = O / l ----
+        // the gate's row comes in under the last product
+        const int64_t t = (int64_t)it.q0 + tok;
+        constexpr int COLS = C::OUT_WARPS ? 0 : D / 2;
+        Vec8<IO> gv[PREFIX || C::OUT_WARPS ? 1 : D / 16];
+        const bool gated = !PREFIX && a.gate.data && live;
+        if (gated) {
+          const IO* gate = reinterpret_cast<const IO*>(a.gate.data) + t * a.gate.token_stride +
+                           h * a.gate.head_stride + half * (D / 2);
+          const bool sectors = (reinterpret_cast<uintptr_t>(gate) & 31u) == 0;
 #pragma unroll
-        for (int v = 0; v < (PREFIX ? 2 : D / 16); v += 2) {
-          if (sectors) {
-            ld_global_32b(gate + 8 * v, gv[v].w, gv[v + 1].w);
-          } else {
-            gv[v].load(gate + 8 * v);
-            gv[v + 1].load(gate + 8 * v + 8);
-          }
+          for (int n = 0; n < (PREFIX ? 0 : COLS); n += 32) get_32(gate + n, sectors, gv + n / 8);
         }
-      }
-      flip ^= 1;
-      sh->red[flip][half][row] = l;
-      pair_bar(1 + quarter);
-      l += sh->red[flip][half ^ 1][row];
-      if (blocks > 0) {
-        wait_on(ok, &sh->o_done[b], turn, wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) ok = false;
-        tc_fence_after();
-      }
-      const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no key: zeros; NaN stays
-      IO* out = reinterpret_cast<IO*>(a.o) + (t * a.h_q + h) * D;
-      const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
-      const int64_t slot = PREFIX ? ((int64_t)it.split * a.total_q + (live ? tok : 0)) * a.h_q + h : 0;
-      if (PREFIX && live && half == 0) a.part_ml[slot] = make_float2(m * c, l);
-#pragma unroll
-      for (int n = 0; n < D / 2; n += 32) {
-        uint32_t o[32];
-        const int col = half * (D / 2) + n;
+        flip ^= 1;
+        sh->red[flip][half][row] = l;
+        pair_bar(1 + quarter);
+        l += sh->red[flip][half ^ 1][row];
         if (blocks > 0) {
-          tmem_ld32_nowait(tmem + lanes + C::TMEM_O + (uint32_t)col, o);
-          tmem_wait_ld(o);
-          if (n + 32 == D / 2) {        // all of O is in registers: the next item may write it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (local)
-                mbar_arrive(&sh->o_free);
-              else
-                arrive_remote(freed);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
+          wait_on(ok, &sh->o_done[b], turn, wait_ns);
+          if (!__all_sync(0xffffffffu, ok)) ok = false;
+          tc_fence_after();
         }
-        if (PREFIX) {
-          if (live && l != 0.f) {
-            float* dst = a.part_o + slot * D + col;
+        const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no key: zeros; NaN stays
+        IO* out = reinterpret_cast<IO*>(a.o) + (t * a.h_q + h) * D + half * (D / 2);
+        const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+        const int64_t slot =
+            PREFIX ? ((int64_t)it.split * a.total_q + (live ? tok : 0)) * a.h_q + h : 0;
+        if (PREFIX && live && half == 0) a.part_ml[slot] = make_float2(m * c, l);
 #pragma unroll
-            for (int k = 0; k < 32; k += 8)
-              st_global_32b(dst + k, o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5],
-                            o[k + 6], o[k + 7]);
-          }
-        } else if (live) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 16) {
-            Vec8<IO> ov[2];
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              float f[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                f[e] = l == 0.f ? 0.f : __uint_as_float(o[k + 8 * v + e]) * inv;
-              if (gated) {
-                float g[8];
-                gv[PREFIX ? 0 : (n + k) / 8 + v].get(g);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] *= gate_sigmoid(g[e]);
+        for (int n = 0; n < COLS; n += 32) {
+          uint32_t o[32];
+          const int col = half * (D / 2) + n;
+          if (blocks > 0) {
+            tmem_ld32_nowait(tmem + lanes + C::TMEM_O + (uint32_t)col, o);
+            tmem_wait_ld(o);
+            if (n + 32 == D / 2) {      // all of O is in registers: the next item may write it
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (local)
+                  mbar_arrive(&sh->o_free);
+                else
+                  arrive_remote(freed);
               }
-              ov[v].set(f);
             }
-            if (wide) {
-              st_global_32b(out + col + k, ov[0].w.x, ov[0].w.y, ov[0].w.z, ov[0].w.w, ov[1].w.x,
-                            ov[1].w.y, ov[1].w.z, ov[1].w.w);
-            } else {
-              ov[0].store(out + col + k);
-              ov[1].store(out + col + k + 8);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          }
+          if (PREFIX) {
+            if (live && l != 0.f) {
+              float* dst = a.part_o + slot * D + col;
+#pragma unroll
+              for (int k = 0; k < 32; k += 8)
+                st_global_32b(dst + k, o[k], o[k + 1], o[k + 2], o[k + 3], o[k + 4], o[k + 5],
+                              o[k + 6], o[k + 7]);
             }
+          } else if (live) {
+            put_32(out + n, wide, o, l, inv, gated, gv + (PREFIX ? 0 : n / 8));
           }
         }
       }
@@ -1144,7 +1256,7 @@ static cudaError_t launch_tc(const GdnAttnArgs& a, int io, cudaStream_t s) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid, 1, 1);
-  cfg.blockDim = dim3(TC_THREADS);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
