@@ -78,6 +78,7 @@ struct DecArgs {
                          // of time before the others (0: no prefix pass)
   int32_t prefix;        // prefix partials per row (0: none)
   int32_t cluster;       // CTAs per item (the form for few keys; 0: runs of units)
+  int32_t merge_rows;    // rows of an item that a CTA of the merge joins
 };
 
 // Keys of sequence b that this pass sees.
@@ -696,7 +697,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
 
 // Joins the partial results of one item (sequence, key/value head, sub):
 //   M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// One CTA per item.  The partials' statistics are fetched side by side and
+// A CTA joins merge_rows rows of it.  The partials' statistics are fetched side by side and
 // turned into one factor per partial and row first, so that the sums over the
 // partial outputs are independent loads (one after the other they would cost a
 // memory latency each).
@@ -712,12 +713,13 @@ static __host__ __device__ __forceinline__ int most_parts(const DecArgs& p) {
 // One item of 16 rows behind a prefix in 152 parts, runs of 456 CTAs: 83 KB.
 constexpr int MERGE_SMEM = 96 * 1024;
 
-template <typename IO, int D>
+template <typename IO, int D, bool SPLIT>
 __global__ void __launch_bounds__(MERGE_THREADS)
     attn_merge_kernel(const __grid_constant__ DecArgs p) {
   extern __shared__ __align__(16) unsigned char merge_smem[];
   __shared__ int64_t sums[MERGE_THREADS / 32], s_mine;
   __shared__ float sum_l[ROWS];
+  __shared__ float4 shares[SPLIT ? MERGE_THREADS : 1];
   const GdnAttnArgs& a = p.a;
   int64_t* first_row = reinterpret_cast<int64_t*>(merge_smem);          // [part]
   float2* ml = reinterpret_cast<float2*>(first_row + most_parts(p));    // [part][row]: statistics,
@@ -725,9 +727,11 @@ __global__ void __launch_bounds__(MERGE_THREADS)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int heads = a.h_kv * p.subs;
   const int n = (int)a.total_q;
-  const int b = blockIdx.x / heads, hs = blockIdx.x % heads;
-  const int h0 = item_head(p, hs);
-  const int rows = item_rows(p, hs);
+  const int slices = SPLIT ? (p.rows + p.merge_rows - 1) / p.merge_rows : 1;
+  const int item = blockIdx.x / slices, r0 = SPLIT ? blockIdx.x % slices * p.merge_rows : 0;
+  const int b = item / heads, hs = item % heads;
+  const int h0 = item_head(p, hs) + r0;
+  const int rows = SPLIT ? min(p.merge_rows, item_rows(p, hs) - r0) : item_rows(p, hs);
   int64_t total = 0;
   for (int base = 0; base < n; base += MERGE_THREADS) {
     const int i = base + tid;
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(MERGE_THREADS)
   const int parts = p.prefix + c1 - c0 + 1;
   for (int i = tid; i < parts; i += MERGE_THREADS) {   // partial i's first row of the workspace
     if (i < p.prefix) {
-      first_row[i] = ((int64_t)i * n + b) * a.h_q + h0;
+      first_row[i] = ((int64_t)i * n + b) * a.h_q + h0 - r0;
     } else if (whole) {
       first_row[i] = p.base_row + (2 * (int64_t)p.ctas + (int64_t)b * heads + hs) * p.rows;
     } else {
@@ -764,10 +768,11 @@ __global__ void __launch_bounds__(MERGE_THREADS)
   }
   pdl_wait();
   if (nt > 0 && whole && p.prefix == 0) return;   // written already
+  if (SPLIT && rows <= 0) return;                 // the last heads' item may be shorter
   __syncthreads();
   for (int i = tid; i < parts * rows; i += MERGE_THREADS)
     ml[i] = first_row[i / rows] < 0 ? make_float2(0.f, 0.f)   // an empty run
-                                    : a.part_ml[first_row[i / rows] + i % rows];
+                                    : a.part_ml[first_row[i / rows] + r0 + i % rows];
   __syncthreads();
   for (int row = warp; row < rows; row += MERGE_THREADS / 32) {
     float mm = -INFINITY, ll = 0.f;
@@ -786,15 +791,13 @@ __global__ void __launch_bounds__(MERGE_THREADS)
     if (lane == 0) sum_l[row] = ll;
   }
   __syncthreads();
-  for (int x = tid; x < rows * (D / 4); x += MERGE_THREADS) {
-    const int row = x / (D / 4), col = x % (D / 4) * 4;
-    float y[4] = {};
+  auto add_up = [&](int row, int col, int first, int step, float (&y)[4]) {
 #pragma unroll 8
-    for (int i = 0; i < parts; ++i) {
+    for (int i = first; i < parts; i += step) {
       const float2 w = ml[i * rows + row];
       // (of an empty run, anything that is there: its factor is 0)
       const float4 v = *reinterpret_cast<const float4*>(
-          a.part_o + (max(first_row[i], (int64_t)0) + row) * D + col);
+          a.part_o + (max(first_row[i], (int64_t)0) + r0 + row) * D + col);
       if (w.y != 0.f) {
         y[0] = fmaf(w.x, v.x, y[0]);
         y[1] = fmaf(w.x, v.y, y[1]);
@@ -802,6 +805,35 @@ __global__ void __launch_bounds__(MERGE_THREADS)
         y[3] = fmaf(w.x, v.w, y[3]);
       }
     }
+  };
+  const int units = rows * (D / 4);
+  const int groups = SPLIT ? MERGE_THREADS / units : 1;
+  if (groups > 1) {
+    // The threads that the rows leave over share the partials: group g takes every
+    // groups-th one, and the groups' sums are added in their order.
+    const int g = tid / units, x = tid - g * units;
+    const int row = x / (D / 4), col = x % (D / 4) * 4;
+    float y[4] = {};
+    if (g < groups) {
+      add_up(row, col, g, groups, y);
+      shares[SPLIT ? tid : 0] = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    __syncthreads();
+    if (g > 0) return;
+    for (int i = 1; i < groups; ++i) {
+      const float4 v = shares[SPLIT ? i * units + x : 0];
+      y[0] += v.x;
+      y[1] += v.y;
+      y[2] += v.z;
+      y[3] += v.w;
+    }
+    put_four<IO, D>(a, b, h0 + row, col, sum_l[row], y);
+    return;
+  }
+  for (int x = tid; x < units; x += MERGE_THREADS) {
+    const int row = x / (D / 4), col = x % (D / 4) * 4;
+    float y[4] = {};
+    add_up(row, col, 0, 1, y);
     put_four<IO, D>(a, b, h0 + row, col, sum_l[row], y);
   }
 }
@@ -867,7 +899,11 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
     if ((e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   (int)C::SMEM)) != cudaSuccess)
       return e;
-    if ((e = cudaFuncSetAttribute(attn_merge_kernel<IO, D>,
+    if ((e = cudaFuncSetAttribute(attn_merge_kernel<IO, D, false>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  MERGE_SMEM)) != cudaSuccess)
+      return e;
+    if ((e = cudaFuncSetAttribute(attn_merge_kernel<IO, D, true>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   MERGE_SMEM)) != cudaSuccess)
       return e;
@@ -903,11 +939,26 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 0 ? 1 : 0;
   if ((e = cudaLaunchKernelEx(&cfg, kernel, p, kmap, vmap)) != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(a.total_q * a.h_kv * p.subs));
+  // The merge: a CTA per item, or where that leaves SMs without one, per row or a few of
+  // them (one sequence of 100,000 keys of 4 heads: 73.9 and 69.2 us, two of 2112 16.0 and 14.1; eight of 3000
+  // with 16 heads of 64, rows alone but their partials shared out: 27.9 and 25.9).
+  // More items cut like that lose as much as they gain or more, their searches being the
+  // longer part then (64 sequences behind 2048 keys: 19.0 and 20.7).
+  p.merge_rows = p.rows;
+  int64_t slices = 1;
+  if (items <= 152)
+    while (p.merge_rows > 1 && items * slices * 2 <= 4 * 152) {
+      p.merge_rows = (p.merge_rows + 1) / 2;
+      slices = (p.rows + p.merge_rows - 1) / p.merge_rows;
+    }
+  const bool split =
+      slices > 1 || (items <= 152 && p.merge_rows * (D / 4) * 2 <= MERGE_THREADS);
+  cfg.gridDim = dim3((unsigned)(items * slices));
   cfg.blockDim = dim3(MERGE_THREADS);
-  cfg.dynamicSmemBytes = (size_t)most_parts(p) * (8 + 8 * p.rows);
+  cfg.dynamicSmemBytes = (size_t)most_parts(p) * (8 + 8 * p.merge_rows);
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_merge_kernel<IO, D>, p);
+  return cudaLaunchKernelEx(
+      &cfg, split ? attn_merge_kernel<IO, D, true> : attn_merge_kernel<IO, D, false>, p);
 }
 
 template <typename IO>
