@@ -240,3 +240,26 @@ def test_a_cache_past_32_bit_offsets(gpu_lib):
         o = gdn.gdn_attn_decode(dims, q.cuda(), kc, vc, table.cuda(), _ints(lens),
                                 _workspace(dims, 2, shared), shared_len=shared)
         _attn.check(o, ref, slack, torch.bfloat16, f"shared {shared}")
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,page,gate,shared", [
+    ([9000], 24, 2, 256, 64, True, 0),            # twelve rows an item
+    ([5000, 1], 10, 2, 64, 64, False, 0),         # five
+    ([4100, 0, 4097], 20, 1, 128, 32, True, 0),   # sixteen and four
+    ([6000, 3000], 7, 7, 64, 128, True, 0),       # one
+    ([3000, 2200, 2048], 36, 2, 128, 16, True, 2048),
+])
+def test_few_long_sequences(gpu_lib, lens, hq, hkv, d, page, gate, shared):
+    """Items cut into many runs, their rows and partials joined by many CTAs."""
+    g = torch.Generator().manual_seed(sum(lens) + hq)
+    dt, n = torch.bfloat16, len(lens)
+    kc, vc, table = _attn.paged(g, lens, hkv, d, page, dt, shared=shared)
+    qg = normal(g, n, hq, 2 * d, dtype=dt).cuda()
+    dims = gdn.make_attn_dims(hq, hkv, d, page_size=page)
+    o = gdn.gdn_attn_decode(dims, qg[..., :d], kc.cuda(), vc.cuda(), table.cuda(), _ints(lens),
+                            _workspace(dims, n, shared), shared_len=shared,
+                            gate=qg[..., d:] if gate else None)
+    qc = qg.cpu()
+    ref, slack = _attn.decode(qc[..., :d], kc, vc, table, lens, qc[..., d:] if gate else None,
+                              _attn.scale_of(d), dt)
+    _attn.check(o, ref, slack, dt, "o")

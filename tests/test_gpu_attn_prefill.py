@@ -215,3 +215,22 @@ def test_a_sequence_alone_and_in_a_batch_gives_the_same_bits(gpu_lib, d):
     o = _run(dims, q, k, v, cu)
     for a, b in zip(cu, cu[1:]):
         assert torch.equal(o[a:b], _run(dims, q[a:b], k[a:b], v[a:b], [0, b - a]))
+
+
+@pytest.mark.parametrize("d,hq,hkv,io,gate", [(64, 6, 6, "bf16", True), (64, 8, 4, "fp16", False),
+                                              (128, 8, 4, "bf16", True), (128, 12, 4, "fp16", False),
+                                              (256, 4, 4, "bf16", True)])
+def test_many_short_items_follow_each_other(gpu_lib, d, hq, hkv, io, gate):
+    """Far more row blocks than the GPU runs at a time, of one key block, of
+    several and of none, so that each stage works on another item."""
+    g = torch.Generator().manual_seed(d + hq)
+    lens_q = [(37 * i) % 97 if i % 7 else 0 for i in range(400)]
+    lens_kv = [n if i % 3 else (0, 1, n + 130, n // 2)[i // 3 % 4] for i, n in enumerate(lens_q)]
+    cu_q, cu_kv, dt = _cu(lens_q), _cu(lens_kv), IO[io]
+    qg, kv = normal(g, cu_q[-1], hq, 2 * d, dtype=dt), normal(g, cu_kv[-1], 2 * hkv, d, dtype=dt)
+    qgd, kvd = qg.cuda(), kv.cuda()
+    o = _run(gdn.make_attn_dims(hq, hkv, d, io=io), qgd[..., :d], kvd[:, :hkv], kvd[:, hkv:], cu_q,
+             cu_kv, qgd[..., d:] if gate else None)
+    ref, slack = _attn.prefill(qg[..., :d], kv[:, :hkv], kv[:, hkv:], cu_q, cu_kv,
+                               qg[..., d:] if gate else None, _attn.scale_of(d), dt)
+    _attn.check(o, ref, slack, dt, "o")
