@@ -50,6 +50,7 @@ constexpr int BM = 128;            // query rows per CTA (tensor-memory lanes)
 constexpr int BN = 128;            // keys per block
 constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ORDER = 10, WARP_OUT = 11;
 constexpr float RESCALE_LOG2 = 8.0f;
+constexpr uint64_t BLOCK_NS = 8192;   // a key block takes a fifth of it: for waits that span items
 constexpr uint32_t MISC_BYTES = 3072;
 constexpr int MAX_RING = 8;
 
@@ -572,6 +573,7 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
       item = -1;
     }
     int asked = 0;
+    uint64_t items_ns = wait_ns;         // the longest items under way, and some more
     for (int k = 0; ok;) {
       bool there = item >= 0;
       TcItem it = {};
@@ -601,7 +603,7 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
       }
       if (there || item < 0) {
         // the first wait of each buffer is for nothing
-        if (k >= C::ITEMS) wait_on(ok, &sh->item_empty[at_item], item_turn ^ 1, wait_ns);
+        if (k >= C::ITEMS) wait_on(ok, &sh->item_empty[at_item], item_turn ^ 1, items_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
@@ -610,12 +612,14 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
         }
         ++k;
         step_item();
+        if (it.blocks > 0)
+          items_ns = max(items_ns, wait_ns + (uint64_t)it.blocks * (C::ITEMS * BLOCK_NS));
         if (item < 0) break;
       }
       // The next one, once this item's buffer after next is free again: a pair
       // holds no more than the item it works on and one more.
       if (there && k >= C::ITEMS)
-        wait_on(ok, &sh->item_empty[at_item], item_turn ^ 1, wait_ns);
+        wait_on(ok, &sh->item_empty[at_item], item_turn ^ 1, items_ns);
       const int s = asked & 1;
       if (rank == 0) {
         if (asked > 0) wait_on(ok, &sh->taken_free, (asked - 1) & 1, wait_ns);
@@ -899,7 +903,7 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
 #pragma unroll
         for (int n = 0; n < (C::OUT_WARPS ? D : 0); n += 32) get_32(gate + n, sectors, gv + n / 8);
       }
-      wait_on(ok, &sh->l_full[at_item], item_turn, wait_ns);
+      wait_on(ok, &sh->l_full[at_item], item_turn, wait_ns + (uint64_t)it.blocks * BLOCK_NS);
       if (!__all_sync(0xffffffffu, ok)) ok = false;
       const float l = sums[at_item][0][row] + sums[at_item][1][row];
       if (it.blocks > 0) {
