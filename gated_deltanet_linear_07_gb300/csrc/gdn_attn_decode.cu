@@ -22,7 +22,10 @@
 // search for the run, no second launch: 700 keys of 4 heads, 8 us instead of 10.
 //
 // Behind a shared prefix (gdn_attn_tc.cu computes it once for all rows) the
-// items start at shared_len and the merge adds the prefix's partials.
+// items start at shared_len and the merge adds the prefix's partials.  A row that
+// ends inside the prefix is not part of that pass, whose products run over all of
+// the prefix's values (a weight of zero does not keep an Inf or NaN out): all of
+// its keys are its own item here, from key 0, in the prefix's pages.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -68,7 +71,8 @@ static_assert(sizeof(DecShared) <= 1024, "shared bookkeeping");
 
 struct DecArgs {
   GdnAttnArgs a;
-  int64_t start;         // first key of this pass: shared_len, or 0
+  int64_t start;         // first key of this pass: shared_len, or 0 (rows that end before it
+                         // have all of theirs here)
   int64_t base_row;      // first row of the partials of this pass
   int32_t rows;          // query heads per item, <= ROWS
   int32_t subs;          // items per (sequence, key/value head)
@@ -81,15 +85,20 @@ struct DecArgs {
   int32_t merge_rows;    // rows of an item that a CTA of the merge joins
 };
 
-// Keys of sequence b that this pass sees.
-__device__ __forceinline__ int64_t own_keys(const DecArgs& p, int b) {
+// Keys of sequence b that this pass sees, from `first` on.
+__device__ __forceinline__ int64_t own_keys(const DecArgs& p, int b, int64_t& first) {
   int64_t len = p.a.seq_lens[b];
   const int64_t cap = (int64_t)p.a.cache.pages_per_seq << p.a.page_shift;
   if (len > cap) {
     set_status(p.a.d_status, GDN_DEV_BAD_LENGTH);
     len = cap;
   }
-  return len > p.start ? len - p.start : 0;
+  first = len < p.start ? 0 : p.start;
+  return len > first ? len - first : 0;
+}
+__device__ __forceinline__ int64_t own_keys(const DecArgs& p, int b) {
+  int64_t first;
+  return own_keys(p, b, first);
 }
 __device__ __forceinline__ int64_t blocks_of(int64_t keys) { return (keys + KEYS - 1) / KEYS; }
 
@@ -246,12 +255,12 @@ __device__ __forceinline__ void put_four(const GdnAttnArgs& a, int b, int h, int
 // The run [w, end) of units, item by item.
 struct Segment {
   int b, hs;             // sequence, and key/value head * subs + sub
-  int64_t keys;          // keys of the sequence in this pass
+  int64_t keys, first;   // keys of the sequence in this pass, from key `first` on
   int64_t t0, t1;        // blocks of the item in this run
   bool whole;            // all of the item is in this run
 };
 struct Walk {
-  int64_t w, end, item_first, nt, keys;
+  int64_t w, end, item_first, nt, keys, first;
   int b, hs;
   __device__ bool next(const DecArgs& p, int heads, Segment& s) {
     if (w >= end) return false;
@@ -261,7 +270,7 @@ struct Walk {
         hs = 0;
         do {
           ++b;
-          keys = own_keys(p, b);
+          keys = own_keys(p, b, first);
           nt = blocks_of(keys);
         } while (nt == 0);
       }
@@ -269,6 +278,7 @@ struct Walk {
     s.b = b;
     s.hs = hs;
     s.keys = keys;
+    s.first = first;
     s.t0 = w - item_first;
     s.t1 = min(end - item_first, nt);
     s.whole = s.t0 == 0 && s.t1 == nt;
@@ -333,7 +343,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
     const int item = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
     walk.b = item / heads;
     walk.hs = item % heads;
-    walk.keys = own_keys(p, walk.b);
+    walk.keys = own_keys(p, walk.b, walk.first);
     walk.nt = blocks_of(walk.keys);
     walk.item_first = 0;
     w0 = walk.nt * rank / p.cluster;
@@ -374,7 +384,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
     walk.end = w1;
     if (!FEW) {
       walk.b = sh->found;
-      walk.keys = own_keys(p, walk.b);
+      walk.keys = own_keys(p, walk.b, walk.first);
       walk.nt = blocks_of(walk.keys);
       walk.hs = (int)((w0 - sh->found_first) / walk.nt);
       walk.item_first = sh->found_first + walk.hs * walk.nt;
@@ -390,7 +400,9 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
       const int kb = box % (D / 64), r = box / (D / 64) * p.box_rows;
       while (ok && walk.next(p, heads, g)) {
         const int kvh = g.hs / p.subs;
-        const int32_t* table = a.cache.block_table + (int64_t)g.b * a.cache.pages_per_seq;
+        // the prefix's pages are those of row 0
+        const int32_t* table =
+            a.cache.block_table + (int64_t)(g.first < p.start ? 0 : g.b) * a.cache.pages_per_seq;
         // the item's queries, once the consumers have the last item's in registers
         if (items > 0) ok = mbar_wait(&sh->q_empty, (items - 1) & 1, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -408,7 +420,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
         auto page_at = [&](int64_t t) {
           const int64_t pos = t * KEYS + r;
           return lane < 2 * per_kv && t < g.t1 && pos < g.keys
-                     ? __ldg(table + ((p.start + pos) >> a.page_shift))
+                     ? __ldg(table + ((g.first + pos) >> a.page_shift))
                      : 0;
         };
         int32_t page = page_at(g.t0);
@@ -428,7 +440,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
               set_status(a.d_status, GDN_DEV_BAD_PAGE);
               page = 0;
             }
-            const int64_t pos = p.start + t * KEYS + r;
+            const int64_t pos = g.first + t * KEYS + r;
             const int64_t row = (((int64_t)page * a.h_kv + kvh) << a.page_shift) +
                                 (pos & ((1 << a.page_shift) - 1));
             tma_box(ring + (uint32_t)s * C::STAGE + (is_v ? C::TILE : 0u) +

@@ -968,8 +968,8 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
       // that they ask for no mask of their own
       const int vt = live ? tok : it.len_q - 1;
       int lim;
-      if (PREFIX) {
-        lim = min(max(a.seq_lens[vt], 0), it.len_k);
+      if (PREFIX) {   // all of the prefix, or none: a shorter row is not part of this pass
+        lim = a.seq_lens[vt] < it.len_k ? 0 : it.len_k;
       } else {
         lim = vt + it.len_k - it.len_q + 1;   // causal: the queries are the last of the keys
         lim = lim < 0 ? 0 : lim;

@@ -586,7 +586,9 @@ size_t gdn_attn_decode_workspace_size(const gdn_attn_dims* dims, int32_t n, int6
  *   shared_len tokens at the start that every sequence of the call shares, a
  *              multiple of page_size (0: none).  Their pages are read from row
  *              0 of the block table, once for the whole batch; the entries of
- *              the other rows there are not looked at
+ *              the other rows there are not looked at.  A row may end inside
+ *              them: it sees its first seq_lens[b] tokens of row 0's pages (read
+ *              for that row alone)
  *   gate       as in gdn_attn_prefill, [n][h_q][d]
  *   o          [n][h_q][d] IO, contiguous, 16-byte aligned
  *   workspace  gdn_attn_decode_workspace_size() bytes, 256-byte aligned,
