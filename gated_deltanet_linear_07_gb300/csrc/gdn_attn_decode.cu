@@ -511,13 +511,13 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
               mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
               mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2));
             }
-            // The reference maximum may lag by 2^8: see gdn_attn_tc.cu.  A row's
+            // The reference maximum may lag (WeightRange).  A row's
             // follows from the row alone, and rows without a head ask for nothing.
             bool far[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
               far[r] = qrow + 8 * r < rows && mt[r] > m[r] &&
-                       (m[r] == -INFINITY || (mt[r] - m[r]) * c > 8.0f);
+                       (m[r] == -INFINITY || (mt[r] - m[r]) * c > WeightRange<IO>::LAG_LOG2);
             if (__any_sync(0xffffffffu, far[0] || far[1])) {
               float f[2];
 #pragma unroll
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
             uint32_t pa[4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float nm = m[r] == -INFINITY ? 0.f : -m[r] * c;
+              const float nm = weight_offset<IO>(m[r], c);
 #pragma unroll
               for (int nt = 0; nt < 2; ++nt) {
                 const float e0 = fast_exp2(fmaf(x[nt][2 * r], c, nm));

@@ -7,8 +7,8 @@
 //   l = l 2^(c (m - m')) + rowsum P,    O = O 2^(c (m - m')) + P V,
 // and o = O / l at the end.  S and O live in tensor memory (fp32); P goes
 // back there in the I/O type as the A operand of the second product.  The
-// reference maximum m may lag behind the true one by up to 2^RESCALE_LOG2: P
-// is then larger than one but the quotient is the same, and O is rescaled
+// reference maximum m may lag behind the true one by up to 2^LAG_LOG2 (WeightRange):
+// P is then larger than one but the quotient is the same, and O is rescaled
 // only when a row really passes that, which is rare after the first blocks.
 //
 // Rows: a key/value head's query heads are packed with the tokens, so that
@@ -49,7 +49,6 @@ using namespace gdn::tc;
 constexpr int BM = 128;            // query rows per CTA (tensor-memory lanes)
 constexpr int BN = 128;            // keys per block
 constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ORDER = 10, WARP_OUT = 11;
-constexpr float RESCALE_LOG2 = 8.0f;
 constexpr uint64_t BLOCK_NS = 8192;   // a key block takes a fifth of it: for waits that span items
 constexpr uint32_t MISC_BYTES = 3072;
 constexpr int MAX_RING = 8;
@@ -1022,7 +1021,7 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
         pair_bar(1 + quarter);
         mt = fmaxf(mt, sh->red[flip][half ^ 1][row]);
         // both warps of a row see the same maxima and so decide alike
-        const bool far = live && mt > m && (m == -INFINITY || (mt - m) * c > RESCALE_LOG2);
+        const bool far = live && mt > m && (m == -INFINITY || (mt - m) * c > WeightRange<IO>::LAG_LOG2);
         if (__any_sync(0xffffffffu, far)) {
           // a row's reference follows from the row alone: the others of the warp keep
           // theirs (factor 1), and rows that are not there ask for nothing
@@ -1047,7 +1046,7 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
           }
           l *= f;
         }
-        const float nm = m == -INFINITY ? 0.f : -m * c;
+        const float nm = weight_offset<IO>(m, c);
         const uint64_t c2 = pk(c, c), nm2 = pk(nm, nm);
         uint32_t w[32];
         uint64_t sum[4] = {0, 0, 0, 0};

@@ -560,7 +560,8 @@ int gdn_kv_append(const gdn_attn_dims* dims, const gdn_rope_params* params, cons
  *              sigmoid(gate)
  *   o          [total_q][h_q][d] IO, contiguous, 16-byte aligned, not an input
  * Scores, softmax statistics and the accumulated output are fp32; the softmax
- * weights are rounded to IO for the product with v.  Keys and values outside a
+ * weights are rounded to IO for the product with v (relative to each, in fp16 down
+ * to 2^-26 of the row's largest).  Keys and values outside a
  * sequence never reach it, whatever they hold; within one, a non-finite v can
  * reach the earlier queries of its sequence that share its block of 128 keys
  * (a weight of zero times it).
