@@ -187,6 +187,7 @@ struct GdnAttnArgs {
   float2* part_ml;             // and their (reference maximum in log2 units, sum)
   int64_t total_q, total_kv, shared_len;
   uint64_t wait_ns;
+  int32_t withhold;            // GDN_TEST_WAIT_TIMEOUT: some hand-overs never come
   float scale_log2;            // scale * log2(e)
   int32_t h_q, h_kv, d, num_seqs, page_shift;
   int32_t splits;              // prefix pass: how many CTA groups share the prefix

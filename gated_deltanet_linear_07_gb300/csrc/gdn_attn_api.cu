@@ -12,7 +12,11 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMostTokens = 0x7fff0000;   // the kernels' block ends stay below 2^31
-constexpr uint64_t kWaitNs = 4000000000ull;
+// Waits give up after 4 s (a block of keys takes microseconds); the test flag shortens
+// that to 2 ms and has some hand-overs withheld.
+uint64_t wait_ns_of(const gdn_attn_dims* d) {
+  return d->flags & GDN_TEST_WAIT_TIMEOUT ? 2000000ull : 4000000000ull;
+}
 
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
@@ -23,7 +27,7 @@ int elem(const gdn_attn_dims* d) { return d->io == GDN_FP32 ? 4 : 2; }
 int check_dims(const gdn_attn_dims* d, bool fp32) {
   if (!d) return GDN_EINVAL;
   if (d->h_q <= 0 || d->h_kv <= 0 || d->h_q % d->h_kv != 0) return GDN_EINVAL;
-  if (d->flags != 0) return GDN_EINVAL;
+  if (d->flags & ~GDN_TEST_WAIT_TIMEOUT) return GDN_EINVAL;
   if (!(d->norm_eps >= 0.f) || d->norm_eps > 1e30f) return GDN_EINVAL;   // also rejects NaN
   if (!(d->scale >= 0.f) || d->scale > 1e30f) return GDN_EINVAL;
   if (d->rope != GDN_ROPE_HALF && d->rope != GDN_ROPE_INTERLEAVED) return GDN_EINVAL;
@@ -171,7 +175,8 @@ GDN_EXPORT int gdn_attn_prefill(const gdn_attn_dims* dims, const gdn_view* q, co
   a.num_seqs = num_seqs;
   a.total_q = total_q; a.total_kv = total_kv;
   a.d_status = d_status;
-  a.wait_ns = kWaitNs;
+  a.wait_ns = wait_ns_of(dims);
+  a.withhold = dims->flags & GDN_TEST_WAIT_TIMEOUT ? 1 : 0;
   a.scale_log2 = scale_log2_of(dims);
   a.h_q = dims->h_q; a.h_kv = dims->h_kv; a.d = dims->d;
   return cuda_rc(gdn_launch_attn_prefill(a, dims->io, reinterpret_cast<cudaStream_t>(stream)));
@@ -222,7 +227,8 @@ GDN_EXPORT int gdn_attn_decode(const gdn_attn_dims* dims, const gdn_view* q,
   a.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(workspace) +
                                         align_up((size_t)slots * dims->d * 4));
   a.d_status = d_status;
-  a.wait_ns = kWaitNs;
+  a.wait_ns = wait_ns_of(dims);
+  a.withhold = dims->flags & GDN_TEST_WAIT_TIMEOUT ? 1 : 0;
   a.scale_log2 = scale_log2_of(dims);
   a.h_q = dims->h_q; a.h_kv = dims->h_kv; a.d = dims->d;
   return cuda_rc(gdn_launch_attn_decode(a, dims->io, reinterpret_cast<cudaStream_t>(stream)));

@@ -35,6 +35,11 @@
 // (clusterlaunchcontrol), so that the loads and first scores of its next item run
 // under the last blocks and the output of this one.  Launched one by one, an item
 // cost 12 us beside its blocks.  The heaviest items come first.
+//
+// Every wait is bounded.  A warp whose wait ran out hands nothing on any more and
+// writes no output, so that the warps that depend on it run out too; what two warps
+// or two CTAs do together (the row's maxima, the barriers of the end) they still do,
+// and the pair leaves when its copies and products in flight have had time to end.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -50,6 +55,8 @@ constexpr int BM = 128;            // query rows per CTA (tensor-memory lanes)
 constexpr int BN = 128;            // keys per block
 constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ORDER = 10, WARP_OUT = 11;
 constexpr uint64_t BLOCK_NS = 8192;   // a key block takes a fifth of it: for waits that span items
+constexpr uint64_t GRACE_NS = 1000000;   // for what is in flight when a wait has run out (it
+                                         // takes microseconds)
 constexpr uint32_t MISC_BYTES = 3072;
 constexpr int MAX_RING = 8;
 
@@ -95,7 +102,9 @@ struct __align__(16) TcShared {
   uint64_t item_full[3], item_empty[3], taken_full[2], taken_free;
   TcItem item[3];
   uint32_t tmem;
+  uint32_t gave_up;      // a wait of the pair has run out
   int32_t tail_stage[3]; // ring stage of an item's last V block, where it passes the end
+  uint32_t going[2][2][4];   // [turn][column half][quarter]: the warp goes on to the next item
   float red[2][2][BM];   // row maxima of the two column halves, two turns
 };
 static_assert(sizeof(TcShared) <= MISC_BYTES, "shared bookkeeping");
@@ -160,16 +169,18 @@ __device__ __forceinline__ bool elect_one() {
       : "memory");
   return e != 0;
 }
-// The same for arrivals with a release at cluster scope.
+// The same for arrivals with a release at cluster scope.  All lanes together.
 __device__ __forceinline__ void wait_on_cluster(bool& ok, uint64_t* bar, uint32_t parity,
                                                 uint64_t budget_ns) {
-  if (!ok) return;
-  const uint64_t t0 = globaltimer_ns();
-  while (!try_wait_cluster(smem_u32(bar), parity))
-    if (globaltimer_ns() - t0 > budget_ns) {
-      ok = false;
-      return;
-    }
+  if (ok) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!try_wait_cluster(smem_u32(bar), parity))
+      if (globaltimer_ns() - t0 > budget_ns) {
+        ok = false;
+        break;
+      }
+  }
+  ok = __all_sync(0xffffffffu, ok);
 }
 template <int CG>
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
@@ -298,6 +309,14 @@ __device__ __forceinline__ void ld_global_32b(const void* p, uint4& a, uint4& b)
                : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z),
                  "=r"(b.w)
                : "l"(__cvta_generic_to_global(p)));
+}
+// Sets the word at this address of CTA c of the pair.
+template <int CG>
+__device__ __forceinline__ void tell_gave_up(uint32_t addr, uint32_t c) {
+  if (CG == 2)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_cta(addr, c)), "r"(1u) : "memory");
+  else
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(1u) : "memory");
 }
 __device__ __forceinline__ void pair_bar(int id) {   // the two warps that share 32 rows
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
@@ -517,6 +536,7 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
     mbar_init(&sh->taken_full[0], 1);
     mbar_init(&sh->taken_full[1], 1);
     mbar_init(&sh->taken_free, CG);
+    sh->gave_up = 0;
     fence_mbar_init();
   }
   if (warp == WARP_MMA) tmem_alloc_cg<CG>(&sh->tmem, 512);
@@ -734,6 +754,10 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
           }
           if (i >= AHEAD) {      // V block i - AHEAD: this CTA's share of its channels
             if (!room()) break;
+            if (a.withhold && blockIdx.x < CG && used == 0 && i == AHEAD) {   // (the test's)
+              next_stage();
+              continue;
+            }
             const int t = (it.first_block + i - AHEAD) * BN;
             const uint32_t bytes = (uint32_t)rows_of(t, BN, p.v_rows - 1) * (D / CG) * 2;
             // a tail reports here: this CTA clears its rows past the end
@@ -903,14 +927,16 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
         for (int n = 0; n < (C::OUT_WARPS ? D : 0); n += 32) get_32(gate + n, sectors, gv + n / 8);
       }
       wait_on(ok, &sh->l_full[at_item], item_turn, wait_ns + (uint64_t)it.blocks * BLOCK_NS);
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       const float l = sums[at_item][0][row] + sums[at_item][1][row];
       if (it.blocks > 0) {
         // The last scores were formed after the product NS before them, so of the
         // products that report to one of the NS barriers only the last can be under way.
         const int last = nb + it.blocks - 1;
         wait_on(ok, &sh->o_done[last % NS], turn ^ ((last / NS) & 1), wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         turn ^= ((last + 1) / NS) & 1;
         nb = (last + 1) % NS;
         tc_fence_after();
@@ -939,7 +965,6 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
         }
         if (live) put_32(out + n, wide, o, l, inv, gated, gv + n / 8);
       }
-      if (!ok) break;
       item_over();
     }
   } else {
@@ -956,8 +981,23 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
     int flip = 0;
     int tail_at = 0;          // where the next tail reports, and the parity of its phase
     uint32_t tail_turn = 0;
+    const bool stumbles = a.withhold && blockIdx.x / CG == 1 && warp == 5;   // (the test's)
+    uint32_t meet = 0;
+    // The two warps of a row meet at a barrier in every block: they go on to an item
+    // together or leave together, whichever's wait has run out.
+    auto both_next = [&](TcItem& it) {
+      wait_on(ok, &sh->item_full[at_item], item_turn, wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      meet ^= 1;
+      if (lane == 0) sh->going[meet][half][quarter] = ok;
+      pair_bar(1 + quarter);
+      ok = ok && sh->going[meet][half ^ 1][quarter];
+      if (!ok) return false;
+      it = sh->item[at_item];
+      return it.blocks >= 0;
+    };
     TcItem it;
-    while (next_item(it)) {
+    while (both_next(it)) {
       const int blocks = it.blocks;
       const bool tail = has_tail(it) && blocks > 0;
       const int h = it.h0 + (row & (gp - 1));
@@ -981,6 +1021,7 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
       } else {
         low = __shfl_sync(0xffffffffu, lim, 0);
       }
+      if (stumbles) ok = false;
       float m = -INFINITY;      // reference maximum of the raw scores
       float l = 0.f;            // this thread's half of the row sum
 
@@ -990,7 +1031,11 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
         b = b == NS - 1 ? 0 : b + 1;
         turn ^= b == 0;
         wait_on(ok, &sh->s_full[b], turn, wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          pair_bar(1 + quarter);     // where the other warp waits
+          continue;
+        }
         tc_fence_after();
         const uint32_t st = tmem + lanes + (uint32_t)b * BN + (uint32_t)half * 64;
         uint32_t r0[32], r1[32];
@@ -1031,7 +1076,8 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
             // S(i) was formed after product i - NS, so of the products that report
             // to one of the NS barriers at most one is under way
             wait_on(ok, &sh->o_done[last_b], last_turn, wait_ns);
-            if (!__all_sync(0xffffffffu, ok)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
             tc_fence_after();
 #pragma unroll 1
             for (int n = 0; n < D / 2; n += 32) {
@@ -1075,6 +1121,8 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
           // the rows of V past the end are someone else's, or nothing: clear them
           // (a barrier per item under way: the loads may be that far ahead)
           wait_on(ok, &sh->v_tail[tail_at], tail_turn, wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) continue;         // tail_stage has not been written
           const int from = it.len_k - (it.first_block + i) * BN;
           const uint32_t vt2 = ring + (uint32_t)sh->tail_stage[tail_at] * C::STAGE;
           constexpr int ATOMS = D / 64 / CG;
@@ -1097,9 +1145,11 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
       }
 
       if (C::OUT_WARPS) {       // the output warps do the rest
-        sums[at_item][half][row] = l;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->l_full[at_item]);
+        if (ok) {
+          sums[at_item][half][row] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->l_full[at_item]);
+        }
       } else {
         // ---- the end: o = O / l ----
         // the gate's row comes in under the last product
@@ -1120,9 +1170,10 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
         l += sh->red[flip][half ^ 1][row];
         if (blocks > 0) {
           wait_on(ok, &sh->o_done[b], turn, wait_ns);
-          if (!__all_sync(0xffffffffu, ok)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
           tc_fence_after();
         }
+        if (!ok) continue;
         const float inv = l > 0.f ? 1.0f / l : l == 0.f ? 0.f : l;   // no key: zeros; NaN stays
         IO* out = reinterpret_cast<IO*>(a.o) + (t * a.h_q + h) * D + half * (D / 2);
         const bool wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
@@ -1163,16 +1214,25 @@ __global__ void __launch_bounds__(TcCfg<D, CG, PREFIX>::THREADS, 1)
           }
         }
       }
-      if (!ok) break;
-      item_over();
+      if (ok) item_over();
     }
   }
-  if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
+  if (!ok) {
+    set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
+    for (uint32_t c = 0; c < CG; ++c) tell_gave_up<CG>(smem_u32(&sh->gave_up), c);
+  }
   __syncwarp();
   // nothing of the pair is still to arrive at the other's barriers
   tc_fence_before();
   __syncthreads();
   if (CG == 2) cluster_sync_all();
+  if (sh->gave_up) {
+    // Copies, products and answers of the launch control may be in flight that nobody
+    // waited for (a CTA's report to the other's barriers, in phases that will not end):
+    // nothing new is asked for by now, and they end in microseconds.
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < GRACE_NS) __nanosleep(20000);
+  }
   tc_fence_after();
   if (warp == WARP_MMA) tmem_dealloc_cg<CG>(tmem, 512);
 }

@@ -122,7 +122,11 @@ typedef enum { GDN_FP32 = 0, GDN_BF16 = 1, GDN_FP16 = 2 } gdn_dtype;
  *   heads' outputs and final states are not valid), free their tensor memory
  *   and return; the GPU context stays usable.  It takes effect only where the
  *   scan runs beside the prep (at most half as many (sequence, value head)
- *   chains as SMs); elsewhere it is ignored, as it is by the SIMT path. */
+ *   chains as SMs); elsewhere it is ignored, as it is by the SIMT path.
+ *   In gdn_attn_dims.flags: gdn_attn_prefill's waits (4 s otherwise) give up
+ *   after 2 ms, the first CTA pair's loads leave out a block of values and one
+ *   warp of the second pair gives up by itself.  GDN_DEV_WAIT_TIMEOUT is set, and
+ *   the output rows of the items those pairs had taken are not written. */
 #define GDN_TEST_WAIT_TIMEOUT 0x4
 /* GDN_BF16_OPERANDS: the tensor-core prefill feeds its MMAs bf16 operands
  *   (8-bit mantissa, the range of fp32) instead of fp16: the bf16 state option
@@ -480,7 +484,7 @@ typedef struct {
   int32_t page_size; /* tokens per cache page: 16, 32, 64 or 128 */
   float norm_eps;    /* added to the mean of squares inside the root, >= 0 */
   float scale;       /* softmax scale, > 0; 0 means 1 / sqrt(d) */
-  int32_t flags;     /* 0, else GDN_EINVAL */
+  int32_t flags;     /* 0 (tests: GDN_TEST_WAIT_TIMEOUT), else GDN_EINVAL */
 } gdn_attn_dims;
 
 typedef struct {

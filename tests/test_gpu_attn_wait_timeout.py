@@ -1,0 +1,66 @@
+"""The bounded waits of the full-attention kernels, made to run out.
+
+With GDN_TEST_WAIT_TIMEOUT (a test-only flag of gdn_attn_dims) the waits give up
+after 2 ms instead of 4 s and some hand-overs inside the kernels never come:
+whoever waits for them must give up, report GDN_DEV_WAIT_TIMEOUT and end, the
+other work of the call unharmed, the next call on the stream as if nothing had
+been.  Nothing here faults, traps or waits without a bound."""
+import pytest
+import torch
+
+import gated_deltanet_linear_07_gb300 as gdn
+from tests import _attn
+from tests._attn import normal
+
+pytestmark = pytest.mark.gpu
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def _rows_right_or_untouched(o, ref, slack, what):
+    """Every row of o is right, or still the 7.0 it was filled with; returns how many are not."""
+    o = o.cpu()
+    out = (o == 7).all(-1)
+    rows = ~out
+    _attn.check(o[rows], ref[rows], slack[rows], o.dtype, what)
+    return int(out.sum())
+
+
+# Items of one key block whose values end inside it, of whole blocks, of several with an
+# end; pairs (heads of 128 and 256) and single CTAs, with more items than are under way.
+@pytest.mark.parametrize("lens,hq,hkv,d,gate", [
+    ([40], 4, 2, 256, True), ([40, 50, 60], 2, 1, 128, False), ([40] * 5, 2, 2, 64, True),
+    ([512], 2, 2, 256, False), ([512, 256], 2, 1, 128, True), ([512], 2, 2, 64, False),
+    ([700, 1000, 30], 4, 2, 256, True), ([700, 1000, 30], 4, 2, 128, False),
+    ([700, 1000, 30], 4, 2, 64, False), ([150] * 130, 4, 4, 128, False), ([150] * 90, 4, 4, 256, False),
+    ([150] * 130, 4, 4, 64, True),
+])
+def test_prefill(gpu_lib, lens, hq, hkv, d, gate):
+    g = torch.Generator().manual_seed(sum(lens) + d)
+    cu = [0]
+    for v in lens:
+        cu.append(cu[-1] + v)
+    qg, k, v = normal(g, cu[-1], hq, 2 * d), normal(g, cu[-1], hkv, d), normal(g, cu[-1], hkv, d)
+    ref, slack = _attn.prefill(qg[..., :d], k, v, cu, cu, qg[..., d:] if gate else None,
+                               _attn.scale_of(d), torch.bfloat16)
+    qgd, kd, vd = qg.cuda(), k.cuda(), v.cuda()
+
+    def call(flags):
+        o = torch.full((cu[-1], hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        status = _status()
+        gdn.gdn_attn_prefill(gdn.make_attn_dims(hq, hkv, d, flags=flags), qgd[..., :d], kd, vd,
+                             _ints(cu), gate=qgd[..., d:] if gate else None, o=o, d_status=status)
+        torch.cuda.synchronize()
+        return o, status.item()
+    o, status = call(gdn.GDN_TEST_WAIT_TIMEOUT)
+    assert status == gdn.GDN_DEV_WAIT_TIMEOUT
+    assert _rows_right_or_untouched(o, ref, slack, "with waits that ran out") > 0
+    o, status = call(0)
+    assert status == 0
+    _attn.check(o, ref, slack, torch.bfloat16, "the next call")
