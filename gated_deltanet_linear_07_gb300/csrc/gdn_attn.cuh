@@ -10,6 +10,9 @@
 namespace gdn {
 namespace attn {
 
+// For copies and products in flight when a wait has run out (they take microseconds).
+constexpr uint64_t GRACE_NS = 1000000;
+
 // Eight consecutive channels of a row: one 16-byte access (16-bit types) or
 // two (fp32).
 template <typename IO>

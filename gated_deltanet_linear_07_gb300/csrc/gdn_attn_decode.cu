@@ -15,6 +15,9 @@
 // ring that fills shared memory, and four warps take 16 keys of each block
 // with their own m, l and O (the 16 x D accumulator of mma.sync m16n8k16, its
 // 16 rows being the item's query heads): no barrier between them inside a run.
+// Every wait is bounded: a consumer whose wait ran out frees no stage any more and
+// makes the sums of its items NaN, the loading warp then runs out too, and what it
+// has in flight lands before it leaves.
 //
 // Few keys in all (at most FEW_BLOCKS blocks per CTA with a cluster of CTAs to an
 // item and no more CTAs than fit at once): the same kernel with the items cut over
@@ -433,9 +436,11 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
           if (!ok) break;
           const int64_t left = g.keys - t * KEYS;
           const int there = (int)min((int64_t)KEYS, (left + p.box_rows - 1) / p.box_rows * p.box_rows);
-          if (lane == 0) mbar_expect_tx(&sh->full[s], (uint32_t)there * D * 4);
+          // (the test's: of the first CTA, or of the last one of the first cluster)
+          const bool withheld = a.withhold && j == 0 && blockIdx.x == (FEW ? p.cluster - 1 : 0);
+          if (lane == 0 && !withheld) mbar_expect_tx(&sh->full[s], (uint32_t)there * D * 4);
           __syncwarp();
-          if (lane < 2 * per_kv && r < there) {
+          if (lane < 2 * per_kv && r < there && !withheld) {
             if (page < 0 || page >= a.cache.num_pages) {
               set_status(a.d_status, GDN_DEV_BAD_PAGE);
               page = 0;
@@ -450,6 +455,10 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
           page = next;
         }
       }
+      // (the consumers wait for these too, unless they have given up)
+      for (int x = max(0, j - C::STAGES); x < j; ++x)
+        mbar_wait(&sh->full[x % C::STAGES], (x / C::STAGES) & 1, GRACE_NS);
+      if (items > 0) mbar_wait(&sh->q_full, (items - 1) & 1, GRACE_NS);
     } else {
       // ---- 16 keys of every block, with this warp's own m, l, O ----
       const int qrow = lane >> 2, qcol = (lane & 3) * 2;
@@ -472,7 +481,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
                     (uint32_t)(ks * 32 + (mi >> 1) * 16),
                 qa[ks]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->q_empty);
+        if (ok && lane == 0) mbar_arrive(&sh->q_empty);
         float o[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -567,7 +576,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->empty[s]);
+          if (ok && lane == 0) mbar_arrive(&sh->empty[s]);
         }
 
         // ---- join the four warps ----
@@ -575,6 +584,7 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
         for (int r = 0; r < 2; ++r) {
           l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
           l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+          if (!__all_sync(0xffffffffu, ok)) l[r] = NAN;
         }
         if ((lane & 3) == 0) {
 #pragma unroll

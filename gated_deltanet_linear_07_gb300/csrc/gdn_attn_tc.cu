@@ -55,8 +55,6 @@ constexpr int BM = 128;            // query rows per CTA (tensor-memory lanes)
 constexpr int BN = 128;            // keys per block
 constexpr int WARP_LOAD = 8, WARP_MMA = 9, WARP_ORDER = 10, WARP_OUT = 11;
 constexpr uint64_t BLOCK_NS = 8192;   // a key block takes a fifth of it: for waits that span items
-constexpr uint64_t GRACE_NS = 1000000;   // for what is in flight when a wait has run out (it
-                                         // takes microseconds)
 constexpr uint32_t MISC_BYTES = 3072;
 constexpr int MAX_RING = 8;
 

@@ -126,7 +126,9 @@ typedef enum { GDN_FP32 = 0, GDN_BF16 = 1, GDN_FP16 = 2 } gdn_dtype;
  *   In gdn_attn_dims.flags: gdn_attn_prefill's waits (4 s otherwise) give up
  *   after 2 ms, the first CTA pair's loads leave out a block of values and one
  *   warp of the second pair gives up by itself.  GDN_DEV_WAIT_TIMEOUT is set, and
- *   the output rows of the items those pairs had taken are not written. */
+ *   the output rows of the items those pairs had taken are not written.
+ *   gdn_attn_decode alike (one CTA goes without a block of keys; the rows that
+ *   it had a share in are not valid). */
 #define GDN_TEST_WAIT_TIMEOUT 0x4
 /* GDN_BF16_OPERANDS: the tensor-core prefill feeds its MMAs bf16 operands
  *   (8-bit mantissa, the range of fp32) instead of fp16: the bf16 state option

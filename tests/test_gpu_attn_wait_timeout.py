@@ -64,3 +64,43 @@ def test_prefill(gpu_lib, lens, hq, hkv, d, gate):
     o, status = call(0)
     assert status == 0
     _attn.check(o, ref, slack, torch.bfloat16, "the next call")
+
+
+# The form for few keys (a cluster per row), runs of units with a merge, and both passes behind
+# a shared prefix.
+@pytest.mark.parametrize("lens,hq,hkv,d,page,width,gate,shared", [
+    ([700], 16, 4, 256, 64, 704, True, 0), ([300, 40], 4, 2, 128, 16, 320, False, 0),
+    ([500, 20], 8, 8, 64, 32, 512, True, 0), ([3000] * 8, 4, 2, 256, 64, 8192, True, 0),
+    ([6000] * 3, 4, 2, 128, 64, 8192, False, 0), ([2500] * 20, 4, 4, 64, 128, 4096, True, 0),
+    ([3000, 2500, 2100], 8, 2, 256, 64, 4096, True, 2048),
+    ([600, 513], 4, 2, 128, 16, 1024, False, 512), ([2100] * 40, 4, 2, 64, 64, 4096, False, 2048),
+])
+def test_decode(gpu_lib, lens, hq, hkv, d, page, width, gate, shared):
+    g = torch.Generator().manual_seed(sum(lens) + d)
+    n = len(lens)
+    kc, vc, table = _attn.paged(g, lens, hkv, d, page, torch.bfloat16, shared=shared)
+    wide = torch.full((n, width // page), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    qg = normal(g, n, hq, 2 * d)
+    ref, slack = _attn.decode(qg[..., :d], kc, vc, table, lens, qg[..., d:] if gate else None,
+                              _attn.scale_of(d), torch.bfloat16)
+    qgd, kcd, vcd, wide, ln = qg.cuda(), kc.cuda(), vc.cuda(), wide.cuda(), _ints(lens)
+    ws = torch.zeros(gdn.gdn_attn_decode_workspace_size(
+        gdn.make_attn_dims(hq, hkv, d, page_size=page), n, shared), dtype=torch.uint8, device="cuda")
+
+    def call(flags):
+        status = _status()
+        o = gdn.gdn_attn_decode(gdn.make_attn_dims(hq, hkv, d, page_size=page, flags=flags),
+                                qgd[..., :d], kcd, vcd, wide, ln, ws, shared_len=shared,
+                                gate=qgd[..., d:] if gate else None, d_status=status)
+        torch.cuda.synchronize()
+        return o, status.item()
+    o, status = call(gdn.GDN_TEST_WAIT_TIMEOUT)
+    assert status == gdn.GDN_DEV_WAIT_TIMEOUT
+    if not shared:      # rows are right, or seen to be not valid
+        o, bad = o.cpu(), torch.isnan(o.cpu()).any(-1)
+        assert bad.any()
+        _attn.check(o[~bad], ref[~bad], slack[~bad], torch.bfloat16, "with waits that ran out")
+    o, status = call(0)
+    assert status == 0
+    _attn.check(o, ref, slack, torch.bfloat16, "the next call")
