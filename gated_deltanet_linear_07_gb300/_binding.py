@@ -58,7 +58,8 @@ class gdn_view(ctypes.Structure):
 
 class gdn_rope_params(ctypes.Structure):
     _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
-                ("inv_freq", ctypes.c_void_p), ("rope_scale", ctypes.c_float)]
+                ("inv_freq", ctypes.c_void_p), ("rope_scale", ctypes.c_float),
+                ("d_status", ctypes.c_void_p)]
 
 
 class gdn_kv_cache(ctypes.Structure):
@@ -564,13 +565,13 @@ def _ref(v):
 
 
 def gdn_qk_norm_rope(dims, q, k, q_norm, k_norm, inv_freq, positions, q_out=None, k_out=None,
-                     rope_scale=1.0, stream=None):
+                     rope_scale=1.0, stream=None, d_status=None):
     """Per-head norm and rotation of queries and keys (see gdn_qk_norm_rope in
     include/gdn.h): q [n, h_q, d], k [n, h_kv, d] (either may be None), norm
     weights [d] fp32 or None, inv_freq [rot_dim / 2] fp64, positions [n] int32.
     Outputs are allocated when not given.  Returns (q_out, k_out)."""
     return (_calls or _attn_calls()).qk_norm_rope(dims, q, k, q_norm, k_norm, inv_freq, positions,
-                                                  q_out, k_out, rope_scale, stream)
+                                                  q_out, k_out, rope_scale, d_status, stream)
 
 
 def gdn_kv_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions, k_cache, v_cache, block_table,

@@ -219,6 +219,7 @@ static int rope_params(PyObject* const* a, const gdn_attn_dims* d, PyObject* sca
   p->k_norm = k;
   p->inv_freq = f;
   p->rope_scale = (float)PyFloat_AsDouble(scale);
+  p->d_status = NULL;
   return PyErr_Occurred() ? -1 : 0;
 }
 
@@ -271,7 +272,8 @@ static int fits32(int64_t n, const char* name) {
 
 /* ---- the calls -------------------------------------------------------------------- */
 
-/* dims, q, k, q_norm, k_norm, inv_freq, positions, q_out, k_out, rope_scale, stream */
+/* dims, q, k, q_norm, k_norm, inv_freq, positions, q_out, k_out, rope_scale, d_status,
+   stream */
 static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t na) {
   (void)self;
   gdn_attn_dims d;
@@ -279,13 +281,14 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t na)
   gdn_view q, k;
   PyObject* dt;
   int64_t n;
-  void *pos, *qp = NULL, *kp = NULL;
+  void *pos, *status, *qp = NULL, *kp = NULL;
   gdn_stream_t s;
-  if (count(na, 11) || dims_of(a[0], &d, &dt) || method_int(a[6], s_numel, &n) ||
+  if (count(na, 12) || dims_of(a[0], &d, &dt) || method_int(a[6], s_numel, &n) ||
       view(a[1], "q", dt, n, d.h_q, d.d, &q) || view(a[2], "k", dt, n, d.h_kv, d.d, &k) ||
       rope_params(a + 3, &d, a[9], &p) || flat(a[6], "positions", t_int32, n, &pos) ||
-      all_device() || stream_of(a[10], a[6], &s))
+      flat(a[10], "d_status", t_int32, 1, &status) || all_device() || stream_of(a[11], a[6], &s))
     return NULL;
+  p.d_status = status;
   PyObject *qo = Py_NewRef(Py_None), *ko = Py_NewRef(Py_None), *r = NULL;
   if (a[1] != Py_None) Py_SETREF(qo, output(a[7], "q_out", dt, n, d.h_q, d.d, a[1], &qp));
   if (qo && a[2] != Py_None) Py_SETREF(ko, output(a[8], "k_out", dt, n, d.h_kv, d.d, a[2], &kp));

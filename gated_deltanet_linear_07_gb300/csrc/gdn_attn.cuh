@@ -171,6 +171,8 @@ struct GdnRopeArgs {
   gdn_kv_cache cache;
   int32_t* d_status;
   int64_t n;
+  uint64_t wait_ns;
+  int32_t withhold;            // GDN_TEST_WAIT_TIMEOUT: one unit's copies never come
   int32_t h_q, h_kv, d, rot_dim, interleaved, page_shift;
   float eps, rope_scale;
 };

@@ -103,6 +103,8 @@ int rope_impl(const gdn_attn_dims* d, const gdn_rope_params* pr, const gdn_view&
   a.h_q = d->h_q; a.h_kv = d->h_kv; a.d = d->d; a.rot_dim = d->rot_dim;
   a.interleaved = d->rope == GDN_ROPE_INTERLEAVED;
   a.eps = d->norm_eps;
+  a.wait_ns = wait_ns_of(d);
+  a.withhold = d->flags & GDN_TEST_WAIT_TIMEOUT ? 1 : 0;
   return cuda_rc(gdn_launch_rope(a, d->io, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -123,7 +125,7 @@ GDN_EXPORT int gdn_qk_norm_rope(const gdn_attn_dims* dims, const gdn_rope_params
   if (n == 0) return GDN_OK;
   if (!qv.data && !kv.data) return GDN_EINVAL;
   return rope_impl(dims, params, qv, kv, none, positions, nullptr, n, nullptr, q_out, k_out,
-                   nullptr, stream);
+                   params->d_status, stream);
 }
 
 GDN_EXPORT int gdn_kv_append(const gdn_attn_dims* dims, const gdn_rope_params* params,

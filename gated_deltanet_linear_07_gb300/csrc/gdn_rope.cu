@@ -334,7 +334,6 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
   const int64_t units = (a.n + N - 1) / N * parts;
   // each stage: per token cosines, sines, negated sines [3][D / 2] fp32; then the
   // rows: q [token][head][D], k, v alike
-  constexpr uint64_t WAIT_NS = 4000000000ull;
   constexpr int CS = D / 2 * 3;
   constexpr uint32_t CS_BYTES = N * CS * 4;
   constexpr uint32_t ROW_BYTES = D * sizeof(IO);
@@ -376,7 +375,9 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
     fence_mbar_init();
     // the first units are on their way before anything else
     for (int i = 0; i < MANY_STAGES; ++i, advance())
-      if (blockIdx.x + (int64_t)i * gridDim.x < units) load(blockIdx.x + (int64_t)i * gridDim.x);
+      if (blockIdx.x + (int64_t)i * gridDim.x < units &&
+          !(a.withhold && blockIdx.x == 0 && i == 0))   // (the test's)
+        load(blockIdx.x + (int64_t)i * gridDim.x);
   }
   s = 0;
   phase = 0;
@@ -390,6 +391,7 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
     const int half = a.rot_dim / 2;
     const float scale = a.rope_scale;
     bool first = true;
+    int64_t done = 0;        // this CTA's units so far
     for (int64_t base = blockIdx.x; base < units && ok; base += (32LL / N) * gridDim.x) {
       int32_t pos = 0;     // of token lane % N of unit lane / N
       int64_t dst = -1;
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
       }
       for (int k = 0; k < 32 / N && base + (int64_t)k * gridDim.x < units; ++k) {
         if (!(first && k < MANY_STAGES)) {   // those are there already
-          ok = mbar_wait(&sh.empty[s], phase ^ 1, WAIT_NS);
+          ok = mbar_wait(&sh.empty[s], phase ^ 1, a.wait_ns);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane == 0) load(base + (int64_t)k * gridDim.x);
@@ -426,9 +428,14 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.full[s]);
         advance();
+        ++done;
       }
       first = false;
     }
+    // What is in flight lands before this CTA's memory is another's: the consumers wait for
+    // it too, unless a wait of theirs has run out.
+    for (int64_t x = max(done - MANY_STAGES, (int64_t)0); x < done; ++x)
+      mbar_wait(&sh.full[x % MANY_STAGES], (uint32_t)(x / MANY_STAGES) & 1, GRACE_NS);
   } else {
     const LanePlace<D> at(a);
     constexpr int GROUPS = MANY_WARPS * 32 / (D / 8);
@@ -446,8 +453,8 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
       const int64_t g = parts == 1 ? u : u / parts;
       const int part = parts == 1 ? 0 : (int)(u - g * parts);
       const int toks = (int)min((int64_t)N, n - g * N);
-      if (ok) ok = mbar_wait(&sh.full[s], phase, WAIT_NS);
-      __syncwarp();
+      ok = mbar_wait(&sh.full[s], phase, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);   // the rows' lanes leave together
       if (!ok) break;
       const unsigned char* stage = smem + (size_t)s * cut.stage_bytes;
       const float* cs = reinterpret_cast<const float*>(stage);

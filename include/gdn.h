@@ -127,8 +127,9 @@ typedef enum { GDN_FP32 = 0, GDN_BF16 = 1, GDN_FP16 = 2 } gdn_dtype;
  *   after 2 ms, the first CTA pair's loads leave out a block of values and one
  *   warp of the second pair gives up by itself.  GDN_DEV_WAIT_TIMEOUT is set, and
  *   the output rows of the items those pairs had taken are not written.
- *   gdn_attn_decode alike (one CTA goes without a block of keys; the rows that
- *   it had a share in are not valid). */
+ *   gdn_qk_norm_rope and gdn_kv_append alike from 640 tokens on (the rows of the
+ *   first CTA's tokens are not written), and gdn_attn_decode (one CTA goes
+ *   without a block of keys; the rows that it had a share in are not valid). */
 #define GDN_TEST_WAIT_TIMEOUT 0x4
 /* GDN_BF16_OPERANDS: the tensor-core prefill feeds its MMAs bf16 operands
  *   (8-bit mantissa, the range of fp32) instead of fp16: the bf16 state option
@@ -501,6 +502,7 @@ typedef struct {
   const double* inv_freq; /* [rot_dim / 2] fp64: radians per position of each pair, after any
                              scaling for long contexts (may be NULL when rot_dim is 0) */
   float rope_scale;       /* factor on the rotated channels (1 unless the scaling has one) */
+  int32_t* d_status;      /* of gdn_qk_norm_rope, or NULL (device; gdn_kv_append takes its own) */
 } gdn_rope_params;
 
 typedef struct {
@@ -524,6 +526,7 @@ typedef struct {
  *   q_out      [n][h_q][d] IO, k_out [n][h_kv][d] IO, contiguous, 16-byte
  *              aligned; each may be its own input where that is contiguous
  * IO is fp32, bf16 or fp16; everything between is fp32, rounded once.
+ * params->d_status reports GDN_DEV_WAIT_TIMEOUT (rows left out: not valid).
  */
 int gdn_qk_norm_rope(const gdn_attn_dims* dims, const gdn_rope_params* params, const gdn_view* q,
                      const gdn_view* k, const int32_t* positions, int64_t n, void* q_out,

@@ -104,3 +104,47 @@ def test_decode(gpu_lib, lens, hq, hkv, d, page, width, gate, shared):
     o, status = call(0)
     assert status == 0
     _attn.check(o, ref, slack, torch.bfloat16, "the next call")
+
+
+@pytest.mark.parametrize("n,hq,hkv,d,io,layout", [
+    (700, 16, 4, 256, "bf16", "half"), (3001, 16, 4, 128, "fp16", "interleaved"),
+    (1000, 40, 8, 256, "bf16", "half"), (2000, 4, 4, 64, "fp32", "interleaved"),
+])
+def test_norm_and_rotation(gpu_lib, n, hq, hkv, d, io, layout):
+    g = torch.Generator().manual_seed(n)
+    dt = _attn.IO[io]
+    q, k, w = normal(g, n, hq, d, dtype=dt), normal(g, n, hkv, d, dtype=dt), 1 + 0.1 * torch.randn(d, generator=g)
+    pos, freq = torch.arange(n, dtype=torch.int32), gdn.rope_frequencies(d // 2, 1e6)[0]
+    refs = [_attn.norm_rope(x, w, 1e-6, pos, freq, layout) for x in (q, k)]
+    qd, kd, wd, posd, freqd = q.cuda(), k.cuda(), w.cuda(), pos.cuda(), freq.cuda()
+    page = 16
+    table = torch.arange(-(-n // page), dtype=torch.int32, device="cuda")[None]
+    seq = torch.zeros(n, dtype=torch.int32, device="cuda")
+
+    def call(flags, append):
+        dims = gdn.make_attn_dims(hq, hkv, d, io=io, rot_dim=d // 2, rope=layout, page_size=page,
+                                  flags=flags)
+        status = _status()
+        qo, ko = (torch.full(x.shape, 7.0, dtype=dt, device="cuda") for x in (q, k))
+        if append:
+            kc = torch.full((table.shape[1], hkv, page, d), 7.0, dtype=dt, device="cuda")
+            vc = kc.clone()
+            gdn.gdn_kv_append(dims, qd, kd, kd, wd, wd, freqd, posd, kc, vc, table, row_seq=seq,
+                              q_out=qo, d_status=status)
+            ko, vo = (c.transpose(1, 2).reshape(-1, hkv, d)[:n] for c in (kc, vc))
+        else:
+            gdn.gdn_qk_norm_rope(dims, qd, kd, wd, wd, freqd, posd, qo, ko, d_status=status)
+            vo = None
+        torch.cuda.synchronize()
+        return (qo, ko, vo), status.item()
+    for append in (False, True):
+        outs, status = call(gdn.GDN_TEST_WAIT_TIMEOUT, append)
+        assert status == gdn.GDN_DEV_WAIT_TIMEOUT
+        for o, (ref, slack) in zip(outs, refs):
+            assert _rows_right_or_untouched(o, ref, slack, "with waits that ran out") > 0
+        outs, status = call(0, append)
+        assert status == 0
+        for o, (ref, slack) in zip(outs, refs):
+            _attn.check(o, ref, slack, dt, "the next call")
+        if append:
+            assert torch.equal(outs[2].cpu(), k)
