@@ -572,8 +572,9 @@ int gdn_kv_append(const gdn_attn_dims* dims, const gdn_rope_params* params, cons
  * weights are rounded to IO for the product with v (relative to each, in fp16 down
  * to 2^-26 of the row's largest).  Keys and values outside a
  * sequence never reach it, whatever they hold; within one, a non-finite v can
- * reach the earlier queries of its sequence that share its block of 128 keys
- * (a weight of zero times it).
+ * reach queries up to 382 tokens before it (a weight of zero times it: the rows
+ * of a block, 256 tokens at most, go through every block of 128 keys up to the
+ * last one that any of them sees).
  */
 int gdn_attn_prefill(const gdn_attn_dims* dims, const gdn_view* q, const gdn_view* k,
                      const gdn_view* v, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
