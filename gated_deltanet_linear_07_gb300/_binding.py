@@ -552,9 +552,11 @@ def _attn_calls():
         from . import _attn_calls as calls
         fns = (lib.gdn_qk_norm_rope, lib.gdn_kv_append, lib.gdn_attn_prefill, lib.gdn_attn_decode)
         # the raw handle of a device's current stream; current_stream() builds an object first
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         calls.setup((torch.float32, torch.bfloat16, torch.float16), torch.int32, torch.float64,
-                    torch.empty, raw, lambda: torch.cuda.current_stream().cuda_stream, GdnError,
+                    torch.empty, raw, device, GdnError,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
         _calls = calls
     return _calls

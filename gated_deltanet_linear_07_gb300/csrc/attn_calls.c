@@ -16,9 +16,10 @@
 #include "gdn.h"
 
 static PyObject *s_shape, *s_stride, *s_dtype, *s_data_ptr, *s_numel, *s_is_contiguous, *s_device,
-    *s_is_cuda, *s_index, *s_element_size;
+    *s_get_device, *s_element_size;
 static PyObject* io_types[3]; /* by gdn_dtype */
-static PyObject *t_int32, *t_float64, *f_empty, *f_stream, *f_current, *c_error, *empty_kw;
+static PyObject *t_int32, *t_float64, *f_empty, *f_stream, *f_device, *c_error,
+    *empty_kw;
 
 typedef int (*norm_rope_fn)(const gdn_attn_dims*, const gdn_rope_params*, const gdn_view*,
                             const gdn_view*, const int32_t*, int64_t, void*, void*, gdn_stream_t);
@@ -60,21 +61,35 @@ static int check_dtype(PyObject* t, const char* name, PyObject* want) {
   Py_DECREF(v);
   return same ? 0 : -1;
 }
-/* The kernels read device memory: a host tensor is refused, once everything else
-   about the call's tensors is right.  (Calls hold the interpreter lock throughout.) */
-static const char* host_tensor;
-static int note_host(PyObject* t, const char* name) {
-  PyObject* v = PyObject_GetAttr(t, s_is_cuda);
-  if (!v) return -1;
-  const int r = PyObject_IsTrue(v);
-  Py_DECREF(v);
-  if (r == 0 && !host_tensor) host_tensor = name;
-  return r < 0 ? -1 : 0;
+/* The kernels read memory of the current device: a tensor of the host or of another
+   device is refused, once everything else about the call's tensors is right.  (Calls
+   hold the interpreter lock throughout.) */
+static const char *host_tensor, *odd_tensor;
+static int64_t call_device, odd_device; /* of the call's first device tensor; < 0: none so far */
+static int note_device(PyObject* t, const char* name) {
+  int64_t d;
+  if (method_int(t, s_get_device, &d)) return -1;
+  if (d < 0) {
+    if (!host_tensor) host_tensor = name;
+  } else if (call_device < 0) {
+    call_device = d;
+  } else if (d != call_device && !odd_tensor) {
+    odd_tensor = name;
+    odd_device = d;
+  }
+  return 0;
 }
 static int all_device(void) {
-  if (!host_tensor) return 0;
-  PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", host_tensor);
-  return -1;
+  if (host_tensor) {
+    PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", host_tensor);
+    return -1;
+  }
+  if (odd_tensor) {
+    PyErr_Format(PyExc_ValueError, "%s is on cuda:%lld, tensors before it on cuda:%lld", odd_tensor,
+                 (long long)odd_device, (long long)call_device);
+    return -1;
+  }
+  return 0;
 }
 /* The integers of a tuple, four at most; their number, or -1. */
 static int integers(PyObject* seq, int64_t dims[4]) {
@@ -122,7 +137,7 @@ static int view(PyObject* t, const char* name, PyObject* dtype, int64_t n, int64
     return -1;
   }
   void* p;
-  if (note_host(t, name) || address(t, &p)) return -1;
+  if (note_device(t, name) || address(t, &p)) return -1;
   v->data = p;
   v->token_stride = strides[0];
   v->head_stride = strides[1];
@@ -149,7 +164,7 @@ static int flat(PyObject* t, const char* name, PyObject* dtype, int64_t numel, v
     if (contiguous == 0) PyErr_Format(PyExc_ValueError, "%s must be contiguous", name);
     return -1;
   }
-  return note_host(t, name) || address(t, p) ? -1 : 0;
+  return note_device(t, name) || address(t, p) ? -1 : 0;
 }
 
 /* An output (new reference) and its address, allocated beside `like` when None. */
@@ -174,7 +189,8 @@ static PyObject* output(PyObject* t, const char* name, PyObject* dtype, int64_t 
 }
 
 static int dims_of(PyObject* o, gdn_attn_dims* d, PyObject** dtype) {
-  host_tensor = NULL;
+  host_tensor = odd_tensor = NULL;
+  call_device = -1;
   Py_buffer b;
   if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE)) return -1;
   const int fits = b.len == (Py_ssize_t)sizeof(*d);
@@ -188,20 +204,23 @@ static int dims_of(PyObject* o, gdn_attn_dims* d, PyObject** dtype) {
   return 0;
 }
 
-/* The stream given, else the current one of t's device. */
-static int stream_of(PyObject* stream, PyObject* t, gdn_stream_t* s) {
-  PyObject* v = NULL;
-  if (stream != Py_None) {
-    v = PyNumber_Long(stream);
-  } else if (f_stream != Py_None) {
-    PyObject* device = PyObject_GetAttr(t, s_device);
-    PyObject* index = device ? PyObject_GetAttr(device, s_index) : NULL;
-    if (index) v = PyObject_CallOneArg(f_stream, index);
-    Py_XDECREF(index);
-    Py_XDECREF(device);
-  } else {
-    v = PyObject_CallNoArgs(f_current);
+/* The stream given, else the current one of the tensors' device, which has to be the
+   current device: the launch goes there. */
+static int stream_of(PyObject* stream, gdn_stream_t* s) {
+  PyObject* v = PyObject_CallNoArgs(f_device);
+  if (!v) return -1;
+  const long long now = PyLong_AsLongLong(v);
+  if (now != call_device) {
+    if (!PyErr_Occurred())
+      PyErr_Format(PyExc_ValueError, "the tensors are on cuda:%lld, the current device is cuda:%lld",
+                   (long long)call_device, now);
+    Py_DECREF(v);
+    return -1;
   }
+  if (stream != Py_None)
+    Py_SETREF(v, PyNumber_Long(stream));
+  else
+    Py_SETREF(v, PyObject_CallOneArg(f_stream, v));
   if (!v) return -1;
   *s = (gdn_stream_t)PyLong_AsVoidPtr(v);
   Py_DECREF(v);
@@ -286,12 +305,14 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t na)
   if (count(na, 12) || dims_of(a[0], &d, &dt) || method_int(a[6], s_numel, &n) ||
       view(a[1], "q", dt, n, d.h_q, d.d, &q) || view(a[2], "k", dt, n, d.h_kv, d.d, &k) ||
       rope_params(a + 3, &d, a[9], &p) || flat(a[6], "positions", t_int32, n, &pos) ||
-      flat(a[10], "d_status", t_int32, 1, &status) || all_device() || stream_of(a[11], a[6], &s))
+      flat(a[10], "d_status", t_int32, 1, &status) || all_device() ||
+      stream_of(a[11], &s))
     return NULL;
   p.d_status = status;
   PyObject *qo = Py_NewRef(Py_None), *ko = Py_NewRef(Py_None), *r = NULL;
   if (a[1] != Py_None) Py_SETREF(qo, output(a[7], "q_out", dt, n, d.h_q, d.d, a[1], &qp));
-  if (qo && a[2] != Py_None) Py_SETREF(ko, output(a[8], "k_out", dt, n, d.h_kv, d.d, a[2], &kp));
+  if (qo && a[2] != Py_None)
+    Py_SETREF(ko, output(a[8], "k_out", dt, n, d.h_kv, d.d, a[2], &kp));
   if (qo && ko) {
     const int rc = call_norm_rope(&d, &p, &q, &k, pos, n, qp, kp, s);
     r = rc ? refused("gdn_qk_norm_rope", rc) : PyTuple_Pack(2, qo, ko);
@@ -320,7 +341,7 @@ static PyObject* kv_append(PyObject* self, PyObject* const* a, Py_ssize_t na) {
       flat(a[11], "row_seq", t_int32, n, &seq) ||
       flat(a[13], "k_out", dt, n * d.h_kv * d.d, &kp) ||
       flat(a[15], "d_status", t_int32, 1, &status) || all_device() ||
-      stream_of(a[16], a[7], &s))
+      stream_of(a[16], &s))
     return NULL;
   PyObject* qo = Py_NewRef(Py_None);
   if (a[1] != Py_None) Py_SETREF(qo, output(a[12], "q_out", dt, n, d.h_q, d.d, a[1], &qp));
@@ -347,7 +368,7 @@ static PyObject* attn_prefill(PyObject* self, PyObject* const* a, Py_ssize_t na)
       flat(a[4], "cu_seqlens", t_int32, ends, &cu) ||
       flat(a[5], "cu_seqlens_kv", t_int32, ends, &cu_kv) ||
       flat(a[8], "d_status", t_int32, 1, &status) || all_device() ||
-      stream_of(a[9], a[1], &s))
+      stream_of(a[9], &s))
     return NULL;
   PyObject* o = output(a[7], "o", dt, sq[0], d.h_q, d.d, a[1], &op);
   if (!o) return NULL;
@@ -374,7 +395,7 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
       view(a[8], "gate", dt, sq[0], d.h_q, d.d, &gate) || cache_of(a + 2, &d, dt, &c) ||
       flat(a[5], "seq_lens", t_int32, sq[0], &lens) ||
       flat(a[10], "d_status", t_int32, 1, &status) || all_device() ||
-      stream_of(a[11], a[1], &s))
+      stream_of(a[11], &s))
     return NULL;
   const int64_t shared = PyLong_AsLongLong(a[7]);
   if (shared == -1 && PyErr_Occurred()) return NULL;
@@ -383,7 +404,7 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
     const int contiguous = c2 ? PyObject_IsTrue(c2) : -1;
     Py_XDECREF(c2);
     if (contiguous == 0) PyErr_SetString(PyExc_ValueError, "workspace must be contiguous");
-    if (contiguous != 1 || note_host(a[6], "workspace") || method_int(a[6], s_numel, &size) ||
+    if (contiguous != 1 || note_device(a[6], "workspace") || method_int(a[6], s_numel, &size) ||
         method_int(a[6], s_element_size, &item) || address(a[6], &ws) || all_device())
       return NULL;
   }
@@ -396,21 +417,21 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
   return refused("gdn_attn_decode", rc);
 }
 
-/* (float32, bfloat16, float16), int32, float64, torch.empty, raw-stream function or
-   None, current-stream function, GdnError, the four entry points' addresses */
+/* (float32, bfloat16, float16), int32, float64, torch.empty, current raw stream of a device, current device, GdnError, the four entry
+   points' addresses */
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
   unsigned long long fn[4];
   if (!PyArg_ParseTuple(args, "(OOO)OOOOOO(KKKK)", &io_types[0], &io_types[1], &io_types[2],
-                        &t_int32, &t_float64, &f_empty, &f_stream, &f_current, &c_error, &fn[0],
-                        &fn[1], &fn[2], &fn[3]))
+                        &t_int32, &t_float64, &f_empty, &f_stream, &f_device, &c_error,
+                        &fn[0], &fn[1], &fn[2], &fn[3]))
     return NULL;
   for (int i = 0; i < 3; ++i) Py_INCREF(io_types[i]);
   Py_INCREF(t_int32);
   Py_INCREF(t_float64);
   Py_INCREF(f_empty);
   Py_INCREF(f_stream);
-  Py_INCREF(f_current);
+  Py_INCREF(f_device);
   Py_INCREF(c_error);
   call_norm_rope = (norm_rope_fn)(uintptr_t)fn[0];
   call_append = (append_fn)(uintptr_t)fn[1];
@@ -436,7 +457,7 @@ PyMODINIT_FUNC PyInit__attn_calls(void) {
     const char* name;
   } names[] = {{&s_shape, "shape"},   {&s_stride, "stride"}, {&s_dtype, "dtype"},
                {&s_data_ptr, "data_ptr"}, {&s_numel, "numel"},   {&s_is_contiguous, "is_contiguous"},
-               {&s_device, "device"}, {&s_is_cuda, "is_cuda"},   {&s_index, "index"},
+               {&s_device, "device"}, {&s_get_device, "get_device"},
                {&s_element_size, "element_size"}};
   for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i)
     if (!(*names[i].at = PyUnicode_InternFromString(names[i].name))) return NULL;
