@@ -556,10 +556,19 @@ def _attn_calls():
             lambda device: torch.cuda.current_stream(device).cuda_stream)
         device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         calls.setup((torch.float32, torch.bfloat16, torch.float16), torch.int32, torch.float64,
-                    torch.empty, raw, device, GdnError,
+                    torch.empty, _empty_on, raw, device, GdnError,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
         _calls = calls
     return _calls
+
+
+def _empty_on(size, dtype, device, stream):
+    """torch.empty from the memory of the stream with this handle."""
+    import torch
+    handle = int(stream)
+    s = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(s):
+        return torch.empty(size, dtype=dtype, device=device)
 
 
 def _ref(v):

@@ -18,7 +18,7 @@
 static PyObject *s_shape, *s_stride, *s_dtype, *s_data_ptr, *s_numel, *s_is_contiguous, *s_device,
     *s_get_device, *s_element_size;
 static PyObject* io_types[3]; /* by gdn_dtype */
-static PyObject *t_int32, *t_float64, *f_empty, *f_stream, *f_device, *c_error,
+static PyObject *t_int32, *t_float64, *f_empty, *f_empty_on, *f_stream, *f_device, *c_error,
     *empty_kw;
 
 typedef int (*norm_rope_fn)(const gdn_attn_dims*, const gdn_rope_params*, const gdn_view*,
@@ -167,9 +167,12 @@ static int flat(PyObject* t, const char* name, PyObject* dtype, int64_t numel, v
   return note_device(t, name) || address(t, p) ? -1 : 0;
 }
 
-/* An output (new reference) and its address, allocated beside `like` when None. */
+/* An output (new reference) and its address, allocated beside `like` when None: from
+   the current stream's memory, or, where the call goes to another stream, from that
+   one's (a block of the current stream's may still be in use there, and may be used
+   there again before the call has run). */
 static PyObject* output(PyObject* t, const char* name, PyObject* dtype, int64_t n, int64_t heads,
-                        int64_t d, PyObject* like, void** p) {
+                        int64_t d, PyObject* like, PyObject* other, void** p) {
   if (t != Py_None) {
     if (flat(t, name, dtype, n * heads * d, p) || all_device()) return NULL;
     Py_INCREF(t);
@@ -179,8 +182,9 @@ static PyObject* output(PyObject* t, const char* name, PyObject* dtype, int64_t 
   PyObject* device = PyObject_GetAttr(like, s_device);
   PyObject* size = Py_BuildValue("(LLL)", (long long)n, (long long)heads, (long long)d);
   if (device && size) {
-    PyObject* args[3] = {size, dtype, device};
-    made = PyObject_Vectorcall(f_empty, args, 1, empty_kw);
+    PyObject* args[4] = {size, dtype, device, other};
+    made = other == Py_None ? PyObject_Vectorcall(f_empty, args, 1, empty_kw)
+                            : PyObject_Vectorcall(f_empty_on, args, 4, NULL);
   }
   Py_XDECREF(size);
   Py_XDECREF(device);
@@ -205,8 +209,10 @@ static int dims_of(PyObject* o, gdn_attn_dims* d, PyObject** dtype) {
 }
 
 /* The stream given, else the current one of the tensors' device, which has to be the
-   current device: the launch goes there. */
-static int stream_of(PyObject* stream, gdn_stream_t* s) {
+   current device: the launch goes there.  *other: a given stream that is not the
+   current one (borrowed), else None. */
+static int stream_of(PyObject* stream, gdn_stream_t* s, PyObject** other) {
+  *other = Py_None;
   PyObject* v = PyObject_CallNoArgs(f_device);
   if (!v) return -1;
   const long long now = PyLong_AsLongLong(v);
@@ -217,14 +223,19 @@ static int stream_of(PyObject* stream, gdn_stream_t* s) {
     Py_DECREF(v);
     return -1;
   }
-  if (stream != Py_None)
-    Py_SETREF(v, PyNumber_Long(stream));
-  else
-    Py_SETREF(v, PyObject_CallOneArg(f_stream, v));
+  Py_SETREF(v, PyObject_CallOneArg(f_stream, v));
   if (!v) return -1;
+  void* current = PyLong_AsVoidPtr(v);
+  Py_DECREF(v);
+  *s = (gdn_stream_t)current;
+  if (!current && PyErr_Occurred()) return -1;
+  if (stream == Py_None) return 0;
+  if (!(v = PyNumber_Long(stream))) return -1;
   *s = (gdn_stream_t)PyLong_AsVoidPtr(v);
   Py_DECREF(v);
-  return !*s && PyErr_Occurred() ? -1 : 0;
+  if (!*s && PyErr_Occurred()) return -1;
+  if ((void*)*s != current) *other = stream;
+  return 0;
 }
 
 static int rope_params(PyObject* const* a, const gdn_attn_dims* d, PyObject* scale,
@@ -298,7 +309,7 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t na)
   gdn_attn_dims d;
   gdn_rope_params p;
   gdn_view q, k;
-  PyObject* dt;
+  PyObject *dt, *other;
   int64_t n;
   void *pos, *status, *qp = NULL, *kp = NULL;
   gdn_stream_t s;
@@ -306,13 +317,13 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t na)
       view(a[1], "q", dt, n, d.h_q, d.d, &q) || view(a[2], "k", dt, n, d.h_kv, d.d, &k) ||
       rope_params(a + 3, &d, a[9], &p) || flat(a[6], "positions", t_int32, n, &pos) ||
       flat(a[10], "d_status", t_int32, 1, &status) || all_device() ||
-      stream_of(a[11], &s))
+      stream_of(a[11], &s, &other))
     return NULL;
   p.d_status = status;
   PyObject *qo = Py_NewRef(Py_None), *ko = Py_NewRef(Py_None), *r = NULL;
-  if (a[1] != Py_None) Py_SETREF(qo, output(a[7], "q_out", dt, n, d.h_q, d.d, a[1], &qp));
+  if (a[1] != Py_None) Py_SETREF(qo, output(a[7], "q_out", dt, n, d.h_q, d.d, a[1], other, &qp));
   if (qo && a[2] != Py_None)
-    Py_SETREF(ko, output(a[8], "k_out", dt, n, d.h_kv, d.d, a[2], &kp));
+    Py_SETREF(ko, output(a[8], "k_out", dt, n, d.h_kv, d.d, a[2], other, &kp));
   if (qo && ko) {
     const int rc = call_norm_rope(&d, &p, &q, &k, pos, n, qp, kp, s);
     r = rc ? refused("gdn_qk_norm_rope", rc) : PyTuple_Pack(2, qo, ko);
@@ -330,7 +341,7 @@ static PyObject* kv_append(PyObject* self, PyObject* const* a, Py_ssize_t na) {
   gdn_rope_params p;
   gdn_view q, k, v;
   gdn_kv_cache c;
-  PyObject* dt;
+  PyObject *dt, *other;
   int64_t n;
   void *pos, *seq, *status, *qp = NULL, *kp;
   gdn_stream_t s;
@@ -341,10 +352,10 @@ static PyObject* kv_append(PyObject* self, PyObject* const* a, Py_ssize_t na) {
       flat(a[11], "row_seq", t_int32, n, &seq) ||
       flat(a[13], "k_out", dt, n * d.h_kv * d.d, &kp) ||
       flat(a[15], "d_status", t_int32, 1, &status) || all_device() ||
-      stream_of(a[16], &s))
+      stream_of(a[16], &s, &other))
     return NULL;
   PyObject* qo = Py_NewRef(Py_None);
-  if (a[1] != Py_None) Py_SETREF(qo, output(a[12], "q_out", dt, n, d.h_q, d.d, a[1], &qp));
+  if (a[1] != Py_None) Py_SETREF(qo, output(a[12], "q_out", dt, n, d.h_q, d.d, a[1], other, &qp));
   if (!qo) return NULL;
   const int rc = call_append(&d, &p, &q, &k, &v, pos, seq, n, &c, qp, kp, status, s);
   if (!rc) return qo;
@@ -357,7 +368,7 @@ static PyObject* attn_prefill(PyObject* self, PyObject* const* a, Py_ssize_t na)
   (void)self;
   gdn_attn_dims d;
   gdn_view q, k, v, gate;
-  PyObject* dt;
+  PyObject *dt, *other;
   int64_t ends, sq[4] = {0}, sk[4] = {0};
   void *cu, *cu_kv, *status, *op;
   gdn_stream_t s;
@@ -368,9 +379,9 @@ static PyObject* attn_prefill(PyObject* self, PyObject* const* a, Py_ssize_t na)
       flat(a[4], "cu_seqlens", t_int32, ends, &cu) ||
       flat(a[5], "cu_seqlens_kv", t_int32, ends, &cu_kv) ||
       flat(a[8], "d_status", t_int32, 1, &status) || all_device() ||
-      stream_of(a[9], &s))
+      stream_of(a[9], &s, &other))
     return NULL;
-  PyObject* o = output(a[7], "o", dt, sq[0], d.h_q, d.d, a[1], &op);
+  PyObject* o = output(a[7], "o", dt, sq[0], d.h_q, d.d, a[1], other, &op);
   if (!o) return NULL;
   const int rc = call_prefill(&d, &q, &k, &v, cu, cu_kv, (int32_t)(ends - 1), sq[0], sk[0], &gate, op,
                               status, s);
@@ -386,7 +397,7 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
   gdn_attn_dims d;
   gdn_view q, gate;
   gdn_kv_cache c;
-  PyObject* dt;
+  PyObject *dt, *other;
   int64_t sq[4] = {0}, size = 0, item = 0;
   void *lens, *status, *op, *ws = NULL;
   gdn_stream_t s;
@@ -395,7 +406,7 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
       view(a[8], "gate", dt, sq[0], d.h_q, d.d, &gate) || cache_of(a + 2, &d, dt, &c) ||
       flat(a[5], "seq_lens", t_int32, sq[0], &lens) ||
       flat(a[10], "d_status", t_int32, 1, &status) || all_device() ||
-      stream_of(a[11], &s))
+      stream_of(a[11], &s, &other))
     return NULL;
   const int64_t shared = PyLong_AsLongLong(a[7]);
   if (shared == -1 && PyErr_Occurred()) return NULL;
@@ -408,7 +419,7 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
         method_int(a[6], s_element_size, &item) || address(a[6], &ws) || all_device())
       return NULL;
   }
-  PyObject* o = output(a[9], "o", dt, sq[0], d.h_q, d.d, a[1], &op);
+  PyObject* o = output(a[9], "o", dt, sq[0], d.h_q, d.d, a[1], other, &op);
   if (!o) return NULL;
   const int rc = call_decode(&d, &q, &c, lens, (int32_t)sq[0], shared, &gate, op, ws,
                              (size_t)(size * item), status, s);
@@ -417,19 +428,21 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
   return refused("gdn_attn_decode", rc);
 }
 
-/* (float32, bfloat16, float16), int32, float64, torch.empty, current raw stream of a device, current device, GdnError, the four entry
+/* (float32, bfloat16, float16), int32, float64, torch.empty, empty(size, dtype, device,
+   stream), current raw stream of a device, current device, GdnError, the four entry
    points' addresses */
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
   unsigned long long fn[4];
-  if (!PyArg_ParseTuple(args, "(OOO)OOOOOO(KKKK)", &io_types[0], &io_types[1], &io_types[2],
-                        &t_int32, &t_float64, &f_empty, &f_stream, &f_device, &c_error,
+  if (!PyArg_ParseTuple(args, "(OOO)OOOOOOO(KKKK)", &io_types[0], &io_types[1], &io_types[2],
+                        &t_int32, &t_float64, &f_empty, &f_empty_on, &f_stream, &f_device, &c_error,
                         &fn[0], &fn[1], &fn[2], &fn[3]))
     return NULL;
   for (int i = 0; i < 3; ++i) Py_INCREF(io_types[i]);
   Py_INCREF(t_int32);
   Py_INCREF(t_float64);
   Py_INCREF(f_empty);
+  Py_INCREF(f_empty_on);
   Py_INCREF(f_stream);
   Py_INCREF(f_device);
   Py_INCREF(c_error);

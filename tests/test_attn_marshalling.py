@@ -1,6 +1,7 @@
 """The attention calls' marshalling on a host without a GPU: stand-ins for
-device tensors, for torch's functions and for the library's entry points.
-Which devices and streams a call takes."""
+device tensors, for torch's functions and for the library's entry points.  On
+which device and stream a call goes, where its outputs are allocated, and what
+it refuses."""
 import ctypes
 
 import pytest
@@ -67,8 +68,12 @@ def calls(monkeypatch):
     def empty(size, dtype, device):
         seen.append(("empty", "current"))
         return Tensor(size, dtype, state.device)
+
+    def empty_on(size, dtype, device, stream):
+        seen.append(("empty", int(stream)))
+        return Tensor(size, dtype, state.device)
     real.setup((torch.float32, torch.bfloat16, torch.float16), torch.int32, torch.float64, empty,
-               lambda device: CURRENT + device, lambda: state.device, gdn.GdnError,
+               empty_on, lambda device: CURRENT + device, lambda: state.device, gdn.GdnError,
                tuple(ctypes.cast(f, P).value for f in keep))
     state.keep = keep
     yield state
@@ -114,6 +119,19 @@ def test_the_current_stream_and_its_memory_by_default(calls, name):
     _call(name, stream=CURRENT)
     assert calls.seen[-1] == (name, CURRENT)
     assert set(calls.seen[:-1]) == {("empty", "current")}
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("stream", [SIDE, 0])
+def test_outputs_of_a_call_on_another_stream_come_from_its_memory(calls, name, stream):
+    _call(name, stream=stream)
+    assert calls.seen[-1] == (name, stream)
+    assert set(calls.seen[:-1]) == {("empty", stream)}
+
+
+def test_a_given_output_is_taken_on_any_stream(calls):
+    _call("prefill", o=True, stream=SIDE)
+    assert calls.seen == [("prefill", SIDE)]
 
 
 @pytest.mark.parametrize("name,odd", [("norm_rope", "k"), ("norm_rope", "positions"), ("append", "v"),
