@@ -543,13 +543,18 @@ def _attn_calls():
     points (its shape, type and layout checks raise as this module's do)."""
     global _calls
     if _calls is None:
+        import importlib.util
+
         import torch
+
+        from ._build import CALLS
         lib = load()
-        path = os.path.join(PKG, "_attn_calls.so")
-        if not os.path.exists(path):
-            raise ImportError(f"{path} is missing: build it first "
+        if not os.path.exists(CALLS):
+            raise ImportError(f"{CALLS} is missing: build it first "
                               "(python -c 'import __graft_entry__ as g; g.build()')")
-        from . import _attn_calls as calls
+        spec = importlib.util.spec_from_file_location(f"{__package__}._attn_calls", CALLS)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
         fns = (lib.gdn_qk_norm_rope, lib.gdn_kv_append, lib.gdn_attn_prefill, lib.gdn_attn_decode)
         # the raw handle of a device's current stream; current_stream() builds an object first
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (

@@ -1,7 +1,8 @@
 """Builds libgdn_gb300.so in-tree with nvcc for sm_103a (one translation unit
 per .cu file, compiled in parallel, linked with -shared).  No cmake, no torch
 extension machinery: the library is a plain C ABI over the CUDA runtime.  Beside
-it goes a small CPython module that marshals the attention calls (gcc)."""
+it goes a small CPython module that marshals the attention calls (gcc and the
+interpreter's headers)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -15,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgdn_gb300.so")
 CALLS_SRC = os.path.join(CSRC, "attn_calls.c")       # the attention calls' marshalling
-CALLS = os.path.join(PKG, "_attn_calls.so")
+# by the interpreter's tag: a module built for one is none for another
+CALLS = os.path.join(PKG, "_attn_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
