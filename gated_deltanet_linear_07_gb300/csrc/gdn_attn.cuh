@@ -10,6 +10,10 @@
 namespace gdn {
 namespace attn {
 
+constexpr int SMS = 152;                 // of the one GPU this is built for
+constexpr int PREFIX_SMS = 96;           // of them, the shared prefix's pass of a decode: about
+                                         // two thirds, a number that 2, 3, 4, 6 and 8 divide
+
 // For copies and products in flight when a wait has run out (they take microseconds).
 constexpr uint64_t GRACE_NS = 1000000;
 

@@ -57,7 +57,7 @@ struct DecCfg {
   // Smaller heads want more warps to keep up with the loads; at 256 one warp's
   // accumulator takes the registers of two.
   static constexpr int PER_SM = D == 256 ? 1 : D == 128 ? 2 : 3;
-  static constexpr int CTAS = 152 * PER_SM;
+  static constexpr int CTAS = SMS * PER_SM;
   static constexpr int FIT = (int)((233472u / PER_SM - 1024u - HEAD) / STAGE);
   static constexpr int STAGES = FIT < DEC_MAX_STAGES ? FIT : DEC_MAX_STAGES;
   static constexpr uint32_t SMEM = HEAD + STAGES * STAGE;
@@ -520,8 +520,8 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
               mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 1));
               mt[r] = fmaxf(mt[r], __shfl_xor_sync(0xffffffffu, mt[r], 2));
             }
-            // The reference maximum may lag (WeightRange).  A row's
-            // follows from the row alone, and rows without a head ask for nothing.
+            // The reference maximum may lag (WeightRange).  A row's follows from the
+            // row alone, and rows without a head ask for nothing.
             bool far[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
@@ -543,6 +543,8 @@ __global__ void __launch_bounds__(DEC_THREADS, DecCfg<D>::PER_SM)
                 o[i][3] *= f[1];
               }
             }
+            // The weights go to the product with v in the I/O type, as the prefill's do (a
+            // prompt's last token and a decoded one round alike); their sum does not.
             uint32_t pa[4];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -732,7 +734,7 @@ static __host__ __device__ __forceinline__ int most_parts(const DecArgs& p) {
   return p.prefix + (p.early > 0 ? p.ctas : p.ctas / (p.a.h_kv * p.subs) + 2);
 }
 
-// One item of 16 rows behind a prefix in 152 parts, runs of 456 CTAs: 83 KB.
+// One item of 16 rows behind a prefix in PREFIX_SMS parts, runs of 3 SMS CTAs: 75 KB.
 constexpr int MERGE_SMEM = 96 * 1024;
 
 template <typename IO, int D, bool SPLIT>
@@ -885,7 +887,7 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
     // The SMs that the prefix pass leaves free, and its length in units of 64 keys:
     // 128 keys of it take about as long as 0.8 units, or 0.6 below head dim 256
     // where the units are smaller, and it starts and ends in about 5.
-    const int left = 152 - gdn_attn_prefix_ctas(a.h_q, a.h_kv, D, (int)a.total_q, a.shared_len);
+    const int left = SMS - gdn_attn_prefix_ctas(a.h_q, a.h_kv, D, (int)a.total_q, a.shared_len);
     if (left > 0) {
       const int64_t blocks = ((a.shared_len + 127) / 128 + a.splits - 1) / a.splits;
       p.early = left * C::PER_SM;
@@ -968,13 +970,13 @@ static cudaError_t launch_decode(const GdnAttnArgs& a, int io, cudaStream_t s) {
   // longer part then (64 sequences behind 2048 keys: 19.0 and 20.7).
   p.merge_rows = p.rows;
   int64_t slices = 1;
-  if (items <= 152)
-    while (p.merge_rows > 1 && items * slices * 2 <= 4 * 152) {
+  if (items <= SMS)
+    while (p.merge_rows > 1 && items * slices * 2 <= 4 * SMS) {
       p.merge_rows = (p.merge_rows + 1) / 2;
       slices = (p.rows + p.merge_rows - 1) / p.merge_rows;
     }
   const bool split =
-      slices > 1 || (items <= 152 && p.merge_rows * (D / 4) * 2 <= MERGE_THREADS);
+      slices > 1 || (items <= SMS && p.merge_rows * (D / 4) * 2 <= MERGE_THREADS);
   cfg.gridDim = dim3((unsigned)(items * slices));
   cfg.blockDim = dim3(MERGE_THREADS);
   cfg.dynamicSmemBytes = (size_t)most_parts(p) * (8 + 8 * p.merge_rows);

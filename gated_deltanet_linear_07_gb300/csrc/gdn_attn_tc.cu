@@ -1370,7 +1370,7 @@ int gdn_attn_prefix_splits(int h_q, int h_kv, int d, int n, int64_t shared_len) 
   int cg;
   const int64_t items = prefix_items(h_q, h_kv, d, n, cg);
   const int64_t blocks = (shared_len + gdn::attn::BN - 1) / gdn::attn::BN;
-  int64_t splits = (96 / cg) / items;
+  int64_t splits = (gdn::attn::PREFIX_SMS / cg) / items;
   if (splits > (blocks + 1) / 2) splits = (blocks + 1) / 2;
   if (splits < 1) splits = 1;
   return (int)splits;
@@ -1380,7 +1380,7 @@ int gdn_attn_prefix_ctas(int h_q, int h_kv, int d, int n, int64_t shared_len) {
   int cg;
   const int64_t items = prefix_items(h_q, h_kv, d, n, cg);
   const int64_t ctas = items * gdn_attn_prefix_splits(h_q, h_kv, d, n, shared_len) * cg;
-  return ctas < 152 ? (int)ctas : 152;
+  return ctas < gdn::attn::SMS ? (int)ctas : gdn::attn::SMS;
 }
 
 cudaError_t gdn_launch_attn_prefix(const GdnAttnArgs& a, int io, cudaStream_t s) {

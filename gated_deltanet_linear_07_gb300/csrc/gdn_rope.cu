@@ -296,7 +296,7 @@ constexpr int MANY_THREADS = 32 * (MANY_WARPS + 1);
 constexpr int MANY_TOKENS = 4;                         // tokens of a stage
 constexpr int MANY_STAGES = 2;
 constexpr int MANY_PER_SM = 2;
-constexpr int MANY_CTAS = MANY_PER_SM * 152;
+constexpr int MANY_CTAS = MANY_PER_SM * SMS;
 constexpr uint32_t STAGE_ROWS_BYTES = 49152;           // rows of one stage, at most
 
 struct ManyShared {

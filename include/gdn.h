@@ -517,15 +517,16 @@ typedef struct {
 /*
  * gdn_qk_norm_rope -- per-head RMS norm of queries and keys and the rotation
  * by position, in one pass: with c, s the cosine and sine of
- * positions[t] * inv_freq[i] (the angle is reduced in fp64, so positions of
- * any size keep fp32 accuracy), pair (a, b) -> rope_scale * (a c - b s,
- * a s + b c); channels from rot_dim on are only normalised.
+ * positions[t] * inv_freq[i] (the angle as a 64-bit fixed-point fraction of a
+ * turn: positions of any size are as accurate as small ones), pair (a, b) ->
+ * rope_scale * (a c - b s, a s + b c); channels from rot_dim on are only normalised.
  *   q, k       views [n][h_q][d] and [n][h_kv][d] IO; a view with null data
  *              is left out (its output too)
  *   positions  [n] int32 (device)
  *   q_out      [n][h_q][d] IO, k_out [n][h_kv][d] IO, contiguous, 16-byte
  *              aligned; each may be its own input where that is contiguous
- * IO is fp32, bf16 or fp16; everything between is fp32, rounded once.
+ * IO is fp32, bf16 or fp16; everything between is fp32, rounded once (cosine and
+ * sine within 2^-20.5 for the 16-bit types, a few ulp for fp32).
  * params->d_status reports GDN_DEV_WAIT_TIMEOUT (rows left out: not valid).
  */
 int gdn_qk_norm_rope(const gdn_attn_dims* dims, const gdn_rope_params* params, const gdn_view* q,
@@ -604,7 +605,9 @@ size_t gdn_attn_decode_workspace_size(const gdn_attn_dims* dims, int32_t n, int6
  *   o          [n][h_q][d] IO, contiguous, 16-byte aligned
  *   workspace  gdn_attn_decode_workspace_size() bytes, 256-byte aligned,
  *              clobbered; it needs no initial value
- * What the cache holds beyond a sequence's length never reaches its output.
+ * Arithmetic as in gdn_attn_prefill: the softmax weights are rounded to IO for the
+ * product with v, all else is fp32.  What the cache holds beyond a sequence's length
+ * never reaches its output.
  */
 int gdn_attn_decode(const gdn_attn_dims* dims, const gdn_view* q, const gdn_kv_cache* cache,
                     const int32_t* seq_lens, int32_t n, int64_t shared_len, const gdn_view* gate,
