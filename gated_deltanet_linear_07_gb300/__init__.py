@@ -20,5 +20,9 @@ from ._binding import (GDN_BF16, GDN_DEV_BAD_CU_SEQLENS, GDN_DEV_BAD_SLOT,  # no
                        GDN_FP16, GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED, GDN_DEV_BAD_PAGE,
                        GDN_DEV_BAD_LENGTH, gdn_attn_dims, gdn_view, gdn_rope_params, gdn_kv_cache,
                        make_attn_dims, rope_frequencies, gdn_qk_norm_rope, gdn_kv_append,
-                       gdn_attn_prefill, gdn_attn_decode, gdn_attn_decode_workspace_size)
+                       gdn_attn_prefill, gdn_attn_decode, gdn_attn_decode_workspace_size,
+                       gdn_rope_axes, gdn_kv8_cache, Kv8Cache, GDN_KV8_BLOCK, GDN_ROPE_MAX_AXES,
+                       rope_sections, make_rope_axes, make_kv8_cache, gdn_qk_norm_rope_axes,
+                       gdn_kv8_append, gdn_kv8_gather, gdn_attn_decode_kv8,
+                       gdn_attn_decode_kv8_workspace_size, gdn_kv8_evict)
 from ._build import build  # noqa: F401

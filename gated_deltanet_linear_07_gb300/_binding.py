@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgdn_gb300.so")
@@ -64,6 +65,20 @@ class gdn_rope_params(ctypes.Structure):
 
 class gdn_kv_cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32)]
+
+
+GDN_ROPE_MAX_AXES, GDN_KV8_BLOCK = 4, 16
+
+
+class gdn_rope_axes(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int32), ("pair", ctypes.c_uint8 * 128)]
+
+
+class gdn_kv8_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
                 ("pages_per_seq", ctypes.c_int32)]
 
@@ -145,6 +160,19 @@ def load() -> ctypes.CDLL:
     lib.gdn_attn_decode_workspace_size.restype = SZ
     lib.gdn_attn_decode.argtypes = [A, V, KV, P, I32, I64, V, P, P, SZ, P, P]
     lib.gdn_attn_decode.restype = ctypes.c_int
+    X, K8 = ctypes.POINTER(gdn_rope_axes), ctypes.POINTER(gdn_kv8_cache)
+    lib.gdn_qk_norm_rope_axes.argtypes = [A, RP, X, V, V, P, I64, P, P, P]
+    lib.gdn_qk_norm_rope_axes.restype = ctypes.c_int
+    lib.gdn_kv8_append.argtypes = [A, RP, X, V, V, V, P, P, P, I32, I64, K8, P, P, P, P]
+    lib.gdn_kv8_append.restype = ctypes.c_int
+    lib.gdn_kv8_gather.argtypes = [A, K8, P, I32, I64, P, P, P, P]
+    lib.gdn_kv8_gather.restype = ctypes.c_int
+    lib.gdn_attn_decode_kv8_workspace_size.argtypes = [A, I32, I64]
+    lib.gdn_attn_decode_kv8_workspace_size.restype = SZ
+    lib.gdn_attn_decode_kv8.argtypes = [A, V, K8, P, I32, V, P, P, P, SZ, P, P]
+    lib.gdn_attn_decode_kv8.restype = ctypes.c_int
+    lib.gdn_kv8_evict.argtypes = [A, K8, P, P, I32, I32, I32, I32, K8, P, P, P, P, P]
+    lib.gdn_kv8_evict.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -563,6 +591,10 @@ def _attn_calls():
         calls.setup((torch.float32, torch.bfloat16, torch.float16), torch.int32, torch.float64,
                     torch.empty, _empty_on, raw, device, GdnError,
                     tuple(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
+        fns = (lib.gdn_qk_norm_rope_axes, lib.gdn_kv8_append, lib.gdn_kv8_gather,
+               lib.gdn_attn_decode_kv8, lib.gdn_kv8_evict)
+        calls.setup_kv8(torch.float8_e4m3fn,
+                        tuple(ctypes.cast(f, ctypes.c_void_p).value for f in fns))
         _calls = calls
     return _calls
 
@@ -626,3 +658,113 @@ def gdn_attn_decode(dims, q, k_cache, v_cache, block_table, seq_lens, workspace,
     return (_calls or _attn_calls()).attn_decode(dims, q, k_cache, v_cache, block_table, seq_lens,
                                                  workspace, int(shared_len), gate, o, d_status,
                                                  stream)
+
+
+# ---- positions with several axes, the cache held in 8 bits --------------------
+
+
+def rope_sections(sections, interleaved=False):
+    """The axis of each pair of channels, for make_rope_axes: sections[a] pairs for
+    axis a, one section after the other, or, interleaved, taking turns as long
+    as a section lasts (0, 1, 2, 0, 1, 2, ..., 0, 0)."""
+    left = [int(s) for s in sections]
+    if any(s < 0 for s in left):
+        raise ValueError("sections must not be negative")
+    if not interleaved:
+        return [a for a, s in enumerate(left) for _ in range(s)]
+    out = []
+    while any(left):
+        for a, s in enumerate(left):
+            if s:
+                out.append(a)
+                left[a] -= 1
+    return out
+
+
+def make_rope_axes(axis_of_pair) -> gdn_rope_axes:
+    """gdn_rope_axes from the axis of each pair of channels (rot_dim / 2 of them; see
+    rope_sections)."""
+    axis = [int(a) for a in axis_of_pair]
+    if len(axis) > 128 or any(not 0 <= a < GDN_ROPE_MAX_AXES for a in axis):
+        raise ValueError(f"at most 128 pairs, of axes 0 to {GDN_ROPE_MAX_AXES - 1}")
+    return gdn_rope_axes(max(axis, default=0) + 1, (ctypes.c_uint8 * 128)(*axis))
+
+
+class Kv8Cache(NamedTuple):
+    """A paged cache held in 8 bits (see gdn_kv8_cache in include/gdn.h)."""
+    k: Any             # [num_pages, h_kv, page_size, d] float8_e4m3fn
+    v: Any
+    k_scale: Any       # [num_pages, h_kv, page_size / 16] fp32
+    v_scale: Any
+    block_table: Any   # [num_seqs, pages_per_seq] int32
+
+
+def make_kv8_cache(dims, num_pages, block_table) -> Kv8Cache:
+    """A Kv8Cache of zeros beside block_table ([num_seqs, pages_per_seq] int32)."""
+    import torch
+    dev = block_table.device
+    shape = (int(num_pages), dims.h_kv, dims.page_size, dims.d)
+
+    def codes():
+        return torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+
+    def scales():
+        return torch.zeros((*shape[:2], dims.page_size // GDN_KV8_BLOCK), device=dev)
+    return Kv8Cache(codes(), codes(), scales(), scales(), block_table)
+
+
+def gdn_qk_norm_rope_axes(dims, q, k, q_norm, k_norm, inv_freq, positions, axes, q_out=None,
+                          k_out=None, rope_scale=1.0, stream=None, d_status=None):
+    """gdn_qk_norm_rope with a position on each of several axes (see
+    gdn_qk_norm_rope_axes in include/gdn.h): positions [axes' count, n] int32,
+    axes from make_rope_axes.  Returns (q_out, k_out)."""
+    return (_calls or _attn_calls()).qk_norm_rope_axes(dims, q, k, q_norm, k_norm, inv_freq,
+                                                       positions, axes, q_out, k_out, rope_scale,
+                                                       d_status, stream)
+
+
+def gdn_kv8_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions, cache, starts,
+                   cu_seqlens=None, axes=None, q_out=None, k_out=None, rope_scale=1.0,
+                   d_status=None, stream=None):
+    """Norm and rotate q and k, and store k and v in an 8-bit cache (see
+    gdn_kv8_append in include/gdn.h): positions [n] or [axes' count, n] int32, cache a
+    Kv8Cache, starts [num_seqs] int32 (tokens that each sequence holds already),
+    cu_seqlens [num_seqs + 1] int32 (None: row t is sequence t), k_out [n, h_kv, d]
+    or None.  Returns q_out (None when q is None)."""
+    return (_calls or _attn_calls()).kv8_append(dims, q, k, v, q_norm, k_norm, inv_freq, positions,
+                                                cache, starts, cu_seqlens, axes, q_out, k_out,
+                                                rope_scale, d_status, stream)
+
+
+def gdn_kv8_gather(dims, cache, cu_seqlens, total, k_out=None, v_out=None, d_status=None,
+                   stream=None):
+    """The cached tokens as packed keys and values (see gdn_kv8_gather in
+    include/gdn.h): row cu_seqlens[b] + p is place p of sequence b, total =
+    cu_seqlens[-1] rows.  Returns (k, v), each [total, h_kv, d]."""
+    return (_calls or _attn_calls()).kv8_gather(dims, cache, cu_seqlens, int(total), k_out, v_out,
+                                                d_status, stream)
+
+
+def gdn_attn_decode_kv8_workspace_size(dims, n: int, capacity: int = 0) -> int:
+    """capacity: tokens of a block table row where weights are collected, else 0."""
+    return int(load().gdn_attn_decode_kv8_workspace_size(ctypes.byref(dims), int(n), int(capacity)))
+
+
+def gdn_attn_decode_kv8(dims, q, cache, seq_lens, workspace, gate=None, weights=None, o=None,
+                        d_status=None, stream=None):
+    """One query token per sequence against an 8-bit cache (see
+    gdn_attn_decode_kv8 in include/gdn.h): q [n, h_q, d], seq_lens [n] int32; weights
+    [num_seqs, h_kv, pages_per_seq * page_size] fp32, to which what each cached token
+    receives is added, or None.  Returns o."""
+    return (_calls or _attn_calls()).attn_decode_kv8(dims, q, cache, seq_lens, workspace, gate,
+                                                     weights, o, d_status, stream)
+
+
+def gdn_kv8_evict(dims, cache, weights, seq_lens, keep, to, weights_out=None, first=0, last=0,
+                  new_lens=None, kept=None, d_status=None, stream=None):
+    """Cut sequences down to `keep` cached tokens each, copied to the pages of the
+    Kv8Cache `to`: the first and last ones and those with the greatest weights (see
+    gdn_kv8_evict in include/gdn.h).  Returns (new_lens [n], kept [n, h_kv, keep])."""
+    return (_calls or _attn_calls()).kv8_evict(dims, cache, weights, seq_lens, int(keep), to,
+                                               weights_out, int(first), int(last), new_lens, kept,
+                                               d_status, stream)

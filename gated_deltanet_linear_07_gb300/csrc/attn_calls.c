@@ -32,10 +32,33 @@ typedef int (*prefill_fn)(const gdn_attn_dims*, const gdn_view*, const gdn_view*
 typedef int (*decode_fn)(const gdn_attn_dims*, const gdn_view*, const gdn_kv_cache*, const int32_t*,
                          int32_t, int64_t, const gdn_view*, void*, void*, size_t, int32_t*,
                          gdn_stream_t);
+typedef int (*norm_rope_axes_fn)(const gdn_attn_dims*, const gdn_rope_params*, const gdn_rope_axes*,
+                                 const gdn_view*, const gdn_view*, const int32_t*, int64_t, void*,
+                                 void*, gdn_stream_t);
+typedef int (*kv8_append_fn)(const gdn_attn_dims*, const gdn_rope_params*, const gdn_rope_axes*,
+                             const gdn_view*, const gdn_view*, const gdn_view*, const int32_t*,
+                             const int32_t*, const int32_t*, int32_t, int64_t,
+                             const gdn_kv8_cache*, void*, void*, int32_t*, gdn_stream_t);
+typedef int (*kv8_gather_fn)(const gdn_attn_dims*, const gdn_kv8_cache*, const int32_t*, int32_t,
+                             int64_t, void*, void*, int32_t*, gdn_stream_t);
+typedef int (*decode_kv8_fn)(const gdn_attn_dims*, const gdn_view*, const gdn_kv8_cache*,
+                             const int32_t*, int32_t, const gdn_view*, float*, void*, void*, size_t,
+                             int32_t*, gdn_stream_t);
+typedef int (*kv8_evict_fn)(const gdn_attn_dims*, const gdn_kv8_cache*, const float*,
+                            const int32_t*, int32_t, int32_t, int32_t, int32_t,
+                            const gdn_kv8_cache*, float*, int32_t*, int32_t*, int32_t*,
+                            gdn_stream_t);
 static norm_rope_fn call_norm_rope;
 static append_fn call_append;
 static prefill_fn call_prefill;
 static decode_fn call_decode;
+/* Of the 8-bit cache and its positions (setup_kv8). */
+static PyObject* t_e4m3;
+static norm_rope_axes_fn call_norm_rope_axes;
+static kv8_append_fn call_kv8_append;
+static kv8_gather_fn call_kv8_gather;
+static decode_kv8_fn call_decode_kv8;
+static kv8_evict_fn call_kv8_evict;
 
 /* ---- attributes of a tensor (0: fine; -1: an exception is set) ---------------- */
 
@@ -167,28 +190,34 @@ static int flat(PyObject* t, const char* name, PyObject* dtype, int64_t numel, v
   return note_device(t, name) || address(t, p) ? -1 : 0;
 }
 
-/* An output (new reference) and its address, allocated beside `like` when None: from
-   the current stream's memory, or, where the call goes to another stream, from that
-   one's (a block of the current stream's may still be in use there, and may be used
-   there again before the call has run). */
-static PyObject* output(PyObject* t, const char* name, PyObject* dtype, int64_t n, int64_t heads,
-                        int64_t d, PyObject* like, PyObject* other, void** p) {
+/* An output of this shape (new reference) and its address, allocated beside `like` when
+   None: from the current stream's memory, or, where the call goes to another stream,
+   from that one's (a block of the current stream's may still be in use there, and may be
+   used there again before the call has run). */
+static PyObject* shaped(PyObject* t, const char* name, PyObject* dtype, PyObject* size,
+                        int64_t numel, PyObject* like, PyObject* other, void** p) {
+  if (!size) return NULL;
   if (t != Py_None) {
-    if (flat(t, name, dtype, n * heads * d, p) || all_device()) return NULL;
+    if (flat(t, name, dtype, numel, p) || all_device()) return NULL;
     Py_INCREF(t);
     return t;
   }
   PyObject* made = NULL;
   PyObject* device = PyObject_GetAttr(like, s_device);
-  PyObject* size = Py_BuildValue("(LLL)", (long long)n, (long long)heads, (long long)d);
-  if (device && size) {
+  if (device) {
     PyObject* args[4] = {size, dtype, device, other};
     made = other == Py_None ? PyObject_Vectorcall(f_empty, args, 1, empty_kw)
                             : PyObject_Vectorcall(f_empty_on, args, 4, NULL);
   }
-  Py_XDECREF(size);
   Py_XDECREF(device);
   if (made && address(made, p)) Py_CLEAR(made);
+  return made;
+}
+static PyObject* output(PyObject* t, const char* name, PyObject* dtype, int64_t n, int64_t heads,
+                        int64_t d, PyObject* like, PyObject* other, void** p) {
+  PyObject* size = Py_BuildValue("(LLL)", (long long)n, (long long)heads, (long long)d);
+  PyObject* made = shaped(t, name, dtype, size, n * heads * d, like, other, p);
+  Py_XDECREF(size);
   return made;
 }
 
@@ -277,6 +306,23 @@ static int cache_of(PyObject* const* a, const gdn_attn_dims* d, PyObject* dtype,
   c->num_pages = k[0];
   c->num_seqs = (int32_t)t[0];
   c->pages_per_seq = (int32_t)t[1];
+  return 0;
+}
+
+/* Address and bytes of a workspace of any type; None: null. */
+static int workspace_of(PyObject* t, void** p, size_t* bytes) {
+  int64_t size = 0, item = 0;
+  *p = NULL;
+  *bytes = 0;
+  if (t == Py_None) return 0;
+  PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+  const int contiguous = c ? PyObject_IsTrue(c) : -1;
+  Py_XDECREF(c);
+  if (contiguous == 0) PyErr_SetString(PyExc_ValueError, "workspace must be contiguous");
+  if (contiguous != 1 || note_device(t, "workspace") || method_int(t, s_numel, &size) ||
+      method_int(t, s_element_size, &item) || address(t, p))
+    return -1;
+  *bytes = (size_t)(size * item);
   return 0;
 }
 
@@ -398,8 +444,9 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
   gdn_view q, gate;
   gdn_kv_cache c;
   PyObject *dt, *other;
-  int64_t sq[4] = {0}, size = 0, item = 0;
-  void *lens, *status, *op, *ws = NULL;
+  int64_t sq[4] = {0};
+  size_t size;
+  void *lens, *status, *op, *ws;
   gdn_stream_t s;
   if (count(na, 12) || dims_of(a[0], &d, &dt) || shape_of(a[1], sq) < 0 || fits32(sq[0], "q") ||
       view(a[1], "q", dt, sq[0], d.h_q, d.d, &q) ||
@@ -410,22 +457,271 @@ static PyObject* attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t na) 
     return NULL;
   const int64_t shared = PyLong_AsLongLong(a[7]);
   if (shared == -1 && PyErr_Occurred()) return NULL;
-  if (a[6] != Py_None) {
-    PyObject* c2 = PyObject_CallMethodNoArgs(a[6], s_is_contiguous);
-    const int contiguous = c2 ? PyObject_IsTrue(c2) : -1;
-    Py_XDECREF(c2);
-    if (contiguous == 0) PyErr_SetString(PyExc_ValueError, "workspace must be contiguous");
-    if (contiguous != 1 || note_device(a[6], "workspace") || method_int(a[6], s_numel, &size) ||
-        method_int(a[6], s_element_size, &item) || address(a[6], &ws) || all_device())
-      return NULL;
-  }
+  if (workspace_of(a[6], &ws, &size) || all_device()) return NULL;
   PyObject* o = output(a[9], "o", dt, sq[0], d.h_q, d.d, a[1], other, &op);
   if (!o) return NULL;
-  const int rc = call_decode(&d, &q, &c, lens, (int32_t)sq[0], shared, &gate, op, ws,
-                             (size_t)(size * item), status, s);
+  const int rc = call_decode(&d, &q, &c, lens, (int32_t)sq[0], shared, &gate, op, ws, size, status, s);
   if (!rc) return o;
   Py_DECREF(o);
   return refused("gdn_attn_decode", rc);
+}
+
+/* ---- positions with several axes, the 8-bit cache ---------------------------------- */
+
+/* The axes of a gdn_rope_axes; None: null. */
+static int axes_of(PyObject* o, gdn_rope_axes* a, const gdn_rope_axes** p) {
+  *p = NULL;
+  if (o == Py_None) return 0;
+  Py_buffer b;
+  if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE)) return -1;
+  const int fits = b.len == (Py_ssize_t)sizeof(*a);
+  if (fits) memcpy(a, b.buf, sizeof(*a));
+  PyBuffer_Release(&b);
+  if (!fits) {
+    PyErr_SetString(PyExc_TypeError, "axes must be a gdn_rope_axes");
+    return -1;
+  }
+  *p = a;
+  return 0;
+}
+/* How many positions each of n tokens has. */
+static int64_t per_token(const gdn_rope_axes* a) {
+  return a && a->count >= 0 && a->count <= GDN_ROPE_MAX_AXES ? a->count : 1;
+}
+
+/* A Kv8Cache: (k, v, k_scale, v_scale, block_table). */
+static int kv8_of(PyObject* o, const char* name, const gdn_attn_dims* d, gdn_kv8_cache* c) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) {
+    PyErr_Format(PyExc_TypeError, "%s must be a Kv8Cache", name);
+    return -1;
+  }
+  PyObject** t = &PyTuple_GET_ITEM(o, 0);
+  int64_t k[4], b[4];
+  const int nk = shape_of(t[0], k);
+  if (nk < 0) return -1;
+  if (nk != 4 || k[1] != d->h_kv || k[2] != d->page_size || k[3] != d->d) {
+    PyErr_Format(PyExc_ValueError, "%s.k must be [num_pages, %d, %d, %d]", name, d->h_kv,
+                 d->page_size, d->d);
+    return -1;
+  }
+  const int nb = shape_of(t[4], b);
+  if (nb < 0) return -1;
+  if (nb != 2 || b[0] > INT32_MAX || b[1] > INT32_MAX) {
+    PyErr_Format(PyExc_ValueError, "%s.block_table must be [num_seqs, pages_per_seq]", name);
+    return -1;
+  }
+  const int64_t rows = k[0] * k[1] * k[2], scales = k[0] * k[1] * (k[2] / GDN_KV8_BLOCK);
+  void *ks, *vs, *table;
+  if (flat(t[0], "k", t_e4m3, rows * k[3], &c->k) || flat(t[1], "v", t_e4m3, rows * k[3], &c->v) ||
+      flat(t[2], "k_scale", io_types[GDN_FP32], scales, &ks) ||
+      flat(t[3], "v_scale", io_types[GDN_FP32], scales, &vs) ||
+      flat(t[4], "block_table", t_int32, b[0] * b[1], &table))
+    return -1;
+  c->k_scale = ks;
+  c->v_scale = vs;
+  c->block_table = table;
+  c->num_pages = k[0];
+  c->num_seqs = (int32_t)b[0];
+  c->pages_per_seq = (int32_t)b[1];
+  return 0;
+}
+/* An integer argument that the ABI takes in 32 bits. */
+static int int32_of(PyObject* o, const char* name, int32_t* out) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) return -1;
+  if (v > INT32_MAX || v < INT32_MIN) {
+    PyErr_Format(PyExc_ValueError, "%s does not fit in 32 bits", name);
+    return -1;
+  }
+  *out = (int32_t)v;
+  return 0;
+}
+
+/* dims, q, k, q_norm, k_norm, inv_freq, positions, axes, q_out, k_out, rope_scale,
+   d_status, stream */
+static PyObject* qk_norm_rope_axes(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  gdn_attn_dims d;
+  gdn_rope_params p;
+  gdn_rope_axes axes;
+  const gdn_rope_axes* ax;
+  gdn_view q, k;
+  PyObject *dt, *other;
+  int64_t total;
+  void *pos, *status, *qp = NULL, *kp = NULL;
+  gdn_stream_t s;
+  if (count(na, 13) || dims_of(a[0], &d, &dt) || axes_of(a[7], &axes, &ax) ||
+      method_int(a[6], s_numel, &total))
+    return NULL;
+  if (!ax) {
+    PyErr_SetString(PyExc_TypeError, "axes must be a gdn_rope_axes");
+    return NULL;
+  }
+  const int64_t n = per_token(ax) ? total / per_token(ax) : 0;
+  if (view(a[1], "q", dt, n, d.h_q, d.d, &q) || view(a[2], "k", dt, n, d.h_kv, d.d, &k) ||
+      rope_params(a + 3, &d, a[10], &p) ||
+      flat(a[6], "positions", t_int32, n * per_token(ax), &pos) ||
+      flat(a[11], "d_status", t_int32, 1, &status) || all_device() ||
+      stream_of(a[12], &s, &other))
+    return NULL;
+  p.d_status = status;
+  PyObject *qo = Py_NewRef(Py_None), *ko = Py_NewRef(Py_None), *r = NULL;
+  if (a[1] != Py_None) Py_SETREF(qo, output(a[8], "q_out", dt, n, d.h_q, d.d, a[1], other, &qp));
+  if (qo && a[2] != Py_None)
+    Py_SETREF(ko, output(a[9], "k_out", dt, n, d.h_kv, d.d, a[2], other, &kp));
+  if (qo && ko) {
+    const int rc = call_norm_rope_axes(&d, &p, ax, &q, &k, pos, n, qp, kp, s);
+    r = rc ? refused("gdn_qk_norm_rope_axes", rc) : PyTuple_Pack(2, qo, ko);
+  }
+  Py_XDECREF(qo);
+  Py_XDECREF(ko);
+  return r;
+}
+
+/* dims, q, k, v, q_norm, k_norm, inv_freq, positions, cache, starts, cu_seqlens, axes,
+   q_out, k_out, rope_scale, d_status, stream */
+static PyObject* kv8_append(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  gdn_attn_dims d;
+  gdn_rope_params p;
+  gdn_rope_axes axes;
+  const gdn_rope_axes* ax;
+  gdn_view q, k, v;
+  gdn_kv8_cache c;
+  PyObject *dt, *other;
+  int64_t sk[4] = {0}, seqs;
+  void *pos, *starts, *cu, *status, *qp = NULL, *kp;
+  gdn_stream_t s;
+  if (count(na, 17) || dims_of(a[0], &d, &dt) || axes_of(a[11], &axes, &ax) ||
+      shape_of(a[2], sk) < 0 || method_int(a[9], s_numel, &seqs) || fits32(seqs, "starts"))
+    return NULL;
+  const int64_t n = sk[0];
+  if (view(a[1], "q", dt, n, d.h_q, d.d, &q) || view(a[2], "k", dt, n, d.h_kv, d.d, &k) ||
+      view(a[3], "v", dt, n, d.h_kv, d.d, &v) || rope_params(a + 4, &d, a[14], &p) ||
+      flat(a[7], "positions", t_int32, n * per_token(ax), &pos) || kv8_of(a[8], "cache", &d, &c) ||
+      flat(a[9], "starts", t_int32, seqs, &starts) ||
+      flat(a[10], "cu_seqlens", t_int32, seqs + 1, &cu) ||
+      flat(a[13], "k_out", dt, n * d.h_kv * d.d, &kp) ||
+      flat(a[15], "d_status", t_int32, 1, &status) || all_device() ||
+      stream_of(a[16], &s, &other))
+    return NULL;
+  PyObject* qo = Py_NewRef(Py_None);
+  if (a[1] != Py_None) Py_SETREF(qo, output(a[12], "q_out", dt, n, d.h_q, d.d, a[1], other, &qp));
+  if (!qo) return NULL;
+  const int rc = call_kv8_append(&d, &p, ax, &q, &k, &v, pos, cu, starts, (int32_t)seqs, n, &c, qp, kp,
+                                 status, s);
+  if (!rc) return qo;
+  Py_DECREF(qo);
+  return refused("gdn_kv8_append", rc);
+}
+
+/* dims, cache, cu_seqlens, total, k_out, v_out, d_status, stream */
+static PyObject* kv8_gather(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  gdn_attn_dims d;
+  gdn_kv8_cache c;
+  PyObject *dt, *other;
+  int64_t ends;
+  void *cu, *status, *kp, *vp;
+  gdn_stream_t s;
+  if (count(na, 8) || dims_of(a[0], &d, &dt) || kv8_of(a[1], "cache", &d, &c) ||
+      method_int(a[2], s_numel, &ends) || fits32(ends, "cu_seqlens") ||
+      flat(a[2], "cu_seqlens", t_int32, ends, &cu) ||
+      flat(a[6], "d_status", t_int32, 1, &status) || all_device() || stream_of(a[7], &s, &other))
+    return NULL;
+  const int64_t total = PyLong_AsLongLong(a[3]);
+  if (total == -1 && PyErr_Occurred()) return NULL;
+  const int64_t rows = total > 0 ? total : 0;   /* the library refuses less */
+  PyObject* like = PyTuple_GET_ITEM(a[1], 0);
+  PyObject *r = NULL, *vo = NULL, *ko = output(a[4], "k_out", dt, rows, d.h_kv, d.d, like, other, &kp);
+  if (ko) vo = output(a[5], "v_out", dt, rows, d.h_kv, d.d, like, other, &vp);
+  if (vo) {
+    const int rc = call_kv8_gather(&d, &c, cu, (int32_t)(ends - 1), total, kp, vp, status, s);
+    r = rc ? refused("gdn_kv8_gather", rc) : PyTuple_Pack(2, ko, vo);
+  }
+  Py_XDECREF(ko);
+  Py_XDECREF(vo);
+  return r;
+}
+
+/* dims, q, cache, seq_lens, workspace, gate, weights, o, d_status, stream */
+static PyObject* attn_decode_kv8(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  gdn_attn_dims d;
+  gdn_view q, gate;
+  gdn_kv8_cache c;
+  PyObject *dt, *other;
+  int64_t sq[4] = {0};
+  size_t size;
+  void *lens, *weights, *status, *op, *ws;
+  gdn_stream_t s;
+  if (count(na, 10) || dims_of(a[0], &d, &dt) || shape_of(a[1], sq) < 0 || fits32(sq[0], "q") ||
+      view(a[1], "q", dt, sq[0], d.h_q, d.d, &q) || kv8_of(a[2], "cache", &d, &c) ||
+      view(a[5], "gate", dt, sq[0], d.h_q, d.d, &gate) ||
+      flat(a[3], "seq_lens", t_int32, sq[0], &lens) ||
+      flat(a[6], "weights", io_types[GDN_FP32],
+           (int64_t)c.num_seqs * d.h_kv * c.pages_per_seq * d.page_size, &weights) ||
+      flat(a[8], "d_status", t_int32, 1, &status) || workspace_of(a[4], &ws, &size) ||
+      all_device() || stream_of(a[9], &s, &other))
+    return NULL;
+  PyObject* o = output(a[7], "o", dt, sq[0], d.h_q, d.d, a[1], other, &op);
+  if (!o) return NULL;
+  const int rc =
+      call_decode_kv8(&d, &q, &c, lens, (int32_t)sq[0], &gate, weights, op, ws, size, status, s);
+  if (!rc) return o;
+  Py_DECREF(o);
+  return refused("gdn_attn_decode_kv8", rc);
+}
+
+/* dims, from, weights, seq_lens, keep, to, weights_out, first, last, new_lens, kept,
+   d_status, stream */
+static PyObject* kv8_evict(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  gdn_attn_dims d;
+  gdn_kv8_cache c, to;
+  PyObject *dt, *other;
+  int64_t n;
+  int32_t keep, first, last;
+  void *weights, *lens, *out, *status, *np, *kp;
+  gdn_stream_t s;
+  if (count(na, 13) || dims_of(a[0], &d, &dt) || kv8_of(a[1], "cache", &d, &c) ||
+      kv8_of(a[5], "to", &d, &to) || method_int(a[3], s_numel, &n) || fits32(n, "seq_lens") ||
+      flat(a[2], "weights", io_types[GDN_FP32],
+           (int64_t)c.num_seqs * d.h_kv * c.pages_per_seq * d.page_size, &weights) ||
+      flat(a[6], "weights_out", io_types[GDN_FP32],
+           (int64_t)to.num_seqs * d.h_kv * to.pages_per_seq * d.page_size, &out) ||
+      flat(a[3], "seq_lens", t_int32, n, &lens) || int32_of(a[4], "keep", &keep) ||
+      int32_of(a[7], "first", &first) || int32_of(a[8], "last", &last) ||
+      flat(a[11], "d_status", t_int32, 1, &status) || all_device() || stream_of(a[12], &s, &other))
+    return NULL;
+  const int64_t rows = keep > 0 ? keep : 0;   /* the library refuses less */
+  PyObject *r = NULL, *ko = NULL, *size = Py_BuildValue("(L)", (long long)n);
+  PyObject* no = shaped(a[9], "new_lens", t_int32, size, n, a[3], other, &np);
+  Py_XDECREF(size);
+  if (no) ko = output(a[10], "kept", t_int32, n, d.h_kv, rows, a[3], other, &kp);
+  if (ko) {
+    const int rc = call_kv8_evict(&d, &c, weights, lens, (int32_t)n, keep, first, last, &to, out, np, kp,
+                                  status, s);
+    r = rc ? refused("gdn_kv8_evict", rc) : PyTuple_Pack(2, no, ko);
+  }
+  Py_XDECREF(no);
+  Py_XDECREF(ko);
+  return r;
+}
+
+/* After setup: float8_e4m3fn, the entry points' addresses. */
+static PyObject* setup_kv8(PyObject* self, PyObject* args) {
+  (void)self;
+  unsigned long long fn[5];
+  if (!PyArg_ParseTuple(args, "O(KKKKK)", &t_e4m3, &fn[0], &fn[1], &fn[2], &fn[3], &fn[4]))
+    return NULL;
+  Py_INCREF(t_e4m3);
+  call_norm_rope_axes = (norm_rope_axes_fn)(uintptr_t)fn[0];
+  call_kv8_append = (kv8_append_fn)(uintptr_t)fn[1];
+  call_kv8_gather = (kv8_gather_fn)(uintptr_t)fn[2];
+  call_decode_kv8 = (decode_kv8_fn)(uintptr_t)fn[3];
+  call_kv8_evict = (kv8_evict_fn)(uintptr_t)fn[4];
+  Py_RETURN_NONE;
 }
 
 /* (float32, bfloat16, float16), int32, float64, torch.empty, empty(size, dtype, device,
@@ -459,6 +755,12 @@ static PyMethodDef methods[] = {
     {"kv_append", (PyCFunction)(void (*)(void))kv_append, METH_FASTCALL, NULL},
     {"attn_prefill", (PyCFunction)(void (*)(void))attn_prefill, METH_FASTCALL, NULL},
     {"attn_decode", (PyCFunction)(void (*)(void))attn_decode, METH_FASTCALL, NULL},
+    {"setup_kv8", setup_kv8, METH_VARARGS, NULL},
+    {"qk_norm_rope_axes", (PyCFunction)(void (*)(void))qk_norm_rope_axes, METH_FASTCALL, NULL},
+    {"kv8_append", (PyCFunction)(void (*)(void))kv8_append, METH_FASTCALL, NULL},
+    {"kv8_gather", (PyCFunction)(void (*)(void))kv8_gather, METH_FASTCALL, NULL},
+    {"attn_decode_kv8", (PyCFunction)(void (*)(void))attn_decode_kv8, METH_FASTCALL, NULL},
+    {"kv8_evict", (PyCFunction)(void (*)(void))kv8_evict, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls",
                                     "Marshalling of the full-attention calls.", -1, methods,

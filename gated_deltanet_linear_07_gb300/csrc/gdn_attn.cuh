@@ -162,7 +162,7 @@ __device__ __forceinline__ float gate_sigmoid(float x) {
 }  // namespace attn
 }  // namespace gdn
 
-// One call of gdn_qk_norm_rope or gdn_kv_append.
+// One call of gdn_qk_norm_rope, gdn_qk_norm_rope_axes or gdn_kv_append.
 struct GdnRopeArgs {
   gdn_view q, k, v;            // null data: left out (v: no append)
   void* q_out;
@@ -179,6 +179,7 @@ struct GdnRopeArgs {
   int32_t withhold;            // GDN_TEST_WAIT_TIMEOUT: one unit's copies never come
   int32_t h_q, h_kv, d, rot_dim, interleaved, page_shift;
   float eps, rope_scale;
+  gdn_rope_axes axes;          // count 0: one axis; else positions [count][n]
 };
 
 // One attention call; the prefix pass of gdn_attn_decode uses the same kernel

@@ -1,0 +1,562 @@
+// gdn_kv8.cu -- the paged cache held in 8 bits: new tokens go in (normed, rotated
+// and quantised on the way), cached tokens come out packed, and the kept tokens
+// of a sequence move to other pages.  (gdn_kv8_decode.cu is the attention.)
+//
+// A block is KV8_BLOCK = 16 tokens of one head; its largest value decides its scale, a
+// power of two.  A number of t bits of mantissa and a floating point is rounded to
+// the same relative error under any scale that keeps it out of the subnormals, so
+// powers of two lose nothing, and a scale that grows (a later token with a larger
+// value) divides what the block holds by a power of two: exactly but for the
+// subnormals.  Everything here is bound by the bytes that it moves.
+#include "gdn_attn_device.cuh"
+#include "gdn_kv8.cuh"
+#include "gdn_rope.cuh"
+
+namespace gdn {
+namespace attn {
+
+// ---- which rows a CTA has ------------------------------------------------------
+
+// Rows of one sequence that go to one block.
+struct Run {
+  int64_t t0;      // first row of the call
+  int64_t place;   // its place in the sequence; < 0: padding rows
+  int32_t b, rows;
+};
+
+// Run number `index` of packed sequences, by the whole CTA (WARPS warps); false: there
+// is none, or cu is not a sequence of ends (reported).  starts null: places count from
+// 0.  The runs before it are counted sequence by sequence, in one pass over cu that
+// checks it too.
+template <int WARPS>
+__device__ __forceinline__ bool find_run(const int32_t* cu, const int32_t* starts, int num_seqs,
+                                         int64_t n, int64_t index, int32_t* d_status, Run& run) {
+  __shared__ int64_t sums[WARPS];
+  __shared__ Run found;
+  if (!cu) {   // a row of its own for every sequence
+    run = {index, (int64_t)starts[index], (int32_t)index, 1};
+    return true;
+  }
+  if (threadIdx.x == 0) found.rows = 0;
+  bool bad = cu[0] != 0 || cu[num_seqs] != n;
+  int64_t seen = 0;
+  for (int base = 0; base < num_seqs; base += 32 * WARPS) {
+    const int b = base + threadIdx.x;
+    int64_t c0 = 0, len = 0, count = 0;
+    int32_t start = 0;
+    if (b < num_seqs) {
+      c0 = cu[b];
+      len = (int64_t)cu[b + 1] - c0;
+      start = starts ? starts[b] : 0;
+      bad |= len < 0;
+    }
+    const int r = start < 0 ? 0 : start % KV8_BLOCK;
+    if (len > 0) count = (r + len + KV8_BLOCK - 1) / KV8_BLOCK;
+    int64_t before;
+    const int64_t all = block_scan(count, sums, WARPS, before);
+    const int64_t mine = index - seen - before;
+    if (mine >= 0 && mine < count) {
+      const int64_t i0 = max(mine * KV8_BLOCK - r, (int64_t)0);
+      const int64_t i1 = min(mine * KV8_BLOCK - r + KV8_BLOCK, len);
+      found = {c0 + i0, start < 0 ? -1 : start + i0, b, (int32_t)(i1 - i0)};
+    }
+    seen += all;
+  }
+  if (__syncthreads_or(bad)) {
+    if (index == 0 && threadIdx.x == 0) set_status(d_status, GDN_DEV_BAD_CU_SEQLENS);
+    return false;
+  }
+  run = found;
+  return run.rows > 0;
+}
+
+// Page of a sequence's block that starts at or before `place` (uniform over the
+// CTA); < 0: none, and reported.
+__device__ __forceinline__ int64_t page_of(const gdn_kv8_cache& c, int page_shift, int b,
+                                           int64_t place, int32_t* d_status) {
+  const int64_t pg = place >> page_shift;
+  if (pg >= c.pages_per_seq) {
+    set_status(d_status, GDN_DEV_BAD_LENGTH);
+    return -1;
+  }
+  const int32_t page = __ldg(c.block_table + (int64_t)b * c.pages_per_seq + pg);
+  if (page < 0 || page >= c.num_pages) {
+    set_status(d_status, GDN_DEV_BAD_PAGE);
+    return -1;
+  }
+  return page;
+}
+
+// Most runs that n rows of num_seqs sequences can be: each may start and end inside a block.
+static int64_t most_runs(int64_t n, int64_t num_seqs) {
+  const int64_t most = n / KV8_BLOCK + 2 * num_seqs;
+  return most < n ? most : n;
+}
+
+// ---- append --------------------------------------------------------------------
+
+// A CTA has one run, of up to 16 rows, and forms its rows' cosines and sines once.  A tile
+// is a run's rows of one head (q, k or v), by a team of TEAM threads: eight channels
+// per lane, D / 8 lanes per row, the rows at their slots of the block, so that what
+// the block held before lies in the lanes of its own slots.
+constexpr int TEAM = 128, TEAMS = 2, APPEND_THREADS = TEAM * TEAMS;
+
+__device__ __forceinline__ void team_bar(int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TEAM) : "memory");
+}
+
+template <typename IO, int D>
+__global__ void __launch_bounds__(APPEND_THREADS)
+    kv8_append_kernel(const __grid_constant__ GdnKv8AppendArgs p) {
+  constexpr int N = KV8_BLOCK * (D / 8) / TEAM;   // rows of a lane
+  constexpr int CS = D / 2 * 3;
+  extern __shared__ __align__(16) float cs[];     // [slot][cosines, sines, negated sines]
+  __shared__ uint64_t fraction[D / 2];
+  __shared__ float red[2][TEAMS][TEAM / 32];
+  const GdnRopeArgs& a = p.r;
+  const int tid = threadIdx.x, team = tid / TEAM, tt = tid % TEAM, lane = tid & 31;
+  const int half = a.rot_dim / 2;
+  for (int i = tid; i < half; i += APPEND_THREADS) fraction[i] = turn_fraction(a.inv_freq[i]);
+  Run run;
+  if (!find_run<APPEND_THREADS / 32>(p.cu, p.starts, p.num_seqs, a.n, blockIdx.x, a.d_status, run))
+    return;
+  __syncthreads();
+  const bool padding = run.place < 0;
+  const int r = padding ? 0 : (int)(run.place % KV8_BLOCK);   // the first row's slot
+  const int64_t page =
+      padding ? -1 : page_of(p.cache, a.page_shift, run.b, run.place, a.d_status);
+  if (half > 0) {
+    const int per = APPEND_THREADS / half, u0 = tid / half, i = tid - u0 * half;
+    if (u0 < per) {
+      const int32_t* pos = a.positions + (a.axes.count ? a.axes.pair[i] * a.n : 0) + run.t0;
+      for (int u = u0; u < run.rows; u += per)
+        put_angle<IO, D>(cs + (r + u) * CS, i, pos[u], fraction[i], a.rope_scale);
+    }
+  }
+  __syncthreads();
+
+  const LanePlace<D> at(a);
+  const int slot0 = tt / (D / 8) * N;          // of this lane's rows
+  const int nq = a.q.data ? a.h_q : 0, tiles = nq + 2 * a.h_kv;
+  const int block = padding ? 0 : (int)(run.place & ((1 << a.page_shift) - 1)) / KV8_BLOCK;
+  const int step = TEAMS * gridDim.y;
+  auto load = [&](int tile, Vec8<IO> (&x)[N]) {
+    const gdn_view& v = tile < nq ? a.q : tile < nq + a.h_kv ? a.k : a.v;
+    const int head = tile < nq ? tile : (tile - nq) % a.h_kv;
+    const IO* src = reinterpret_cast<const IO*>(v.data) + run.t0 * v.token_stride +
+                    head * v.head_stride + 8 * at.part;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int row = slot0 + u - r;
+      if (row >= 0 && row < run.rows && !padding)
+        x[u].load(src + row * v.token_stride);
+      else
+        x[u].w = make_uint4(0, 0, 0, 0);
+    }
+  };
+  Vec8<IO> x[N];
+  int tile = blockIdx.y * TEAMS + team;
+  if (tile < tiles) load(tile, x);
+  for (int it = 0; tile < tiles; ++it) {
+    const bool is_q = tile < nq, is_v = tile >= nq + a.h_kv;
+    const int head = is_q ? tile : (tile - nq) % a.h_kv;
+    uint64_t y[N][4];
+    if (is_v) {
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        float f[8];
+        x[u].get(f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[u][i] = pk(f[2 * i], f[2 * i + 1]);
+      }
+    } else {
+      const float* wp = is_q ? a.q_norm : a.k_norm;
+      float4 wt[2] = {};
+      if (wp) {
+        wt[0] = __ldg(reinterpret_cast<const float4*>(wp + 8 * at.part));
+        wt[1] = __ldg(reinterpret_cast<const float4*>(wp + 8 * at.part + 4));
+      }
+      norm_rotate_fp32<IO, D, N>(at, N, wp != nullptr, a.interleaved, half > 0, a.eps, wt,
+                                 cs + slot0 * CS, x, y);
+    }
+    const int next = tile + step;
+    if (next < tiles) load(next, x);
+    // the packed rows
+    IO* out = reinterpret_cast<IO*>(is_q ? a.q_out : is_v ? nullptr : a.k_out);
+    if (out) {
+      const int heads = is_q ? a.h_q : a.h_kv;
+      out += (run.t0 * heads + head) * D + 8 * at.part;
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const int row = slot0 + u - r;
+        if (row < 0 || row >= run.rows) continue;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpk(y[u][i], f[2 * i], f[2 * i + 1]);
+        Vec8<IO> w;
+        w.set(f);
+        if (padding) w.w = make_uint4(0, 0, 0, 0);
+        w.store(out + (int64_t)row * heads * D);
+      }
+    }
+    if (!is_q && page >= 0) {   // the same for the whole team
+      const int64_t first = (page * a.h_kv + head) << a.page_shift;
+      float* sp = (is_v ? p.cache.v_scale : p.cache.k_scale) + first / KV8_BLOCK + block;
+      unsigned char* codes = reinterpret_cast<unsigned char*>(is_v ? p.cache.v : p.cache.k) +
+                             (first + block * KV8_BLOCK) * D + 8 * at.part;
+      const float held = r > 0 ? *sp : 0.f;
+      float top = 0.f;
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const int row = slot0 + u - r;
+        if (row < 0 || row >= run.rows) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float f0, f1;
+          unpk(y[u][i], f0, f1);
+          f0 = fabsf(f0);
+          f1 = fabsf(f1);
+          if (f0 < INFINITY) top = fmaxf(top, f0);
+          if (f1 < INFINITY) top = fmaxf(top, f1);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) red[it & 1][team][tt >> 5] = top;
+      team_bar(team);
+#pragma unroll
+      for (int i = 0; i < TEAM / 32; ++i) top = fmaxf(top, red[it & 1][team][i]);
+      const int e = kv8_exponent(top);
+      float scale = pow2(e), inv = pow2(-e);
+      if (kv8_scale_ok(held)) {
+        if (held >= scale) {
+          scale = held;
+          inv = 1.0f / held;
+        } else {   // what the block holds already, at the new scale
+          const float f = held * inv;
+#pragma unroll
+          for (int u = 0; u < N; ++u)
+            if (slot0 + u < r) {
+              uint2* w = reinterpret_cast<uint2*>(codes + (slot0 + u) * D);
+              const uint2 old = *w;
+              const float4 lo = from_e4m3x4(old.x), hi = from_e4m3x4(old.y);
+              *w = make_uint2(to_e4m3x4(lo.x * f, lo.y * f, lo.z * f, lo.w * f),
+                              to_e4m3x4(hi.x * f, hi.y * f, hi.z * f, hi.w * f));
+            }
+        }
+      }
+      if (tt == 0) *sp = scale;
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const int row = slot0 + u - r;
+        if (row < 0 || row >= run.rows) continue;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpk(y[u][i], f[2 * i], f[2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = fabsf(f[i]) < INFINITY ? f[i] * inv : NAN;
+        *reinterpret_cast<uint2*>(codes + (slot0 + u) * D) = make_uint2(
+            to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
+      }
+    }
+    tile = next;
+  }
+}
+
+template <typename IO, int D>
+static cudaError_t launch_append_d(const GdnKv8AppendArgs& a, cudaStream_t s) {
+  const int64_t runs = a.cu ? most_runs(a.r.n, a.num_seqs) : a.r.n;
+  const int tiles = (a.r.q.data ? a.r.h_q : 0) + 2 * a.r.h_kv;
+  // few runs: their tiles over several CTAs
+  const int most = (tiles + TEAMS - 1) / TEAMS;
+  int split = 1;
+  while (split < most && runs * split < 8 * SMS) ++split;
+  const size_t smem = a.r.rot_dim > 0 ? KV8_BLOCK * (D / 2 * 3) * sizeof(float) : 0;
+  kv8_append_kernel<IO, D>
+      <<<dim3((unsigned)runs, (unsigned)split), APPEND_THREADS, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+// ---- gather ---------------------------------------------------------------------
+
+constexpr int GATHER_THREADS = 256;
+
+// Sixteen numbers of a row: one 16-byte load, two 16-byte stores.
+template <typename IO>
+__device__ __forceinline__ void put_sixteen(IO* dst, uint4 w, float scale) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 v = from_e4m3x4(u[2 * h + i]);
+      f[4 * i] = v.x * scale;
+      f[4 * i + 1] = v.y * scale;
+      f[4 * i + 2] = v.z * scale;
+      f[4 * i + 3] = v.w * scale;
+    }
+    Vec8<IO> o;
+    o.set(f);
+    o.store(dst + 8 * h);
+  }
+}
+
+template <typename IO, int D>
+__global__ void __launch_bounds__(GATHER_THREADS)
+    kv8_gather_kernel(const __grid_constant__ GdnKv8GatherArgs p) {
+  constexpr int PARTS = D / 16, TILE = KV8_BLOCK * PARTS, UNROLL = 4;
+  Run run;
+  if (!find_run<GATHER_THREADS / 32>(p.cu, nullptr, p.num_seqs, p.total, blockIdx.x, p.d_status,
+                                     run))
+    return;
+  const int64_t page = page_of(p.cache, p.page_shift, run.b, run.place, p.d_status);
+  const int block = (int)(run.place & ((1 << p.page_shift) - 1)) / KV8_BLOCK;
+  const int kinds = (p.k_out ? 1 : 0) + (p.v_out ? 1 : 0), all = TILE * p.h_kv * kinds;
+  for (int base = threadIdx.x; base < all; base += UNROLL * GATHER_THREADS) {
+    uint4 w[UNROLL];
+    float scale[UNROLL];
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) {
+      const int i = base + j * GATHER_THREADS, tile = i / TILE, row = i % TILE / PARTS;
+      w[j] = make_uint4(0, 0, 0, 0);
+      scale[j] = 0.f;
+      if (i >= all || row >= run.rows || page < 0) continue;
+      const int head = tile % p.h_kv;
+      const bool is_v = !p.k_out || tile >= p.h_kv;
+      const int64_t first = (page * p.h_kv + head) << p.page_shift;
+      w[j] = __ldcs(reinterpret_cast<const uint4*>(
+          reinterpret_cast<const unsigned char*>(is_v ? p.cache.v : p.cache.k) +
+          (first + block * KV8_BLOCK + row) * D + i % PARTS * 16));
+      scale[j] = __ldg((is_v ? p.cache.v_scale : p.cache.k_scale) + first / KV8_BLOCK + block);
+    }
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) {
+      const int i = base + j * GATHER_THREADS, tile = i / TILE, row = i % TILE / PARTS;
+      if (i >= all || row >= run.rows) continue;
+      const int head = tile % p.h_kv;
+      const bool is_v = !p.k_out || tile >= p.h_kv;
+      put_sixteen<IO>(reinterpret_cast<IO*>(is_v ? p.v_out : p.k_out) +
+                          ((run.t0 + row) * p.h_kv + head) * D + i % PARTS * 16,
+                      w[j], scale[j]);
+    }
+  }
+}
+
+template <typename IO, int D>
+static cudaError_t launch_gather_d(const GdnKv8GatherArgs& a, cudaStream_t s) {
+  kv8_gather_kernel<IO, D>
+      <<<(unsigned)most_runs(a.total, a.num_seqs), GATHER_THREADS, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// ---- evict ----------------------------------------------------------------------
+
+constexpr int SELECT_THREADS = 512, SELECT_WARPS = SELECT_THREADS / 32;
+constexpr int RADIX = 256;
+
+// A weight's rank as an unsigned number: bits of a float that is not negative.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  return __float_as_uint(fmaxf(w, 0.f)) & 0x7fffffffu;   // NaN: 0
+}
+
+__device__ __forceinline__ int64_t evict_len(const GdnKv8EvictArgs& p, int b) {
+  const int64_t cap = (int64_t)p.from.pages_per_seq << p.page_shift;
+  int64_t len = max(p.seq_lens[b], 0);
+  if (len > cap) {
+    set_status(p.d_status, GDN_DEV_BAD_LENGTH);
+    len = cap;
+  }
+  return len;
+}
+
+// The places of one sequence and head that are kept.  The m-th largest weight of the
+// middle is found digit by digit, eight bits at a time from the top (a histogram of
+// those that share the digits so far), then one ordered pass writes the places: all
+// above that weight and, of those equal to it, the lowest.
+__global__ void __launch_bounds__(SELECT_THREADS)
+    kv8_select_kernel(const __grid_constant__ GdnKv8EvictArgs p) {
+  __shared__ uint32_t hist[SELECT_WARPS][RADIX];
+  __shared__ uint32_t s_digit, s_above;
+  __shared__ int64_t sums[SELECT_WARPS];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int b = blockIdx.x / p.h_kv, j = blockIdx.x % p.h_kv;
+  const int64_t cap = (int64_t)p.from.pages_per_seq << p.page_shift;
+  const int64_t cap_to = (int64_t)p.to.pages_per_seq << p.page_shift;
+  const int64_t len = evict_len(p, b), now = min(len, (int64_t)p.keep);
+  const float* w = p.weights + ((int64_t)b * p.h_kv + j) * cap;
+  float* w_out = p.weights_out ? p.weights_out + ((int64_t)b * p.h_kv + j) * cap_to : nullptr;
+  int32_t* kept = p.kept + ((int64_t)b * p.h_kv + j) * p.keep;
+  if (j == 0 && tid == 0) p.new_lens[b] = (int32_t)now;
+  for (int64_t i = now + tid; i < p.keep; i += SELECT_THREADS) kept[i] = -1;
+  if (w_out)
+    for (int64_t i = now + tid; i < cap_to; i += SELECT_THREADS) w_out[i] = 0.f;
+  if (len <= p.keep) {
+    for (int64_t i = tid; i < len; i += SELECT_THREADS) {
+      kept[i] = (int32_t)i;
+      if (w_out) w_out[i] = w[i];
+    }
+    return;
+  }
+  const int64_t lo = p.first, hi = len - p.last;   // the middle; longer than what it keeps
+  uint32_t want = (uint32_t)(p.keep - p.first - p.last);   // of those that share the digits so far
+  uint32_t prefix = 0;
+  if (want > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      for (int i = tid; i < SELECT_WARPS * RADIX; i += SELECT_THREADS) (&hist[0][0])[i] = 0;
+      __syncthreads();
+      for (int64_t i = lo + tid; i < hi; i += SELECT_THREADS) {
+        const uint32_t key = weight_key(w[i]);
+        if (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8))
+          atomicAdd(&hist[warp][key >> shift & (RADIX - 1)], 1u);
+      }
+      __syncthreads();
+      // digits from the top: thread t has digit 255 - t
+      uint32_t count = 0;
+      if (tid < RADIX)
+        for (int v = 0; v < SELECT_WARPS; ++v) count += hist[v][RADIX - 1 - tid];
+      int64_t before;
+      block_scan(count, sums, SELECT_WARPS, before);
+      if (tid < RADIX && before < want && before + count >= want) {
+        s_digit = RADIX - 1 - tid;
+        s_above = (uint32_t)before;
+      }
+      __syncthreads();
+      prefix |= s_digit << shift;
+      want -= s_above;
+      __syncthreads();
+    }
+  } else {
+    prefix = 0xffffffffu;   // above every weight
+  }
+  // in order: the counts of the kept ones (upper half) and of those equal to the border
+  int64_t seen = 0;
+  for (int64_t base = 0; base < len; base += SELECT_THREADS) {
+    const int64_t i = base + tid;
+    bool sure = false, tie = false;
+    if (i < len) {
+      const uint32_t key = i >= lo && i < hi ? weight_key(w[i]) : 0;
+      sure = i < lo || i >= hi || key > prefix;
+      tie = !sure && key == prefix;
+    }
+    int64_t before;
+    const int64_t all =
+        block_scan(((int64_t)sure << 32) | (int64_t)tie, sums, SELECT_WARPS, before);
+    before += seen;
+    seen += all;
+    const uint32_t ties = (uint32_t)before;
+    if (sure || (tie && ties < want)) {
+      const int64_t at = (before >> 32) + min(ties, want);
+      kept[at] = (int32_t)i;
+      if (w_out) w_out[at] = w[i];
+    }
+  }
+}
+
+constexpr int MOVE_WARPS = 8;
+
+// One warp per (sequence, head, block of the new pages, keys or values): up to 16
+// kept rows from wherever they were.
+template <int D>
+__global__ void __launch_bounds__(32 * MOVE_WARPS)
+    kv8_move_kernel(const __grid_constant__ GdnKv8EvictArgs p) {
+  constexpr int PARTS = D / 16, PASS = 32 / PARTS, N = KV8_BLOCK / PASS;   // rows of a pass, passes
+  const int lane = threadIdx.x & 31;
+  const int blocks = (p.keep + KV8_BLOCK - 1) / KV8_BLOCK;
+  const int64_t unit = (int64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
+  if (unit >= (int64_t)p.n * p.h_kv * blocks * 2) return;
+  const bool is_v = unit & 1;
+  const int64_t item = (unit >> 1) / blocks;
+  const int block = (int)((unit >> 1) % blocks);
+  const int b = (int)(item / p.h_kv), j = (int)(item % p.h_kv);
+  // each of the first 16 lanes looks up one row
+  int64_t row = -1;
+  float scale = 0.f;
+  const int i = block * KV8_BLOCK + lane;
+  if (lane < KV8_BLOCK && i < p.keep) {
+    const int32_t place = p.kept[item * p.keep + i];
+    if (place >= 0) {
+      const int64_t page = page_of(p.from, p.page_shift, b, place, p.d_status);
+      if (page >= 0) {
+        row = ((page * p.h_kv + j) << p.page_shift) + (place & ((1 << p.page_shift) - 1));
+        scale = (is_v ? p.from.v_scale : p.from.k_scale)[row / KV8_BLOCK];
+      }
+    }
+  }
+  if (!__any_sync(0xffffffffu, row >= 0)) return;
+  const int64_t page =
+      page_of(p.to, p.page_shift, b, (int64_t)block * KV8_BLOCK, p.d_status);
+  if (page < 0) return;
+  const int64_t to = ((page * p.h_kv + j) << p.page_shift) +
+                     (block * KV8_BLOCK & ((1 << p.page_shift) - 1));
+  const unsigned char* src = reinterpret_cast<const unsigned char*>(is_v ? p.from.v : p.from.k);
+  unsigned char* dst = reinterpret_cast<unsigned char*>(is_v ? p.to.v : p.to.k) + to * D;
+  uint4 x[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int64_t at = __shfl_sync(0xffffffffu, row, u * PASS + lane / PARTS);
+    if (at >= 0) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + at * D + lane % PARTS * 16));
+  }
+  float top = scale;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top = __shfl_sync(0xffffffffu, top, 0);
+  const float ratio = top > 0.f ? scale / top : 1.f;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int s = u * PASS + lane / PARTS;
+    const int64_t at = __shfl_sync(0xffffffffu, row, s);
+    const float f = __shfl_sync(0xffffffffu, ratio, s);
+    if (at < 0) continue;
+    if (f != 1.f) {
+      uint32_t* v = reinterpret_cast<uint32_t*>(&x[u]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 y = from_e4m3x4(v[e]);
+        v[e] = to_e4m3x4(y.x * f, y.y * f, y.z * f, y.w * f);
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + s * D + lane % PARTS * 16) = x[u];
+  }
+  if (lane == 0) (is_v ? p.to.v_scale : p.to.k_scale)[to / KV8_BLOCK] = top;
+}
+
+template <int D>
+static cudaError_t launch_move_d(const GdnKv8EvictArgs& a, cudaStream_t s) {
+  const int64_t units = (int64_t)a.n * a.h_kv * ((a.keep + KV8_BLOCK - 1) / KV8_BLOCK) * 2;
+  const int64_t ctas = (units + MOVE_WARPS - 1) / MOVE_WARPS;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  kv8_move_kernel<D><<<(unsigned)ctas, 32 * MOVE_WARPS, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename IO>
+static cudaError_t launch_append_io(const GdnKv8AppendArgs& a, cudaStream_t s) {
+  return a.r.d == 64 ? launch_append_d<IO, 64>(a, s)
+                     : a.r.d == 128 ? launch_append_d<IO, 128>(a, s) : launch_append_d<IO, 256>(a, s);
+}
+template <typename IO>
+static cudaError_t launch_gather_io(const GdnKv8GatherArgs& a, cudaStream_t s) {
+  return a.d == 64 ? launch_gather_d<IO, 64>(a, s)
+                   : a.d == 128 ? launch_gather_d<IO, 128>(a, s) : launch_gather_d<IO, 256>(a, s);
+}
+
+}  // namespace attn
+}  // namespace gdn
+
+cudaError_t gdn_launch_kv8_append(const GdnKv8AppendArgs& a, int io, cudaStream_t s) {
+  using namespace gdn::attn;
+  return io == GDN_BF16 ? launch_append_io<__nv_bfloat16>(a, s) : launch_append_io<__half>(a, s);
+}
+cudaError_t gdn_launch_kv8_gather(const GdnKv8GatherArgs& a, int io, cudaStream_t s) {
+  using namespace gdn::attn;
+  return io == GDN_BF16 ? launch_gather_io<__nv_bfloat16>(a, s) : launch_gather_io<__half>(a, s);
+}
+cudaError_t gdn_launch_kv8_evict(const GdnKv8EvictArgs& a, cudaStream_t s) {
+  using namespace gdn::attn;
+  kv8_select_kernel<<<(unsigned)(a.n * a.h_kv), SELECT_THREADS, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return a.d == 64 ? launch_move_d<64>(a, s)
+                   : a.d == 128 ? launch_move_d<128>(a, s) : launch_move_d<256>(a, s);
+}

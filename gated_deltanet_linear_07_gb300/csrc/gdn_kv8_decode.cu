@@ -1,0 +1,910 @@
+// gdn_kv8_decode.cu -- one query token per sequence against the cache held in 8
+// bits.  With k8, v8 the stored numbers and a, b their blocks' scales,
+//
+//   s_p = c a_p (q . k8_p),   o = sum_p 2^(s_p - M) b_p v8_p / sum_p 2^(s_p - M).
+//
+// Every cached byte is used for one token's few query heads only, so the reads of the
+// cache bound it; at half the bytes per key, what a key costs to compute has half the time.
+// The products therefore have the keys, and the channels of the values, on the
+// 16-row side of mma.sync m16n8k16 and the query heads on its 8-row side: S^T = K Q^T
+// and O^T = V^T P^T, half the instructions and half the exponentials of the
+// other way round for up to 8 heads.  An e4m3 number is an fp16 number: one conversion of
+// two numbers per register pair, no scale applied to any of them.  K's fragments
+// come straight from ldmatrix of bytes, with the channels of a 16-byte chunk in an order that
+// Q's share (a sum does not mind); V's from its transposing form, two keys' bytes
+// put side by side by one permutation.  P^T passes from the accumulators' layout
+// to the operand's by a transpose between lanes.
+//
+// Two references per head: M for the sum of the weights, and M' for the largest
+// contribution s_p + log2 b_p, by which the weights are scaled for the product with v
+// in fp16: blocks of large and small values may follow each other in any order
+// without either leaving fp16's range unless it is negligible beside the other.
+//
+// The work is cut by bytes: all units of 128 keys of all (sequence, key/value head)
+// items form one line, which the resident CTAs share in equal runs.  A run that
+// covers an item writes its output; an item cut by a run's border leaves
+// partial results that the merge kernel joins (the borders follow from seq_lens
+// alone).  Few keys in all: a cluster of CTAs per item, joined through distributed shared
+// memory, no second launch.  Within a CTA one warp keeps TMA loads in flight, eight warps
+// take one block of 16 keys of each unit, with one scale each for K and V.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "gdn_attn_device.cuh"
+#include "gdn_kv8.cuh"
+
+namespace gdn {
+namespace attn {
+
+using namespace gdn::tc;
+
+constexpr int K8_KEYS = 128;             // keys per unit
+constexpr int K8_WARPS = 8;              // consumer warps, one block of 16 keys of a unit each
+constexpr int K8_THREADS = 32 * (K8_WARPS + 1);
+constexpr int K8_MAX_STAGES = 8;
+constexpr int K8_FEW_UNITS = 4;
+static_assert(K8_KEYS == K8_WARPS * KV8_BLOCK, "a warp's keys are one block");
+
+// NT: query heads of an item in eights.
+template <int D, int NT>
+struct K8Cfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr uint32_t TILE = K8_KEYS * D;            // one of K, V
+  static constexpr uint32_t STAGE = 2 * TILE;
+  static constexpr uint32_t OBUF = ROWS * D * 4;           // joining the warps' O
+  // Q's fragments in registers, unless they and O do not fit there.
+  static constexpr bool Q_REGS = NT * D <= 256;
+  static constexpr uint32_t QBUF = Q_REGS ? 0 : D / 16 * NT * 32 * 8;
+  static constexpr uint32_t HEAD = (3072 + OBUF + QBUF + 1023) / 1024 * 1024;
+  static constexpr int PER_SM = D == 256 ? 1 : 2;
+  static constexpr int CTAS = SMS * PER_SM;
+  static constexpr int FIT = (int)((233472u / PER_SM - 1024u - HEAD) / STAGE);
+  static constexpr int STAGES = FIT < K8_MAX_STAGES ? FIT : K8_MAX_STAGES;
+  static constexpr uint32_t SMEM = HEAD + STAGES * STAGE;
+  static_assert(STAGES >= 2, "a unit in flight beside the one in use");
+};
+
+struct __align__(16) K8Shared {
+  uint64_t full[K8_MAX_STAGES], empty[K8_MAX_STAGES];
+  float scale[K8_MAX_STAGES][2 * K8_WARPS];   // of the unit's blocks: keys', values'
+  float m[K8_WARPS][16], l[K8_WARPS][16];
+  float2 ml[16];         // of the whole CTA, for its cluster
+  int64_t sum[K8_WARPS + 1], found_first;
+  int32_t found;
+};
+static_assert(sizeof(K8Shared) <= 3072, "shared bookkeeping");
+
+struct K8Args {
+  GdnKv8DecodeArgs a;
+  int32_t rows;          // query heads per item, <= 8 NT
+  int32_t subs;          // items per (sequence, key/value head)
+  int32_t box_rows;      // rows per TMA box
+  int32_t ctas;          // CTAs that share the units
+  int32_t cluster;       // CTAs per item (the form for few keys; 0: runs of units)
+  int32_t merge_rows;    // rows of an item that a CTA of the merge joins
+};
+
+__device__ __forceinline__ int64_t k8_len(const K8Args& p, int b) {
+  int64_t len = p.a.seq_lens[b];
+  if (len > p.a.capacity) {
+    set_status(p.a.d_status, GDN_DEV_BAD_LENGTH);
+    len = p.a.capacity;
+  }
+  return len > 0 ? len : 0;
+}
+__device__ __forceinline__ int64_t units_of(int64_t keys) { return (keys + K8_KEYS - 1) / K8_KEYS; }
+
+// Run c of the line is [start(c), start(c + 1)).
+struct K8Line {
+  int64_t units;
+  int ctas;
+  __device__ __forceinline__ K8Line(int64_t n, int most) : units(n), ctas(n < most ? (int)n : most) {}
+  __device__ __forceinline__ int64_t start(int c) const { return units * c / ctas; }
+  // The CTA whose run holds unit u: the last whose run starts at or before it.
+  __device__ __forceinline__ int owner(int64_t u) const {
+    return (int)(((u + 1) * ctas - 1) / units);
+  }
+};
+
+// First query head and number of query heads of item hs of a sequence.
+template <int NT>
+__device__ __forceinline__ int k8_head(const K8Args& p, int hs) {
+  return hs / p.subs * (p.a.h_q / p.a.h_kv) + hs % p.subs * (8 * NT);
+}
+template <int NT>
+__device__ __forceinline__ int k8_rows(const K8Args& p, int hs) {
+  return min(p.rows, p.a.h_q / p.a.h_kv - hs % p.subs * (8 * NT));
+}
+
+// Four channels of a finished output: y / l, gated (zeros where no key was seen).
+template <typename IO, int D>
+__device__ __forceinline__ void k8_put_four(const GdnKv8DecodeArgs& a, int b, int h, int col, float l,
+                                            float (&y)[4]) {
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] *= inv;
+  if (a.gate.data && l != 0.f) {
+    const uint2 g = *reinterpret_cast<const uint2*>(reinterpret_cast<const IO*>(a.gate.data) +
+                                                    (int64_t)b * a.gate.token_stride +
+                                                    h * a.gate.head_stride + col);
+    const float2 g0 = unpack2<IO>(g.x), g1 = unpack2<IO>(g.y);
+    y[0] *= gate_sigmoid(g0.x);
+    y[1] *= gate_sigmoid(g0.y);
+    y[2] *= gate_sigmoid(g1.x);
+    y[3] *= gate_sigmoid(g1.y);
+  }
+  *reinterpret_cast<uint2*>(reinterpret_cast<IO*>(a.o) + ((int64_t)b * a.h_q + h) * D + col) =
+      make_uint2(pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3]));
+}
+
+// The run [w, end) of units, item by item.
+struct K8Segment {
+  int b, hs;             // sequence, and key/value head * subs + sub
+  int64_t keys;          // of the sequence
+  int64_t t0, t1;        // units of the item in this run
+  bool whole;            // all of the item is in this run
+};
+struct K8Walk {
+  int64_t w, end, item_first, nt, keys;
+  int b, hs;
+  __device__ bool next(const K8Args& p, int heads, K8Segment& s) {
+    if (w >= end) return false;
+    while (w >= item_first + nt) {   // on to the item that holds unit w
+      item_first += nt;
+      if (++hs == heads) {
+        hs = 0;
+        do {
+          ++b;
+          keys = k8_len(p, b);
+          nt = units_of(keys);
+        } while (nt == 0);
+      }
+    }
+    s.b = b;
+    s.hs = hs;
+    s.keys = keys;
+    s.t0 = w - item_first;
+    s.t1 = min(end - item_first, nt);
+    s.whole = s.t0 == 0 && s.t1 == nt;
+    w = item_first + s.t1;
+    return true;
+  }
+};
+
+// Byte offset of a 16-byte chunk of a key's row in a tile: column blocks of up to 128
+// bytes, each [key][bytes], swizzled as TMA leaves them (row: key % 8).
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int key, int row, int chunk) {
+  if (D == 64) return (uint32_t)(key * 64 + ((chunk ^ (row >> 1)) << 4));
+  return (uint32_t)((chunk >> 3) * K8_KEYS * 128 + key * 128 + (((chunk & 7) ^ row) << 4));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void k8_consumers_bar() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * K8_WARPS) : "memory");
+}
+template <typename IO, int D, int NT, bool FEW>
+__global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
+    kv8_decode_kernel(const __grid_constant__ K8Args p, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+  using C = K8Cfg<D, NT>;
+  constexpr int CHUNKS = D / 16;
+  constexpr float UP = WeightRange<__half>::SCALE_LOG2, LAG = WeightRange<__half>::LAG_LOG2;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  K8Shared* sh = reinterpret_cast<K8Shared*>(smem);
+  float* obuf = reinterpret_cast<float*>(smem + 3072);
+  uint2* qbuf = reinterpret_cast<uint2*>(smem + 3072 + C::OBUF);   // [chunk][nt][lane]
+  const GdnKv8DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t ring = smem_u32(smem) + C::HEAD;
+  const int heads = a.h_kv * p.subs;
+  const int n = a.n;
+
+  pdl_launch();
+  if (tid == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], K8_WARPS);
+    }
+    fence_mbar_init();
+  }
+  K8Walk walk;
+  int64_t w0, w1;
+  if (FEW) {
+    // ---- this CTA's share of its cluster's item ----
+    const int item = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+    walk.b = item / heads;
+    walk.hs = item % heads;
+    walk.keys = k8_len(p, walk.b);
+    walk.nt = units_of(walk.keys);
+    walk.item_first = 0;
+    w0 = walk.nt * rank / p.cluster;
+    w1 = walk.nt * (rank + 1) / p.cluster;
+    if (tid < 16) sh->ml[tid] = make_float2(-INFINITY, 0.f);
+    __syncthreads();
+  } else {
+    // ---- this CTA's run of units ----
+    int64_t total = 0, units = 0, before = 0;
+    for (int base = 0; base < n; base += K8_THREADS) {
+      const int b = base + tid;
+      units = b < n ? units_of(k8_len(p, b)) * heads : 0;
+      total += block_scan(units, sh->sum, K8_WARPS + 1, before);
+    }
+    const K8Line line(total, p.ctas);
+    const int c = (int)blockIdx.x;
+    w0 = c < line.ctas ? line.start(c) : 0;
+    w1 = c < line.ctas ? line.start(c + 1) : 0;
+    int64_t seen = 0;
+    for (int base = 0; base < n && w0 < w1; base += K8_THREADS) {
+      const int b = base + tid;
+      int64_t all = total;
+      if (n > K8_THREADS) {   // else the scan above has it all
+        units = b < n ? units_of(k8_len(p, b)) * heads : 0;
+        all = block_scan(units, sh->sum, K8_WARPS + 1, before);
+      }
+      if (w0 >= seen + before && w0 < seen + before + units) {
+        sh->found = b;
+        sh->found_first = seen + before;
+      }
+      seen += all;
+    }
+    __syncthreads();
+  }
+
+  if (w0 < w1) {
+    walk.w = w0;
+    walk.end = w1;
+    if (!FEW) {
+      walk.b = sh->found;
+      walk.keys = k8_len(p, walk.b);
+      walk.nt = units_of(walk.keys);
+      walk.hs = (int)((w0 - sh->found_first) / walk.nt);
+      walk.item_first = sh->found_first + walk.hs * walk.nt;
+    }
+    K8Segment g;
+    bool ok = true;
+    int j = 0;                       // units so far: the ring's position
+    if (warp == K8_WARPS) {
+      // ---- loads: each lane one box of the unit (K or V, rows, column block), and one
+      // of its 16 blocks' scales ----
+      constexpr int COLS = D == 256 ? 2 : 1;
+      const int per_kv = (K8_KEYS / p.box_rows) * COLS;
+      const bool boxed = lane < 2 * per_kv, is_v = lane >= per_kv;
+      const int box = is_v ? lane - per_kv : lane;
+      const int cb = box % COLS, r = box / COLS * p.box_rows;
+      const int sr = lane % K8_WARPS * KV8_BLOCK;
+      const float* const scales = lane < K8_WARPS ? a.cache.k_scale : a.cache.v_scale;
+      while (ok && walk.next(p, heads, g)) {
+        const int kvh = g.hs / p.subs;
+        const int32_t* table = a.cache.block_table + (int64_t)g.b * a.cache.pages_per_seq;
+        auto page_at = [&](int64_t t, int row) {
+          const int64_t pos = t * K8_KEYS + row;
+          return t < g.t1 && pos < g.keys ? __ldg(table + (pos >> a.page_shift)) : 0;
+        };
+        auto scale_at = [&](int64_t t, int32_t page) {
+          const int64_t pos = t * K8_KEYS + sr;
+          if (lane >= 2 * K8_WARPS || t >= g.t1 || pos >= g.keys || page < 0 ||
+              page >= a.cache.num_pages)
+            return 0.f;
+          return __ldg(scales + ((((int64_t)page * a.h_kv + kvh) << a.page_shift) +
+                                 (pos & ((1 << a.page_shift) - 1))) / KV8_BLOCK);
+        };
+        // two units ahead: pages; one ahead: scales
+        int32_t page = boxed ? page_at(g.t0, r) : 0, page1 = boxed ? page_at(g.t0 + 1, r) : 0;
+        int32_t spage1 = page_at(g.t0 + 1, sr);
+        float scale = scale_at(g.t0, page_at(g.t0, sr));
+        for (int64_t t = g.t0; t < g.t1 && ok; ++t, ++j) {
+          const float scale1 = scale_at(t + 1, spage1);
+          const int32_t page2 = boxed ? page_at(t + 2, r) : 0, spage2 = page_at(t + 2, sr);
+          const int s = j % C::STAGES;
+          if (j >= C::STAGES)
+            ok = mbar_wait(&sh->empty[s], ((j / C::STAGES) - 1) & 1, a.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int64_t left = g.keys - t * K8_KEYS;
+          const int there =
+              (int)min((int64_t)K8_KEYS, (left + p.box_rows - 1) / p.box_rows * p.box_rows);
+          // (the test's: of the first CTA, or of the last one of the first cluster)
+          const bool withheld = a.withhold && j == 0 && blockIdx.x == (FEW ? p.cluster - 1 : 0);
+          if (lane < 2 * K8_WARPS) sh->scale[s][lane] = scale;
+          __syncwarp();
+          if (lane == 0 && !withheld) mbar_expect_tx(&sh->full[s], (uint32_t)there * D * 2);
+          __syncwarp();
+          if (boxed && r < there && !withheld) {
+            if (page < 0 || page >= a.cache.num_pages) {
+              set_status(a.d_status, GDN_DEV_BAD_PAGE);
+              page = 0;
+            }
+            const int64_t row = (((int64_t)page * a.h_kv + kvh) << a.page_shift) +
+                                ((t * K8_KEYS + r) & ((1 << a.page_shift) - 1));
+            tma_box(ring + (uint32_t)s * C::STAGE + (is_v ? C::TILE : 0u) +
+                        (uint32_t)(cb * K8_KEYS + r) * (D < 128 ? 64u : 128u),
+                    is_v ? &vmap : &kmap, (int)row, cb, &sh->full[s]);
+          }
+          page = page1;
+          page1 = page2;
+          spage1 = spage2;
+          scale = scale1;
+        }
+      }
+      // (the consumers wait for these too, unless they have given up)
+      for (int x = max(0, j - C::STAGES); x < j; ++x)
+        mbar_wait(&sh->full[x % C::STAGES], (x / C::STAGES) & 1, GRACE_NS);
+    } else {
+      // ---- 16 keys of every unit, with this warp's own references, sums and O ----
+      const int row8 = lane >> 2, col = (lane & 3) * 2;   // key or channel pair; heads col, col + 1
+      const int mi = lane >> 3, mr = lane & 7;            // this lane's row of an ldmatrix
+      const int l_key = warp * KV8_BLOCK + (mi & 1) * 8 + mr, l_chunk = mi >> 1;
+      while (walk.next(p, heads, g)) {
+        const int h0 = k8_head<NT>(p, g.hs), rows = k8_rows<NT>(p, g.hs);
+        // Q: head row8 of each eight; the channels of a chunk in the order of K's bytes.
+        // Each row times a power of two that brings its largest element to [1, 2).
+        uint2 q[C::Q_REGS ? CHUNKS : 1][NT];
+        float cs[NT][2];                                  // scale of heads col, col + 1
+        if (!C::Q_REGS) k8_consumers_bar();               // the last item's are in use until here
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int head = nt * 8 + row8;
+          uint2 w[CHUNKS];
+          float top = 0.f;
+#pragma unroll
+          for (int ch = 0; ch < CHUNKS; ++ch) {
+            w[ch] = make_uint2(0, 0);
+            if (head < rows)
+              w[ch] = *reinterpret_cast<const uint2*>(
+                  reinterpret_cast<const IO*>(a.q.data) + (int64_t)g.b * a.q.token_stride +
+                  (int64_t)(h0 + head) * a.q.head_stride + ch * 16 + (lane & 3) * 4);
+            const float2 x = unpack2<IO>(w[ch].x), y = unpack2<IO>(w[ch].y);
+            top = max3(max3(top, fabsf(x.x), fabsf(x.y)), fabsf(y.x), fabsf(y.y));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // (an Inf, and a row of zeros or of subnormals, as it is)
+          const uint32_t ex = __float_as_uint(top) >> 23;
+          const bool plain = ex == 0 || ex == 255;
+          const int up = plain ? 0 : max(-126, min(127, 127 - (int)ex));
+          const float f = pow2(up);
+#pragma unroll
+          for (int ch = 0; ch < CHUNKS; ++ch) {
+            const float2 x = unpack2<IO>(w[ch].x), y = unpack2<IO>(w[ch].y);
+            w[ch] = make_uint2(pack2<__half>(x.x * f, x.y * f), pack2<__half>(y.x * f, y.y * f));
+            if (C::Q_REGS) q[ch][nt] = w[ch];
+            else if (warp == nt) qbuf[(ch * NT + nt) * 32 + lane] = w[ch];
+          }
+          const float back = a.scale_log2 * pow2(-up);
+          cs[nt][0] = __shfl_sync(0xffffffffu, back, col * 4);
+          cs[nt][1] = __shfl_sync(0xffffffffu, back, col * 4 + 4);
+        }
+        if (!C::Q_REGS) k8_consumers_bar();
+        float o[CHUNKS][NT][4];
+#pragma unroll
+        for (int ch = 0; ch < CHUNKS; ++ch)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            o[ch][nt][0] = o[ch][nt][1] = o[ch][nt][2] = o[ch][nt][3] = 0.f;
+        // of heads col, col + 1: references of the sum and of the contributions, sum
+        float m[NT][2], mv[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            m[nt][e] = mv[nt][e] = -INFINITY;
+            l[nt][e] = 0.f;
+          }
+
+        for (int64_t t = g.t0; t < g.t1; ++t, ++j) {
+          const int s = j % C::STAGES;
+          if (ok) ok = mbar_wait(&sh->full[s], (j / C::STAGES) & 1, a.wait_ns);
+          __syncwarp();
+          const int left = (int)min((int64_t)K8_KEYS, g.keys - t * K8_KEYS) - warp * KV8_BLOCK;
+          const uint32_t kt = ring + (uint32_t)s * C::STAGE, vt = kt + C::TILE;
+          if (left > 0) {
+            const float ks = sh->scale[s][warp], vs = sh->scale[s][K8_WARPS + warp];
+            float sc[2][NT][4] = {};
+#pragma unroll
+            for (int ch = 0; ch < CHUNKS; ch += 2) {
+              uint32_t w[4];
+              ldsm4(kt + chunk_at<D>(l_key, mr, ch + l_chunk), w);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t ka[4];
+                e4m3x4_to_f16(w[2 * i], ka[0], ka[2]);
+                e4m3x4_to_f16(w[2 * i + 1], ka[1], ka[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint2 b = C::Q_REGS ? q[C::Q_REGS ? ch + i : 0][nt]
+                                            : qbuf[((ch + i) * NT + nt) * 32 + lane];
+                  mma16816<__half>(sc[i][nt], ka, b.x, b.y);
+                }
+              }
+            }
+            uint32_t pb[NT][2];
+            float mt[NT][2], x[NT][4];
+            const float lv = __log2f(vs);
+            bool far = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float f = cs[nt][e] * ks;
+                x[nt][e] = row8 < left ? (sc[0][nt][e] + sc[1][nt][e]) * f : -INFINITY;
+                x[nt][2 + e] = row8 + 8 < left ? (sc[0][nt][2 + e] + sc[1][nt][2 + e]) * f : -INFINITY;
+                float v = fmaxf(x[nt][e], x[nt][2 + e]);
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                mt[nt][e] = v;
+                far |= v > m[nt][e] + LAG || v + lv > mv[nt][e] + LAG;
+              }
+            }
+            // A head's references follow from the head alone (they may lag behind by LAG).
+            if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float f[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  f[e] = 1.f;
+                  if (mt[nt][e] > m[nt][e] + LAG) {
+                    l[nt][e] *= ex2(m[nt][e] - mt[nt][e]);
+                    m[nt][e] = mt[nt][e];
+                  }
+                  if (mt[nt][e] + lv > mv[nt][e] + LAG) {
+                    f[e] = ex2(mv[nt][e] - (mt[nt][e] + lv));
+                    mv[nt][e] = mt[nt][e] + lv;
+                  }
+                }
+#pragma unroll
+                for (int ch = 0; ch < CHUNKS; ++ch) {
+                  o[ch][nt][0] *= f[0];
+                  o[ch][nt][1] *= f[1];
+                  o[ch][nt][2] *= f[0];
+                  o[ch][nt][3] *= f[1];
+                }
+              }
+            }
+            if (a.weights) {   // the scores, for the weights' sums
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int head = nt * 8 + col + (e & 1), key = row8 + (e >> 1) * 8;
+                  if (head < rows && key < left)
+                    a.scores[((int64_t)g.b * a.h_q + h0 + head) * a.capacity + t * K8_KEYS +
+                             warp * KV8_BLOCK + key] = x[nt][e];
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float y[4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float nm = m[nt][e] == -INFINITY ? 0.f : -m[nt][e];
+                const float f = mv[nt][e] == -INFINITY ? 0.f : vs * ex2(m[nt][e] - mv[nt][e] + UP);
+                const float e0 = ex2(x[nt][e] + nm), e1 = ex2(x[nt][2 + e] + nm);
+                l[nt][e] += e0 + e1;
+                y[e] = e0 * f;
+                y[2 + e] = e1 * f;
+              }
+              pb[nt][0] = transpose_8x8(pack2<__half>(y[0], y[1]));
+              pb[nt][1] = transpose_8x8(pack2<__half>(y[2], y[3]));
+            }
+            // values past the end may be anything: cleared, as 0 x NaN is not 0
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+            if (left < KV8_BLOCK) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int k = e * 8 + col;
+                keep[e] = (k < left ? 0x0000ffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
+              }
+            }
+#pragma unroll
+            for (int ch = 0; ch < CHUNKS; ch += 2) {
+              uint32_t w[4];
+              ldsm4t(vt + chunk_at<D>(l_key, mr, ch + l_chunk), w);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                uint32_t va[4];   // channels 2 row8 (even rows) and 2 row8 + 1 of the chunk
+                e4m3x4_to_f16(__byte_perm(w[2 * i] & keep[0], 0, 0x3120), va[0], va[1]);
+                e4m3x4_to_f16(__byte_perm(w[2 * i + 1] & keep[1], 0, 0x3120), va[2], va[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16816<__half>(o[ch + i][nt], va, pb[nt][0], pb[nt][1]);
+              }
+            }
+          }
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&sh->empty[s]);
+        }
+
+        // ---- join the warps, by the sums' reference ----
+        const bool all_ok = __all_sync(0xffffffffu, ok);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+            l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+            l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+            if (!all_ok) l[nt][e] = NAN;
+            if (row8 == 0) {
+              sh->m[warp][nt * 8 + col + e] = m[nt][e];
+              sh->l[warp][nt * 8 + col + e] = l[nt][e];
+            }
+          }
+        k8_consumers_bar();
+        float f[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mm = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < K8_WARPS; ++w) mm = fmaxf(mm, sh->m[w][nt * 8 + col + e]);
+            f[nt][e] = mv[nt][e] == -INFINITY ? 0.f : ex2(mv[nt][e] - UP - mm);
+          }
+        // The warps add up in one slab, a share of the channels at a time, each at another
+        // one: every sum has a fixed order.
+#pragma unroll
+        for (int st = 0; st < K8_WARPS; ++st) {
+          const int part = (warp + st) % K8_WARPS;
+#pragma unroll
+          for (int ch = 0; ch < CHUNKS; ++ch) {
+            if (ch % K8_WARPS != part) continue;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int row = nt * 8 + col + e;
+                if (row >= rows) continue;
+                float2* dst = reinterpret_cast<float2*>(obuf + row * D + ch * 16 + row8 * 2);
+                float2 v = make_float2(o[ch][nt][e] * f[nt][e], o[ch][nt][2 + e] * f[nt][e]);
+                if (st > 0) {
+                  const float2 w = *dst;
+                  v.x += w.x;
+                  v.y += w.y;
+                }
+                *dst = v;
+              }
+          }
+          k8_consumers_bar();
+        }
+        // ---- out: the output itself, or a partial result ----
+        const bool direct = !FEW && g.whole;
+        const int64_t part = (2 * (int64_t)blockIdx.x + (g.t0 > 0 ? 0 : 1)) * p.rows;
+        for (int i = tid; i < rows * (D / 4); i += 32 * K8_WARPS) {
+          const int row = i / (D / 4), c4 = i % (D / 4) * 4;
+          float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+          for (int w = 0; w < K8_WARPS; ++w) mm = fmaxf(mm, sh->m[w][row]);
+#pragma unroll
+          for (int w = 0; w < K8_WARPS; ++w)
+            ll += mm == -INFINITY ? sh->l[w][row] : sh->l[w][row] * ex2(sh->m[w][row] - mm);
+          const float4 v = *reinterpret_cast<const float4*>(obuf + row * D + c4);
+          if (FEW) {
+            if (c4 == 0) sh->ml[row] = make_float2(mm, ll);
+          } else if (direct) {
+            float y[4] = {v.x, v.y, v.z, v.w};
+            k8_put_four<IO, D>(a, g.b, h0 + row, c4, ll, y);
+            if (a.weights && c4 == 0) a.row_ml[(int64_t)g.b * a.h_q + h0 + row] = make_float2(mm, ll);
+          } else {
+            *reinterpret_cast<float4*>(a.part_o + (part + row) * D + c4) = v;
+            if (c4 == 0) a.part_ml[part + row] = make_float2(mm, ll);
+          }
+        }
+        k8_consumers_bar();   // obuf and m, l are free again
+      }
+    }
+    if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
+  }
+  if (FEW) {
+    // ---- the cluster's partials joined, a share of the channels by each CTA ----
+    __syncwarp();
+    cluster_barrier();
+    const int rank = blockIdx.x % p.cluster;
+    const int rows = k8_rows<NT>(p, walk.hs), h0 = k8_head<NT>(p, walk.hs);
+    const uint32_t ml_at = smem_u32(sh->ml), o_at = smem_u32(obuf);
+    for (int x = rank * K8_THREADS + tid; x < rows * (D / 4); x += p.cluster * K8_THREADS) {
+      const int row = x / (D / 4), c4 = x % (D / 4) * 4;
+      float mm = -INFINITY, ll = 0.f;
+      for (int r = 0; r < p.cluster; ++r)
+        mm = fmaxf(mm, ld_peer_8(peer_addr(ml_at + 8u * row, r)).x);
+      float y[4] = {};
+      for (int r = 0; r < p.cluster; ++r) {
+        const float2 v = ld_peer_8(peer_addr(ml_at + 8u * row, r));
+        if (v.y == 0.f) continue;   // saw no key
+        const float f = ex2(v.x - mm);
+        const float4 o = ld_peer_16(peer_addr(o_at + (uint32_t)(row * D + c4) * 4u, r));
+        ll += f * v.y;
+        y[0] = fmaf(f, o.x, y[0]);
+        y[1] = fmaf(f, o.y, y[1]);
+        y[2] = fmaf(f, o.z, y[2]);
+        y[3] = fmaf(f, o.w, y[3]);
+      }
+      k8_put_four<IO, D>(a, walk.b, h0 + row, c4, ll, y);
+      if (a.weights && c4 == 0)
+        a.row_ml[(int64_t)walk.b * a.h_q + h0 + row] = make_float2(mm, ll);
+    }
+    cluster_barrier();   // the others may still read this CTA's
+  }
+}
+
+// ---- merge ------------------------------------------------------------------------
+
+// Joins the partial results of one item, merge_rows rows of it per CTA:
+//   M = max m_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+constexpr int K8_MERGE_THREADS = 256;
+
+// Partials of one item, at most: with equal runs every head of a sequence has as
+// many units, so an item is at most 1 / heads of the line, and its ends cut two runs.
+static __host__ __device__ __forceinline__ int k8_most_parts(const K8Args& p) {
+  return p.ctas / (p.a.h_kv * p.subs) + 2;
+}
+
+template <typename IO, int D, int NT>
+__global__ void __launch_bounds__(K8_MERGE_THREADS)
+    kv8_merge_kernel(const __grid_constant__ K8Args p) {
+  extern __shared__ __align__(16) float2 ml[];   // [part][row]: statistics, then (factor, sum)
+  __shared__ int64_t sums[K8_MERGE_THREADS / 32], s_mine;
+  __shared__ float sum_l[16];
+  __shared__ float4 shares[K8_MERGE_THREADS];
+  const GdnKv8DecodeArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int heads = a.h_kv * p.subs;
+  const int n = a.n;
+  const int slices = (p.rows + p.merge_rows - 1) / p.merge_rows;
+  const int item = blockIdx.x / slices, r0 = blockIdx.x % slices * p.merge_rows;
+  const int b = item / heads, hs = item % heads;
+  const int h0 = k8_head<NT>(p, hs) + r0;
+  const int rows = min(p.merge_rows, k8_rows<NT>(p, hs) - r0);
+  int64_t total = 0;
+  for (int base = 0; base < n; base += K8_MERGE_THREADS) {
+    const int i = base + tid;
+    int64_t before;
+    const int64_t u = i < n ? units_of(k8_len(p, i)) * heads : 0;
+    const int64_t all = block_scan(u, sums, K8_MERGE_THREADS / 32, before);
+    if (i == b) s_mine = total + before;
+    total += all;
+  }
+  __syncthreads();
+  const int64_t nt = units_of(k8_len(p, b));
+  const int64_t u0 = s_mine + hs * nt, u1 = u0 + nt;
+  const K8Line line(total, p.ctas);
+  int c0 = 0, c1 = -1;
+  if (nt > 0) {   // the CTAs whose runs meet [u0, u1)
+    c0 = line.owner(u0);
+    c1 = line.owner(u1 - 1);
+  }
+  const int parts = c1 - c0 + 1;
+  pdl_wait();
+  if (nt > 0 && c0 == c1) return;   // written already
+  if (rows <= 0) return;            // the last heads' item may be shorter
+  // a run that starts inside the item left its first partial, else its last
+  auto first_row = [&](int i) {
+    const int c = c0 + i;
+    return (2 * (int64_t)c + (line.start(c) > u0 ? 0 : 1)) * p.rows + r0;
+  };
+  for (int i = tid; i < parts * rows; i += K8_MERGE_THREADS)
+    ml[i] = a.part_ml[first_row(i / rows) + i % rows];
+  __syncthreads();
+  for (int row = warp; row < rows; row += K8_MERGE_THREADS / 32) {
+    float mm = -INFINITY, ll = 0.f;
+    for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, ml[i * rows + row].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    for (int i = lane; i < parts; i += 32) {
+      const float2 v = ml[i * rows + row];
+      const float f = v.y == 0.f ? 0.f : ex2(v.x - mm);
+      ll += v.y == 0.f ? 0.f : f * v.y;
+      ml[i * rows + row].x = f;
+    }
+    ll = warp_sum(ll);
+    if (lane == 0) {
+      sum_l[row] = ll;
+      if (a.weights) a.row_ml[(int64_t)b * a.h_q + h0 + row] = make_float2(mm, ll);
+    }
+  }
+  __syncthreads();
+  // The threads that the rows leave over share the partials: group g takes every
+  // groups-th one, and the groups' sums are added in their order.
+  const int units = rows * (D / 4), groups = max(1, K8_MERGE_THREADS / units);
+  for (int x0 = 0; x0 < units; x0 += K8_MERGE_THREADS) {
+    const int g = groups > 1 ? tid / units : 0, x = groups > 1 ? tid - g * units : x0 + tid;
+    const int row = x / (D / 4), col = x % (D / 4) * 4;
+    float y[4] = {};
+    const bool mine = x < units && g < groups;
+    if (mine) {
+#pragma unroll 8
+      for (int i = g; i < parts; i += groups) {
+        const float2 w = ml[i * rows + row];
+        const float4 v =
+            *reinterpret_cast<const float4*>(a.part_o + (first_row(i) + row) * D + col);
+        if (w.y != 0.f) {
+          y[0] = fmaf(w.x, v.x, y[0]);
+          y[1] = fmaf(w.x, v.y, y[1]);
+          y[2] = fmaf(w.x, v.z, y[2]);
+          y[3] = fmaf(w.x, v.w, y[3]);
+        }
+      }
+    }
+    if (groups > 1) {
+      if (mine) shares[tid] = make_float4(y[0], y[1], y[2], y[3]);
+      __syncthreads();
+      for (int i = 1; i < groups && g == 0; ++i) {
+        const float4 v = shares[i * units + x];
+        y[0] += v.x;
+        y[1] += v.y;
+        y[2] += v.z;
+        y[3] += v.w;
+      }
+    }
+    if (mine && g == 0) k8_put_four<IO, D>(a, b, h0 + row, col, sum_l[row], y);
+  }
+}
+
+// ---- what the cached tokens received -----------------------------------------------
+
+// weights[b][j][p] += sum over head j's query heads of 2^(s_p - M) / l.
+constexpr int RECEIVED_THREADS = 256, RECEIVED_KEYS = 4 * RECEIVED_THREADS;
+
+__global__ void __launch_bounds__(RECEIVED_THREADS)
+    kv8_received_kernel(const __grid_constant__ GdnKv8DecodeArgs a, int across) {
+  const int group = a.h_q / a.h_kv;
+  const int item = blockIdx.x / across, b = item / a.h_kv, j = item % a.h_kv;
+  int64_t len = a.seq_lens[b];
+  len = min(len, a.capacity);
+  const float2* ml = a.row_ml + (int64_t)b * a.h_q + j * group;
+  const float* s = a.scores + ((int64_t)b * a.h_q + j * group) * a.capacity;
+  float* w = a.weights + ((int64_t)b * a.h_kv + j) * a.capacity;
+  for (int64_t p0 = (int64_t)(blockIdx.x % across) * RECEIVED_KEYS; p0 < len;
+       p0 += (int64_t)across * RECEIVED_KEYS) {
+    const int64_t p = p0 + threadIdx.x * 4;      // capacity is a multiple of 16
+    if (p >= len) continue;
+    float y[4] = {};
+    for (int h = 0; h < group; ++h) {
+      const float2 v = __ldg(ml + h);
+      const float4 x = *reinterpret_cast<const float4*>(s + h * a.capacity + p);
+      const float inv = 1.0f / v.y;
+      y[0] = fmaf(ex2(x.x - v.x), inv, y[0]);
+      y[1] = fmaf(ex2(x.y - v.x), inv, y[1]);
+      y[2] = fmaf(ex2(x.z - v.x), inv, y[2]);
+      y[3] = fmaf(ex2(x.w - v.x), inv, y[3]);
+    }
+    if (p + 4 <= len) {
+      float4* at = reinterpret_cast<float4*>(w + p);
+      const float4 old = *at;
+      *at = make_float4(old.x + y[0], old.y + y[1], old.z + y[2], old.w + y[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (p + e < len) w[p + e] += y[e];
+    }
+  }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+template <typename IO, int D, int NT>
+static cudaError_t launch_decode(const GdnKv8DecodeArgs& a, cudaStream_t s) {
+  using C = K8Cfg<D, NT>;
+  cudaError_t e = cudaSuccess;
+  K8Args p;
+  p.a = a;
+  const int group = a.h_q / a.h_kv;
+  p.rows = group < C::ROWS ? group : C::ROWS;
+  p.subs = (group + C::ROWS - 1) / C::ROWS;
+  p.ctas = C::CTAS;
+  const int page = 1 << a.page_shift;
+  p.box_rows = page < K8_KEYS ? page : K8_KEYS;
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn_tensor_map_encoder());
+  if (!enc) return cudaErrorNotSupported;
+  CUtensorMap kmap, vmap;
+  constexpr int WIDE = D < 128 ? 64 : 128;
+  for (int i = 0; i < 2; ++i) {   // cache rows: (channel, row of the pool, column block)
+    const cuuint64_t dims[3] = {WIDE, (cuuint64_t)a.cache.num_pages * a.h_kv << a.page_shift,
+                                D / WIDE};
+    const cuuint64_t strides[2] = {D, WIDE};
+    const cuuint32_t box[3] = {WIDE, (cuuint32_t)p.box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(i ? &vmap : &kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, i ? a.cache.v : a.cache.k, dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            WIDE == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  auto kernel = kv8_decode_kernel<IO, D, NT, false>;
+  auto few = kv8_decode_kernel<IO, D, NT, true>;
+  auto merge = kv8_merge_kernel<IO, D, NT>;
+  static int opted_in[64] = {};
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !opted_in[dev]) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)C::SMEM)) != cudaSuccess)
+      return e;
+    if ((e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)C::SMEM)) != cudaSuccess)
+      return e;
+    if (dev >= 0 && dev < 64) opted_in[dev] = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(K8_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  // Few keys: the block table bounds the sequences' lengths, which are not known here.
+  p.cluster = 1;
+  const int64_t items = (int64_t)a.n * a.h_kv * p.subs;
+  const int64_t units = (a.capacity + K8_KEYS - 1) / K8_KEYS;
+  while (p.cluster < 8 && items * p.cluster * 2 <= C::CTAS && p.cluster < units) p.cluster *= 2;
+  if (items * p.cluster <= C::CTAS && units <= (int64_t)K8_FEW_UNITS * p.cluster) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(items * p.cluster));
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, few, p, kmap, vmap)) != cudaSuccess) return e;
+  } else {
+    p.cluster = 0;
+    cfg.gridDim = dim3((unsigned)p.ctas);
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, p, kmap, vmap)) != cudaSuccess) return e;
+    // The merge: a CTA per item, or per row or a few of them where that leaves SMs without one.
+    p.merge_rows = p.rows;
+    int64_t slices = 1;
+    if (items <= SMS)
+      while (p.merge_rows > 1 && items * slices * 2 <= 4 * SMS) {
+        p.merge_rows = (p.merge_rows + 1) / 2;
+        slices = (p.rows + p.merge_rows - 1) / p.merge_rows;
+      }
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(items * slices));
+    cfg.blockDim = dim3(K8_MERGE_THREADS);
+    cfg.dynamicSmemBytes = (size_t)k8_most_parts(p) * 8 * p.merge_rows;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, merge, p)) != cudaSuccess) return e;
+  }
+  if (!a.weights) return cudaSuccess;
+  const int64_t most = (a.capacity + RECEIVED_KEYS - 1) / RECEIVED_KEYS;
+  const int across = most < 64 ? (int)most : 64;
+  kv8_received_kernel<<<(unsigned)(a.n * a.h_kv * across), RECEIVED_THREADS, 0, s>>>(a, across);
+  return cudaGetLastError();
+}
+
+// Up to eight query heads of a key/value head: one eight of them; more: two.
+template <typename IO, int D>
+static cudaError_t launch_decode_n(const GdnKv8DecodeArgs& a, cudaStream_t s) {
+  return a.h_q / a.h_kv <= 8 ? launch_decode<IO, D, 1>(a, s) : launch_decode<IO, D, 2>(a, s);
+}
+template <typename IO>
+static cudaError_t launch_decode_d(const GdnKv8DecodeArgs& a, cudaStream_t s) {
+  return a.d == 64 ? launch_decode_n<IO, 64>(a, s)
+                   : a.d == 128 ? launch_decode_n<IO, 128>(a, s) : launch_decode_n<IO, 256>(a, s);
+}
+
+}  // namespace attn
+}  // namespace gdn
+
+int64_t gdn_kv8_decode_slots(int h_q, int h_kv, int d) {
+  using namespace gdn::attn;
+  const int group = h_q / h_kv, most = group <= 8 ? 8 : 16;
+  // two cut items per CTA
+  return 2 * (d == 256 ? K8Cfg<256, 1>::CTAS : K8Cfg<128, 1>::CTAS) * (int64_t)(group < most ? group : most);
+}
+
+cudaError_t gdn_launch_kv8_decode(const GdnKv8DecodeArgs& a, int io, cudaStream_t s) {
+  using namespace gdn::attn;
+  return io == GDN_BF16 ? launch_decode_d<__nv_bfloat16>(a, s) : launch_decode_d<__half>(a, s);
+}

@@ -16,6 +16,9 @@
 // of the turn exactly as the product of integers: no far position loses bits,
 // and no fp64 arithmetic runs per angle (this GPU has little of it).
 //
+// With several axes (images, video) pair i turns by its axis's position,
+// positions[axis of i][t]: only the forming of the angles differs.
+//
 // Two kernels of the same arithmetic: few tokens are spread as thinly as they
 // go (one lane group per row where they are very few: 2.3 us for one token);
 // many go through a ring of shared-memory stages that one warp per CTA keeps
@@ -28,6 +31,7 @@
 #include <cudaTypedefs.h>
 
 #include "gdn_attn.cuh"
+#include "gdn_rope.cuh"
 #include "gdn_tc.cuh"
 
 namespace gdn {
@@ -39,37 +43,6 @@ using gdn::tc::mbar_expect_tx;
 using gdn::tc::mbar_init;
 using gdn::tc::mbar_wait;
 using gdn::tc::smem_u32;
-
-// f radians per position as a fraction of a turn, in 2^-64 of it.
-__device__ __forceinline__ uint64_t turn_fraction(double f) {
-  const double t = f * 0.15915494309189533577;
-  return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
-}
-// Cosine and sine of position p, from the top 32 bits of the turn's fraction
-// as a signed one in half turns.  For 16-bit rows they come from the
-// special-function unit, within 2^-20.5 on this range (the rows are rounded by
-// 2^-12 or more): the warp that forms the angles would otherwise be what bounds
-// wholly rotated heads (30011 tokens of 40 heads of 128: 119 us with sincospif).
-template <typename IO>
-__device__ __forceinline__ void angle(int32_t p, uint64_t fraction, float scale, float& c, float& s) {
-  const uint64_t turn = (uint64_t)(int64_t)p * fraction;
-  const float x = (float)(int32_t)(turn >> 32);
-  if (sizeof(IO) == 2) {
-    const float r = x * (0x1p-31f * 3.14159265358979f);
-    asm("cos.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(r));
-    asm("sin.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(r));
-  } else {
-    sincospif(x * 0x1p-31f, &s, &c);
-  }
-  c *= scale;
-  s *= scale;
-}
-
-__device__ __forceinline__ float fast_rsqrt(float x) {   // special-function unit, 2 ulp
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // The rows of one token, in this order: q heads, k heads, v heads.
 enum RowKind { ROW_Q, ROW_K, ROW_V };
@@ -90,128 +63,6 @@ template <typename IO>
 __device__ __forceinline__ const IO* row_ptr(const GdnRopeArgs& a, Row w, int64_t t) {
   const gdn_view& v = w.kind == ROW_Q ? a.q : w.kind == ROW_K ? a.k : a.v;
   return reinterpret_cast<const IO*>(v.data) + t * v.token_stride + w.head * v.head_stride;
-}
-
-// A lane's place in a row of D channels (eight per lane) and, in the half
-// layout, the lane that holds the other channels of its pairs.
-template <int D>
-struct LanePlace {
-  static constexpr int LPR = D / 8;
-  int part, other, i0;
-  uint32_t mask;
-  bool rotated, low;
-  __device__ __forceinline__ explicit LanePlace(const GdnRopeArgs& a) {
-    const int half = a.rot_dim >> 1, lane = threadIdx.x & 31;
-    part = lane % LPR;
-    mask = LPR == 32 ? 0xffffffffu : ((1u << (LPR & 31)) - 1u) << (lane / LPR * LPR);
-    rotated = 8 * part < a.rot_dim;
-    low = 8 * part < half;
-    other = !rotated || a.interleaved ? part : low ? part + (half >> 3) : part - (half >> 3);
-    i0 = !rotated ? 0 : a.interleaved ? 4 * part : low ? 8 * part : 8 * part - half;
-  }
-};
-
-// A token's cosines, sines and negated sines, D / 2 floats each: the low half of
-// a pair takes the negated sine, so that no lane has a sign to apply.
-template <typename IO, int D>
-__device__ __forceinline__ void put_angle(float* cs, int i, int32_t pos, uint64_t fraction,
-                                          float scale) {
-  float c, s;
-  angle<IO>(pos, fraction, scale, c, s);
-  cs[i] = c;
-  cs[D / 2 + i] = s;
-  cs[D + i] = -s;
-}
-
-// Norm (w: this lane's weights; norm false: neither root nor weights) and
-// rotation (cs: the tokens', as above, 3 D / 2 floats each) of one head's rows of
-// the first `toks` of N tokens, step by step side by side: one row alone is a
-// chain of thirteen shuffles.  By the lanes of the row together.
-template <typename IO, int D, int N>
-__device__ __forceinline__ void norm_rotate(const LanePlace<D>& at, int toks, bool norm,
-                                            bool interleaved, bool rotate, float eps,
-                                            const float4 (&w)[2], const float* cs,
-                                            Vec8<IO> (&x)[N]) {
-  uint64_t y[N][4];
-#pragma unroll
-  for (int u = 0; u < N; ++u) {
-    float f[8];
-    x[u].get(f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[u][i] = pk(f[2 * i], f[2 * i + 1]);
-  }
-  if (norm) {
-    float ss[N];
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      uint64_t sq = mul2(y[u][0], y[u][0]);
-#pragma unroll
-      for (int i = 1; i < 4; ++i) sq = fma2(y[u][i], y[u][i], sq);
-      float s0, s1;
-      unpk(sq, s0, s1);
-      ss[u] = s0 + s1;
-    }
-#pragma unroll
-    for (int m = at.LPR / 2; m > 0; m >>= 1)
-#pragma unroll
-      for (int u = 0; u < N; ++u) ss[u] += __shfl_xor_sync(at.mask, ss[u], m, at.LPR);
-    const uint64_t w2[4] = {pk(w[0].x, w[0].y), pk(w[0].z, w[0].w), pk(w[1].x, w[1].y),
-                            pk(w[1].z, w[1].w)};
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const float inv = fast_rsqrt(ss[u] * (1.0f / D) + eps);
-      const uint64_t inv2 = pk(inv, inv);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) y[u][i] = mul2(mul2(y[u][i], inv2), w2[i]);
-    }
-  }
-  if (rotate && interleaved) {
-    if (at.rotated) {
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        if (N > 1 && u >= toks) break;
-        const float4 c = *reinterpret_cast<const float4*>(cs + u * (D / 2 * 3) + at.i0);
-        const float4 s = *reinterpret_cast<const float4*>(cs + u * (D / 2 * 3) + D / 2 + at.i0);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float ya, yb;
-          unpk(y[u][i], ya, yb);
-          y[u][i] = fma2(y[u][i], pk(cc[i], cc[i]), mul2(pk(yb, ya), pk(-sn[i], sn[i])));
-        }
-      }
-    }
-  } else if (rotate) {
-    const float* cp = cs + at.i0;
-    const float* sp = cp + (at.low ? D : D / 2);
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      uint64_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float ya, yb;
-        unpk(y[u][i], ya, yb);
-        o[i] = pk(__shfl_sync(at.mask, ya, at.other, at.LPR),
-                  __shfl_sync(at.mask, yb, at.other, at.LPR));
-      }
-      if (at.rotated && (N == 1 || u < toks)) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float4 c = *reinterpret_cast<const float4*>(cp + u * (D / 2 * 3) + 4 * q);
-          const float4 s = *reinterpret_cast<const float4*>(sp + u * (D / 2 * 3) + 4 * q);
-          y[u][2 * q] = fma2(y[u][2 * q], pk(c.x, c.y), mul2(o[2 * q], pk(s.x, s.y)));
-          y[u][2 * q + 1] = fma2(y[u][2 * q + 1], pk(c.z, c.w), mul2(o[2 * q + 1], pk(s.z, s.w)));
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < N; ++u) {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) unpk(y[u][i], f[2 * i], f[2 * i + 1]);
-    x[u].set(f);
-  }
 }
 
 // Row of the cache pool (before the head) that token t's keys and values go
@@ -269,7 +120,8 @@ __global__ void __launch_bounds__(FEW_THREADS)
   const int32_t pos = a.positions[t];
   const int64_t dst = a.v.data ? cache_row(a, t, pos) : -1;
   for (int i = threadIdx.x; i < a.rot_dim / 2; i += FEW_THREADS)
-    put_angle<IO, D>(cs, i, pos, turn_fraction(a.inv_freq[i]), a.rope_scale);
+    put_angle<IO, D>(cs, i, a.axes.count ? a.positions[a.axes.pair[i] * a.n + t] : pos,
+                     turn_fraction(a.inv_freq[i]), a.rope_scale);
   __syncthreads();
   for (; r < per; r += step) {
     const Row w = set[r];
@@ -299,10 +151,11 @@ constexpr int MANY_PER_SM = 2;
 constexpr int MANY_CTAS = MANY_PER_SM * SMS;
 constexpr uint32_t STAGE_ROWS_BYTES = 49152;           // rows of one stage, at most
 
-struct ManyShared {
+struct __align__(16) ManyShared {
   uint64_t full[MANY_STAGES], empty[MANY_STAGES];
   int64_t dst[MANY_STAGES][MANY_TOKENS];
   int32_t pos[MANY_STAGES][MANY_TOKENS];
+  int32_t axis_pos[GDN_ROPE_MAX_AXES][32];   // of the loading warp's eight units' tokens
 };
 
 // How a unit is cut: `parts` of a token's heads, hq q heads and hkv k and v heads
@@ -328,6 +181,7 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
   __shared__ __align__(16) ManyShared sh;
   __shared__ __align__(16) float wts[2][D];
   __shared__ uint64_t fraction[D / 2];
+  __shared__ uint8_t axis_of[D / 2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = cut.parts;
   const int nq = a.q.data ? cut.hq : 0, nk = a.k.data ? cut.hkv : 0, nv = a.v.data ? cut.hkv : 0;
@@ -384,12 +238,17 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
   for (int i = tid; i < D; i += MANY_THREADS) {
     wts[0][i] = a.q_norm ? a.q_norm[i] : 1.f;
     wts[1][i] = a.k_norm ? a.k_norm[i] : 1.f;
-    if (i < a.rot_dim / 2) fraction[i] = turn_fraction(a.inv_freq[i]);
+    if (i < a.rot_dim / 2) {
+      fraction[i] = turn_fraction(a.inv_freq[i]);
+      axis_of[i] = a.axes.pair[i];
+    }
   }
   __syncthreads();
   if (warp == MANY_WARPS) {
     const int half = a.rot_dim / 2;
     const float scale = a.rope_scale;
+    const int axes = a.axes.count;
+    static_assert(N == 4, "positions are read as one int4");
     bool first = true;
     int64_t done = 0;        // this CTA's units so far
     for (int64_t base = blockIdx.x; base < units && ok; base += (32LL / N) * gridDim.x) {
@@ -400,6 +259,12 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
       if (unit < units && mine < a.n) {
         pos = a.positions[mine];
         if (a.v.data) dst = cache_row(a, mine, pos);
+      }
+      if (axes) {
+        __syncwarp();
+        for (int x = 0; x < axes; ++x)
+          sh.axis_pos[x][lane] = unit < units && mine < a.n ? a.positions[x * a.n + mine] : 0;
+        __syncwarp();
       }
       for (int k = 0; k < 32 / N && base + (int64_t)k * gridDim.x < units; ++k) {
         if (!(first && k < MANY_STAGES)) {   // those are there already
@@ -422,6 +287,13 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
         }
         for (int i = lane; i < half; i += 32) {
           const uint64_t f = fraction[i];
+          if (axes) {   // this pair's positions, four tokens at a time
+            const int4 v = *reinterpret_cast<const int4*>(&sh.axis_pos[axis_of[i]][k * N]);
+            p[0] = v.x;
+            p[1] = v.y;
+            p[2] = v.z;
+            p[3] = v.w;
+          }
 #pragma unroll
           for (int tt = 0; tt < N; ++tt) put_angle<IO, D>(cs + tt * CS, i, p[tt], f, scale);
         }

@@ -505,6 +505,14 @@ typedef struct {
   int32_t* d_status;      /* of gdn_qk_norm_rope, or NULL (device; gdn_kv_append takes its own) */
 } gdn_rope_params;
 
+/* Positions with several axes (time, height and width of images and video): pair i
+ * of channels turns by the position on its own axis. */
+#define GDN_ROPE_MAX_AXES 4
+typedef struct {
+  int32_t count;     /* axes, 1 .. GDN_ROPE_MAX_AXES */
+  uint8_t pair[128]; /* [rot_dim / 2 are read] axis of each pair, below count */
+} gdn_rope_axes;
+
 typedef struct {
   void* k;                    /* [num_pages][h_kv][page_size][d] IO, 16-byte aligned */
   void* v;                    /* the same */
@@ -532,6 +540,19 @@ typedef struct {
 int gdn_qk_norm_rope(const gdn_attn_dims* dims, const gdn_rope_params* params, const gdn_view* q,
                      const gdn_view* k, const int32_t* positions, int64_t n, void* q_out,
                      void* k_out, gdn_stream_t stream);
+
+/*
+ * gdn_qk_norm_rope_axes -- gdn_qk_norm_rope where every token has a position on
+ * each of several axes: pair i turns by positions[axes->pair[i]][t] * inv_freq[i].
+ *   axes       read on the host during the call; a count outside its range, or
+ *              a pair below rot_dim / 2 whose axis is not below it: GDN_EINVAL
+ *   positions  [axes->count][n] int32 (device)
+ * All else as in gdn_qk_norm_rope, which it equals where all axes agree.
+ */
+int gdn_qk_norm_rope_axes(const gdn_attn_dims* dims, const gdn_rope_params* params,
+                          const gdn_rope_axes* axes, const gdn_view* q, const gdn_view* k,
+                          const int32_t* positions, int64_t n, void* q_out, void* k_out,
+                          gdn_stream_t stream);
 
 /*
  * gdn_kv_append -- the new tokens' keys and values go into the paged cache,
@@ -613,6 +634,128 @@ int gdn_attn_decode(const gdn_attn_dims* dims, const gdn_view* q, const gdn_kv_c
                     const int32_t* seq_lens, int32_t n, int64_t shared_len, const gdn_view* gate,
                     void* o, void* workspace, size_t workspace_bytes, int32_t* d_status,
                     gdn_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * A paged cache held in 8 bits: half the bytes that a decoded token reads.  Keys
+ * and values are e4m3 numbers (four significant bits, largest 448), and every
+ * GDN_KV8_BLOCK tokens of one head share a scale for their keys and one for their
+ * values; a stored number stands for itself times its block's scale.
+ *   k, v       [num_pages][h_kv][page_size][d] e4m3
+ *   k_scale, v_scale  [num_pages][h_kv][page_size / GDN_KV8_BLOCK] fp32
+ * gdn_kv8_append makes each scale a power of two: the smallest 2^e, e from -40 to 40,
+ * with which the largest of the block's values so far is at most 448.  (A number with
+ * a floating point gains nothing from finer scales, and where a later token makes
+ * a block's scale grow, what it holds already is divided by a power of two:
+ * exact but for the smallest, which lose the bits below 2^-9 of the new scale.)
+ * Values above 448 * 2^40 are stored as that, Inf and NaN as NaN.
+ * The calls below take GDN_BF16 and GDN_FP16, and a token's place in the cache
+ * apart from its rotary positions: places count a sequence's cached tokens
+ * from 0, whatever positions they were rotated by and whichever were evicted
+ * between them.  The scales need no initial value.
+ * ------------------------------------------------------------------------- */
+#define GDN_KV8_BLOCK 16
+
+typedef struct {
+  void* k;                    /* e4m3, 16-byte aligned */
+  void* v;                    /* the same */
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table; /* [num_seqs][pages_per_seq] int32 (device) */
+  int64_t num_pages;
+  int32_t num_seqs;
+  int32_t pages_per_seq;
+} gdn_kv8_cache;
+
+/*
+ * gdn_kv8_append -- norm and rotate q and k as gdn_qk_norm_rope (axes null) or
+ * gdn_qk_norm_rope_axes does, and store k and v in the cache (from fp32, rounded
+ * once).  Sequence b of the call, 0 <= b < num_seqs <= cache->num_seqs, has the
+ * rows cu_seqlens[b] .. cu_seqlens[b+1], which go to its places starts[b],
+ * starts[b] + 1, ...
+ *   positions  [axes' count, or 1][n] int32 (device): for the rotation alone
+ *   cu_seqlens [num_seqs+1] int32 (device): 0 = cu[0] <= cu[1] <= ... = n, else
+ *              GDN_DEV_BAD_CU_SEQLENS and nothing is written.  NULL: row t is
+ *              sequence t (a decode step), num_seqs = n (else GDN_EINVAL)
+ *   starts     [num_seqs] int32 (device): tokens that the sequence holds already.
+ *              < 0: its rows are padding (q_out and k_out zeroed, nothing stored)
+ *   q_out      [n][h_q][d] IO; k_out [n][h_kv][d] IO or NULL: the packed keys
+ *              too, as gdn_qk_norm_rope_axes would leave them
+ * A row whose place its block table row cannot hold sets GDN_DEV_BAD_LENGTH, one whose
+ * page is outside [0, num_pages) GDN_DEV_BAD_PAGE; such a row is not stored (its
+ * q_out and k_out are written).  A place at a multiple of GDN_KV8_BLOCK starts its
+ * block anew; places behind the appended ones are left as they were.  No two
+ * sequences of a call may store into one page.
+ */
+int gdn_kv8_append(const gdn_attn_dims* dims, const gdn_rope_params* params,
+                   const gdn_rope_axes* axes, const gdn_view* q, const gdn_view* k,
+                   const gdn_view* v, const int32_t* positions, const int32_t* cu_seqlens,
+                   const int32_t* starts, int32_t num_seqs, int64_t n, const gdn_kv8_cache* cache,
+                   void* q_out, void* k_out, int32_t* d_status, gdn_stream_t stream);
+
+/*
+ * gdn_kv8_gather -- the cached tokens as packed keys and values, for a prompt
+ * that continues behind them (gdn_attn_prefill with these as its keys): row
+ * cu_seqlens[b] + p receives place p of sequence b, rounded to IO.
+ *   cu_seqlens [num_seqs+1] int32 (device), as gdn_kv8_append takes it with n = total
+ *   k_out, v_out  [total][h_kv][d] IO, 16-byte aligned; either may be NULL
+ * A place that the block table row cannot hold sets GDN_DEV_BAD_LENGTH, a page outside
+ * [0, num_pages) GDN_DEV_BAD_PAGE; such rows are zeros.
+ */
+int gdn_kv8_gather(const gdn_attn_dims* dims, const gdn_kv8_cache* cache,
+                   const int32_t* cu_seqlens, int32_t num_seqs, int64_t total, void* k_out,
+                   void* v_out, int32_t* d_status, gdn_stream_t stream);
+
+/* Bytes of device workspace gdn_attn_decode_kv8 needs for n rows (0 on bad
+ * arguments); capacity: 0, or with weights the tokens of a block table row,
+ * pages_per_seq * page_size. */
+size_t gdn_attn_decode_kv8_workspace_size(const gdn_attn_dims* dims, int32_t n, int64_t capacity);
+
+/*
+ * gdn_attn_decode_kv8 -- gdn_attn_decode over the 8-bit cache: one query token
+ * for each of n rows, row b seeing the first seq_lens[b] places of sequence b.
+ *   seq_lens, gate, o, workspace  as in gdn_attn_decode
+ *   weights    [num_seqs][h_kv][pages_per_seq * page_size] fp32 (device) or NULL: what
+ *              each cached token receives is added to it, weights[b][j][p] += the sum
+ *              over head j's query heads of the softmax weight of place p (nothing
+ *              else of it is touched)
+ * Scores, softmax statistics, weights and the accumulated output are fp32; a query
+ * row is taken in fp16, times a power of two of its own (a bf16 one keeps all its
+ * bits but those below 2^-24 of its largest element), and the softmax weights, times
+ * the values' scale, are rounded to fp16 for the product with v (relative to each,
+ * down to 2^-26 of the row's largest contribution).  The stored numbers
+ * enter both products as they are.  Scales have to be 0, or finite and from 2^-40
+ * to 2^40.  What the cache holds beyond a sequence's length never reaches its output.
+ */
+int gdn_attn_decode_kv8(const gdn_attn_dims* dims, const gdn_view* q, const gdn_kv8_cache* cache,
+                        const int32_t* seq_lens, int32_t n, const gdn_view* gate, float* weights,
+                        void* o, void* workspace, size_t workspace_bytes, int32_t* d_status,
+                        gdn_stream_t stream);
+
+/*
+ * gdn_kv8_evict -- cuts sequences down to `keep` cached tokens, each key/value head
+ * its own: of a sequence b with more, head j keeps the first `first` places, the
+ * last `last` ones and those between with the greatest weights[b][j][p] (negative
+ * and NaN count as 0; of equal ones the lowest place), in the order that they have.
+ * What is kept is copied to the pages of `to`, whose blocks take the largest of
+ * their tokens' scales; the old pages are left as they were (a prefix that other
+ * sequences share stays theirs) and are the caller's again after the call.
+ * A shorter sequence is copied whole.
+ *   weights      [from->num_seqs][h_kv][from's pages_per_seq * page_size] fp32
+ *   seq_lens     [n] int32 (device), n <= from->num_seqs, to->num_seqs; 0 or less: nothing
+ *   to           cache with pages_per_seq * page_size >= keep, none of whose pages
+ *                for these sequences may be one that they read
+ *   weights_out  [to->num_seqs][h_kv][to's pages_per_seq * page_size] fp32 or NULL: the kept
+ *                tokens' weights, zeros behind them; not weights itself
+ *   new_lens     [n] int32: min(seq_lens, keep); not seq_lens itself
+ *   kept         [n][h_kv][keep] int32: the places that were kept, -1 behind the last
+ * keep > 0; first, last >= 0; first + last <= keep.  A sequence that its block table
+ * row cannot hold sets GDN_DEV_BAD_LENGTH and is cut to what it holds; a page outside
+ * [0, num_pages) sets GDN_DEV_BAD_PAGE and its rows are not copied.
+ */
+int gdn_kv8_evict(const gdn_attn_dims* dims, const gdn_kv8_cache* from, const float* weights,
+                  const int32_t* seq_lens, int32_t n, int32_t keep, int32_t first, int32_t last,
+                  const gdn_kv8_cache* to, float* weights_out, int32_t* new_lens, int32_t* kept,
+                  int32_t* d_status, gdn_stream_t stream);
 
 /* Static description of a gdn_status code (library plumbing).  The string is
  * owned by the library and valid for the life of the process. */
