@@ -4,29 +4,36 @@
 //   s_p = c a_p (q . k8_p),   o = sum_p 2^(s_p - M) b_p v8_p / sum_p 2^(s_p - M).
 //
 // Every cached byte is used for one token's few query heads only, so the reads of the
-// cache bound it; at half the bytes per key, what a key costs to compute has half the time.
-// The products therefore have the keys, and the channels of the values, on the
+// cache bound it, and at half the bytes per key, what a key costs to compute has half the
+// time.  The products therefore have the keys, and the channels of the values, on the
 // 16-row side of mma.sync m16n8k16 and the query heads on its 8-row side: S^T = K Q^T
 // and O^T = V^T P^T, half the instructions and half the exponentials of the
-// other way round for up to 8 heads.  An e4m3 number is an fp16 number: one conversion of
-// two numbers per register pair, no scale applied to any of them.  K's fragments
-// come straight from ldmatrix of bytes, with the channels of a 16-byte chunk in an order that
-// Q's share (a sum does not mind); V's from its transposing form, two keys' bytes
-// put side by side by one permutation.  P^T passes from the accumulators' layout
-// to the operand's by a transpose between lanes.
+// other way round for up to 8 heads.  An e4m3 number is an fp16 number: one conversion
+// for two of them, no scale applied to any.  (mma.sync of e4m3 itself is put together
+// from conversions and fp16 products here: 29 cycles of a scheduler where an m16n8k16
+// takes 8.5, and with the operands in two or three terms each the step of 64
+// sequences took 165 us instead of 123.)  K's fragments come straight from ldmatrix of
+// bytes, with the channels of a 16-byte chunk in an order that Q's share (a sum does
+// not mind); V's from its transposing form, two keys' bytes put side by side by one
+// permutation.  P^T passes from the accumulators' layout to the operand's by a transpose
+// between lanes.
 //
 // Two references per head: M for the sum of the weights, and M' for the largest
 // contribution s_p + log2 b_p, by which the weights are scaled for the product with v
 // in fp16: blocks of large and small values may follow each other in any order
-// without either leaving fp16's range unless it is negligible beside the other.
+// without either leaving fp16's range unless it is negligible beside the other.  Both may
+// lag behind the true maxima by 2^3.9 (M by more), so that they move at the first keys only
+// and no lane asks the others for a maximum in between.
 //
-// The work is cut by bytes: all units of 128 keys of all (sequence, key/value head)
-// items form one line, which the resident CTAs share in equal runs.  A run that
-// covers an item writes its output; an item cut by a run's border leaves
-// partial results that the merge kernel joins (the borders follow from seq_lens
-// alone).  Few keys in all: a cluster of CTAs per item, joined through distributed shared
-// memory, no second launch.  Within a CTA one warp keeps TMA loads in flight, eight warps
-// take one block of 16 keys of each unit, with one scale each for K and V.
+// The work is cut by bytes: all units of 64 keys of all (sequence, key/value head)
+// items form one line, with a little added for the beginning and end of each item, which
+// the resident CTAs share in equal runs.  A run that covers an item writes its output; an
+// item cut by a run's border leaves partial results that the merge kernel joins (the
+// borders follow from seq_lens alone).  Few keys in all: a cluster of CTAs per item, joined
+// through distributed shared memory, no second launch.  Within a CTA one warp keeps TMA
+// loads in flight (each item's queries among them); two warps take 32 keys of a unit
+// each, and two groups of two every other unit.  Two small CTAs per SM: one's products fill
+// the time that the other takes to join its warps between items.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -38,41 +45,55 @@ namespace attn {
 
 using namespace gdn::tc;
 
-constexpr int K8_KEYS = 128;             // keys per unit
-constexpr int K8_WARPS = 8;              // consumer warps, one block of 16 keys of a unit each
+constexpr int K8_KEYS = 64;              // keys per unit
+constexpr int K8_TILE = 32;              // keys of a warp's tile: two blocks
+constexpr int K8_GROUP = K8_KEYS / K8_TILE;   // warps that share a unit
+constexpr int K8_BLOCKS = K8_KEYS / KV8_BLOCK;
+constexpr int K8_WARPS = 4;              // consumer warps
 constexpr int K8_THREADS = 32 * (K8_WARPS + 1);
 constexpr int K8_MAX_STAGES = 8;
-constexpr int K8_FEW_UNITS = 4;
-static_assert(K8_KEYS == K8_WARPS * KV8_BLOCK, "a warp's keys are one block");
+constexpr int K8_FEW_UNITS = 8;
+// What a unit and the ends of an item cost, as far as the cut goes.
+constexpr int K8_UNIT_COST = 4, K8_ITEM_COST = 3;
 
 // NT: query heads of an item in eights.
 template <int D, int NT>
 struct K8Cfg {
   static constexpr int ROWS = 8 * NT;
+  // O^T takes 4 NT registers per 16 channels.  Where a warp does not have them, the two groups
+  // of warps take every unit and half of the channels each (the scores twice).
+  static constexpr bool HALVES = NT * D > 256;
+  static constexpr int JOIN = HALVES ? K8_GROUP : K8_WARPS;   // warps that add up their O
   static constexpr uint32_t TILE = K8_KEYS * D;            // one of K, V
   static constexpr uint32_t STAGE = 2 * TILE;
   static constexpr uint32_t OBUF = ROWS * D * 4;           // joining the warps' O
   // Q's fragments in registers, unless they and O do not fit there.
-  static constexpr bool Q_REGS = NT * D <= 256;
+  static constexpr bool Q_REGS = NT == 1;
   static constexpr uint32_t QBUF = Q_REGS ? 0 : D / 16 * NT * 32 * 8;
-  static constexpr uint32_t HEAD = (3072 + OBUF + QBUF + 1023) / 1024 * 1024;
-  static constexpr int PER_SM = D == 256 ? 1 : 2;
+  static constexpr uint32_t Q_ROW = D * 2 + 16;            // an item's queries as they come
+  static constexpr uint32_t HEAD = (2048 + OBUF + QBUF + ROWS * Q_ROW + 1023) / 1024 * 1024;
+  static constexpr int PER_SM = D == 64 ? 3 : 2;
   static constexpr int CTAS = SMS * PER_SM;
   static constexpr int FIT = (int)((233472u / PER_SM - 1024u - HEAD) / STAGE);
   static constexpr int STAGES = FIT < K8_MAX_STAGES ? FIT : K8_MAX_STAGES;
+  // An odd number of stages passes each from group to group.  A wait by parity tells a phase from
+  // the next one only, so each group has barriers of its own for each stage then.
+  static constexpr int BARS = HALVES || STAGES % 2 == 0 ? STAGES : 2 * STAGES;
   static constexpr uint32_t SMEM = HEAD + STAGES * STAGE;
+  static_assert(BARS <= 2 * K8_MAX_STAGES, "room for the barriers");
   static_assert(STAGES >= 2, "a unit in flight beside the one in use");
 };
 
 struct __align__(16) K8Shared {
-  uint64_t full[K8_MAX_STAGES], empty[K8_MAX_STAGES];
-  float scale[K8_MAX_STAGES][2 * K8_WARPS];   // of the unit's blocks: keys', values'
-  float m[K8_WARPS][16], l[K8_WARPS][16];
+  uint64_t full[2 * K8_MAX_STAGES], empty[2 * K8_MAX_STAGES], q_full, q_empty;
+  float scale[K8_MAX_STAGES][2 * K8_BLOCKS];   // of the unit's blocks: keys', values'
+  float m[2][K8_WARPS][16], l[2][K8_WARPS][16];   // of every other item
   float2 ml[16];         // of the whole CTA, for its cluster
   int64_t sum[K8_WARPS + 1], found_first;
+  int64_t walk[K8_WARPS + 1][5];   // each warp's K8Walk
   int32_t found;
 };
-static_assert(sizeof(K8Shared) <= 3072, "shared bookkeeping");
+static_assert(sizeof(K8Shared) <= 2048, "shared bookkeeping");
 
 struct K8Args {
   GdnKv8DecodeArgs a;
@@ -84,25 +105,36 @@ struct K8Args {
   int32_t merge_rows;    // rows of an item that a CTA of the merge joins
 };
 
-__device__ __forceinline__ int64_t k8_len(const K8Args& p, int b) {
-  int64_t len = p.a.seq_lens[b];
+// Keys of a sequence by its entry of seq_lens (a block table row holds fewer than 2^31).
+__device__ __forceinline__ int k8_clip(const K8Args& p, int len) {
   if (len > p.a.capacity) {
     set_status(p.a.d_status, GDN_DEV_BAD_LENGTH);
-    len = p.a.capacity;
+    len = (int)p.a.capacity;
   }
-  return len > 0 ? len : 0;
+  return max(len, 0);
 }
-__device__ __forceinline__ int64_t units_of(int64_t keys) { return (keys + K8_KEYS - 1) / K8_KEYS; }
+__device__ __forceinline__ int k8_len(const K8Args& p, int b) {
+  return k8_clip(p, p.a.seq_lens[b]);
+}
+__device__ __forceinline__ int units_of(int keys) {
+  return keys / K8_KEYS + (keys % K8_KEYS != 0 ? 1 : 0);
+}
 
-// Run c of the line is [start(c), start(c + 1)).
+// An item's place on the line: nt units and its ends.
+__device__ __forceinline__ int64_t span_of(int nt) {
+  return nt > 0 ? (int64_t)nt * K8_UNIT_COST + K8_ITEM_COST : 0;
+}
+// Run c of the line is [start(c), start(c + 1)); a unit is in the run that its first point is
+// in.  (No run is shorter than a unit.)
 struct K8Line {
-  int64_t units;
+  int64_t length;
   int ctas;
-  __device__ __forceinline__ K8Line(int64_t n, int most) : units(n), ctas(n < most ? (int)n : most) {}
-  __device__ __forceinline__ int64_t start(int c) const { return units * c / ctas; }
-  // The CTA whose run holds unit u: the last whose run starts at or before it.
+  __device__ __forceinline__ K8Line(int64_t n, int most)
+      : length(n), ctas(n < (int64_t)most * K8_UNIT_COST ? max((int)(n / K8_UNIT_COST), 1) : most) {}
+  __device__ __forceinline__ int64_t start(int c) const { return length * c / ctas; }
+  // The CTA whose run holds point u: the last whose run starts at or before it.
   __device__ __forceinline__ int owner(int64_t u) const {
-    return (int)(((u + 1) * ctas - 1) / units);
+    return (int)(((u + 1) * ctas - 1) / length);
   }
 };
 
@@ -137,37 +169,43 @@ __device__ __forceinline__ void k8_put_four(const GdnKv8DecodeArgs& a, int b, in
       make_uint2(pack2<IO>(y[0], y[1]), pack2<IO>(y[2], y[3]));
 }
 
-// The run [w, end) of units, item by item.
+// The run [w, end) of the line, item by item.  (In shared memory, one for each warp: only
+// looked at between items, when the accumulators leave no registers for it.)
 struct K8Segment {
   int b, hs;             // sequence, and key/value head * subs + sub
-  int64_t keys;          // of the sequence
-  int64_t t0, t1;        // units of the item in this run
-  bool whole;            // all of the item is in this run
+  int keys;              // of the sequence
+  int t0, t1;            // units of the item in this run
+  int whole;             // all of the item is in this run
 };
 struct K8Walk {
-  int64_t w, end, item_first, nt, keys;
-  int b, hs;
-  __device__ bool next(const K8Args& p, int heads, K8Segment& s) {
-    if (w >= end) return false;
-    while (w >= item_first + nt) {   // on to the item that holds unit w
-      item_first += nt;
+  int64_t w, end, item_first;
+  int nt, keys, b, hs;   // of the item to come
+  // ahead: the entry of seq_lens of sequence b + 1, on its way while the items of b are worked on.
+  __device__ bool next(const K8Args& p, int heads, K8Segment& s, int& ahead) {
+    for (;;) {
+      if (b >= p.a.n || item_first >= end) return false;
+      const int64_t from = max(w - item_first, (int64_t)0);
+      const int64_t to = (end - item_first + K8_UNIT_COST - 1) / K8_UNIT_COST;
+      s.t0 = (int)min((from + K8_UNIT_COST - 1) / K8_UNIT_COST, (int64_t)nt);
+      s.t1 = (int)min(to, (int64_t)nt);
+      s.whole = s.t0 == 0 && s.t1 == nt;
+      s.b = b;
+      s.hs = hs;
+      s.keys = keys;
+      item_first += span_of(nt);
       if (++hs == heads) {
         hs = 0;
-        do {
-          ++b;
-          keys = k8_len(p, b);
+        ++b;
+        keys = k8_clip(p, ahead);
+        nt = units_of(keys);
+        while (b < p.a.n && nt == 0) {
+          if (++b < p.a.n) keys = k8_len(p, b);
           nt = units_of(keys);
-        } while (nt == 0);
+        }
+        if (b + 1 < p.a.n) ahead = p.a.seq_lens[b + 1];
       }
+      if (s.t0 < s.t1) return true;
     }
-    s.b = b;
-    s.hs = hs;
-    s.keys = keys;
-    s.t0 = w - item_first;
-    s.t1 = min(end - item_first, nt);
-    s.whole = s.t0 == 0 && s.t1 == nt;
-    w = item_first + s.t1;
-    return true;
   }
 };
 
@@ -199,10 +237,12 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
   using C = K8Cfg<D, NT>;
   constexpr int CHUNKS = D / 16;
   constexpr float UP = WeightRange<__half>::SCALE_LOG2, LAG = WeightRange<__half>::LAG_LOG2;
+  constexpr int W = K8_WARPS, OWN = C::HALVES ? CHUNKS / 2 : CHUNKS;   // chunks of a warp's O
   extern __shared__ __align__(1024) unsigned char smem[];
   K8Shared* sh = reinterpret_cast<K8Shared*>(smem);
-  float* obuf = reinterpret_cast<float*>(smem + 3072);
-  uint2* qbuf = reinterpret_cast<uint2*>(smem + 3072 + C::OBUF);   // [chunk][nt][lane]
+  float* obuf = reinterpret_cast<float*>(smem + 2048);
+  const unsigned char* q_in = smem + 2048 + C::OBUF;
+  uint2* qbuf = reinterpret_cast<uint2*>(smem + 2048 + C::OBUF + C::ROWS * C::Q_ROW);   // [chunk][nt][lane]
   const GdnKv8DecodeArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(smem) + C::HEAD;
@@ -211,10 +251,12 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
 
   pdl_launch();
   if (tid == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < C::BARS; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], K8_WARPS);
+      mbar_init(&sh->empty[s], C::HALVES ? W : K8_GROUP);
     }
+    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, W);
     fence_mbar_init();
   }
   K8Walk walk;
@@ -227,31 +269,31 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
     walk.keys = k8_len(p, walk.b);
     walk.nt = units_of(walk.keys);
     walk.item_first = 0;
-    w0 = walk.nt * rank / p.cluster;
-    w1 = walk.nt * (rank + 1) / p.cluster;
+    w0 = (int64_t)walk.nt * rank / p.cluster * K8_UNIT_COST;
+    w1 = (int64_t)walk.nt * (rank + 1) / p.cluster * K8_UNIT_COST;
     if (tid < 16) sh->ml[tid] = make_float2(-INFINITY, 0.f);
     __syncthreads();
   } else {
-    // ---- this CTA's run of units ----
-    int64_t total = 0, units = 0, before = 0;
+    // ---- this CTA's run of the line ----
+    int64_t total = 0, span = 0, before = 0;
     for (int base = 0; base < n; base += K8_THREADS) {
       const int b = base + tid;
-      units = b < n ? units_of(k8_len(p, b)) * heads : 0;
-      total += block_scan(units, sh->sum, K8_WARPS + 1, before);
+      span = b < n ? span_of(units_of(k8_len(p, b))) * heads : 0;
+      total += block_scan(span, sh->sum, W + 1, before);
     }
     const K8Line line(total, p.ctas);
     const int c = (int)blockIdx.x;
-    w0 = c < line.ctas ? line.start(c) : 0;
-    w1 = c < line.ctas ? line.start(c + 1) : 0;
+    w0 = total > 0 && c < line.ctas ? line.start(c) : 0;
+    w1 = total > 0 && c < line.ctas ? line.start(c + 1) : 0;
     int64_t seen = 0;
     for (int base = 0; base < n && w0 < w1; base += K8_THREADS) {
       const int b = base + tid;
       int64_t all = total;
       if (n > K8_THREADS) {   // else the scan above has it all
-        units = b < n ? units_of(k8_len(p, b)) * heads : 0;
-        all = block_scan(units, sh->sum, K8_WARPS + 1, before);
+        span = b < n ? span_of(units_of(k8_len(p, b))) * heads : 0;
+        all = block_scan(span, sh->sum, W + 1, before);
       }
-      if (w0 >= seen + before && w0 < seen + before + units) {
+      if (w0 >= seen + before && w0 < seen + before + span) {
         sh->found = b;
         sh->found_first = seen + before;
       }
@@ -267,13 +309,32 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
       walk.b = sh->found;
       walk.keys = k8_len(p, walk.b);
       walk.nt = units_of(walk.keys);
-      walk.hs = (int)((w0 - sh->found_first) / walk.nt);
-      walk.item_first = sh->found_first + walk.hs * walk.nt;
+      walk.hs = (int)((w0 - sh->found_first) / span_of(walk.nt));
+      walk.item_first = sh->found_first + walk.hs * span_of(walk.nt);
     }
-    K8Segment g;
+    static_assert(sizeof(K8Walk) <= sizeof(sh->walk[0]), "room for a walk");
+    K8Walk& at = *reinterpret_cast<K8Walk*>(sh->walk[warp]);
+    if (lane == 0) at = walk;
+    __syncwarp();
+    // one lane walks, all of them read what it found
+    int ahead = 0;
+    if (lane == 0 && walk.b + 1 < n) ahead = a.seq_lens[walk.b + 1];
+    auto next = [&](K8Segment& g) {
+      int found = 0;
+      if (lane == 0) found = at.next(p, heads, g, ahead);
+      found = __shfl_sync(0xffffffffu, found, 0);
+      g.b = __shfl_sync(0xffffffffu, g.b, 0);
+      g.hs = __shfl_sync(0xffffffffu, g.hs, 0);
+      g.keys = __shfl_sync(0xffffffffu, g.keys, 0);
+      g.t0 = __shfl_sync(0xffffffffu, g.t0, 0);
+      g.t1 = __shfl_sync(0xffffffffu, g.t1, 0);
+      g.whole = __shfl_sync(0xffffffffu, g.whole, 0);
+      return found != 0;
+    };
+    K8Segment g = {};
     bool ok = true;
-    int j = 0;                       // units so far: the ring's position
-    if (warp == K8_WARPS) {
+    int j = 0, items = 0;            // units and items so far: the rings' positions
+    if (warp == W) {
       // ---- loads: each lane one box of the unit (K or V, rows, column block), and one
       // of its 16 blocks' scales ----
       constexpr int COLS = D == 256 ? 2 : 1;
@@ -281,18 +342,31 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
       const bool boxed = lane < 2 * per_kv, is_v = lane >= per_kv;
       const int box = is_v ? lane - per_kv : lane;
       const int cb = box % COLS, r = box / COLS * p.box_rows;
-      const int sr = lane % K8_WARPS * KV8_BLOCK;
-      const float* const scales = lane < K8_WARPS ? a.cache.k_scale : a.cache.v_scale;
-      while (ok && walk.next(p, heads, g)) {
+      const int sr = lane % K8_BLOCKS * KV8_BLOCK;
+      const float* const scales = lane < K8_BLOCKS ? a.cache.k_scale : a.cache.v_scale;
+      while (ok && next(g)) {
         const int kvh = g.hs / p.subs;
         const int32_t* table = a.cache.block_table + (int64_t)g.b * a.cache.pages_per_seq;
-        auto page_at = [&](int64_t t, int row) {
-          const int64_t pos = t * K8_KEYS + row;
+        // the item's queries, once the consumers have the last item's
+        if (items > 0) ok = mbar_wait(&sh->q_empty, (items - 1) & 1, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ++items;
+        const int rows = k8_rows<NT>(p, g.hs);
+        if (lane == 0) mbar_expect_tx(&sh->q_full, (uint32_t)rows * D * 2);
+        __syncwarp();
+        if (lane < rows)
+          bulk_load(smem_u32(q_in) + (uint32_t)lane * C::Q_ROW,
+                    reinterpret_cast<const IO*>(a.q.data) + (int64_t)g.b * a.q.token_stride +
+                        (int64_t)(k8_head<NT>(p, g.hs) + lane) * a.q.head_stride,
+                    D * 2, &sh->q_full);
+        auto page_at = [&](int t, int row) {
+          const int64_t pos = (int64_t)t * K8_KEYS + row;
           return t < g.t1 && pos < g.keys ? __ldg(table + (pos >> a.page_shift)) : 0;
         };
-        auto scale_at = [&](int64_t t, int32_t page) {
-          const int64_t pos = t * K8_KEYS + sr;
-          if (lane >= 2 * K8_WARPS || t >= g.t1 || pos >= g.keys || page < 0 ||
+        auto scale_at = [&](int t, int32_t page) {
+          const int64_t pos = (int64_t)t * K8_KEYS + sr;
+          if (lane >= 2 * K8_BLOCKS || t >= g.t1 || pos >= g.keys || page < 0 ||
               page >= a.cache.num_pages)
             return 0.f;
           return __ldg(scales + ((((int64_t)page * a.h_kv + kvh) << a.page_shift) +
@@ -302,22 +376,24 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
         int32_t page = boxed ? page_at(g.t0, r) : 0, page1 = boxed ? page_at(g.t0 + 1, r) : 0;
         int32_t spage1 = page_at(g.t0 + 1, sr);
         float scale = scale_at(g.t0, page_at(g.t0, sr));
-        for (int64_t t = g.t0; t < g.t1 && ok; ++t, ++j) {
+        for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
           const float scale1 = scale_at(t + 1, spage1);
           const int32_t page2 = boxed ? page_at(t + 2, r) : 0, spage2 = page_at(t + 2, sr);
           const int s = j % C::STAGES;
-          if (j >= C::STAGES)
-            ok = mbar_wait(&sh->empty[s], ((j / C::STAGES) - 1) & 1, a.wait_ns);
+          uint64_t* full = &sh->full[j % C::BARS];
+          if (j >= C::STAGES) {
+            const int was = j - C::STAGES;
+            ok = mbar_wait(&sh->empty[was % C::BARS], (was / C::BARS) & 1, a.wait_ns);
+          }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const int64_t left = g.keys - t * K8_KEYS;
-          const int there =
-              (int)min((int64_t)K8_KEYS, (left + p.box_rows - 1) / p.box_rows * p.box_rows);
+          const int left = min(g.keys - t * K8_KEYS, K8_KEYS);
+          const int there = (left + p.box_rows - 1) / p.box_rows * p.box_rows;
           // (the test's: of the first CTA, or of the last one of the first cluster)
           const bool withheld = a.withhold && j == 0 && blockIdx.x == (FEW ? p.cluster - 1 : 0);
-          if (lane < 2 * K8_WARPS) sh->scale[s][lane] = scale;
+          if (lane < 2 * K8_BLOCKS) sh->scale[s][lane] = scale;
           __syncwarp();
-          if (lane == 0 && !withheld) mbar_expect_tx(&sh->full[s], (uint32_t)there * D * 2);
+          if (lane == 0 && !withheld) mbar_expect_tx(full, (uint32_t)there * D * 2);
           __syncwarp();
           if (boxed && r < there && !withheld) {
             if (page < 0 || page >= a.cache.num_pages) {
@@ -328,7 +404,7 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
                                 ((t * K8_KEYS + r) & ((1 << a.page_shift) - 1));
             tma_box(ring + (uint32_t)s * C::STAGE + (is_v ? C::TILE : 0u) +
                         (uint32_t)(cb * K8_KEYS + r) * (D < 128 ? 64u : 128u),
-                    is_v ? &vmap : &kmap, (int)row, cb, &sh->full[s]);
+                    is_v ? &vmap : &kmap, (int)row, cb, full);
           }
           page = page1;
           page1 = page2;
@@ -338,133 +414,173 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
       }
       // (the consumers wait for these too, unless they have given up)
       for (int x = max(0, j - C::STAGES); x < j; ++x)
-        mbar_wait(&sh->full[x % C::STAGES], (x / C::STAGES) & 1, GRACE_NS);
+        mbar_wait(&sh->full[x % C::BARS], (x / C::BARS) & 1, GRACE_NS);
+      if (items > 0) mbar_wait(&sh->q_full, (items - 1) & 1, GRACE_NS);
     } else {
-      // ---- 16 keys of every unit, with this warp's own references, sums and O ----
+      // ---- 32 keys of every unit of this warp's group, with its own reference, sum and O ----
+      const int group = warp / K8_GROUP, part = warp % K8_GROUP;
+      const int ch0 = C::HALVES ? group * OWN : 0;
       const int row8 = lane >> 2, col = (lane & 3) * 2;   // key or channel pair; heads col, col + 1
       const int mi = lane >> 3, mr = lane & 7;            // this lane's row of an ldmatrix
-      const int l_key = warp * KV8_BLOCK + (mi & 1) * 8 + mr, l_chunk = mi >> 1;
-      while (walk.next(p, heads, g)) {
+      const int k_key = part * K8_TILE + (mi & 1) * 8 + mr, v_key = part * K8_TILE + mi * 8 + mr;
+      while (next(g)) {
         const int h0 = k8_head<NT>(p, g.hs), rows = k8_rows<NT>(p, g.hs);
         // Q: head row8 of each eight; the channels of a chunk in the order of K's bytes.
         // Each row times a power of two that brings its largest element to [1, 2).
         uint2 q[C::Q_REGS ? CHUNKS : 1][NT];
         float cs[NT][2];                                  // scale of heads col, col + 1
         if (!C::Q_REGS) k8_consumers_bar();               // the last item's are in use until here
+        if (ok) ok = mbar_wait(&sh->q_full, items & 1, a.wait_ns);
+        __syncwarp();
+        ++items;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int head = nt * 8 + row8;
+          const unsigned char* src = q_in + head * C::Q_ROW + (lane & 3) * 8;
           uint2 w[CHUNKS];
           float top = 0.f;
 #pragma unroll
           for (int ch = 0; ch < CHUNKS; ++ch) {
-            w[ch] = make_uint2(0, 0);
-            if (head < rows)
-              w[ch] = *reinterpret_cast<const uint2*>(
-                  reinterpret_cast<const IO*>(a.q.data) + (int64_t)g.b * a.q.token_stride +
-                  (int64_t)(h0 + head) * a.q.head_stride + ch * 16 + (lane & 3) * 4);
+            w[ch] = head < rows ? *reinterpret_cast<const uint2*>(src + ch * 32) : make_uint2(0, 0);
             const float2 x = unpack2<IO>(w[ch].x), y = unpack2<IO>(w[ch].y);
             top = max3(max3(top, fabsf(x.x), fabsf(x.y)), fabsf(y.x), fabsf(y.y));
           }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           // (an Inf, and a row of zeros or of subnormals, as it is)
-          const uint32_t ex = __float_as_uint(top) >> 23;
-          const bool plain = ex == 0 || ex == 255;
-          const int up = plain ? 0 : max(-126, min(127, 127 - (int)ex));
+          const int ex = (int)(__float_as_uint(top) >> 23);
+          const int up = ex == 0 || ex == 255 ? 0 : max(-126, min(126, 127 - ex));
           const float f = pow2(up);
 #pragma unroll
           for (int ch = 0; ch < CHUNKS; ++ch) {
             const float2 x = unpack2<IO>(w[ch].x), y = unpack2<IO>(w[ch].y);
             w[ch] = make_uint2(pack2<__half>(x.x * f, x.y * f), pack2<__half>(y.x * f, y.y * f));
-            if (C::Q_REGS) q[ch][nt] = w[ch];
+            if (C::Q_REGS) q[C::Q_REGS ? ch : 0][nt] = w[ch];
             else if (warp == nt) qbuf[(ch * NT + nt) * 32 + lane] = w[ch];
           }
           const float back = a.scale_log2 * pow2(-up);
           cs[nt][0] = __shfl_sync(0xffffffffu, back, col * 4);
           cs[nt][1] = __shfl_sync(0xffffffffu, back, col * 4 + 4);
         }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&sh->q_empty);
         if (!C::Q_REGS) k8_consumers_bar();
-        float o[CHUNKS][NT][4];
+        float o[OWN][NT][4];
 #pragma unroll
-        for (int ch = 0; ch < CHUNKS; ++ch)
+        for (int ch = 0; ch < OWN; ++ch)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
             o[ch][nt][0] = o[ch][nt][1] = o[ch][nt][2] = o[ch][nt][3] = 0.f;
-        // of heads col, col + 1: references of the sum and of the contributions, sum
-        float m[NT][2], mv[NT][2], l[NT][2];
+        // of heads col, col + 1: references of the sum and of the contributions, sum, and what
+        // a weight is scaled by for the product, 2^(M - M' + UP)
+        float m[NT][2], mv[NT][2], l[NT][2], pf[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             m[nt][e] = mv[nt][e] = -INFINITY;
-            l[nt][e] = 0.f;
+            l[nt][e] = pf[nt][e] = 0.f;
           }
 
-        for (int64_t t = g.t0; t < g.t1; ++t, ++j) {
+        for (int t = g.t0; t < g.t1; ++t, ++j) {
+          if (!C::HALVES && (j & 1) != group) continue;
           const int s = j % C::STAGES;
-          if (ok) ok = mbar_wait(&sh->full[s], (j / C::STAGES) & 1, a.wait_ns);
+          if (ok) ok = mbar_wait(&sh->full[j % C::BARS], (j / C::BARS) & 1, a.wait_ns);
           __syncwarp();
-          const int left = (int)min((int64_t)K8_KEYS, g.keys - t * K8_KEYS) - warp * KV8_BLOCK;
+          const int left = min(K8_KEYS, g.keys - t * K8_KEYS) - part * K8_TILE;
           const uint32_t kt = ring + (uint32_t)s * C::STAGE, vt = kt + C::TILE;
           if (left > 0) {
-            const float ks = sh->scale[s][warp], vs = sh->scale[s][K8_WARPS + warp];
-            float sc[2][NT][4] = {};
+            float x[2][NT][4];   // [block][eight][key row8: 2 heads, row8 + 8: 2 heads]
+            {
+              float sc[2][2][NT][4] = {};   // [block][sums of even and odd chunks]
 #pragma unroll
-            for (int ch = 0; ch < CHUNKS; ch += 2) {
-              uint32_t w[4];
-              ldsm4(kt + chunk_at<D>(l_key, mr, ch + l_chunk), w);
+              for (int ch = 0; ch < CHUNKS; ch += 2) {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t ka[4];
-                e4m3x4_to_f16(w[2 * i], ka[0], ka[2]);
-                e4m3x4_to_f16(w[2 * i + 1], ka[1], ka[3]);
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t w[4];
+                  ldsm4(kt + chunk_at<D>(k_key + i * KV8_BLOCK, mr, ch + (mi >> 1)), w);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const uint2 b = C::Q_REGS ? q[C::Q_REGS ? ch + i : 0][nt]
-                                            : qbuf[((ch + i) * NT + nt) * 32 + lane];
-                  mma16816<__half>(sc[i][nt], ka, b.x, b.y);
+                  for (int h = 0; h < 2; ++h) {
+                    uint32_t ka[4];
+                    e4m3x4_to_f16(w[2 * h], ka[0], ka[2]);
+                    e4m3x4_to_f16(w[2 * h + 1], ka[1], ka[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                      const uint2 b = C::Q_REGS ? q[C::Q_REGS ? ch + h : 0][nt]
+                                                : qbuf[((ch + h) * NT + nt) * 32 + lane];
+                      mma16816<__half>(sc[i][h][nt], ka, b.x, b.y);
+                    }
+                  }
                 }
               }
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) x[i][nt][e] = sc[i][0][nt][e] + sc[i][1][nt][e];
             }
-            uint32_t pb[NT][2];
-            float mt[NT][2], x[NT][4];
-            const float lv = __log2f(vs);
+            if (left < K8_TILE) {
+              // Values past the end may be anything, and 0 x NaN is not 0: cleared.
+              constexpr int ROW = D / 16;
+              for (int i = lane; i < (K8_TILE - left) * ROW; i += 32) {
+                const int key = part * K8_TILE + left + i / ROW;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                 vt + chunk_at<D>(key, key & 7, i % ROW)),
+                             "r"(0)
+                             : "memory");
+              }
+              __syncwarp();
+            }
+            const float2 ks = *reinterpret_cast<const float2*>(&sh->scale[s][2 * part]);
+            const float2 vs = *reinterpret_cast<const float2*>(&sh->scale[s][K8_BLOCKS + 2 * part]);
+            const float lv[2] = {__log2f(vs.x), __log2f(vs.y)};
+            // A score in log2 units, less the reference.  (No fma: the reference is such a
+            // rounded product, and of scores beyond 2^30 the rounding alone would be more than an
+            // exponential can take.)
+            auto score = [&](int i, int nt, int e) {
+              const float y = __fmul_rn(x[i][nt][e], cs[nt][e & 1] * (i ? ks.y : ks.x));
+              return left < K8_TILE && i * KV8_BLOCK + row8 + (e >> 1) * 8 >= left ? -INFINITY : y;
+            };
             bool far = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float f = cs[nt][e] * ks;
-                x[nt][e] = row8 < left ? (sc[0][nt][e] + sc[1][nt][e]) * f : -INFINITY;
-                x[nt][2 + e] = row8 + 8 < left ? (sc[0][nt][2 + e] + sc[1][nt][2 + e]) * f : -INFINITY;
-                float v = fmaxf(x[nt][e], x[nt][2 + e]);
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                mt[nt][e] = v;
-                far |= v > m[nt][e] + LAG || v + lv > mv[nt][e] + LAG;
-              }
-            }
-            // A head's references follow from the head alone (they may lag behind by LAG).
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float y = fmaxf(score(i, nt, e), score(i, nt, 2 + e));
+                  far |= y > m[nt][e] + LAG || y + lv[i] > mv[nt][e] + LAG;
+                }
+            // A head's references follow from the head alone.
             if (__any_sync(0xffffffffu, far)) {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 float f[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                  const float y0 = fmaxf(score(0, nt, e), score(0, nt, 2 + e));
+                  const float y1 = fmaxf(score(1, nt, e), score(1, nt, 2 + e));
+                  float top = fmaxf(y0, y1), topv = fmaxf(y0 + lv[0], y1 + lv[1]);
+#pragma unroll
+                  for (int o = 4; o < 32; o <<= 1) {
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
+                  }
                   f[e] = 1.f;
-                  if (mt[nt][e] > m[nt][e] + LAG) {
-                    l[nt][e] *= ex2(m[nt][e] - mt[nt][e]);
-                    m[nt][e] = mt[nt][e];
+                  if (top > m[nt][e] + LAG) {
+                    l[nt][e] *= ex2(m[nt][e] - top);
+                    m[nt][e] = top;
                   }
-                  if (mt[nt][e] + lv > mv[nt][e] + LAG) {
-                    f[e] = ex2(mv[nt][e] - (mt[nt][e] + lv));
-                    mv[nt][e] = mt[nt][e] + lv;
+                  if (topv > mv[nt][e] + LAG) {
+                    f[e] = ex2(mv[nt][e] - topv);
+                    mv[nt][e] = topv;
                   }
+                  // (with a weight of 0 until there is a contribution; far below it, 0 too)
+                  pf[nt][e] = mv[nt][e] == -INFINITY ? 0.f : ex2(fminf(m[nt][e] - mv[nt][e], 80.f) + UP);
                 }
 #pragma unroll
-                for (int ch = 0; ch < CHUNKS; ++ch) {
+                for (int ch = 0; ch < OWN; ++ch) {
                   o[ch][nt][0] *= f[0];
                   o[ch][nt][1] *= f[1];
                   o[ch][nt][2] *= f[0];
@@ -474,59 +590,60 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
             }
             if (a.weights) {   // the scores, for the weights' sums
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+              for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const int head = nt * 8 + col + (e & 1), key = row8 + (e >> 1) * 8;
-                  if (head < rows && key < left)
-                    a.scores[((int64_t)g.b * a.h_q + h0 + head) * a.capacity + t * K8_KEYS +
-                             warp * KV8_BLOCK + key] = x[nt][e];
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const int head = nt * 8 + col + (e & 1);
+                    const int key = i * KV8_BLOCK + row8 + (e >> 1) * 8;
+                    if (head < rows && key < left)
+                      a.scores[((int64_t)g.b * a.h_q + h0 + head) * a.capacity + t * K8_KEYS +
+                               part * K8_TILE + key] = score(i, nt, e);
+                  }
+            }
+            uint32_t pb[2][NT][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float f = pf[nt][e] * (i ? vs.y : vs.x);
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) {
+                    const float w = ex2(score(i, nt, 2 * r + e) - m[nt][e]);
+                    l[nt][e] += w;
+                    y[2 * r + e] = w * f;
+                  }
                 }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float y[4];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float nm = m[nt][e] == -INFINITY ? 0.f : -m[nt][e];
-                const float f = mv[nt][e] == -INFINITY ? 0.f : vs * ex2(m[nt][e] - mv[nt][e] + UP);
-                const float e0 = ex2(x[nt][e] + nm), e1 = ex2(x[nt][2 + e] + nm);
-                l[nt][e] += e0 + e1;
-                y[e] = e0 * f;
-                y[2 + e] = e1 * f;
+                pb[i][nt][0] = transpose_8x8(pack2<__half>(y[0], y[1]));
+                pb[i][nt][1] = transpose_8x8(pack2<__half>(y[2], y[3]));
               }
-              pb[nt][0] = transpose_8x8(pack2<__half>(y[0], y[1]));
-              pb[nt][1] = transpose_8x8(pack2<__half>(y[2], y[3]));
-            }
-            // values past the end may be anything: cleared, as 0 x NaN is not 0
-            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-            if (left < KV8_BLOCK) {
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int k = e * 8 + col;
-                keep[e] = (k < left ? 0x0000ffffu : 0u) | (k + 1 < left ? 0xffff0000u : 0u);
-              }
-            }
-#pragma unroll
-            for (int ch = 0; ch < CHUNKS; ch += 2) {
+            for (int ch = 0; ch < OWN; ++ch) {
               uint32_t w[4];
-              ldsm4t(vt + chunk_at<D>(l_key, mr, ch + l_chunk), w);
+              ldsm4t(vt + chunk_at<D>(v_key, mr, ch0 + ch), w);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 uint32_t va[4];   // channels 2 row8 (even rows) and 2 row8 + 1 of the chunk
-                e4m3x4_to_f16(__byte_perm(w[2 * i] & keep[0], 0, 0x3120), va[0], va[1]);
-                e4m3x4_to_f16(__byte_perm(w[2 * i + 1] & keep[1], 0, 0x3120), va[2], va[3]);
+                e4m3x4_to_f16(__byte_perm(w[2 * i], 0, 0x3120), va[0], va[1]);
+                e4m3x4_to_f16(__byte_perm(w[2 * i + 1], 0, 0x3120), va[2], va[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma16816<__half>(o[ch + i][nt], va, pb[nt][0], pb[nt][1]);
+                  mma16816<__half>(o[ch][nt], va, pb[i][nt][0], pb[i][nt][1]);
               }
             }
+            // the cleared rows are written by a copy next
+            if (left < K8_TILE) fence_async_smem();
           }
           __syncwarp();
-          if (ok && lane == 0) mbar_arrive(&sh->empty[s]);
+          if (ok && lane == 0) mbar_arrive(&sh->empty[j % C::BARS]);
         }
 
-        // ---- join the warps, by the sums' reference ----
+        // ---- join the warps ----
+        const int par = items & 1;
         const bool all_ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -537,11 +654,11 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
             l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
             if (!all_ok) l[nt][e] = NAN;
             if (row8 == 0) {
-              sh->m[warp][nt * 8 + col + e] = m[nt][e];
-              sh->l[warp][nt * 8 + col + e] = l[nt][e];
+              sh->m[par][warp][nt * 8 + col + e] = m[nt][e];
+              sh->l[par][warp][nt * 8 + col + e] = l[nt][e];
             }
           }
-        k8_consumers_bar();
+        k8_consumers_bar();   // (and the last item's output has been read from obuf)
         float f[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -549,24 +666,24 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
           for (int e = 0; e < 2; ++e) {
             float mm = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < K8_WARPS; ++w) mm = fmaxf(mm, sh->m[w][nt * 8 + col + e]);
+            for (int w = 0; w < C::JOIN; ++w) mm = fmaxf(mm, sh->m[par][w][nt * 8 + col + e]);
             f[nt][e] = mv[nt][e] == -INFINITY ? 0.f : ex2(mv[nt][e] - UP - mm);
           }
         // The warps add up in one slab, a share of the channels at a time, each at another
         // one: every sum has a fixed order.
 #pragma unroll
-        for (int st = 0; st < K8_WARPS; ++st) {
-          const int part = (warp + st) % K8_WARPS;
+        for (int st = 0; st < C::JOIN; ++st) {
+          const int share = (warp + st) % C::JOIN;
 #pragma unroll
-          for (int ch = 0; ch < CHUNKS; ++ch) {
-            if (ch % K8_WARPS != part) continue;
+          for (int ch = 0; ch < OWN; ++ch) {
+            if (ch % C::JOIN != share) continue;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int row = nt * 8 + col + e;
                 if (row >= rows) continue;
-                float2* dst = reinterpret_cast<float2*>(obuf + row * D + ch * 16 + row8 * 2);
+                float2* dst = reinterpret_cast<float2*>(obuf + row * D + (ch0 + ch) * 16 + row8 * 2);
                 float2 v = make_float2(o[ch][nt][e] * f[nt][e], o[ch][nt][2 + e] * f[nt][e]);
                 if (st > 0) {
                   const float2 w = *dst;
@@ -580,15 +697,16 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
         }
         // ---- out: the output itself, or a partial result ----
         const bool direct = !FEW && g.whole;
-        const int64_t part = (2 * (int64_t)blockIdx.x + (g.t0 > 0 ? 0 : 1)) * p.rows;
-        for (int i = tid; i < rows * (D / 4); i += 32 * K8_WARPS) {
+        const int64_t slot = (2 * (int64_t)blockIdx.x + (g.t0 > 0 ? 0 : 1)) * p.rows;
+        for (int i = tid; i < rows * (D / 4); i += 32 * W) {
           const int row = i / (D / 4), c4 = i % (D / 4) * 4;
           float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-          for (int w = 0; w < K8_WARPS; ++w) mm = fmaxf(mm, sh->m[w][row]);
+          for (int w = 0; w < C::JOIN; ++w) mm = fmaxf(mm, sh->m[par][w][row]);
 #pragma unroll
-          for (int w = 0; w < K8_WARPS; ++w)
-            ll += mm == -INFINITY ? sh->l[w][row] : sh->l[w][row] * ex2(sh->m[w][row] - mm);
+          for (int w = 0; w < C::JOIN; ++w)
+            ll += mm == -INFINITY ? sh->l[par][w][row]
+                                  : sh->l[par][w][row] * ex2(sh->m[par][w][row] - mm);
           const float4 v = *reinterpret_cast<const float4*>(obuf + row * D + c4);
           if (FEW) {
             if (c4 == 0) sh->ml[row] = make_float2(mm, ll);
@@ -597,11 +715,10 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
             k8_put_four<IO, D>(a, g.b, h0 + row, c4, ll, y);
             if (a.weights && c4 == 0) a.row_ml[(int64_t)g.b * a.h_q + h0 + row] = make_float2(mm, ll);
           } else {
-            *reinterpret_cast<float4*>(a.part_o + (part + row) * D + c4) = v;
-            if (c4 == 0) a.part_ml[part + row] = make_float2(mm, ll);
+            *reinterpret_cast<float4*>(a.part_o + (slot + row) * D + c4) = v;
+            if (c4 == 0) a.part_ml[slot + row] = make_float2(mm, ll);
           }
         }
-        k8_consumers_bar();   // obuf and m, l are free again
       }
     }
     if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
@@ -670,19 +787,19 @@ __global__ void __launch_bounds__(K8_MERGE_THREADS)
   for (int base = 0; base < n; base += K8_MERGE_THREADS) {
     const int i = base + tid;
     int64_t before;
-    const int64_t u = i < n ? units_of(k8_len(p, i)) * heads : 0;
+    const int64_t u = i < n ? span_of(units_of(k8_len(p, i))) * heads : 0;
     const int64_t all = block_scan(u, sums, K8_MERGE_THREADS / 32, before);
     if (i == b) s_mine = total + before;
     total += all;
   }
   __syncthreads();
-  const int64_t nt = units_of(k8_len(p, b));
-  const int64_t u0 = s_mine + hs * nt, u1 = u0 + nt;
+  const int nt = units_of(k8_len(p, b));
+  const int64_t u0 = s_mine + hs * span_of(nt);
   const K8Line line(total, p.ctas);
   int c0 = 0, c1 = -1;
-  if (nt > 0) {   // the CTAs whose runs meet [u0, u1)
+  if (nt > 0) {   // the CTAs whose runs hold its first and last unit
     c0 = line.owner(u0);
-    c1 = line.owner(u1 - 1);
+    c1 = line.owner(u0 + (int64_t)(nt - 1) * K8_UNIT_COST);
   }
   const int parts = c1 - c0 + 1;
   pdl_wait();
@@ -901,7 +1018,7 @@ int64_t gdn_kv8_decode_slots(int h_q, int h_kv, int d) {
   using namespace gdn::attn;
   const int group = h_q / h_kv, most = group <= 8 ? 8 : 16;
   // two cut items per CTA
-  return 2 * (d == 256 ? K8Cfg<256, 1>::CTAS : K8Cfg<128, 1>::CTAS) * (int64_t)(group < most ? group : most);
+  return 2 * (d == 64 ? K8Cfg<64, 1>::CTAS : K8Cfg<256, 1>::CTAS) * (int64_t)(group < most ? group : most);
 }
 
 cudaError_t gdn_launch_kv8_decode(const GdnKv8DecodeArgs& a, int io, cudaStream_t s) {

@@ -45,6 +45,7 @@ CASES = [   # lengths, hq, hkv, d, page, io, gate
     ([3] * 400, 2, 1, 64, 16, "bf16", False),           # more rows than a CTA has threads
     ([1500, 40, 900], 48, 2, 64, 64, "bf16", True),     # groups of 24
     ([2000, 1100], 8, 8, 128, 64, "fp16", False),
+    ([30_001, 3], 4, 1, 256, 128, "bf16", False),
 ]
 
 
@@ -77,6 +78,38 @@ def test_decode(gpu_lib, lens, hq, hkv, d, page, io, gate, weights):
         _attn.check(o, ref, slack, dt, what)
         if weights:
             _kv8.check_weights(got, old, w, ws, what)
+
+
+@pytest.mark.parametrize("hq,hkv,d,page,io", [(8, 2, 256, 64, "bf16"), (12, 1, 256, 16, "fp16"),
+                                               (8, 2, 128, 128, "fp16"), (32, 2, 128, 32, "bf16"),
+                                               (4, 4, 64, 64, "bf16"), (10, 1, 64, 16, "bf16")])
+def test_runs_that_go_round_the_stages_many_times(gpu_lib, hq, hkv, d, page, io):
+    """The same keys again and again (pages that a block table names many times) leave the softmax's
+    average as it is: the reference is one cycle."""
+    g = torch.Generator().manual_seed(d + hq)
+    n, cycle, times = 9, 1024, 128
+    dt = IO[io]
+    cache = _kv8.paged(g, [cycle] * n, hkv, d, page)
+    table = cache[4].repeat(1, times)
+    q = normal(g, n, hq, d, dtype=dt)
+    ref, slack, w, ws = _kv8.decode(q, cache, [cycle] * n, None, _attn.scale_of(d), dt)
+    # the sums are of `times` as many terms
+    slack += cycle * times * 2.0 ** -24 * ref.abs().max() * 4
+    dims = gdn.make_attn_dims(hq, hkv, d, io=io, page_size=page)
+    c, cap = _on_gpu((*cache[:4], table)), cycle * times
+    status, got = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(n, hkv, cap, device="cuda")
+    for lens in ([cap] * n, [cap - 1, 1, 5] * 3):
+        got.zero_()
+        o = gdn.gdn_attn_decode_kv8(dims, q.cuda(), c, _ints(lens), _workspace(dims, n, cap),
+                                    weights=got, d_status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        if lens[1] == cap:
+            _attn.check(o, ref, slack, dt, "o")
+            for t in (0, 1, times // 2, times - 1):
+                part = got[..., t * cycle:(t + 1) * cycle].double().cpu()
+                off = (part - w / times).abs() - ws / times - cycle * times * 2.0 ** -24 * part
+                assert (off <= 2.0 ** -116).all(), float(off.max())
 
 
 def _rescaled(cache, lens, page, exps, which):
