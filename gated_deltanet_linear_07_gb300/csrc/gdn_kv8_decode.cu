@@ -148,17 +148,22 @@ __device__ __forceinline__ int k8_rows(const K8Args& p, int hs) {
   return min(p.rows, p.a.h_q / p.a.h_kv - hs % p.subs * (8 * NT));
 }
 
-// Four channels of a finished output: y / l, gated (zeros where no key was seen).
+// The gate of four channels of an output, and four channels of a finished one: y / l, gated
+// (zeros where no key was seen).
+template <typename IO>
+__device__ __forceinline__ uint2 k8_gate(const GdnKv8DecodeArgs& a, int b, int h, int col) {
+  if (!a.gate.data) return make_uint2(0, 0);
+  return *reinterpret_cast<const uint2*>(reinterpret_cast<const IO*>(a.gate.data) +
+                                         (int64_t)b * a.gate.token_stride +
+                                         (int64_t)h * a.gate.head_stride + col);
+}
 template <typename IO, int D>
 __device__ __forceinline__ void k8_put_four(const GdnKv8DecodeArgs& a, int b, int h, int col, float l,
-                                            float (&y)[4]) {
+                                            float (&y)[4], uint2 g) {
   const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] *= inv;
   if (a.gate.data && l != 0.f) {
-    const uint2 g = *reinterpret_cast<const uint2*>(reinterpret_cast<const IO*>(a.gate.data) +
-                                                    (int64_t)b * a.gate.token_stride +
-                                                    h * a.gate.head_stride + col);
     const float2 g0 = unpack2<IO>(g.x), g1 = unpack2<IO>(g.y);
     y[0] *= gate_sigmoid(g0.x);
     y[1] *= gate_sigmoid(g0.y);
@@ -335,18 +340,45 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
     bool ok = true;
     int j = 0, items = 0;            // units and items so far: the rings' positions
     if (warp == W) {
-      // ---- loads: each lane one box of the unit (K or V, rows, column block), and one
-      // of its 16 blocks' scales ----
+      // ---- loads: each lane one box of a unit (K or V, rows, column block) ----
       constexpr int COLS = D == 256 ? 2 : 1;
       const int per_kv = (K8_KEYS / p.box_rows) * COLS;
-      const bool boxed = lane < 2 * per_kv, is_v = lane >= per_kv;
+      const bool is_v = lane >= per_kv;
       const int box = is_v ? lane - per_kv : lane;
       const int cb = box % COLS, r = box / COLS * p.box_rows;
-      const int sr = lane % K8_BLOCKS * KV8_BLOCK;
-      const float* const scales = lane < K8_BLOCKS ? a.cache.k_scale : a.cache.v_scale;
-      while (ok && next(g)) {
+      // Pages and scales are looked up for four units at a time, a lane for each block's K or V
+      // scale: pages two batches ahead, scales, by them, one; and the first ones of the item to
+      // come.  (One unit ahead, each unit waited for a memory latency: 200 rows of 8 heads of 128
+      // 143 us.)
+      constexpr int BATCH = 32 / (2 * K8_BLOCKS);
+      const int bu = lane / (2 * K8_BLOCKS), brow = lane % K8_BLOCKS * KV8_BLOCK;
+      const float* const scales = lane % (2 * K8_BLOCKS) < K8_BLOCKS ? a.cache.k_scale : a.cache.v_scale;
+      auto page_at = [&](const K8Segment& g, int t) {
+        t += bu;
+        const int64_t pos = (int64_t)t * K8_KEYS + brow;
+        return t < g.t1 && pos < g.keys
+                   ? __ldg(a.cache.block_table + (int64_t)g.b * a.cache.pages_per_seq +
+                           (pos >> a.page_shift))
+                   : 0;
+      };
+      auto scale_at = [&](const K8Segment& g, int t, int32_t page) {
+        t += bu;
+        const int64_t pos = (int64_t)t * K8_KEYS + brow;
+        if (t >= g.t1 || pos >= g.keys || page < 0 || page >= a.cache.num_pages) return 0.f;
+        return __ldg(scales + ((((int64_t)page * a.h_kv + g.hs / p.subs) << a.page_shift) +
+                               (pos & ((1 << a.page_shift) - 1))) / KV8_BLOCK);
+      };
+      K8Segment h = {};
+      bool more = next(h);
+      int32_t page_h = more ? page_at(h, h.t0) : 0;
+      float scale_h = more ? scale_at(h, h.t0, page_h) : 0.f;
+      while (ok && more) {
+        g = h;
+        int32_t page = page_h, page1 = page_at(g, g.t0 + BATCH);
+        float scale = scale_h;
+        more = next(h);
+        if (more) page_h = page_at(h, h.t0);
         const int kvh = g.hs / p.subs;
-        const int32_t* table = a.cache.block_table + (int64_t)g.b * a.cache.pages_per_seq;
         // the item's queries, once the consumers have the last item's
         if (items > 0) ok = mbar_wait(&sh->q_empty, (items - 1) & 1, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
@@ -360,55 +392,41 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
                     reinterpret_cast<const IO*>(a.q.data) + (int64_t)g.b * a.q.token_stride +
                         (int64_t)(k8_head<NT>(p, g.hs) + lane) * a.q.head_stride,
                     D * 2, &sh->q_full);
-        auto page_at = [&](int t, int row) {
-          const int64_t pos = (int64_t)t * K8_KEYS + row;
-          return t < g.t1 && pos < g.keys ? __ldg(table + (pos >> a.page_shift)) : 0;
-        };
-        auto scale_at = [&](int t, int32_t page) {
-          const int64_t pos = (int64_t)t * K8_KEYS + sr;
-          if (lane >= 2 * K8_BLOCKS || t >= g.t1 || pos >= g.keys || page < 0 ||
-              page >= a.cache.num_pages)
-            return 0.f;
-          return __ldg(scales + ((((int64_t)page * a.h_kv + kvh) << a.page_shift) +
-                                 (pos & ((1 << a.page_shift) - 1))) / KV8_BLOCK);
-        };
-        // two units ahead: pages; one ahead: scales
-        int32_t page = boxed ? page_at(g.t0, r) : 0, page1 = boxed ? page_at(g.t0 + 1, r) : 0;
-        int32_t spage1 = page_at(g.t0 + 1, sr);
-        float scale = scale_at(g.t0, page_at(g.t0, sr));
-        for (int t = g.t0; t < g.t1 && ok; ++t, ++j) {
-          const float scale1 = scale_at(t + 1, spage1);
-          const int32_t page2 = boxed ? page_at(t + 2, r) : 0, spage2 = page_at(t + 2, sr);
-          const int s = j % C::STAGES;
-          uint64_t* full = &sh->full[j % C::BARS];
-          if (j >= C::STAGES) {
-            const int was = j - C::STAGES;
-            ok = mbar_wait(&sh->empty[was % C::BARS], (was / C::BARS) & 1, a.wait_ns);
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const int left = min(g.keys - t * K8_KEYS, K8_KEYS);
-          const int there = (left + p.box_rows - 1) / p.box_rows * p.box_rows;
-          // (the test's: of the first CTA, or of the last one of the first cluster)
-          const bool withheld = a.withhold && j == 0 && blockIdx.x == (FEW ? p.cluster - 1 : 0);
-          if (lane < 2 * K8_BLOCKS) sh->scale[s][lane] = scale;
-          __syncwarp();
-          if (lane == 0 && !withheld) mbar_expect_tx(full, (uint32_t)there * D * 2);
-          __syncwarp();
-          if (boxed && r < there && !withheld) {
-            if (page < 0 || page >= a.cache.num_pages) {
-              set_status(a.d_status, GDN_DEV_BAD_PAGE);
-              page = 0;
+        if (more) scale_h = scale_at(h, h.t0, page_h);
+        for (int tb = g.t0; tb < g.t1 && ok; tb += BATCH) {
+          const float scale1 = scale_at(g, tb + BATCH, page1);
+          const int32_t page2 = page_at(g, tb + 2 * BATCH);
+          for (int u = 0; u < BATCH && tb + u < g.t1; ++u, ++j) {
+            const int t = tb + u, s = j % C::STAGES;
+            uint64_t* full = &sh->full[j % C::BARS];
+            if (j >= C::STAGES) {
+              const int was = j - C::STAGES;
+              ok = mbar_wait(&sh->empty[was % C::BARS], (was / C::BARS) & 1, a.wait_ns);
             }
-            const int64_t row = (((int64_t)page * a.h_kv + kvh) << a.page_shift) +
-                                ((t * K8_KEYS + r) & ((1 << a.page_shift) - 1));
-            tma_box(ring + (uint32_t)s * C::STAGE + (is_v ? C::TILE : 0u) +
-                        (uint32_t)(cb * K8_KEYS + r) * (D < 128 ? 64u : 128u),
-                    is_v ? &vmap : &kmap, (int)row, cb, full);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const int left = min(g.keys - t * K8_KEYS, K8_KEYS);
+            const int there = (left + p.box_rows - 1) / p.box_rows * p.box_rows;
+            // (the test's: of the first CTA, or of the last one of the first cluster)
+            const bool withheld = a.withhold && j == 0 && blockIdx.x == (FEW ? p.cluster - 1 : 0);
+            if (bu == u) sh->scale[s][lane % (2 * K8_BLOCKS)] = scale;
+            int32_t pg = __shfl_sync(0xffffffffu, page, u * 2 * K8_BLOCKS + r / KV8_BLOCK % K8_BLOCKS);
+            if (lane == 0 && !withheld) mbar_expect_tx(full, (uint32_t)there * D * 2);
+            __syncwarp();
+            if (lane < 2 * per_kv && r < there && !withheld) {
+              if (pg < 0 || pg >= a.cache.num_pages) {
+                set_status(a.d_status, GDN_DEV_BAD_PAGE);
+                pg = 0;
+              }
+              const int64_t row = (((int64_t)pg * a.h_kv + kvh) << a.page_shift) +
+                                  ((t * K8_KEYS + r) & ((1 << a.page_shift) - 1));
+              tma_box(ring + (uint32_t)s * C::STAGE + (is_v ? C::TILE : 0u) +
+                          (uint32_t)(cb * K8_KEYS + r) * (D < 128 ? 64u : 128u),
+                      is_v ? &vmap : &kmap, (int)row, cb, full);
+            }
           }
           page = page1;
           page1 = page2;
-          spage1 = spage2;
           scale = scale1;
         }
       }
@@ -642,6 +660,17 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
           if (ok && lane == 0) mbar_arrive(&sh->empty[j % C::BARS]);
         }
 
+        // the gate of this thread's part of the output, on its way while the warps join
+        constexpr int OUT = C::ROWS * (D / 4) / (32 * W);
+        uint2 gate[OUT] = {};
+        const bool direct = !FEW && g.whole;
+        if (direct)
+#pragma unroll
+          for (int k = 0; k < OUT; ++k) {
+            const int i = tid + k * 32 * W, row = i / (D / 4);
+            if (row < rows)
+              gate[k] = k8_gate<IO>(a, g.b, h0 + row, i % (D / 4) * 4);
+          }
         // ---- join the warps ----
         const int par = items & 1;
         const bool all_ok = __all_sync(0xffffffffu, ok);
@@ -696,10 +725,11 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
           k8_consumers_bar();
         }
         // ---- out: the output itself, or a partial result ----
-        const bool direct = !FEW && g.whole;
         const int64_t slot = (2 * (int64_t)blockIdx.x + (g.t0 > 0 ? 0 : 1)) * p.rows;
-        for (int i = tid; i < rows * (D / 4); i += 32 * W) {
-          const int row = i / (D / 4), c4 = i % (D / 4) * 4;
+#pragma unroll
+        for (int k = 0; k < OUT; ++k) {
+          const int i = tid + k * 32 * W, row = i / (D / 4), c4 = i % (D / 4) * 4;
+          if (row >= rows) break;
           float mm = -INFINITY, ll = 0.f;
 #pragma unroll
           for (int w = 0; w < C::JOIN; ++w) mm = fmaxf(mm, sh->m[par][w][row]);
@@ -712,7 +742,7 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
             if (c4 == 0) sh->ml[row] = make_float2(mm, ll);
           } else if (direct) {
             float y[4] = {v.x, v.y, v.z, v.w};
-            k8_put_four<IO, D>(a, g.b, h0 + row, c4, ll, y);
+            k8_put_four<IO, D>(a, g.b, h0 + row, c4, ll, y, gate[k]);
             if (a.weights && c4 == 0) a.row_ml[(int64_t)g.b * a.h_q + h0 + row] = make_float2(mm, ll);
           } else {
             *reinterpret_cast<float4*>(a.part_o + (slot + row) * D + c4) = v;
@@ -747,7 +777,7 @@ __global__ void __launch_bounds__(K8_THREADS, K8Cfg<D, NT>::PER_SM)
         y[2] = fmaf(f, o.z, y[2]);
         y[3] = fmaf(f, o.w, y[3]);
       }
-      k8_put_four<IO, D>(a, walk.b, h0 + row, c4, ll, y);
+      k8_put_four<IO, D>(a, walk.b, h0 + row, c4, ll, y, k8_gate<IO>(a, walk.b, h0 + row, c4));
       if (a.weights && c4 == 0)
         a.row_ml[(int64_t)walk.b * a.h_q + h0 + row] = make_float2(mm, ll);
     }
@@ -770,7 +800,7 @@ static __host__ __device__ __forceinline__ int k8_most_parts(const K8Args& p) {
 template <typename IO, int D, int NT>
 __global__ void __launch_bounds__(K8_MERGE_THREADS)
     kv8_merge_kernel(const __grid_constant__ K8Args p) {
-  extern __shared__ __align__(16) float2 ml[];   // [part][row]: statistics, then (factor, sum)
+  extern __shared__ __align__(16) unsigned char merge_smem[];
   __shared__ int64_t sums[K8_MERGE_THREADS / 32], s_mine;
   __shared__ float sum_l[16];
   __shared__ float4 shares[K8_MERGE_THREADS];
@@ -778,6 +808,8 @@ __global__ void __launch_bounds__(K8_MERGE_THREADS)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int heads = a.h_kv * p.subs;
   const int n = a.n;
+  float2* ml = reinterpret_cast<float2*>(merge_smem);   // [part][row]: statistics, then (factor, sum)
+  int32_t* first_row = reinterpret_cast<int32_t*>(ml + (size_t)k8_most_parts(p) * p.merge_rows);
   const int slices = (p.rows + p.merge_rows - 1) / p.merge_rows;
   const int item = blockIdx.x / slices, r0 = blockIdx.x % slices * p.merge_rows;
   const int b = item / heads, hs = item % heads;
@@ -802,16 +834,15 @@ __global__ void __launch_bounds__(K8_MERGE_THREADS)
     c1 = line.owner(u0 + (int64_t)(nt - 1) * K8_UNIT_COST);
   }
   const int parts = c1 - c0 + 1;
+  // partial i's first row: a run that starts inside the item left its first partial, else its last
+  for (int i = tid; i < parts; i += K8_MERGE_THREADS)
+    first_row[i] = (2 * (c0 + i) + (line.start(c0 + i) > u0 ? 0 : 1)) * p.rows + r0;
   pdl_wait();
   if (nt > 0 && c0 == c1) return;   // written already
   if (rows <= 0) return;            // the last heads' item may be shorter
-  // a run that starts inside the item left its first partial, else its last
-  auto first_row = [&](int i) {
-    const int c = c0 + i;
-    return (2 * (int64_t)c + (line.start(c) > u0 ? 0 : 1)) * p.rows + r0;
-  };
+  __syncthreads();
   for (int i = tid; i < parts * rows; i += K8_MERGE_THREADS)
-    ml[i] = a.part_ml[first_row(i / rows) + i % rows];
+    ml[i] = a.part_ml[first_row[i / rows] + i % rows];
   __syncthreads();
   for (int row = warp; row < rows; row += K8_MERGE_THREADS / 32) {
     float mm = -INFINITY, ll = 0.f;
@@ -844,7 +875,7 @@ __global__ void __launch_bounds__(K8_MERGE_THREADS)
       for (int i = g; i < parts; i += groups) {
         const float2 w = ml[i * rows + row];
         const float4 v =
-            *reinterpret_cast<const float4*>(a.part_o + (first_row(i) + row) * D + col);
+            *reinterpret_cast<const float4*>(a.part_o + (int64_t)(first_row[i] + row) * D + col);
         if (w.y != 0.f) {
           y[0] = fmaf(w.x, v.x, y[0]);
           y[1] = fmaf(w.x, v.y, y[1]);
@@ -864,7 +895,8 @@ __global__ void __launch_bounds__(K8_MERGE_THREADS)
         y[3] += v.w;
       }
     }
-    if (mine && g == 0) k8_put_four<IO, D>(a, b, h0 + row, col, sum_l[row], y);
+    if (mine && g == 0)
+      k8_put_four<IO, D>(a, b, h0 + row, col, sum_l[row], y, k8_gate<IO>(a, b, h0 + row, col));
   }
 }
 
@@ -988,7 +1020,7 @@ static cudaError_t launch_decode(const GdnKv8DecodeArgs& a, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(items * slices));
     cfg.blockDim = dim3(K8_MERGE_THREADS);
-    cfg.dynamicSmemBytes = (size_t)k8_most_parts(p) * 8 * p.merge_rows;
+    cfg.dynamicSmemBytes = (size_t)k8_most_parts(p) * (8 * p.merge_rows + 4);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, merge, p)) != cudaSuccess) return e;
