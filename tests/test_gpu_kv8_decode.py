@@ -46,6 +46,9 @@ CASES = [   # lengths, hq, hkv, d, page, io, gate
     ([1500, 40, 900], 48, 2, 64, 64, "bf16", True),     # groups of 24
     ([2000, 1100], 8, 8, 128, 64, "fp16", False),
     ([30_001, 3], 4, 1, 256, 128, "bf16", False),
+    # many short rows beside a long one: a merge by borders, an item of nearly all runs
+    ([5] * 400 + [9000, 0, 300] + [7] * 300, 16, 1, 64, 16, "bf16", False),
+    ([1, 0, 70] * 120 + [2500], 4, 2, 128, 64, "fp16", True),
 ]
 
 
