@@ -8,6 +8,9 @@
 // powers of two lose nothing, and a scale that grows (a later token with a larger
 // value) divides what the block holds by a power of two: exactly but for the
 // subnormals.  Everything here is bound by the bytes that it moves.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "gdn_attn_device.cuh"
 #include "gdn_kv8.cuh"
 #include "gdn_rope.cuh"
@@ -99,46 +102,187 @@ static int64_t most_runs(int64_t n, int64_t num_seqs) {
 // is a run's rows of one head (q, k or v), by a team of TEAM threads: eight channels
 // per lane, D / 8 lanes per row, the rows at their slots of the block, so that what
 // the block held before lies in the lanes of its own slots.
+//
+// Two kernels of the same arithmetic: few rows are loaded straight into registers, their tiles
+// spread over CTAs; many go through a ring of tiles that one warp keeps filled by TMA
+// (16,384 tokens of 16 + 4 heads of 256: 117 us with loads into registers).
 constexpr int TEAM = 128, TEAMS = 2, APPEND_THREADS = TEAM * TEAMS;
 
 __device__ __forceinline__ void team_bar(int team) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TEAM) : "memory");
 }
 
+template <int D>
+struct AppendCfg {
+  static constexpr int N = KV8_BLOCK * (D / 8) / TEAM;   // rows of a lane
+  static constexpr int CS = D / 2 * 3;                   // a slot's cosines, sines, negated sines
+  static constexpr uint32_t ANGLES = KV8_BLOCK * CS * 4;
+};
+
+// What a CTA knows of its run.
+struct RunPlace {
+  Run run;
+  int64_t page;    // < 0: nothing is stored
+  int r, block;    // the first row's slot; the block's place in its page
+  bool padding;
+};
+__device__ __forceinline__ RunPlace place_of(const GdnKv8AppendArgs& p, const Run& run) {
+  RunPlace w;
+  w.run = run;
+  w.padding = run.place < 0;
+  w.r = w.padding ? 0 : (int)(run.place % KV8_BLOCK);
+  w.page = w.padding ? -1 : page_of(p.cache, p.r.page_shift, run.b, run.place, p.r.d_status);
+  w.block = w.padding ? 0 : (int)(run.place & ((1 << p.r.page_shift) - 1)) / KV8_BLOCK;
+  return w;
+}
+
+// The rows' cosines and sines at their slots, by the first `threads` of the CTA.
+template <typename IO, int D>
+__device__ __forceinline__ void put_angles(const GdnRopeArgs& a, const RunPlace& w,
+                                           const uint64_t* fraction, float* cs, int threads) {
+  const int half = a.rot_dim / 2;
+  if (half == 0) return;
+  const int per = threads / half, u0 = threadIdx.x / half, i = threadIdx.x - u0 * half;
+  if (u0 >= per) return;
+  const int32_t* pos = a.positions + (a.axes.count ? a.axes.pair[i] * a.n : 0) + w.run.t0;
+  for (int u = u0; u < w.run.rows; u += per)
+    put_angle<IO, D>(cs + (w.r + u) * AppendCfg<D>::CS, i, pos[u], fraction[i], a.rope_scale);
+}
+
+// One tile's rows x (of slots slot0 ..), normed, rotated and stored; by a team (the block's
+// largest value passes through red).  live: false leaves the stores out.
+template <typename IO, int D>
+__device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const RunPlace& w,
+                                            const LanePlace<D>& at, int tile, int nq, int slot0,
+                                            int team, const float* cs, float (&red)[TEAM / 32],
+                                            const Vec8<IO> (&x)[AppendCfg<D>::N], bool live) {
+  constexpr int N = AppendCfg<D>::N, CS = AppendCfg<D>::CS;
+  const GdnRopeArgs& a = p.r;
+  const int tt = threadIdx.x % TEAM, lane = threadIdx.x & 31;
+  const Run& run = w.run;
+  const int r = w.r;
+  const bool is_q = tile < nq, is_v = tile >= nq + a.h_kv;
+  const int head = is_q ? tile : is_v ? tile - nq - a.h_kv : tile - nq;
+  uint64_t y[N][4];
+  if (is_v) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      float f[8];
+      x[u].get(f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[u][i] = pk(f[2 * i], f[2 * i + 1]);
+    }
+  } else {
+    const float* wp = is_q ? a.q_norm : a.k_norm;
+    float4 wt[2] = {};
+    if (wp) {
+      wt[0] = __ldg(reinterpret_cast<const float4*>(wp + 8 * at.part));
+      wt[1] = __ldg(reinterpret_cast<const float4*>(wp + 8 * at.part + 4));
+    }
+    norm_rotate_fp32<IO, D, N>(at, N, wp != nullptr, a.interleaved, a.rot_dim > 0, a.eps, wt,
+                               cs + slot0 * CS, x, y);
+  }
+  // the packed rows
+  IO* out = reinterpret_cast<IO*>(is_q ? a.q_out : is_v ? nullptr : a.k_out);
+  if (out && live) {
+    const int heads = is_q ? a.h_q : a.h_kv;
+    out += (run.t0 * heads + head) * D + 8 * at.part;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int row = slot0 + u - r;
+      if (row < 0 || row >= run.rows) continue;
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) unpk(y[u][i], f[2 * i], f[2 * i + 1]);
+      Vec8<IO> v;
+      v.set(f);
+      if (w.padding) v.w = make_uint4(0, 0, 0, 0);
+      v.store(out + (int64_t)row * heads * D);
+    }
+  }
+  if (is_q || w.page < 0) return;   // the same for the whole team
+  const int64_t first = (w.page * a.h_kv + head) << a.page_shift;
+  float* sp = (is_v ? p.cache.v_scale : p.cache.k_scale) + first / KV8_BLOCK + w.block;
+  unsigned char* codes = reinterpret_cast<unsigned char*>(is_v ? p.cache.v : p.cache.k) +
+                         (first + w.block * KV8_BLOCK) * D + 8 * at.part;
+  const float held = r > 0 ? *sp : 0.f;
+  float top = 0.f;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int row = slot0 + u - r;
+    if (row < 0 || row >= run.rows) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f0, f1;
+      unpk(y[u][i], f0, f1);
+      f0 = fabsf(f0);
+      f1 = fabsf(f1);
+      if (f0 < INFINITY) top = fmaxf(top, f0);
+      if (f1 < INFINITY) top = fmaxf(top, f1);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) red[tt >> 5] = top;
+  team_bar(team);
+#pragma unroll
+  for (int i = 0; i < TEAM / 32; ++i) top = fmaxf(top, red[i]);
+  if (!live) return;
+  const int e = kv8_exponent(top);
+  float scale = pow2(e), inv = pow2(-e);
+  if (kv8_scale_ok(held)) {
+    if (held >= scale) {
+      scale = held;
+      inv = 1.0f / held;
+    } else {   // what the block holds already, at the new scale
+      const float f = held * inv;
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (slot0 + u < r) {
+          uint2* c = reinterpret_cast<uint2*>(codes + (slot0 + u) * D);
+          const uint2 old = *c;
+          const float4 lo = from_e4m3x4(old.x), hi = from_e4m3x4(old.y);
+          *c = make_uint2(to_e4m3x4(lo.x * f, lo.y * f, lo.z * f, lo.w * f),
+                          to_e4m3x4(hi.x * f, hi.y * f, hi.z * f, hi.w * f));
+        }
+    }
+  }
+  if (tt == 0) *sp = scale;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const int row = slot0 + u - r;
+    if (row < 0 || row >= run.rows) continue;
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpk(y[u][i], f[2 * i], f[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fabsf(f[i]) < INFINITY ? f[i] * inv : NAN;
+    *reinterpret_cast<uint2*>(codes + (slot0 + u) * D) = make_uint2(
+        to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
+  }
+}
+
 template <typename IO, int D>
 __global__ void __launch_bounds__(APPEND_THREADS)
     kv8_append_kernel(const __grid_constant__ GdnKv8AppendArgs p) {
-  constexpr int N = KV8_BLOCK * (D / 8) / TEAM;   // rows of a lane
-  constexpr int CS = D / 2 * 3;
+  constexpr int N = AppendCfg<D>::N;
   extern __shared__ __align__(16) float cs[];     // [slot][cosines, sines, negated sines]
   __shared__ uint64_t fraction[D / 2];
-  __shared__ float red[2][TEAMS][TEAM / 32];
+  __shared__ float red[2][TEAMS][TEAM / 32];      // of every other tile: one barrier per tile
   const GdnRopeArgs& a = p.r;
-  const int tid = threadIdx.x, team = tid / TEAM, tt = tid % TEAM, lane = tid & 31;
-  const int half = a.rot_dim / 2;
-  for (int i = tid; i < half; i += APPEND_THREADS) fraction[i] = turn_fraction(a.inv_freq[i]);
+  const int tid = threadIdx.x, team = tid / TEAM, tt = tid % TEAM;
+  for (int i = tid; i < a.rot_dim / 2; i += APPEND_THREADS) fraction[i] = turn_fraction(a.inv_freq[i]);
   Run run;
   if (!find_run<APPEND_THREADS / 32>(p.cu, p.starts, p.num_seqs, a.n, blockIdx.x, a.d_status, run))
     return;
   __syncthreads();
-  const bool padding = run.place < 0;
-  const int r = padding ? 0 : (int)(run.place % KV8_BLOCK);   // the first row's slot
-  const int64_t page =
-      padding ? -1 : page_of(p.cache, a.page_shift, run.b, run.place, a.d_status);
-  if (half > 0) {
-    const int per = APPEND_THREADS / half, u0 = tid / half, i = tid - u0 * half;
-    if (u0 < per) {
-      const int32_t* pos = a.positions + (a.axes.count ? a.axes.pair[i] * a.n : 0) + run.t0;
-      for (int u = u0; u < run.rows; u += per)
-        put_angle<IO, D>(cs + (r + u) * CS, i, pos[u], fraction[i], a.rope_scale);
-    }
-  }
+  const RunPlace w = place_of(p, run);
+  put_angles<IO, D>(a, w, fraction, cs, APPEND_THREADS);
   __syncthreads();
 
   const LanePlace<D> at(a);
   const int slot0 = tt / (D / 8) * N;          // of this lane's rows
   const int nq = a.q.data ? a.h_q : 0, tiles = nq + 2 * a.h_kv;
-  const int block = padding ? 0 : (int)(run.place & ((1 << a.page_shift) - 1)) / KV8_BLOCK;
   const int step = TEAMS * gridDim.y;
   auto load = [&](int tile, Vec8<IO> (&x)[N]) {
     const gdn_view& v = tile < nq ? a.q : tile < nq + a.h_kv ? a.k : a.v;
@@ -147,131 +291,156 @@ __global__ void __launch_bounds__(APPEND_THREADS)
                     head * v.head_stride + 8 * at.part;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      const int row = slot0 + u - r;
-      if (row >= 0 && row < run.rows && !padding)
+      const int row = slot0 + u - w.r;
+      if (row >= 0 && row < run.rows && !w.padding)
         x[u].load(src + row * v.token_stride);
       else
         x[u].w = make_uint4(0, 0, 0, 0);
     }
   };
   Vec8<IO> x[N];
-  int tile = blockIdx.y * TEAMS + team;
-  if (tile < tiles) load(tile, x);
-  for (int it = 0; tile < tiles; ++it) {
-    const bool is_q = tile < nq, is_v = tile >= nq + a.h_kv;
-    const int head = is_q ? tile : (tile - nq) % a.h_kv;
-    uint64_t y[N][4];
-    if (is_v) {
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        float f[8];
-        x[u].get(f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[u][i] = pk(f[2 * i], f[2 * i + 1]);
-      }
-    } else {
-      const float* wp = is_q ? a.q_norm : a.k_norm;
-      float4 wt[2] = {};
-      if (wp) {
-        wt[0] = __ldg(reinterpret_cast<const float4*>(wp + 8 * at.part));
-        wt[1] = __ldg(reinterpret_cast<const float4*>(wp + 8 * at.part + 4));
-      }
-      norm_rotate_fp32<IO, D, N>(at, N, wp != nullptr, a.interleaved, half > 0, a.eps, wt,
-                                 cs + slot0 * CS, x, y);
-    }
-    const int next = tile + step;
-    if (next < tiles) load(next, x);
-    // the packed rows
-    IO* out = reinterpret_cast<IO*>(is_q ? a.q_out : is_v ? nullptr : a.k_out);
-    if (out) {
-      const int heads = is_q ? a.h_q : a.h_kv;
-      out += (run.t0 * heads + head) * D + 8 * at.part;
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        const int row = slot0 + u - r;
-        if (row < 0 || row >= run.rows) continue;
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpk(y[u][i], f[2 * i], f[2 * i + 1]);
-        Vec8<IO> w;
-        w.set(f);
-        if (padding) w.w = make_uint4(0, 0, 0, 0);
-        w.store(out + (int64_t)row * heads * D);
-      }
-    }
-    if (!is_q && page >= 0) {   // the same for the whole team
-      const int64_t first = (page * a.h_kv + head) << a.page_shift;
-      float* sp = (is_v ? p.cache.v_scale : p.cache.k_scale) + first / KV8_BLOCK + block;
-      unsigned char* codes = reinterpret_cast<unsigned char*>(is_v ? p.cache.v : p.cache.k) +
-                             (first + block * KV8_BLOCK) * D + 8 * at.part;
-      const float held = r > 0 ? *sp : 0.f;
-      float top = 0.f;
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        const int row = slot0 + u - r;
-        if (row < 0 || row >= run.rows) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float f0, f1;
-          unpk(y[u][i], f0, f1);
-          f0 = fabsf(f0);
-          f1 = fabsf(f1);
-          if (f0 < INFINITY) top = fmaxf(top, f0);
-          if (f1 < INFINITY) top = fmaxf(top, f1);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) red[it & 1][team][tt >> 5] = top;
-      team_bar(team);
-#pragma unroll
-      for (int i = 0; i < TEAM / 32; ++i) top = fmaxf(top, red[it & 1][team][i]);
-      const int e = kv8_exponent(top);
-      float scale = pow2(e), inv = pow2(-e);
-      if (kv8_scale_ok(held)) {
-        if (held >= scale) {
-          scale = held;
-          inv = 1.0f / held;
-        } else {   // what the block holds already, at the new scale
-          const float f = held * inv;
-#pragma unroll
-          for (int u = 0; u < N; ++u)
-            if (slot0 + u < r) {
-              uint2* w = reinterpret_cast<uint2*>(codes + (slot0 + u) * D);
-              const uint2 old = *w;
-              const float4 lo = from_e4m3x4(old.x), hi = from_e4m3x4(old.y);
-              *w = make_uint2(to_e4m3x4(lo.x * f, lo.y * f, lo.z * f, lo.w * f),
-                              to_e4m3x4(hi.x * f, hi.y * f, hi.z * f, hi.w * f));
-            }
-        }
-      }
-      if (tt == 0) *sp = scale;
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        const int row = slot0 + u - r;
-        if (row < 0 || row >= run.rows) continue;
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpk(y[u][i], f[2 * i], f[2 * i + 1]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = fabsf(f[i]) < INFINITY ? f[i] * inv : NAN;
-        *reinterpret_cast<uint2*>(codes + (slot0 + u) * D) = make_uint2(
-            to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
-      }
-    }
-    tile = next;
+  for (int tile = blockIdx.y * TEAMS + team, it = 0; tile < tiles; tile += step, ++it) {
+    load(tile, x);
+    append_tile<IO, D>(p, w, at, tile, nq, slot0, team, cs, red[it & 1][team], x, true);
   }
+}
+
+// ---- many rows: a ring of tiles -------------------------------------------------
+
+template <int D>
+struct RingCfg {
+  static constexpr uint32_t TILE = KV8_BLOCK * D * 2;
+  static constexpr int STAGES = D == 256 ? 8 : 16;      // even: each stage is one team's
+  static constexpr uint32_t ANGLES = (AppendCfg<D>::ANGLES + 127) / 128 * 128;
+  static constexpr uint32_t SMEM = ANGLES + STAGES * TILE;
+};
+constexpr int RING_THREADS = APPEND_THREADS + 32;
+
+template <typename IO, int D>
+__global__ void __launch_bounds__(RING_THREADS, 2)
+    kv8_append_ring_kernel(const __grid_constant__ GdnKv8AppendArgs p,
+                           const __grid_constant__ CUtensorMap qmap,
+                           const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap) {
+  using C = RingCfg<D>;
+  using namespace gdn::tc;
+  constexpr int N = AppendCfg<D>::N;
+  extern __shared__ __align__(128) unsigned char ring_smem[];
+  __shared__ uint64_t fraction[D / 2];
+  __shared__ float red[2][TEAMS][TEAM / 32];
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  float* cs = reinterpret_cast<float*>(ring_smem);
+  const uint32_t ring = smem_u32(ring_smem) + C::ANGLES;
+  const GdnRopeArgs& a = p.r;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < a.rot_dim / 2; i += RING_THREADS) fraction[i] = turn_fraction(a.inv_freq[i]);
+  if (tid == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], TEAM / 32);
+    }
+    fence_mbar_init();
+  }
+  Run run;
+  if (!find_run<RING_THREADS / 32>(p.cu, p.starts, p.num_seqs, a.n, blockIdx.x, a.d_status, run))
+    return;
+  __syncthreads();
+  const int nq = a.q.data ? a.h_q : 0, tiles = nq + 2 * a.h_kv;
+  bool ok = true;
+  if (warp == APPEND_THREADS / 32) {
+    // ---- loads: a tile per box; rows past the run, and past the end as zeros, come along ----
+    int j = 0;
+    for (; j < tiles; ++j) {
+      const int s = j % C::STAGES;
+      if (j >= C::STAGES) ok = mbar_wait(&empty[s], (j / C::STAGES - 1) & 1, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0 && !(a.withhold && blockIdx.x == 0 && j == 0)) {   // (the test's)
+        mbar_expect_tx(&full[s], C::TILE);
+        const int head = j < nq ? j : j < nq + a.h_kv ? j - nq : j - nq - a.h_kv;
+        tma_box_at(ring + s * C::TILE, j < nq ? &qmap : j < nq + a.h_kv ? &kmap : &vmap, head,
+                   (int)run.t0, &full[s]);
+      }
+      __syncwarp();
+    }
+    // What is in flight lands before this CTA's memory is another's.
+    for (int x = max(j - C::STAGES, 0); x < j; ++x)
+      mbar_wait(&full[x % C::STAGES], (x / C::STAGES) & 1, GRACE_NS);
+    __syncthreads();   // the angles
+  } else {
+    const int team = tid / TEAM, tt = tid % TEAM;
+    const RunPlace w = place_of(p, run);
+    put_angles<IO, D>(a, w, fraction, cs, APPEND_THREADS);
+    asm volatile("bar.sync 3, %0;" ::"n"(APPEND_THREADS) : "memory");
+    const LanePlace<D> at(a);
+    const int slot0 = tt / (D / 8) * N;
+    for (int tile = team, it = 0; tile < tiles; tile += TEAMS, ++it) {
+      const int s = tile % C::STAGES;
+      // (a wait that ran out keeps the barriers' counts: only the stores are left out)
+      if (ok) ok = mbar_wait(&full[s], (tile / C::STAGES) & 1, a.wait_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      const IO* in = reinterpret_cast<const IO*>(ring_smem + C::ANGLES + s * C::TILE) + 8 * at.part;
+      Vec8<IO> x[N];
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const int row = slot0 + u - w.r;
+        if (row >= 0 && row < run.rows)
+          x[u].load(in + row * D);
+        else
+          x[u].w = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&empty[s]);
+      append_tile<IO, D>(p, w, at, tile, nq, slot0, team, cs, red[it & 1][team], x, ok);
+    }
+    __syncthreads();
+  }
+  if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
 }
 
 template <typename IO, int D>
 static cudaError_t launch_append_d(const GdnKv8AppendArgs& a, cudaStream_t s) {
   const int64_t runs = a.cu ? most_runs(a.r.n, a.num_seqs) : a.r.n;
   const int tiles = (a.r.q.data ? a.r.h_q : 0) + 2 * a.r.h_kv;
+  // Whole blocks for the most part, and enough of them for all SMs.
+  if (a.r.n >= 8 * runs && runs >= SMS) {
+    const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn_tensor_map_encoder());
+    if (!enc) return cudaErrorNotSupported;
+    CUtensorMap map[3] = {};
+    const gdn_view* views[3] = {&a.r.q, &a.r.k, &a.r.v};
+    for (int i = 0; i < 3; ++i) {   // rows of a view as (channel, head, token); a box: a tile
+      if (!views[i]->data) continue;
+      const int heads = i ? a.r.h_kv : a.r.h_q;
+      const cuuint64_t dims[3] = {D, (cuuint64_t)heads, (cuuint64_t)a.r.n};
+      // the stride of an axis of extent one is never used: any legal value does
+      const cuuint64_t strides[2] = {heads > 1 ? (cuuint64_t)views[i]->head_stride * 2 : 16,
+                                     (cuuint64_t)views[i]->token_stride * 2};
+      const cuuint32_t box[3] = {D, 1, KV8_BLOCK};
+      const cuuint32_t estr[3] = {1, 1, 1};
+      if (enc(&map[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(views[i]->data), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    }
+    auto kernel = kv8_append_ring_kernel<IO, D>;
+    static int opted_in[64] = {};
+    int dev = 0;
+    cudaError_t e;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !opted_in[dev]) {
+      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)RingCfg<D>::SMEM)) != cudaSuccess)
+        return e;
+      if (dev >= 0 && dev < 64) opted_in[dev] = 1;
+    }
+    kernel<<<(unsigned)runs, RING_THREADS, RingCfg<D>::SMEM, s>>>(a, map[0], map[1], map[2]);
+    return cudaGetLastError();
+  }
   // few runs: their tiles over several CTAs
   const int most = (tiles + TEAMS - 1) / TEAMS;
   int split = 1;
   while (split < most && runs * split < 8 * SMS) ++split;
-  const size_t smem = a.r.rot_dim > 0 ? KV8_BLOCK * (D / 2 * 3) * sizeof(float) : 0;
+  const size_t smem = a.r.rot_dim > 0 ? AppendCfg<D>::ANGLES : 0;
   kv8_append_kernel<IO, D>
       <<<dim3((unsigned)runs, (unsigned)split), APPEND_THREADS, smem, s>>>(a);
   return cudaGetLastError();

@@ -54,6 +54,10 @@ CASES = [   # calls: rows per sequence of each, hq, hkv, d, rot, page, io
     ([[300] + [2] * 20, [1] * 21], 2, 2, 256, 0, 32, "fp16"),
     ([[5] * 300], 2, 1, 64, 16, 16, "bf16"),        # more sequences than a CTA has threads
     ([[700], [900]], 16, 4, 256, 64, 64, "bf16"),
+    # whole blocks enough for the ring of tiles, odd starts behind an earlier call
+    ([[5, 0, 30], [1300, 1111, 202]], 3, 1, 256, 64, 32, "bf16"),
+    ([[2500], [7]], 2, 2, 128, 32, 128, "fp16"),
+    ([[1400, 9, 1300]], 4, 4, 64, 64, 16, "bf16"),
 ]
 
 
