@@ -690,13 +690,27 @@ def make_rope_axes(axis_of_pair) -> gdn_rope_axes:
     return gdn_rope_axes(max(axis, default=0) + 1, (ctypes.c_uint8 * 128)(*axis))
 
 
-class Kv8Cache(NamedTuple):
-    """A paged cache held in 8 bits (see gdn_kv8_cache in include/gdn.h)."""
+class _Kv8Tensors(NamedTuple):
     k: Any             # [num_pages, h_kv, page_size, d] float8_e4m3fn
     v: Any
     k_scale: Any       # [num_pages, h_kv, page_size / 16] fp32
     v_scale: Any
     block_table: Any   # [num_seqs, pages_per_seq] int32
+
+
+class Kv8Cache(_Kv8Tensors):
+    """A paged cache held in 8 bits (see gdn_kv8_cache in include/gdn.h): (k, v, k_scale,
+    v_scale, block_table).  Made once for its tensors, whose shapes and addresses it keeps
+    for the calls (they may be written to, not moved)."""
+
+    def __new__(cls, k, v, k_scale, v_scale, block_table):
+        self = super().__new__(cls, k, v, k_scale, v_scale, block_table)
+        self.handle = (_calls or _attn_calls()).kv8_make(k, v, k_scale, v_scale, block_table)
+        return self
+
+    @classmethod
+    def _make(cls, tensors):
+        return cls(*tensors)
 
 
 def make_kv8_cache(dims, num_pages, block_table) -> Kv8Cache:

@@ -16,7 +16,7 @@
 #include "gdn.h"
 
 static PyObject *s_shape, *s_stride, *s_dtype, *s_data_ptr, *s_numel, *s_is_contiguous, *s_device,
-    *s_get_device, *s_element_size;
+    *s_get_device, *s_element_size, *s_handle;
 static PyObject* io_types[3]; /* by gdn_dtype */
 static PyObject *t_int32, *t_float64, *f_empty, *f_empty_on, *f_stream, *f_device, *c_error,
     *empty_kw;
@@ -489,40 +489,83 @@ static int64_t per_token(const gdn_rope_axes* a) {
   return a && a->count >= 0 && a->count <= GDN_ROPE_MAX_AXES ? a->count : 1;
 }
 
-/* A Kv8Cache: (k, v, k_scale, v_scale, block_table). */
+/* What a Kv8Cache keeps of its tensors, looked at once when it is made. */
+typedef struct {
+  gdn_kv8_cache c;
+  int64_t h_kv, page_size, d, device;
+} kv8_handle;
+
+/* k, v, k_scale, v_scale, block_table -> the handle, as bytes */
+static PyObject* kv8_make(PyObject* self, PyObject* const* t, Py_ssize_t na) {
+  (void)self;
+  kv8_handle h;
+  memset(&h, 0, sizeof(h));
+  host_tensor = odd_tensor = NULL;
+  call_device = -1;
+  if (count(na, 5)) return NULL;
+  int64_t k[4], b[4];
+  const int nk = shape_of(t[0], k);
+  if (nk < 0) return NULL;
+  if (nk != 4 || k[2] % GDN_KV8_BLOCK) {
+    PyErr_Format(PyExc_ValueError, "k must be [num_pages, h_kv, page_size, d], pages of whole blocks of %d",
+                 GDN_KV8_BLOCK);
+    return NULL;
+  }
+  const int nb = shape_of(t[4], b);
+  if (nb < 0) return NULL;
+  if (nb != 2 || b[0] > INT32_MAX || b[1] > INT32_MAX) {
+    PyErr_SetString(PyExc_ValueError, "block_table must be [num_seqs, pages_per_seq]");
+    return NULL;
+  }
+  const int64_t rows = k[0] * k[1] * k[2], scales = rows / GDN_KV8_BLOCK;
+  void *ks, *vs, *table;
+  if (flat(t[0], "k", t_e4m3, rows * k[3], &h.c.k) || flat(t[1], "v", t_e4m3, rows * k[3], &h.c.v) ||
+      flat(t[2], "k_scale", io_types[GDN_FP32], scales, &ks) ||
+      flat(t[3], "v_scale", io_types[GDN_FP32], scales, &vs) ||
+      flat(t[4], "block_table", t_int32, b[0] * b[1], &table))
+    return NULL;
+  if (odd_tensor || (host_tensor && call_device >= 0)) {
+    PyErr_Format(PyExc_ValueError, "a cache's tensors must be on one device");
+    return NULL;
+  }
+  h.c.k_scale = ks;
+  h.c.v_scale = vs;
+  h.c.block_table = table;
+  h.c.num_pages = k[0];
+  h.c.num_seqs = (int32_t)b[0];
+  h.c.pages_per_seq = (int32_t)b[1];
+  h.h_kv = k[1];
+  h.page_size = k[2];
+  h.d = k[3];
+  h.device = call_device;
+  return PyBytes_FromStringAndSize((const char*)&h, sizeof(h));
+}
+
+/* A Kv8Cache, by its handle. */
 static int kv8_of(PyObject* o, const char* name, const gdn_attn_dims* d, gdn_kv8_cache* c) {
-  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) {
+  PyObject* b = PyObject_GetAttr(o, s_handle);
+  if (!b || !PyBytes_Check(b) || PyBytes_GET_SIZE(b) != (Py_ssize_t)sizeof(kv8_handle)) {
+    Py_XDECREF(b);
     PyErr_Format(PyExc_TypeError, "%s must be a Kv8Cache", name);
     return -1;
   }
-  PyObject** t = &PyTuple_GET_ITEM(o, 0);
-  int64_t k[4], b[4];
-  const int nk = shape_of(t[0], k);
-  if (nk < 0) return -1;
-  if (nk != 4 || k[1] != d->h_kv || k[2] != d->page_size || k[3] != d->d) {
+  kv8_handle h;
+  memcpy(&h, PyBytes_AS_STRING(b), sizeof(h));
+  Py_DECREF(b);
+  if (h.h_kv != d->h_kv || h.page_size != d->page_size || h.d != d->d) {
     PyErr_Format(PyExc_ValueError, "%s.k must be [num_pages, %d, %d, %d]", name, d->h_kv,
                  d->page_size, d->d);
     return -1;
   }
-  const int nb = shape_of(t[4], b);
-  if (nb < 0) return -1;
-  if (nb != 2 || b[0] > INT32_MAX || b[1] > INT32_MAX) {
-    PyErr_Format(PyExc_ValueError, "%s.block_table must be [num_seqs, pages_per_seq]", name);
-    return -1;
+  *c = h.c;
+  if (h.device < 0) {
+    if (!host_tensor) host_tensor = name;
+  } else if (call_device < 0) {
+    call_device = h.device;
+  } else if (h.device != call_device && !odd_tensor) {
+    odd_tensor = name;
+    odd_device = h.device;
   }
-  const int64_t rows = k[0] * k[1] * k[2], scales = k[0] * k[1] * (k[2] / GDN_KV8_BLOCK);
-  void *ks, *vs, *table;
-  if (flat(t[0], "k", t_e4m3, rows * k[3], &c->k) || flat(t[1], "v", t_e4m3, rows * k[3], &c->v) ||
-      flat(t[2], "k_scale", io_types[GDN_FP32], scales, &ks) ||
-      flat(t[3], "v_scale", io_types[GDN_FP32], scales, &vs) ||
-      flat(t[4], "block_table", t_int32, b[0] * b[1], &table))
-    return -1;
-  c->k_scale = ks;
-  c->v_scale = vs;
-  c->block_table = table;
-  c->num_pages = k[0];
-  c->num_seqs = (int32_t)b[0];
-  c->pages_per_seq = (int32_t)b[1];
   return 0;
 }
 /* An integer argument that the ABI takes in 32 bits. */
@@ -632,7 +675,7 @@ static PyObject* kv8_gather(PyObject* self, PyObject* const* a, Py_ssize_t na) {
   const int64_t total = PyLong_AsLongLong(a[3]);
   if (total == -1 && PyErr_Occurred()) return NULL;
   const int64_t rows = total > 0 ? total : 0;   /* the library refuses less */
-  PyObject* like = PyTuple_GET_ITEM(a[1], 0);
+  PyObject* like = a[2];
   PyObject *r = NULL, *vo = NULL, *ko = output(a[4], "k_out", dt, rows, d.h_kv, d.d, like, other, &kp);
   if (ko) vo = output(a[5], "v_out", dt, rows, d.h_kv, d.d, like, other, &vp);
   if (vo) {
@@ -756,6 +799,7 @@ static PyMethodDef methods[] = {
     {"attn_prefill", (PyCFunction)(void (*)(void))attn_prefill, METH_FASTCALL, NULL},
     {"attn_decode", (PyCFunction)(void (*)(void))attn_decode, METH_FASTCALL, NULL},
     {"setup_kv8", setup_kv8, METH_VARARGS, NULL},
+    {"kv8_make", (PyCFunction)(void (*)(void))kv8_make, METH_FASTCALL, NULL},
     {"qk_norm_rope_axes", (PyCFunction)(void (*)(void))qk_norm_rope_axes, METH_FASTCALL, NULL},
     {"kv8_append", (PyCFunction)(void (*)(void))kv8_append, METH_FASTCALL, NULL},
     {"kv8_gather", (PyCFunction)(void (*)(void))kv8_gather, METH_FASTCALL, NULL},
@@ -773,7 +817,7 @@ PyMODINIT_FUNC PyInit__attn_calls(void) {
   } names[] = {{&s_shape, "shape"},   {&s_stride, "stride"}, {&s_dtype, "dtype"},
                {&s_data_ptr, "data_ptr"}, {&s_numel, "numel"},   {&s_is_contiguous, "is_contiguous"},
                {&s_device, "device"}, {&s_get_device, "get_device"},
-               {&s_element_size, "element_size"}};
+               {&s_element_size, "element_size"}, {&s_handle, "handle"}};
   for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i)
     if (!(*names[i].at = PyUnicode_InternFromString(names[i].name))) return NULL;
   if (!(empty_kw = Py_BuildValue("(ss)", "dtype", "device"))) return NULL;

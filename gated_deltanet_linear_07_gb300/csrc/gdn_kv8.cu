@@ -521,8 +521,9 @@ static cudaError_t launch_gather_d(const GdnKv8GatherArgs& a, cudaStream_t s) {
 
 // ---- evict ----------------------------------------------------------------------
 
-constexpr int SELECT_THREADS = 512, SELECT_WARPS = SELECT_THREADS / 32;
-constexpr int RADIX = 256;
+constexpr int SELECT_THREADS = 1024, SELECT_WARPS = SELECT_THREADS / 32;
+constexpr int SELECT_BINS = 2 * SELECT_THREADS;   // of eleven bits
+constexpr int SELECT_KEYS = 48 * 1024;            // weights, at most, that stay in shared memory
 
 // A weight's rank as an unsigned number: bits of a float that is not negative.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -539,16 +540,48 @@ __device__ __forceinline__ int64_t evict_len(const GdnKv8EvictArgs& p, int b) {
   return len;
 }
 
-// The places of one sequence and head that are kept.  The m-th largest weight of the
-// middle is found digit by digit, eight bits at a time from the top (a histogram of
-// those that share the digits so far), then one ordered pass writes the places: all
-// above that weight and, of those equal to it, the lowest.
+struct __align__(16) SelectShared {
+  uint32_t hist[SELECT_BINS];
+  int64_t sums[2][SELECT_WARPS];
+  uint32_t digit, above;
+};
+
+// Sum of v over the CTA's threads and, in `before`, over the threads below this one: as
+// block_scan, whose sum over the warps is one thread's work here times 32.  Calls take turns.
+__device__ __forceinline__ int64_t select_scan(int64_t v, SelectShared& sh, int turn, int64_t& before) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) sh.sums[turn & 1][warp] = incl;
+  __syncthreads();
+  const int64_t mine = sh.sums[turn & 1][lane];
+  int64_t sum = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
+  }
+  before = __shfl_sync(0xffffffffu, sum - mine, warp) + incl - v;
+  return __shfl_sync(0xffffffffu, sum, 31);
+}
+static_assert(SELECT_WARPS == 32, "a lane per warp");
+
+// The places of one sequence and head that are kept.  The rank of the last one that the middle
+// keeps is found digit by digit, eleven bits at a time from the top (a histogram of those that
+// share the digits so far: after the first one they are few), then one ordered pass writes the
+// places: all above that rank and, of those equal to it, the lowest.  The ranks stay in shared
+// memory, or are read again for each digit where they do not fit.  A chain of latencies more than
+// anything else, its instructions' own among them: each runs once, so the loops are short
+// and not unrolled (in registers, unrolled: 24 us where this takes SELECT_US).
 __global__ void __launch_bounds__(SELECT_THREADS)
-    kv8_select_kernel(const __grid_constant__ GdnKv8EvictArgs p) {
-  __shared__ uint32_t hist[SELECT_WARPS][RADIX];
-  __shared__ uint32_t s_digit, s_above;
-  __shared__ int64_t sums[SELECT_WARPS];
-  const int tid = threadIdx.x, warp = tid >> 5;
+    kv8_select_kernel(const __grid_constant__ GdnKv8EvictArgs p, int room) {
+  extern __shared__ __align__(16) uint32_t ranks[];   // [room]
+  __shared__ SelectShared sh;
+  const int tid = threadIdx.x;
   const int b = blockIdx.x / p.h_kv, j = blockIdx.x % p.h_kv;
   const int64_t cap = (int64_t)p.from.pages_per_seq << p.page_shift;
   const int64_t cap_to = (int64_t)p.to.pages_per_seq << p.page_shift;
@@ -557,75 +590,97 @@ __global__ void __launch_bounds__(SELECT_THREADS)
   float* w_out = p.weights_out ? p.weights_out + ((int64_t)b * p.h_kv + j) * cap_to : nullptr;
   int32_t* kept = p.kept + ((int64_t)b * p.h_kv + j) * p.keep;
   if (j == 0 && tid == 0) p.new_lens[b] = (int32_t)now;
-  for (int64_t i = now + tid; i < p.keep; i += SELECT_THREADS) kept[i] = -1;
-  if (w_out)
-    for (int64_t i = now + tid; i < cap_to; i += SELECT_THREADS) w_out[i] = 0.f;
   if (len <= p.keep) {
     for (int64_t i = tid; i < len; i += SELECT_THREADS) {
       kept[i] = (int32_t)i;
       if (w_out) w_out[i] = w[i];
     }
-    return;
-  }
-  const int64_t lo = p.first, hi = len - p.last;   // the middle; longer than what it keeps
-  uint32_t want = (uint32_t)(p.keep - p.first - p.last);   // of those that share the digits so far
-  uint32_t prefix = 0;
-  if (want > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < SELECT_WARPS * RADIX; i += SELECT_THREADS) (&hist[0][0])[i] = 0;
-      __syncthreads();
-      for (int64_t i = lo + tid; i < hi; i += SELECT_THREADS) {
-        const uint32_t key = weight_key(w[i]);
-        if (shift == 24 || key >> (shift + 8) == prefix >> (shift + 8))
-          atomicAdd(&hist[warp][key >> shift & (RADIX - 1)], 1u);
-      }
-      __syncthreads();
-      // digits from the top: thread t has digit 255 - t
-      uint32_t count = 0;
-      if (tid < RADIX)
-        for (int v = 0; v < SELECT_WARPS; ++v) count += hist[v][RADIX - 1 - tid];
-      int64_t before;
-      block_scan(count, sums, SELECT_WARPS, before);
-      if (tid < RADIX && before < want && before + count >= want) {
-        s_digit = RADIX - 1 - tid;
-        s_above = (uint32_t)before;
-      }
-      __syncthreads();
-      prefix |= s_digit << shift;
-      want -= s_above;
-      __syncthreads();
-    }
   } else {
-    prefix = 0xffffffffu;   // above every weight
-  }
-  // in order: the counts of the kept ones (upper half) and of those equal to the border
-  int64_t seen = 0;
-  for (int64_t base = 0; base < len; base += SELECT_THREADS) {
-    const int64_t i = base + tid;
-    bool sure = false, tie = false;
-    if (i < len) {
-      const uint32_t key = i >= lo && i < hi ? weight_key(w[i]) : 0;
-      sure = i < lo || i >= hi || key > prefix;
-      tie = !sure && key == prefix;
+    const int64_t lo = p.first, hi = len - p.last;   // the middle; longer than what it keeps
+    const bool here = len <= room;
+    if (here)   // (rows of weights are a multiple of 16 long)
+#pragma unroll 4
+      for (int i = 4 * tid; i < len; i += 4 * SELECT_THREADS) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(w + i));
+        *reinterpret_cast<uint4*>(ranks + i) =
+            make_uint4(weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w));
+      }
+    uint32_t want = (uint32_t)(p.keep - p.first - p.last);   // of those that share the digits so far
+    uint32_t prefix = want > 0 ? 0 : 0xffffffffu;            // (above every weight)
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && want > 0; ++pass) {
+      const int shift = pass == 0 ? 20 : pass == 1 ? 9 : 0, shared = pass == 0 ? 31 : pass == 1 ? 20 : 9;
+      const uint32_t mask = pass < 2 ? 2047 : 511;
+      sh.hist[2 * tid] = sh.hist[2 * tid + 1] = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int64_t i = lo + tid; i < hi; i += SELECT_THREADS) {
+        const uint32_t k = here ? ranks[i] : weight_key(w[i]);
+        if (k >> shared == prefix >> shared) atomicAdd(&sh.hist[k >> shift & mask], 1u);
+      }
+      __syncthreads();
+      // from the top: this thread's two bins
+      const int bin = SELECT_BINS - 2 - 2 * tid;
+      const uint32_t upper = sh.hist[bin + 1], lower = sh.hist[bin];
+      int64_t before;
+      select_scan((int64_t)upper + lower, sh, pass, before);
+      if (before < want && before + upper + lower >= want) {
+        const bool first = before + upper >= want;
+        sh.digit = bin + (first ? 1 : 0);
+        sh.above = (uint32_t)before + (first ? 0 : upper);
+      }
+      __syncthreads();
+      prefix |= sh.digit << shift;
+      want -= sh.above;
     }
-    int64_t before;
-    const int64_t all =
-        block_scan(((int64_t)sure << 32) | (int64_t)tie, sums, SELECT_WARPS, before);
-    before += seen;
-    seen += all;
-    const uint32_t ties = (uint32_t)before;
-    if (sure || (tie && ties < want)) {
-      const int64_t at = (before >> 32) + min(ties, want);
-      kept[at] = (int32_t)i;
-      if (w_out) w_out[at] = w[i];
+    __syncthreads();
+    // in order: the counts of the kept ones (upper half) and of those equal to the border
+    int64_t seen = 0;
+    int turn = 0;
+#pragma unroll 1
+    for (int64_t base = 0; base < len; base += 4 * SELECT_THREADS) {
+      const int64_t i0 = base + 4 * tid;
+      uint32_t state = 0;   // two bits for each of four: 2 kept, 1 if there is room
+      int above = 0, equal = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t i = i0 + e;
+        if (i >= len) continue;
+        const uint32_t k = here ? ranks[i] : weight_key(w[i]);
+        const bool sure = i < lo || i >= hi || (prefix != 0xffffffffu && k > prefix);
+        state |= (sure ? 2u : k == prefix ? 1u : 0u) << 2 * e;
+        above += sure;
+        equal += !sure && k == prefix;
+      }
+      int64_t before;
+      const int64_t all =
+          select_scan(((int64_t)above << 32) | (int64_t)equal, sh, turn++, before);
+      before += seen;
+      seen += all;
+      int64_t at = before >> 32;
+      uint32_t tied = (uint32_t)before;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t c = state >> 2 * e & 3;
+        if (c == 2 || (c == 1 && tied < want)) {
+          const int64_t to = at + min(tied, want);
+          kept[to] = (int32_t)(i0 + e);
+          if (w_out) w_out[to] = w[i0 + e];
+        }
+        at += c == 2;
+        tied += c == 1;
+      }
     }
   }
+  for (int64_t i = now + tid; i < p.keep; i += SELECT_THREADS) kept[i] = -1;
+  if (w_out)
+    for (int64_t i = now + tid; i < cap_to; i += SELECT_THREADS) w_out[i] = 0.f;
 }
 
 constexpr int MOVE_WARPS = 8;
 
 // One warp per (sequence, head, block of the new pages, keys or values): up to 16
-// kept rows from wherever they were.
+// kept rows from wherever they were.  (Keys and values by one look-up: 93 us for 85.)
 template <int D>
 __global__ void __launch_bounds__(32 * MOVE_WARPS)
     kv8_move_kernel(const __grid_constant__ GdnKv8EvictArgs p) {
@@ -723,9 +778,20 @@ cudaError_t gdn_launch_kv8_gather(const GdnKv8GatherArgs& a, int io, cudaStream_
 }
 cudaError_t gdn_launch_kv8_evict(const GdnKv8EvictArgs& a, cudaStream_t s) {
   using namespace gdn::attn;
-  kv8_select_kernel<<<(unsigned)(a.n * a.h_kv), SELECT_THREADS, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  const int64_t cap = (int64_t)a.from.pages_per_seq << a.page_shift;
+  const int room = cap < SELECT_KEYS ? (int)cap : SELECT_KEYS;
+  cudaError_t e;
+  static int opted_in[64] = {};
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !opted_in[dev]) {
+    if ((e = cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  SELECT_KEYS * 4)) != cudaSuccess)
+      return e;
+    if (dev >= 0 && dev < 64) opted_in[dev] = 1;
+  }
+  kv8_select_kernel<<<(unsigned)(a.n * a.h_kv), SELECT_THREADS, (size_t)room * 4, s>>>(a, room);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return a.d == 64 ? launch_move_d<64>(a, s)
                    : a.d == 128 ? launch_move_d<128>(a, s) : launch_move_d<256>(a, s);
 }

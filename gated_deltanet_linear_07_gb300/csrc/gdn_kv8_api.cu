@@ -165,7 +165,8 @@ GDN_EXPORT int gdn_kv8_evict(const gdn_attn_dims* dims, const gdn_kv8_cache* fro
   if (n == 0) return GDN_OK;
   if (!weights || !seq_lens || !new_lens || !kept) return GDN_EINVAL;
   if (weights_out == weights || new_lens == seq_lens) return GDN_EINVAL;
-  // one CTA per (sequence, head), eight warps of 16 rows' keys or values
+  if (!aligned16(weights)) return GDN_EALIGN;
+  // one CTA per (sequence, head); eight warps of 16 rows' keys or values
   const int64_t units = (int64_t)n * dims->h_kv * ((keep + KV8_BLOCK - 1) / KV8_BLOCK) * 2;
   if ((int64_t)n * dims->h_kv > 0x7fffffffLL || units / 8 >= 0x7fffffffLL) return GDN_EUNSUPPORTED;
   GdnKv8EvictArgs a;

@@ -251,6 +251,15 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
     static_assert(N == 4, "positions are read as one int4");
     bool first = true;
     int64_t done = 0;        // this CTA's units so far
+    int32_t axis_next[GDN_ROPE_MAX_AXES] = {};
+    auto axis_ahead = [&](int64_t base) {
+      const int64_t unit = base + (int64_t)(lane / N) * gridDim.x;
+      const int64_t mine = (parts == 1 ? unit : unit / parts) * N + lane % N;
+#pragma unroll
+      for (int x = 0; x < GDN_ROPE_MAX_AXES; ++x)
+        axis_next[x] = x < axes && unit < units && mine < a.n ? a.positions[x * a.n + mine] : 0;
+    };
+    if (axes) axis_ahead(blockIdx.x);
     for (int64_t base = blockIdx.x; base < units && ok; base += (32LL / N) * gridDim.x) {
       int32_t pos = 0;     // of token lane % N of unit lane / N
       int64_t dst = -1;
@@ -261,10 +270,13 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
         if (a.v.data) dst = cache_row(a, mine, pos);
       }
       if (axes) {
+        // this batch's, and the next one's on their way (loaded here they cost every eight units
+        // a memory latency per axis: 16411 tokens of 40 heads of 128 78 us)
         __syncwarp();
-        for (int x = 0; x < axes; ++x)
-          sh.axis_pos[x][lane] = unit < units && mine < a.n ? a.positions[x * a.n + mine] : 0;
+#pragma unroll
+        for (int x = 0; x < GDN_ROPE_MAX_AXES; ++x) sh.axis_pos[x][lane] = axis_next[x];
         __syncwarp();
+        axis_ahead(base + (32LL / N) * gridDim.x);
       }
       for (int k = 0; k < 32 / N && base + (int64_t)k * gridDim.x < units; ++k) {
         if (!(first && k < MANY_STAGES)) {   // those are there already

@@ -41,6 +41,8 @@ CASES = [   # lengths, hkv, d, pages from and to (tokens), keep, first, last, we
     ([200] * 60, 2, 64, 16, 199, 0, 1, "odd"),
     ([48, 50], 2, 256, 16, 47, 47, 0, "any"),
     ([9000, 5000], 1, 64, 64, 4096, 0, 0, "ties"),
+    ([33_000, 49_153, 8192, 8193], 1, 64, 128, 3000, 7, 200, "odd"),   # more than registers hold
+    ([40_000], 1, 64, 128, 1024, 0, 0, "same"),
     ([90], 2, 128, 16, 200, 3, 3, "any"),                 # keeps more than there is
 ]
 
