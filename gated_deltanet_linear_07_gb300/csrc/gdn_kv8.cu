@@ -576,11 +576,13 @@ static_assert(SELECT_WARPS == 32, "a lane per warp");
 // places: all above that rank and, of those equal to it, the lowest.  The ranks stay in shared
 // memory, or are read again for each digit where they do not fit.  A chain of latencies more than
 // anything else, its instructions' own among them: each runs once, so the loops are short
-// and not unrolled (in registers, unrolled: 24 us where this takes SELECT_US).
+// and not unrolled (in registers, unrolled: 24 us where this takes 10, one
+// sequence of 5120).
 __global__ void __launch_bounds__(SELECT_THREADS)
     kv8_select_kernel(const __grid_constant__ GdnKv8EvictArgs p, int room) {
   extern __shared__ __align__(16) uint32_t ranks[];   // [room]
   __shared__ SelectShared sh;
+  pdl_launch();
   const int tid = threadIdx.x;
   const int b = blockIdx.x / p.h_kv, j = blockIdx.x % p.h_kv;
   const int64_t cap = (int64_t)p.from.pages_per_seq << p.page_shift;
@@ -687,6 +689,7 @@ __global__ void __launch_bounds__(32 * MOVE_WARPS)
   constexpr int PARTS = D / 16, PASS = 32 / PARTS, N = KV8_BLOCK / PASS;   // rows of a pass, passes
   const int lane = threadIdx.x & 31;
   const int blocks = (p.keep + KV8_BLOCK - 1) / KV8_BLOCK;
+  pdl_wait();   // the selection's places
   const int64_t unit = (int64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
   if (unit >= (int64_t)p.n * p.h_kv * blocks * 2) return;
   const bool is_v = unit & 1;
@@ -750,8 +753,16 @@ static cudaError_t launch_move_d(const GdnKv8EvictArgs& a, cudaStream_t s) {
   const int64_t units = (int64_t)a.n * a.h_kv * ((a.keep + KV8_BLOCK - 1) / KV8_BLOCK) * 2;
   const int64_t ctas = (units + MOVE_WARPS - 1) / MOVE_WARPS;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kv8_move_kernel<D><<<(unsigned)ctas, 32 * MOVE_WARPS, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};   // (on its way while the selection ends)
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(32 * MOVE_WARPS);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_move_kernel<D>, a);
 }
 
 template <typename IO>

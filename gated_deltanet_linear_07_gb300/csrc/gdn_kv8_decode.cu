@@ -51,8 +51,10 @@ constexpr int K8_MAX_WARPS = 8;          // that consume; two more warps load
 constexpr int K8_MAX_BARS = 8;
 constexpr int K8_FEW_KEYS = 512;         // of a CTA of a cluster, at most
 constexpr int K8_SCALES = 16;            // units whose scales are kept: the stages' and two batches
-// What a unit and the ends of an item cost, as far as the cut goes.
-constexpr int K8_UNIT_COST = 4, K8_ITEM_COST = 3;
+// What a unit and the ends of an item cost, as far as the cut goes: an item about four units
+// (200 rows of 8 heads of 128: 124 us with nothing for the ends, 116 with 3, 106 with 16, 111 with 36; of 4
+// heads of 256: 137, 127, 114, 114).
+constexpr int K8_UNIT_COST = 4, K8_ITEM_COST = 16;
 
 // NT: query heads of an item in eights.
 template <int D, int NT>
