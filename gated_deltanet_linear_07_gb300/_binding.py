@@ -701,7 +701,7 @@ class _Kv8Tensors(NamedTuple):
 class Kv8Cache(_Kv8Tensors):
     """A paged cache held in 8 bits (see gdn_kv8_cache in include/gdn.h): (k, v, k_scale,
     v_scale, block_table).  Made once for its tensors, whose shapes and addresses it keeps
-    for the calls (they may be written to, not moved)."""
+    for the calls (they may be written to, not moved: ValueError)."""
 
     def __new__(cls, k, v, k_scale, v_scale, block_table):
         self = super().__new__(cls, k, v, k_scale, v_scale, block_table)
@@ -711,6 +711,9 @@ class Kv8Cache(_Kv8Tensors):
     @classmethod
     def _make(cls, tensors):
         return cls(*tensors)
+
+    def __reduce__(self):   # a copy's tensors have addresses of their own
+        return Kv8Cache, tuple(self)
 
 
 def make_kv8_cache(dims, num_pages, block_table) -> Kv8Cache:

@@ -552,6 +552,21 @@ static int kv8_of(PyObject* o, const char* name, const gdn_attn_dims* d, gdn_kv8
   kv8_handle h;
   memcpy(&h, PyBytes_AS_STRING(b), sizeof(h));
   Py_DECREF(b);
+  /* its tensors are where they were when it was made */
+  const void* made[5] = {h.c.k, h.c.v, h.c.k_scale, h.c.v_scale, h.c.block_table};
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 5) {
+    PyErr_Format(PyExc_TypeError, "%s must be a Kv8Cache", name);
+    return -1;
+  }
+  for (int i = 0; i < 5; ++i) {
+    void* now;
+    if (address(PyTuple_GET_ITEM(o, i), &now)) return -1;
+    if (now != made[i]) {
+      PyErr_Format(PyExc_ValueError, "%s has a tensor whose memory is another than when it was made",
+                   name);
+      return -1;
+    }
+  }
   if (h.h_kv != d->h_kv || h.page_size != d->page_size || h.d != d->d) {
     PyErr_Format(PyExc_ValueError, "%s.k must be [num_pages, %d, %d, %d]", name, d->h_kv,
                  d->page_size, d->d);

@@ -105,7 +105,7 @@ static int64_t most_runs(int64_t n, int64_t num_seqs) {
 //
 // Two kernels of the same arithmetic: few rows are loaded straight into registers, their tiles
 // spread over CTAs; many go through a ring of tiles that one warp keeps filled by TMA
-// (16,384 tokens of 16 + 4 heads of 256: 117 us with loads into registers).
+// (16,384 tokens of 16 + 4 heads of 256: 88 us, 117 with loads into registers).
 constexpr int TEAM = 128, TEAMS = 2, APPEND_THREADS = TEAM * TEAMS;
 
 __device__ __forceinline__ void team_bar(int team) {

@@ -105,5 +105,5 @@ cudaError_t gdn_launch_kv8_append(const GdnKv8AppendArgs& a, int io, cudaStream_
 cudaError_t gdn_launch_kv8_gather(const GdnKv8GatherArgs& a, int io, cudaStream_t s);
 cudaError_t gdn_launch_kv8_evict(const GdnKv8EvictArgs& a, cudaStream_t s);
 // Slots of partial results that a decode of these heads needs.
-int64_t gdn_kv8_decode_slots(int h_q, int h_kv, int d);
+int64_t gdn_kv8_decode_slots(int h_q, int h_kv);
 cudaError_t gdn_launch_kv8_decode(const GdnKv8DecodeArgs& a, int io, cudaStream_t s);

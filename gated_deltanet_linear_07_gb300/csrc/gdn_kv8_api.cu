@@ -30,7 +30,7 @@ bool scores_ok(const gdn_attn_dims* d, int64_t n, int64_t capacity) {
 struct DecodeWorkspace {
   size_t part_ml, row_ml, scores, size;
   DecodeWorkspace(const gdn_attn_dims* d, int64_t n, int64_t capacity) {
-    const size_t slots = (size_t)gdn_kv8_decode_slots(d->h_q, d->h_kv, d->d);
+    const size_t slots = (size_t)gdn_kv8_decode_slots(d->h_q, d->h_kv);
     part_ml = align_up(slots * d->d * 4);
     row_ml = part_ml + align_up(slots * sizeof(float2));
     scores = row_ml + (capacity > 0 ? align_up((size_t)n * d->h_q * sizeof(float2)) : 0);

@@ -51,7 +51,7 @@ constexpr int K8_MAX_WARPS = 8;          // that consume; two more warps load
 constexpr int K8_MAX_BARS = 8;
 constexpr int K8_FEW_KEYS = 512;         // of a CTA of a cluster, at most
 constexpr int K8_SCALES = 16;            // units whose scales are kept: the stages' and two batches
-// What a unit and the ends of an item cost, as far as the cut goes: an item about four units
+// What a unit and the ends of an item cost, as far as the cut goes: the ends as much as four units
 // (200 rows of 8 heads of 128: 124 us with nothing for the ends, 116 with 3, 106 with 16, 111 with 36; of 4
 // heads of 256: 137, 127, 114, 114).
 constexpr int K8_UNIT_COST = 4, K8_ITEM_COST = 16;
@@ -246,11 +246,7 @@ template <int WARPS>
 __device__ __forceinline__ void k8_consumers_bar() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
+
 template <typename IO, int D, int NT, bool FEW>
 __global__ void __launch_bounds__(K8Cfg<D, NT>::THREADS, K8Cfg<D, NT>::PER_SM)
     kv8_decode_kernel(const __grid_constant__ K8Args p, const __grid_constant__ CUtensorMap kmap,
@@ -370,7 +366,7 @@ __global__ void __launch_bounds__(K8Cfg<D, NT>::THREADS, K8Cfg<D, NT>::PER_SM)
       const bool is_v = warp > W;
       const CUtensorMap* const map = is_v ? &vmap : &kmap;
       const int cb = lane % COLS, r = lane / COLS * p.box_rows;   // of this lane's box of a unit
-      // Pages and scales are looked up for eight units at a time, a lane for each block: pages two
+      // Pages and scales are looked up for BATCH units at a time, a lane for each block: pages two
       // batches ahead, scales, by them, one; and the first ones of the item to come.  What a
       // lane can work out for its block is done there too: from unit to unit this warp is a chain
       // of dependent instructions, and with the rows' coordinates among them it was what
@@ -505,7 +501,7 @@ __global__ void __launch_bounds__(K8Cfg<D, NT>::THREADS, K8Cfg<D, NT>::PER_SM)
           const int row1 = row_at(g, tb + C::BATCH, page1);
           const float scale1 = scale_at(g, tb + C::BATCH, row1);
           page1 = page_at(g, tb + 2 * C::BATCH);
-          // (their places were those of units that are long done with)
+          // (their places were those of the batch before the last: no stage holds one of its units)
           if (early == 0) put_scales(j, scale);
           j += early;
           for (int u = early; u < C::BATCH && tb + u < g.t1; ++u, ++j) {
@@ -1272,11 +1268,10 @@ static cudaError_t launch_decode_d(const GdnKv8DecodeArgs& a, cudaStream_t s) {
 }  // namespace attn
 }  // namespace gdn
 
-int64_t gdn_kv8_decode_slots(int h_q, int h_kv, int d) {
+int64_t gdn_kv8_decode_slots(int h_q, int h_kv) {
   using namespace gdn::attn;
   const int group = h_q / h_kv, most = group <= 8 ? 8 : 16;
   // two cut items per CTA
-  (void)d;
   return 2 * K8Cfg<256, 1>::CTAS * (int64_t)(group < most ? group : most);
 }
 

@@ -128,8 +128,10 @@ typedef enum { GDN_FP32 = 0, GDN_BF16 = 1, GDN_FP16 = 2 } gdn_dtype;
  *   warp of the second pair gives up by itself.  GDN_DEV_WAIT_TIMEOUT is set, and
  *   the output rows of the items those pairs had taken are not written.
  *   gdn_qk_norm_rope and gdn_kv_append alike from 640 tokens on (the rows of the
- *   first CTA's tokens are not written), and gdn_attn_decode (one CTA goes
- *   without a block of keys; the rows that it had a share in are not valid). */
+ *   first CTA's tokens are not written), gdn_kv8_append where many whole blocks go
+ *   in (the first block's rows are not valid, in the cache neither), and
+ *   gdn_attn_decode and gdn_attn_decode_kv8 (one CTA goes without a block of
+ *   keys; the rows that it had a share in, and what their weights receive, are not valid). */
 #define GDN_TEST_WAIT_TIMEOUT 0x4
 /* GDN_BF16_OPERANDS: the tensor-core prefill feeds its MMAs bf16 operands
  *   (8-bit mantissa, the range of fp32) instead of fp16: the bf16 state option
@@ -679,7 +681,8 @@ typedef struct {
  *   starts     [num_seqs] int32 (device): tokens that the sequence holds already.
  *              < 0: its rows are padding (q_out and k_out zeroed, nothing stored)
  *   q_out      [n][h_q][d] IO; k_out [n][h_kv][d] IO or NULL: the packed keys
- *              too, as gdn_qk_norm_rope_axes would leave them
+ *              too, as gdn_qk_norm_rope_axes would leave them.  16-byte aligned;
+ *              each may be its own input where that is contiguous
  * A row whose place its block table row cannot hold sets GDN_DEV_BAD_LENGTH, one whose
  * page is outside [0, num_pages) GDN_DEV_BAD_PAGE; such a row is not stored (its
  * q_out and k_out are written).  A place at a multiple of GDN_KV8_BLOCK starts its
@@ -713,11 +716,12 @@ size_t gdn_attn_decode_kv8_workspace_size(const gdn_attn_dims* dims, int32_t n, 
 /*
  * gdn_attn_decode_kv8 -- gdn_attn_decode over the 8-bit cache: one query token
  * for each of n rows, row b seeing the first seq_lens[b] places of sequence b.
- *   seq_lens, gate, o, workspace  as in gdn_attn_decode
- *   weights    [num_seqs][h_kv][pages_per_seq * page_size] fp32 (device) or NULL: what
- *              each cached token receives is added to it, weights[b][j][p] += the sum
- *              over head j's query heads of the softmax weight of place p (nothing
- *              else of it is touched)
+ *   seq_lens, gate, o, workspace  as in gdn_attn_decode (a row with a page outside
+ *              [0, num_pages): what its weights receive is not valid either)
+ *   weights    [num_seqs][h_kv][pages_per_seq * page_size] fp32 (device, 16-byte
+ *              aligned) or NULL: what each cached token receives is added to it,
+ *              weights[b][j][p] += the sum over head j's query heads of the softmax
+ *              weight of place p (nothing else of it is touched)
  * Scores, softmax statistics, weights and the accumulated output are fp32; a query
  * row is taken in fp16, times a power of two of its own (a bf16 one keeps all its
  * bits but those below 2^-24 of its largest element), and the softmax weights, times
@@ -740,7 +744,7 @@ int gdn_attn_decode_kv8(const gdn_attn_dims* dims, const gdn_view* q, const gdn_
  * their tokens' scales; the old pages are left as they were (a prefix that other
  * sequences share stays theirs) and are the caller's again after the call.
  * A shorter sequence is copied whole.
- *   weights      [from->num_seqs][h_kv][from's pages_per_seq * page_size] fp32
+ *   weights      [from->num_seqs][h_kv][from's pages_per_seq * page_size] fp32, 16-byte aligned
  *   seq_lens     [n] int32 (device), n <= from->num_seqs, to->num_seqs; 0 or less: nothing
  *   to           cache with pages_per_seq * page_size >= keep, none of whose pages
  *                for these sequences may be one that they read
