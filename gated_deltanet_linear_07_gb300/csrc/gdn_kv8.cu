@@ -27,6 +27,26 @@ struct Run {
   int32_t b, rows;
 };
 
+// A sequence's rows of the call and the number of its runs.
+struct SequenceRuns {
+  int64_t c0, len, count;
+  int32_t start;
+  int r;           // the first row's slot in its block
+  __device__ __forceinline__ SequenceRuns(const int32_t* cu, const int32_t* starts, int num_seqs, int b)
+      : c0(0), len(0), count(0), start(0), r(0) {
+    if (b >= num_seqs) return;
+    c0 = cu[b];
+    len = (int64_t)cu[b + 1] - c0;
+    start = starts ? starts[b] : 0;
+    r = start < 0 ? 0 : start % KV8_BLOCK;
+    if (len > 0) count = (r + len + KV8_BLOCK - 1) / KV8_BLOCK;
+  }
+  __device__ __forceinline__ Run run(int b, int64_t i) const {
+    const int64_t i0 = max(i * KV8_BLOCK - r, (int64_t)0), i1 = min(i * KV8_BLOCK - r + KV8_BLOCK, len);
+    return {c0 + i0, start < 0 ? -1 : start + i0, b, (int32_t)(i1 - i0)};
+  }
+};
+
 // Run number `index` of packed sequences, by the whole CTA (WARPS warps); false: there
 // is none, or cu is not a sequence of ends (reported).  starts null: places count from
 // 0.  The runs before it are counted sequence by sequence, in one pass over cu that
@@ -45,24 +65,12 @@ __device__ __forceinline__ bool find_run(const int32_t* cu, const int32_t* start
   int64_t seen = 0;
   for (int base = 0; base < num_seqs; base += 32 * WARPS) {
     const int b = base + threadIdx.x;
-    int64_t c0 = 0, len = 0, count = 0;
-    int32_t start = 0;
-    if (b < num_seqs) {
-      c0 = cu[b];
-      len = (int64_t)cu[b + 1] - c0;
-      start = starts ? starts[b] : 0;
-      bad |= len < 0;
-    }
-    const int r = start < 0 ? 0 : start % KV8_BLOCK;
-    if (len > 0) count = (r + len + KV8_BLOCK - 1) / KV8_BLOCK;
+    const SequenceRuns s(cu, starts, num_seqs, b);
+    bad |= s.len < 0;
     int64_t before;
-    const int64_t all = block_scan(count, sums, WARPS, before);
+    const int64_t all = block_scan(s.count, sums, WARPS, before);
     const int64_t mine = index - seen - before;
-    if (mine >= 0 && mine < count) {
-      const int64_t i0 = max(mine * KV8_BLOCK - r, (int64_t)0);
-      const int64_t i1 = min(mine * KV8_BLOCK - r + KV8_BLOCK, len);
-      found = {c0 + i0, start < 0 ? -1 : start + i0, b, (int32_t)(i1 - i0)};
-    }
+    if (mine >= 0 && mine < s.count) found = s.run(b, mine);
     seen += all;
   }
   if (__syncthreads_or(bad)) {
@@ -71,6 +79,21 @@ __device__ __forceinline__ bool find_run(const int32_t* cu, const int32_t* start
   }
   run = found;
   return run.rows > 0;
+}
+
+// Number of runs; < 0: cu is not a sequence of ends.
+template <int WARPS>
+__device__ __forceinline__ int64_t count_runs(const int32_t* cu, const int32_t* starts, int num_seqs,
+                                              int64_t n, int64_t* sums) {
+  bool bad = cu[0] != 0 || cu[num_seqs] != n;
+  int64_t count = 0, before;
+  for (int b = threadIdx.x; b < num_seqs; b += 32 * WARPS) {
+    const SequenceRuns s(cu, starts, num_seqs, b);
+    bad |= s.len < 0;
+    count += s.count;
+  }
+  count = block_scan(count, sums, WARPS, before);
+  return __syncthreads_or(bad) ? -1 : count;
 }
 
 // Page of a sequence's block that starts at or before `place` (uniform over the
@@ -136,6 +159,23 @@ __device__ __forceinline__ RunPlace place_of(const GdnKv8AppendArgs& p, const Ru
   return w;
 }
 
+// The runs r0 .. r1 into places[0 ..].run, by the whole CTA (cu is known to be sound).
+template <int WARPS>
+__device__ __forceinline__ void find_runs(const int32_t* cu, const int32_t* starts, int num_seqs,
+                                          int64_t r0, int64_t r1, int64_t* sums, RunPlace* places) {
+  int64_t seen = 0;
+  for (int base = 0; base < num_seqs && seen < r1; base += 32 * WARPS) {
+    const int b = base + threadIdx.x;
+    const SequenceRuns s(cu, starts, num_seqs, b);
+    int64_t before;
+    const int64_t all = block_scan(s.count, sums, WARPS, before);
+    const int64_t first = seen + before;
+    for (int64_t i = max(first, r0); i < min(first + s.count, r1); ++i) places[i - r0].run = s.run(b, i - first);
+    seen += all;
+  }
+  __syncthreads();
+}
+
 // The rows' cosines and sines at their slots, by the first `threads` of the CTA.
 template <typename IO, int D>
 __device__ __forceinline__ void put_angles(const GdnRopeArgs& a, const RunPlace& w,
@@ -149,13 +189,23 @@ __device__ __forceinline__ void put_angles(const GdnRopeArgs& a, const RunPlace&
     put_angle<IO, D>(cs + (w.r + u) * AppendCfg<D>::CS, i, pos[u], fraction[i], a.rope_scale);
 }
 
-// One tile's rows x (of slots slot0 ..), normed, rotated and stored; by a team (the block's
+// A lane's weights of the norm that a tile's rows have.
+__device__ __forceinline__ void load_weights(const GdnRopeArgs& a, int tile, int nq, int part,
+                                             float4 (&wt)[2]) {
+  const float* wp = tile < nq ? a.q_norm : tile < nq + a.h_kv ? a.k_norm : nullptr;
+  if (!wp) return;
+  wt[0] = __ldg(reinterpret_cast<const float4*>(wp + 8 * part));
+  wt[1] = __ldg(reinterpret_cast<const float4*>(wp + 8 * part + 4));
+}
+
+// One tile's rows x (of slots slot0 .., others zeros), normed with the weights wt, rotated and stored; by a team (the block's
 // largest value passes through red).  live: false leaves the stores out.
 template <typename IO, int D>
 __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const RunPlace& w,
                                             const LanePlace<D>& at, int tile, int nq, int slot0,
                                             int team, const float* cs, float (&red)[TEAM / 32],
-                                            const Vec8<IO> (&x)[AppendCfg<D>::N], bool live) {
+                                            const float4 (&wt)[2], const Vec8<IO> (&x)[AppendCfg<D>::N],
+                                            bool live) {
   constexpr int N = AppendCfg<D>::N, CS = AppendCfg<D>::CS;
   const GdnRopeArgs& a = p.r;
   const int tt = threadIdx.x % TEAM, lane = threadIdx.x & 31;
@@ -173,13 +223,7 @@ __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const Run
       for (int i = 0; i < 4; ++i) y[u][i] = pk(f[2 * i], f[2 * i + 1]);
     }
   } else {
-    const float* wp = is_q ? a.q_norm : a.k_norm;
-    float4 wt[2] = {};
-    if (wp) {
-      wt[0] = __ldg(reinterpret_cast<const float4*>(wp + 8 * at.part));
-      wt[1] = __ldg(reinterpret_cast<const float4*>(wp + 8 * at.part + 4));
-    }
-    norm_rotate_fp32<IO, D, N>(at, N, wp != nullptr, a.interleaved, a.rot_dim > 0, a.eps, wt,
+    norm_rotate_fp32<IO, D, N>(at, N, (is_q ? a.q_norm : a.k_norm) != nullptr, a.interleaved, a.rot_dim > 0, a.eps, wt,
                                cs + slot0 * CS, x, y);
   }
   // the packed rows
@@ -206,27 +250,41 @@ __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const Run
   unsigned char* codes = reinterpret_cast<unsigned char*>(is_v ? p.cache.v : p.cache.k) +
                          (first + w.block * KV8_BLOCK) * D + 8 * at.part;
   const float held = r > 0 ? *sp : 0.f;
+  // (rows outside the run are zeros; a maximum passes over NaN)
   float top = 0.f;
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
-    const int row = slot0 + u - r;
-    if (row < 0 || row >= run.rows) continue;
+  for (int u = 0; u < N; ++u)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float f0, f1;
       unpk(y[u][i], f0, f1);
-      f0 = fabsf(f0);
-      f1 = fabsf(f1);
-      if (f0 < INFINITY) top = fmaxf(top, f0);
-      if (f1 < INFINITY) top = fmaxf(top, f1);
+      top = max3(top, fabsf(f0), fabsf(f1));
     }
+  auto over_team = [&] {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[tt >> 5] = top;
+    team_bar(team);
+#pragma unroll
+    for (int i = 0; i < TEAM / 32; ++i) top = fmaxf(top, red[i]);
+  };
+  over_team();
+  if (top == INFINITY) {   // an Inf is stored as NaN and has no part in the scale; the whole team
+    top = 0.f;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f0, f1;
+        unpk(y[u][i], f0, f1);
+        f0 = fabsf(f0) == INFINITY ? NAN : f0;
+        f1 = fabsf(f1) == INFINITY ? NAN : f1;
+        y[u][i] = pk(f0, f1);
+        top = max3(top, fabsf(f0), fabsf(f1));
+      }
+    team_bar(team);   // all have read red
+    over_team();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) red[tt >> 5] = top;
-  team_bar(team);
-#pragma unroll
-  for (int i = 0; i < TEAM / 32; ++i) top = fmaxf(top, red[i]);
   if (!live) return;
   const int e = kv8_exponent(top);
   float scale = pow2(e), inv = pow2(-e);
@@ -254,9 +312,7 @@ __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const Run
     if (row < 0 || row >= run.rows) continue;
     float f[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) unpk(y[u][i], f[2 * i], f[2 * i + 1]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fabsf(f[i]) < INFINITY ? f[i] * inv : NAN;
+    for (int i = 0; i < 4; ++i) unpk(mul2(y[u][i], pk(inv, inv)), f[2 * i], f[2 * i + 1]);
     *reinterpret_cast<uint2*>(codes + (slot0 + u) * D) = make_uint2(
         to_e4m3x4(f[0], f[1], f[2], f[3]), to_e4m3x4(f[4], f[5], f[6], f[7]));
   }
@@ -300,8 +356,10 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   };
   Vec8<IO> x[N];
   for (int tile = blockIdx.y * TEAMS + team, it = 0; tile < tiles; tile += step, ++it) {
+    float4 wt[2] = {};
     load(tile, x);
-    append_tile<IO, D>(p, w, at, tile, nq, slot0, team, cs, red[it & 1][team], x, true);
+    load_weights(a, tile, nq, at.part, wt);
+    append_tile<IO, D>(p, w, at, tile, nq, slot0, team, cs, red[it & 1][team], wt, x, true);
   }
 }
 
@@ -313,11 +371,15 @@ struct RingCfg {
   static constexpr int STAGES = D == 256 ? 8 : 16;      // even: each stage is one team's
   static constexpr uint32_t ANGLES = (AppendCfg<D>::ANGLES + 127) / 128 * 128;
   static constexpr uint32_t SMEM = ANGLES + STAGES * TILE;
+  static constexpr int PER_SM = 2, CTAS = SMS * PER_SM;
 };
-constexpr int RING_THREADS = APPEND_THREADS + 32;
+constexpr int RING_THREADS = APPEND_THREADS + 32, RING_WARPS = RING_THREADS / 32;
+constexpr int RING_RUNS = 64;   // that are looked up at a time
 
+// All runs' tiles form one line, which the CTAs share in equal parts: a run is a CTA's from
+// one tile to another.
 template <typename IO, int D>
-__global__ void __launch_bounds__(RING_THREADS, 2)
+__global__ void __launch_bounds__(RING_THREADS, RingCfg<D>::PER_SM)
     kv8_append_ring_kernel(const __grid_constant__ GdnKv8AppendArgs p,
                            const __grid_constant__ CUtensorMap qmap,
                            const __grid_constant__ CUtensorMap kmap,
@@ -329,6 +391,8 @@ __global__ void __launch_bounds__(RING_THREADS, 2)
   __shared__ uint64_t fraction[D / 2];
   __shared__ float red[2][TEAMS][TEAM / 32];
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  __shared__ int64_t sums[RING_WARPS];
+  __shared__ RunPlace places[RING_RUNS];
   float* cs = reinterpret_cast<float*>(ring_smem);
   const uint32_t ring = smem_u32(ring_smem) + C::ANGLES;
   const GdnRopeArgs& a = p.r;
@@ -341,60 +405,84 @@ __global__ void __launch_bounds__(RING_THREADS, 2)
     }
     fence_mbar_init();
   }
-  Run run;
-  if (!find_run<RING_THREADS / 32>(p.cu, p.starts, p.num_seqs, a.n, blockIdx.x, a.d_status, run))
-    return;
-  __syncthreads();
   const int nq = a.q.data ? a.h_q : 0, tiles = nq + 2 * a.h_kv;
+  const int64_t runs = count_runs<RING_WARPS>(p.cu, p.starts, p.num_seqs, a.n, sums);
+  if (runs < 0) {
+    if (blockIdx.x == 0 && tid == 0) set_status(a.d_status, GDN_DEV_BAD_CU_SEQLENS);
+    return;
+  }
+  const int64_t t_end = runs * tiles * (blockIdx.x + 1) / gridDim.x;
   bool ok = true;
-  if (warp == APPEND_THREADS / 32) {
-    // ---- loads: a tile per box; rows past the run, and past the end as zeros, come along ----
-    int j = 0;
-    for (; j < tiles; ++j) {
-      const int s = j % C::STAGES;
-      if (j >= C::STAGES) ok = mbar_wait(&empty[s], (j / C::STAGES - 1) & 1, a.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0 && !(a.withhold && blockIdx.x == 0 && j == 0)) {   // (the test's)
-        mbar_expect_tx(&full[s], C::TILE);
-        const int head = j < nq ? j : j < nq + a.h_kv ? j - nq : j - nq - a.h_kv;
-        tma_box_at(ring + s * C::TILE, j < nq ? &qmap : j < nq + a.h_kv ? &kmap : &vmap, head,
-                   (int)run.t0, &full[s]);
+  int j = 0;   // tiles so far
+  for (int64_t t = runs * tiles * blockIdx.x / gridDim.x; t < t_end;) {
+    const int64_t r0 = t / tiles, r1 = min((t_end + tiles - 1) / tiles, r0 + RING_RUNS);
+    const int64_t stop = min(t_end, r1 * tiles);
+    const int x0 = (int)(t - r0 * tiles), x1 = (int)(stop - r0 * tiles);   // tiles of these runs
+    find_runs<RING_WARPS>(p.cu, p.starts, p.num_seqs, r0, r1, sums, places);
+    if (tid < r1 - r0) places[tid] = place_of(p, places[tid].run);
+    __syncthreads();
+    if (warp == APPEND_THREADS / 32) {
+      // ---- loads: a tile per box; rows past the run, and past the end as zeros, come along ----
+      int tile = x0;
+      const RunPlace* w = places;
+      for (int x = x0; x < x1 && ok; ++x, ++j) {
+        const int s = j % C::STAGES;
+        if (j >= C::STAGES) ok = mbar_wait(&empty[s], (j / C::STAGES - 1) & 1, a.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0 && !(a.withhold && blockIdx.x == 0 && j == 0)) {   // (the test's)
+          mbar_expect_tx(&full[s], C::TILE);
+          const int head = tile < nq ? tile : tile < nq + a.h_kv ? tile - nq : tile - nq - a.h_kv;
+          tma_box_at(ring + s * C::TILE, tile < nq ? &qmap : tile < nq + a.h_kv ? &kmap : &vmap, head,
+                     (int)w->run.t0, &full[s]);
+        }
+        __syncwarp();
+        if (++tile == tiles) {
+          tile = 0;
+          ++w;
+        }
       }
-      __syncwarp();
+    } else {
+      const int team = tid / TEAM, tt = tid % TEAM;
+      const LanePlace<D> at(a);
+      const int slot0 = tt / (D / 8) * N;
+      for (int tile = x0, left = x1, k = 0; left > 0; left -= tiles, tile = 0, ++k) {
+        const RunPlace w = places[k];
+        const int last = min(left, tiles);
+        if (k > 0) asm volatile("bar.sync 3, %0;" ::"n"(APPEND_THREADS) : "memory");   // the run before is done with
+        put_angles<IO, D>(a, w, fraction, cs, APPEND_THREADS);
+        asm volatile("bar.sync 3, %0;" ::"n"(APPEND_THREADS) : "memory");
+        for (; tile < last; ++tile, ++j) {
+          if (j % TEAMS != team) continue;
+          const int s = j % C::STAGES;
+          float4 wt[2] = {};
+          load_weights(a, tile, nq, at.part, wt);
+          // (a wait that ran out keeps the barriers' counts: only the stores are left out)
+          if (ok) ok = mbar_wait(&full[s], (j / C::STAGES) & 1, a.wait_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          const IO* in = reinterpret_cast<const IO*>(ring_smem + C::ANGLES + s * C::TILE) + 8 * at.part;
+          Vec8<IO> v[N];
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            const int row = slot0 + u - w.r;
+            if (row >= 0 && row < w.run.rows)
+              v[u].load(in + row * D);
+            else
+              v[u].w = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(&empty[s]);
+          append_tile<IO, D>(p, w, at, tile, nq, slot0, team, cs, red[j / TEAMS & 1][team], wt, v, ok);
+        }
+      }
     }
-    // What is in flight lands before this CTA's memory is another's.
+    t = stop;
+    __syncthreads();   // the places are free again, the angles too
+  }
+  // What is in flight lands before this CTA's memory is another's.
+  if (warp == APPEND_THREADS / 32)
     for (int x = max(j - C::STAGES, 0); x < j; ++x)
       mbar_wait(&full[x % C::STAGES], (x / C::STAGES) & 1, GRACE_NS);
-    __syncthreads();   // the angles
-  } else {
-    const int team = tid / TEAM, tt = tid % TEAM;
-    const RunPlace w = place_of(p, run);
-    put_angles<IO, D>(a, w, fraction, cs, APPEND_THREADS);
-    asm volatile("bar.sync 3, %0;" ::"n"(APPEND_THREADS) : "memory");
-    const LanePlace<D> at(a);
-    const int slot0 = tt / (D / 8) * N;
-    for (int tile = team, it = 0; tile < tiles; tile += TEAMS, ++it) {
-      const int s = tile % C::STAGES;
-      // (a wait that ran out keeps the barriers' counts: only the stores are left out)
-      if (ok) ok = mbar_wait(&full[s], (tile / C::STAGES) & 1, a.wait_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      const IO* in = reinterpret_cast<const IO*>(ring_smem + C::ANGLES + s * C::TILE) + 8 * at.part;
-      Vec8<IO> x[N];
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        const int row = slot0 + u - w.r;
-        if (row >= 0 && row < run.rows)
-          x[u].load(in + row * D);
-        else
-          x[u].w = make_uint4(0, 0, 0, 0);
-      }
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&empty[s]);
-      append_tile<IO, D>(p, w, at, tile, nq, slot0, team, cs, red[it & 1][team], x, ok);
-    }
-    __syncthreads();
-  }
   if (!ok) set_status(a.d_status, GDN_DEV_WAIT_TIMEOUT);
 }
 
@@ -433,7 +521,8 @@ static cudaError_t launch_append_d(const GdnKv8AppendArgs& a, cudaStream_t s) {
         return e;
       if (dev >= 0 && dev < 64) opted_in[dev] = 1;
     }
-    kernel<<<(unsigned)runs, RING_THREADS, RingCfg<D>::SMEM, s>>>(a, map[0], map[1], map[2]);
+    const unsigned ctas = (unsigned)(runs < RingCfg<D>::CTAS ? runs : RingCfg<D>::CTAS);
+    kernel<<<ctas, RING_THREADS, RingCfg<D>::SMEM, s>>>(a, map[0], map[1], map[2]);
     return cudaGetLastError();
   }
   // few runs: their tiles over several CTAs
