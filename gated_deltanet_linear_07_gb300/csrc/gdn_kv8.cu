@@ -614,9 +614,11 @@ constexpr int SELECT_THREADS = 1024, SELECT_WARPS = SELECT_THREADS / 32;
 constexpr int SELECT_BINS = 2 * SELECT_THREADS;   // of eleven bits
 constexpr int SELECT_KEYS = 48 * 1024;            // weights, at most, that stay in shared memory
 
-// A weight's rank as an unsigned number: bits of a float that is not negative.
-__device__ __forceinline__ uint32_t weight_key(float w) {
-  return __float_as_uint(fmaxf(w, 0.f)) & 0x7fffffffu;   // NaN: 0
+// A weight's rank as an unsigned number from 1 to 2^31: bits of a float that is not negative,
+// and 1.  Places that stay in any case are above all, places past the end below.
+constexpr uint32_t RANK_SURE = 0xffffffffu, RANK_NONE = 0;
+__device__ __forceinline__ uint32_t weight_rank(float w) {
+  return (__float_as_uint(fmaxf(w, 0.f)) & 0x7fffffffu) + 1;   // NaN: as 0
 }
 
 __device__ __forceinline__ int64_t evict_len(const GdnKv8EvictArgs& p, int b) {
@@ -631,43 +633,45 @@ __device__ __forceinline__ int64_t evict_len(const GdnKv8EvictArgs& p, int b) {
 
 struct __align__(16) SelectShared {
   uint32_t hist[SELECT_BINS];
-  int64_t sums[2][SELECT_WARPS];
+  uint64_t sums[SELECT_WARPS];
+  uint32_t sums32[2][SELECT_WARPS];
   uint32_t digit, above;
 };
 
-// Sum of v over the CTA's threads and, in `before`, over the threads below this one: as
-// block_scan, whose sum over the warps is one thread's work here times 32.  Calls take turns.
-__device__ __forceinline__ int64_t select_scan(int64_t v, SelectShared& sh, int turn, int64_t& before) {
+// Sum of v over the threads below this one, as block_scan, whose sum over the warps is one
+// thread's work here times 32.  Calls that follow each other take turns of `sums`.
+template <typename T>
+__device__ __forceinline__ T select_scan(T v, T* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = v;
+  T incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    const T u = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += u;
   }
-  if (lane == 31) sh.sums[turn & 1][warp] = incl;
+  if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  const int64_t mine = sh.sums[turn & 1][lane];
-  int64_t sum = mine;
+  const T mine = sums[lane];
+  T sum = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, sum, o);
+    const T u = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += u;
   }
-  before = __shfl_sync(0xffffffffu, sum - mine, warp) + incl - v;
-  return __shfl_sync(0xffffffffu, sum, 31);
+  return __shfl_sync(0xffffffffu, sum - mine, warp) + incl - v;
 }
 static_assert(SELECT_WARPS == 32, "a lane per warp");
 
 // The places of one sequence and head that are kept.  The rank of the last one that the middle
 // keeps is found digit by digit, eleven bits at a time from the top (a histogram of those that
-// share the digits so far: after the first one they are few), then one ordered pass writes the
-// places: all above that rank and, of those equal to it, the lowest.  The ranks stay in shared
-// memory, or are read again for each digit where they do not fit.  A chain of latencies more than
-// anything else, its instructions' own among them: each runs once, so the loops are short
-// and not unrolled (in registers, unrolled: 24 us where this takes 10, one
-// sequence of 5120).
-__global__ void __launch_bounds__(SELECT_THREADS)
+// share the digits so far), then one ordered pass writes the places: all above that rank and, of
+// those equal to it, the lowest.  The ranks stay in shared memory, or are formed again for each
+// pass where they do not fit.  A chain of latencies and of issue, the instructions' own
+// arrival included: each runs once, so the loops are short, four places at a time
+// and not unrolled (in registers, unrolled: 24 us where this takes 8, one sequence of 5120;
+// with the middle's borders looked at in every pass and the scans of a CTA between them 10, and
+// 19 for 15 of 32 sequences of up to 16384).
+__global__ void __launch_bounds__(SELECT_THREADS, 2)
     kv8_select_kernel(const __grid_constant__ GdnKv8EvictArgs p, int room) {
   extern __shared__ __align__(16) uint32_t ranks[];   // [room]
   __shared__ SelectShared sh;
@@ -676,182 +680,209 @@ __global__ void __launch_bounds__(SELECT_THREADS)
   const int b = blockIdx.x / p.h_kv, j = blockIdx.x % p.h_kv;
   const int64_t cap = (int64_t)p.from.pages_per_seq << p.page_shift;
   const int64_t cap_to = (int64_t)p.to.pages_per_seq << p.page_shift;
-  const int64_t len = evict_len(p, b), now = min(len, (int64_t)p.keep);
+  // (places are counted without a sign: a block table row holds fewer than 2^31 - 65536)
+  const uint32_t len = (uint32_t)evict_len(p, b), now = min(len, (uint32_t)p.keep);
   const float* w = p.weights + ((int64_t)b * p.h_kv + j) * cap;
   float* w_out = p.weights_out ? p.weights_out + ((int64_t)b * p.h_kv + j) * cap_to : nullptr;
   int32_t* kept = p.kept + ((int64_t)b * p.h_kv + j) * p.keep;
   if (j == 0 && tid == 0) p.new_lens[b] = (int32_t)now;
-  if (len <= p.keep) {
-    for (int64_t i = tid; i < len; i += SELECT_THREADS) {
+  if (len <= (uint32_t)p.keep) {
+    for (uint32_t i = tid; i < len; i += SELECT_THREADS) {
       kept[i] = (int32_t)i;
       if (w_out) w_out[i] = w[i];
     }
   } else {
-    const int64_t lo = p.first, hi = len - p.last;   // the middle; longer than what it keeps
-    const bool here = len <= room;
-    if (here)   // (rows of weights are a multiple of 16 long)
-#pragma unroll 4
-      for (int i = 4 * tid; i < len; i += 4 * SELECT_THREADS) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(w + i));
-        *reinterpret_cast<uint4*>(ranks + i) =
-            make_uint4(weight_key(v.x), weight_key(v.y), weight_key(v.z), weight_key(v.w));
-      }
+    const uint32_t lo = p.first, hi = len - p.last;   // the middle; longer than what it keeps
+    const bool here = len <= (uint32_t)room;
+    // of places i .. i + 3, i a multiple of 4 below len (rows of weights are a multiple of 16 long)
+    auto form = [&](uint32_t i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(w + i));
+      const float x[4] = {v.x, v.y, v.z, v.w};
+      uint32_t k[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        k[e] = i + e >= len ? RANK_NONE : i + e < lo || i + e >= hi ? RANK_SURE : weight_rank(x[e]);
+      return make_uint4(k[0], k[1], k[2], k[3]);
+    };
+    if (here)
+#pragma unroll 2
+      for (uint32_t i = 4 * tid; i < len; i += 4 * SELECT_THREADS)
+        *reinterpret_cast<uint4*>(ranks + i) = form(i);
+    auto four = [&](uint32_t i) { return here ? *reinterpret_cast<const uint4*>(ranks + i) : form(i); };
     uint32_t want = (uint32_t)(p.keep - p.first - p.last);   // of those that share the digits so far
-    uint32_t prefix = want > 0 ? 0 : 0xffffffffu;            // (above every weight)
+    uint32_t border = want > 0 ? 0 : RANK_SURE - 1;
 #pragma unroll 1
     for (int pass = 0; pass < 3 && want > 0; ++pass) {
-      const int shift = pass == 0 ? 20 : pass == 1 ? 9 : 0, shared = pass == 0 ? 31 : pass == 1 ? 20 : 9;
-      const uint32_t mask = pass < 2 ? 2047 : 511;
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       sh.hist[2 * tid] = sh.hist[2 * tid + 1] = 0;
       __syncthreads();
 #pragma unroll 1
-      for (int64_t i = lo + tid; i < hi; i += SELECT_THREADS) {
-        const uint32_t k = here ? ranks[i] : weight_key(w[i]);
-        if (k >> shared == prefix >> shared) atomicAdd(&sh.hist[k >> shift & mask], 1u);
+      for (uint32_t i = 4 * tid; i < len; i += 4 * SELECT_THREADS) {
+        const uint4 v = four(i);
+        const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t digits = (k[e] ^ border) >> shift;   // (the border's own are still 0)
+          if (digits >> bits == 0) atomicAdd(&sh.hist[digits], 1u);
+        }
       }
       __syncthreads();
-      // from the top: this thread's two bins
+      // from the top: this thread's two bins (in the first pass those above 1024 are of RANK_SURE)
       const int bin = SELECT_BINS - 2 - 2 * tid;
-      const uint32_t upper = sh.hist[bin + 1], lower = sh.hist[bin];
-      int64_t before;
-      select_scan((int64_t)upper + lower, sh, pass, before);
+      const bool real = pass > 0 || bin <= 1024;
+      const uint32_t upper = real ? sh.hist[bin + 1] : 0, lower = real ? sh.hist[bin] : 0;
+      const uint32_t before = select_scan(upper + lower, sh.sums32[pass & 1]);
       if (before < want && before + upper + lower >= want) {
         const bool first = before + upper >= want;
         sh.digit = bin + (first ? 1 : 0);
-        sh.above = (uint32_t)before + (first ? 0 : upper);
+        sh.above = before + (first ? 0 : upper);
       }
       __syncthreads();
-      prefix |= sh.digit << shift;
+      border |= sh.digit << shift;
       want -= sh.above;
     }
     __syncthreads();
-    // in order: the counts of the kept ones (upper half) and of those equal to the border
-    int64_t seen = 0;
-    int turn = 0;
+    // In order: each warp has a stretch of places.  Of each stretch the numbers of those above
+    // the border (upper half) and of those equal to it, then the places behind what the warps
+    // before have, no warp waiting for another.
+    const int warp = tid >> 5, lane = tid & 31;
+    const uint32_t per = (len + 4 * SELECT_THREADS - 1) / (4 * SELECT_THREADS) * 128;
+    const uint32_t i_first = min(len, warp * per), i_end = min(len, i_first + per);
+    auto count = [&](const uint4& k) {
+      return (uint32_t)((k.x > border) + (k.y > border) + (k.z > border) + (k.w > border)) << 16 |
+             (uint32_t)((k.x == border) + (k.y == border) + (k.z == border) + (k.w == border));
+    };
+    uint64_t mine = 0;
 #pragma unroll 1
-    for (int64_t base = 0; base < len; base += 4 * SELECT_THREADS) {
-      const int64_t i0 = base + 4 * tid;
-      uint32_t state = 0;   // two bits for each of four: 2 kept, 1 if there is room
-      int above = 0, equal = 0;
+    for (uint32_t i = i_first + 4 * lane; i < i_end; i += 128) {
+      const uint32_t c = count(four(i));
+      mine += ((uint64_t)(c >> 16) << 32) | (c & 0xffffu);
+    }
+    uint64_t seen = __shfl_sync(0xffffffffu, select_scan(mine, sh.sums), 0);
+    const bool copy = w_out != nullptr;
+    uint32_t i = i_first + 4 * lane;
+    float4 next = copy && i < i_end ? __ldg(reinterpret_cast<const float4*>(w + i)) : make_float4(0, 0, 0, 0);
+#pragma unroll 1
+    for (uint32_t base = i_first; base < i_end; base += 128, i += 128) {
+      const uint4 v = i < i_end ? four(i) : make_uint4(RANK_NONE, RANK_NONE, RANK_NONE, RANK_NONE);
+      const float x[4] = {next.x, next.y, next.z, next.w};
+      if (copy && i + 128 < i_end) next = __ldg(reinterpret_cast<const float4*>(w + i + 128));
+      const uint32_t k[4] = {v.x, v.y, v.z, v.w}, c = count(v);
+      uint32_t incl = c;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t i = i0 + e;
-        if (i >= len) continue;
-        const uint32_t k = here ? ranks[i] : weight_key(w[i]);
-        const bool sure = i < lo || i >= hi || (prefix != 0xffffffffu && k > prefix);
-        state |= (sure ? 2u : k == prefix ? 1u : 0u) << 2 * e;
-        above += sure;
-        equal += !sure && k == prefix;
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
       }
-      int64_t before;
-      const int64_t all =
-          select_scan(((int64_t)above << 32) | (int64_t)equal, sh, turn++, before);
-      before += seen;
-      seen += all;
-      int64_t at = before >> 32;
-      uint32_t tied = (uint32_t)before;
+      const uint32_t below = incl - c, all = __shfl_sync(0xffffffffu, incl, 31);
+      uint32_t tied = (uint32_t)seen + (below & 0xffffu);
+      uint32_t to = (uint32_t)(seen >> 32) + (below >> 16) + min(tied, want);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t c = state >> 2 * e & 3;
-        if (c == 2 || (c == 1 && tied < want)) {
-          const int64_t to = at + min(tied, want);
-          kept[to] = (int32_t)(i0 + e);
-          if (w_out) w_out[to] = w[i0 + e];
+        if (k[e] > border || (k[e] == border && tied < want)) {
+          kept[to] = (int32_t)(i + e);
+          if (copy) w_out[to] = x[e];
+          ++to;
         }
-        at += c == 2;
-        tied += c == 1;
+        tied += k[e] == border;
       }
+      seen += ((uint64_t)(all >> 16) << 32) | (all & 0xffffu);
     }
   }
-  for (int64_t i = now + tid; i < p.keep; i += SELECT_THREADS) kept[i] = -1;
+  for (uint32_t i = now + tid; i < (uint32_t)p.keep; i += SELECT_THREADS) kept[i] = -1;
   if (w_out)
     for (int64_t i = now + tid; i < cap_to; i += SELECT_THREADS) w_out[i] = 0.f;
 }
 
-constexpr int MOVE_WARPS = 8;
+constexpr int MOVE_WARPS = 8, MOVE_BLOCKS = 16;   // of a CTA, at most
+static_assert(MOVE_BLOCKS * KV8_BLOCK <= 32 * MOVE_WARPS, "a thread per row");
 
-// One warp per (sequence, head, block of the new pages, keys or values): up to 16
-// kept rows from wherever they were.  (Keys and values by one look-up: 93 us for 85.)
+// A CTA has some blocks of the new pages of one sequence and head.  Where their up to 16 kept rows
+// each were is looked up by all threads at once, then a warp moves a block's keys or its values
+// at a time.  (A look-up by each warp for its 16 rows, three dependent latencies for 4 KB: 85 us
+// where this takes 70, 32 sequences of up to 16384 cut to half, 4 heads of 256.)
 template <int D>
-__global__ void __launch_bounds__(32 * MOVE_WARPS)
-    kv8_move_kernel(const __grid_constant__ GdnKv8EvictArgs p) {
+__global__ void __launch_bounds__(32 * MOVE_WARPS, D == 256 ? 4 : 5)
+    kv8_move_kernel(const __grid_constant__ GdnKv8EvictArgs p, int blocks, int across) {
   constexpr int PARTS = D / 16, PASS = 32 / PARTS, N = KV8_BLOCK / PASS;   // rows of a pass, passes
-  const int lane = threadIdx.x & 31;
-  const int blocks = (p.keep + KV8_BLOCK - 1) / KV8_BLOCK;
-  pdl_wait();   // the selection's places
-  const int64_t unit = (int64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
-  if (unit >= (int64_t)p.n * p.h_kv * blocks * 2) return;
-  const bool is_v = unit & 1;
-  const int64_t item = (unit >> 1) / blocks;
-  const int block = (int)((unit >> 1) % blocks);
+  __shared__ int64_t rows[MOVE_BLOCKS * KV8_BLOCK], to_rows[MOVE_BLOCKS];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t item = blockIdx.x / across;
   const int b = (int)(item / p.h_kv), j = (int)(item % p.h_kv);
-  // each of the first 16 lanes looks up one row
-  int64_t row = -1;
-  float scale = 0.f;
-  const int i = block * KV8_BLOCK + lane;
-  if (lane < KV8_BLOCK && i < p.keep) {
-    const int32_t place = p.kept[item * p.keep + i];
+  const int block0 = (int)(blockIdx.x % across) * blocks;
+  pdl_wait();   // the selection's places
+  if (tid < blocks * KV8_BLOCK) {
+    const int64_t i = (int64_t)block0 * KV8_BLOCK + tid;
+    int64_t row = -1;
+    const int32_t place = i < p.keep ? p.kept[item * p.keep + i] : -1;
     if (place >= 0) {
       const int64_t page = page_of(p.from, p.page_shift, b, place, p.d_status);
-      if (page >= 0) {
-        row = ((page * p.h_kv + j) << p.page_shift) + (place & ((1 << p.page_shift) - 1));
-        scale = (is_v ? p.from.v_scale : p.from.k_scale)[row / KV8_BLOCK];
-      }
+      if (page >= 0) row = ((page * p.h_kv + j) << p.page_shift) + (place & ((1 << p.page_shift) - 1));
+    }
+    rows[tid] = row;
+    if (tid % KV8_BLOCK == 0) {   // (a block whose first row is none has none)
+      const int64_t page = place >= 0 ? page_of(p.to, p.page_shift, b, i, p.d_status) : -1;
+      to_rows[tid / KV8_BLOCK] = page < 0 ? -1 : ((page * p.h_kv + j) << p.page_shift) +
+                                                     (i & ((1 << p.page_shift) - 1));
     }
   }
-  if (!__any_sync(0xffffffffu, row >= 0)) return;
-  const int64_t page =
-      page_of(p.to, p.page_shift, b, (int64_t)block * KV8_BLOCK, p.d_status);
-  if (page < 0) return;
-  const int64_t to = ((page * p.h_kv + j) << p.page_shift) +
-                     (block * KV8_BLOCK & ((1 << p.page_shift) - 1));
-  const unsigned char* src = reinterpret_cast<const unsigned char*>(is_v ? p.from.v : p.from.k);
-  unsigned char* dst = reinterpret_cast<unsigned char*>(is_v ? p.to.v : p.to.k) + to * D;
-  uint4 x[N];
+  __syncthreads();
+  for (int unit = tid >> 5; unit < 2 * blocks; unit += MOVE_WARPS) {
+    const bool is_v = unit & 1;
+    const int64_t* const from = rows + (unit >> 1) * KV8_BLOCK;
+    const int64_t to = to_rows[unit >> 1];
+    const int64_t mine = from[lane % KV8_BLOCK];
+    if (to < 0 || !__any_sync(0xffffffffu, mine >= 0)) continue;
+    const unsigned char* src = reinterpret_cast<const unsigned char*>(is_v ? p.from.v : p.from.k);
+    unsigned char* dst = reinterpret_cast<unsigned char*>(is_v ? p.to.v : p.to.k) + to * D;
+    const float scale = mine >= 0 ? (is_v ? p.from.v_scale : p.from.k_scale)[mine / KV8_BLOCK] : 0.f;
+    uint4 x[N];
 #pragma unroll
-  for (int u = 0; u < N; ++u) {
-    const int64_t at = __shfl_sync(0xffffffffu, row, u * PASS + lane / PARTS);
-    if (at >= 0) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + at * D + lane % PARTS * 16));
-  }
-  float top = scale;
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  top = __shfl_sync(0xffffffffu, top, 0);
-  const float ratio = top > 0.f ? scale / top : 1.f;
-#pragma unroll
-  for (int u = 0; u < N; ++u) {
-    const int s = u * PASS + lane / PARTS;
-    const int64_t at = __shfl_sync(0xffffffffu, row, s);
-    const float f = __shfl_sync(0xffffffffu, ratio, s);
-    if (at < 0) continue;
-    if (f != 1.f) {
-      uint32_t* v = reinterpret_cast<uint32_t*>(&x[u]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 y = from_e4m3x4(v[e]);
-        v[e] = to_e4m3x4(y.x * f, y.y * f, y.z * f, y.w * f);
-      }
+    for (int u = 0; u < N; ++u) {
+      const int64_t at = from[u * PASS + lane / PARTS];
+      if (at >= 0) x[u] = __ldcs(reinterpret_cast<const uint4*>(src + at * D + lane % PARTS * 16));
     }
-    *reinterpret_cast<uint4*>(dst + s * D + lane % PARTS * 16) = x[u];
+    float top = scale;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ratio = top > 0.f ? scale / top : 1.f;
+    const bool same = __all_sync(0xffffffffu, ratio == 1.f || mine < 0);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int s = u * PASS + lane / PARTS;
+      if (!same) {
+        const float f = __shfl_sync(0xffffffffu, ratio, s);
+        uint32_t* v = reinterpret_cast<uint32_t*>(&x[u]);
+        if (f != 1.f && from[s] >= 0)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 y = from_e4m3x4(v[e]);
+            v[e] = to_e4m3x4(y.x * f, y.y * f, y.z * f, y.w * f);
+          }
+      }
+      if (from[s] >= 0) *reinterpret_cast<uint4*>(dst + s * D + lane % PARTS * 16) = x[u];
+    }
+    if (lane == 0) (is_v ? p.to.v_scale : p.to.k_scale)[to / KV8_BLOCK] = top;
   }
-  if (lane == 0) (is_v ? p.to.v_scale : p.to.k_scale)[to / KV8_BLOCK] = top;
 }
 
 template <int D>
 static cudaError_t launch_move_d(const GdnKv8EvictArgs& a, cudaStream_t s) {
-  const int64_t units = (int64_t)a.n * a.h_kv * ((a.keep + KV8_BLOCK - 1) / KV8_BLOCK) * 2;
-  const int64_t ctas = (units + MOVE_WARPS - 1) / MOVE_WARPS;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int64_t items = (int64_t)a.n * a.h_kv, all = (a.keep + KV8_BLOCK - 1) / KV8_BLOCK;
+  int blocks = MOVE_BLOCKS;   // fewer where that leaves SMs idle, down to a unit per warp
+  while (blocks > MOVE_WARPS / 2 && items * ((all + blocks - 1) / blocks) < 4 * SMS) blocks /= 2;
+  const int64_t across = (all + blocks - 1) / blocks;
+  if (items * across > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};   // (on its way while the selection ends)
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.gridDim = dim3((unsigned)(items * across));
   cfg.blockDim = dim3(32 * MOVE_WARPS);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_move_kernel<D>, a);
+  return cudaLaunchKernelEx(&cfg, kv8_move_kernel<D>, a, blocks, (int)across);
 }
 
 template <typename IO>
