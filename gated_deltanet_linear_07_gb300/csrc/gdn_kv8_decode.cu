@@ -49,7 +49,9 @@ using namespace gdn::tc;
 constexpr int K8_TILE = 32;              // keys of a warp's tile: two blocks
 constexpr int K8_MAX_WARPS = 8;          // that consume; two more warps load
 constexpr int K8_MAX_BARS = 8;
-constexpr int K8_FEW_KEYS = 512;         // of a CTA of a cluster, at most
+// Keys of a CTA of a cluster, at most (replayed, 16 + 4 heads of 256: 16 sequences of 2048 21 us in
+// clusters, 25 as runs with a merge; one of 4096 13.9 and 14.1, where the two meet).
+constexpr int K8_FEW_KEYS = 512;
 constexpr int K8_SCALES = 16;            // units whose scales are kept: the stages' and two batches
 // What a unit and the ends of an item cost, as far as the cut goes: the ends as much as four units
 // (200 rows of 8 heads of 128: 124 us with nothing for the ends, 116 with 3, 106 with 16, 111 with 36; of 4
