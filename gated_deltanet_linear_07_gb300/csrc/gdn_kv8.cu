@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(APPEND_THREADS)
   __shared__ float red[2][TEAMS][TEAM / 32];      // of every other tile: one barrier per tile
   const GdnRopeArgs& a = p.r;
   const int tid = threadIdx.x, team = tid / TEAM, tt = tid % TEAM;
+  pdl_wait();
   for (int i = tid; i < a.rot_dim / 2; i += APPEND_THREADS) fraction[i] = turn_fraction(a.inv_freq[i]);
   Run run;
   if (!find_run<APPEND_THREADS / 32>(p.cu, p.starts, p.num_seqs, a.n, blockIdx.x, a.d_status, run))
@@ -397,7 +398,6 @@ __global__ void __launch_bounds__(RING_THREADS, RingCfg<D>::PER_SM)
   const uint32_t ring = smem_u32(ring_smem) + C::ANGLES;
   const GdnRopeArgs& a = p.r;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < a.rot_dim / 2; i += RING_THREADS) fraction[i] = turn_fraction(a.inv_freq[i]);
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       mbar_init(&full[i], 1);
@@ -405,6 +405,8 @@ __global__ void __launch_bounds__(RING_THREADS, RingCfg<D>::PER_SM)
     }
     fence_mbar_init();
   }
+  pdl_wait();
+  for (int i = tid; i < a.rot_dim / 2; i += RING_THREADS) fraction[i] = turn_fraction(a.inv_freq[i]);
   const int nq = a.q.data ? a.h_q : 0, tiles = nq + 2 * a.h_kv;
   const int64_t runs = count_runs<RING_WARPS>(p.cu, p.starts, p.num_seqs, a.n, sums);
   if (runs < 0) {
@@ -522,17 +524,15 @@ static cudaError_t launch_append_d(const GdnKv8AppendArgs& a, cudaStream_t s) {
       if (dev >= 0 && dev < 64) opted_in[dev] = 1;
     }
     const unsigned ctas = (unsigned)(runs < RingCfg<D>::CTAS ? runs : RingCfg<D>::CTAS);
-    kernel<<<ctas, RING_THREADS, RingCfg<D>::SMEM, s>>>(a, map[0], map[1], map[2]);
-    return cudaGetLastError();
+    return launch_behind(kernel, dim3(ctas), RING_THREADS, RingCfg<D>::SMEM, s, a, map[0], map[1], map[2]);
   }
   // few runs: their tiles over several CTAs
   const int most = (tiles + TEAMS - 1) / TEAMS;
   int split = 1;
   while (split < most && runs * split < 8 * SMS) ++split;
   const size_t smem = a.r.rot_dim > 0 ? AppendCfg<D>::ANGLES : 0;
-  kv8_append_kernel<IO, D>
-      <<<dim3((unsigned)runs, (unsigned)split), APPEND_THREADS, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_behind(kv8_append_kernel<IO, D>, dim3((unsigned)runs, (unsigned)split), APPEND_THREADS,
+                       smem, s, a);
 }
 
 // ---- gather ---------------------------------------------------------------------
@@ -564,6 +564,7 @@ template <typename IO, int D>
 __global__ void __launch_bounds__(GATHER_THREADS)
     kv8_gather_kernel(const __grid_constant__ GdnKv8GatherArgs p) {
   constexpr int PARTS = D / 16, TILE = KV8_BLOCK * PARTS, UNROLL = 4;
+  pdl_wait();
   Run run;
   if (!find_run<GATHER_THREADS / 32>(p.cu, nullptr, p.num_seqs, p.total, blockIdx.x, p.d_status,
                                      run))
@@ -603,9 +604,8 @@ __global__ void __launch_bounds__(GATHER_THREADS)
 
 template <typename IO, int D>
 static cudaError_t launch_gather_d(const GdnKv8GatherArgs& a, cudaStream_t s) {
-  kv8_gather_kernel<IO, D>
-      <<<(unsigned)most_runs(a.total, a.num_seqs), GATHER_THREADS, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_behind(kv8_gather_kernel<IO, D>, dim3((unsigned)most_runs(a.total, a.num_seqs)),
+                       GATHER_THREADS, 0, s, a);
 }
 
 // ---- evict ----------------------------------------------------------------------
@@ -675,6 +675,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 2)
     kv8_select_kernel(const __grid_constant__ GdnKv8EvictArgs p, int room) {
   extern __shared__ __align__(16) uint32_t ranks[];   // [room]
   __shared__ SelectShared sh;
+  pdl_wait();
   pdl_launch();
   const int tid = threadIdx.x;
   const int b = blockIdx.x / p.h_kv, j = blockIdx.x % p.h_kv;
@@ -873,16 +874,8 @@ static cudaError_t launch_move_d(const GdnKv8EvictArgs& a, cudaStream_t s) {
   while (blocks > MOVE_WARPS / 2 && items * ((all + blocks - 1) / blocks) < 4 * SMS) blocks /= 2;
   const int64_t across = (all + blocks - 1) / blocks;
   if (items * across > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};   // (on its way while the selection ends)
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(items * across));
-  cfg.blockDim = dim3(32 * MOVE_WARPS);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_move_kernel<D>, a, blocks, (int)across);
+  return launch_behind(kv8_move_kernel<D>, dim3((unsigned)(items * across)), 32 * MOVE_WARPS, 0, s, a,
+                       blocks, (int)across);   // (on its way while the selection ends)
 }
 
 template <typename IO>
@@ -921,8 +914,9 @@ cudaError_t gdn_launch_kv8_evict(const GdnKv8EvictArgs& a, cudaStream_t s) {
       return e;
     if (dev >= 0 && dev < 64) opted_in[dev] = 1;
   }
-  kv8_select_kernel<<<(unsigned)(a.n * a.h_kv), SELECT_THREADS, (size_t)room * 4, s>>>(a, room);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch_behind(kv8_select_kernel, dim3((unsigned)(a.n * a.h_kv)), SELECT_THREADS,
+                         (size_t)room * 4, s, a, room)) != cudaSuccess)
+    return e;
   return a.d == 64 ? launch_move_d<64>(a, s)
                    : a.d == 128 ? launch_move_d<128>(a, s) : launch_move_d<256>(a, s);
 }

@@ -275,7 +275,6 @@ __global__ void __launch_bounds__(K8Cfg<D, NT>::THREADS, K8Cfg<D, NT>::PER_SM)
   const int heads = a.h_kv * p.subs;
   const int n = a.n;
 
-  pdl_launch();
   if (tid == 0) {
     for (int s = 0; s < C::BARS; ++s) {
       mbar_init(&sh->full[s], 2);     // keys, values
@@ -287,6 +286,8 @@ __global__ void __launch_bounds__(K8Cfg<D, NT>::THREADS, K8Cfg<D, NT>::PER_SM)
     }
     fence_mbar_init();
   }
+  pdl_wait();
+  pdl_launch();   // (the merge reads seq_lens before it waits: what wrote them is done with here)
   K8Walk walk;
   int64_t w0, w1;
   if (FEW) {
@@ -1123,6 +1124,7 @@ constexpr int RECEIVED_THREADS = 256, RECEIVED_KEYS = 4 * RECEIVED_THREADS;
 
 __global__ void __launch_bounds__(RECEIVED_THREADS)
     kv8_received_kernel(const __grid_constant__ GdnKv8DecodeArgs a, int across) {
+  pdl_wait();
   const int group = a.h_q / a.h_kv;
   const int item = blockIdx.x / across, b = item / a.h_kv, j = item % a.h_kv;
   int64_t len = a.seq_lens[b];
@@ -1213,20 +1215,23 @@ static cudaError_t launch_decode(const GdnKv8DecodeArgs& a, cudaStream_t s) {
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   // Few keys: the block table bounds the sequences' lengths, which are not known here.
   p.cluster = 1;
   const int64_t items = (int64_t)a.n * a.h_kv * p.subs;
   const int64_t units = (a.capacity + C::KEYS - 1) / C::KEYS;
   while (p.cluster < 8 && items * p.cluster * 2 <= C::CTAS && p.cluster < units) p.cluster *= 2;
   if (items * p.cluster <= C::CTAS && a.capacity <= (int64_t)K8_FEW_KEYS * p.cluster) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)p.cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(items * p.cluster));
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     if ((e = cudaLaunchKernelEx(&cfg, few, p, kmap, vmap)) != cudaSuccess) return e;
   } else {
     p.cluster = 0;
@@ -1240,20 +1245,16 @@ static cudaError_t launch_decode(const GdnKv8DecodeArgs& a, cudaStream_t s) {
         p.merge_rows = (p.merge_rows + 1) / 2;
         slices = (p.rows + p.merge_rows - 1) / p.merge_rows;
       }
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)(by_border ? p.ctas - 1 : items * slices));
     cfg.blockDim = dim3(K8_MERGE_THREADS);
     cfg.dynamicSmemBytes = (size_t)k8_most_parts(p) * (8 * p.merge_rows + 4);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, by_border ? border : merge, p)) != cudaSuccess) return e;
   }
   if (!a.weights) return cudaSuccess;
   const int64_t most = (a.capacity + RECEIVED_KEYS - 1) / RECEIVED_KEYS;
   const int across = most < 64 ? (int)most : 64;
-  kv8_received_kernel<<<(unsigned)(a.n * a.h_kv * across), RECEIVED_THREADS, 0, s>>>(a, across);
-  return cudaGetLastError();
+  return launch_behind(kv8_received_kernel, dim3((unsigned)(a.n * a.h_kv * across)), RECEIVED_THREADS, 0,
+                       s, a, across);
 }
 
 // Up to eight query heads of a key/value head: one eight of them; more: two.
