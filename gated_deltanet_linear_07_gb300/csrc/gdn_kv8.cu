@@ -122,21 +122,23 @@ static int64_t most_runs(int64_t n, int64_t num_seqs) {
 // ---- append --------------------------------------------------------------------
 
 // A CTA has one run, of up to 16 rows, and forms its rows' cosines and sines once.  A tile
-// is a run's rows of one head (q, k or v), by a team of TEAM threads: eight channels
+// is a run's rows of one head (q, k or v), by a team of threads: eight channels
 // per lane, D / 8 lanes per row, the rows at their slots of the block, so that what
 // the block held before lies in the lanes of its own slots.
 //
 // Two kernels of the same arithmetic: few rows are loaded straight into registers, their tiles
 // spread over CTAs; many go through a ring of tiles that one warp keeps filled by TMA
-// (16,384 tokens of 16 + 4 heads of 256: 88 us, 117 with loads into registers).
-constexpr int TEAM = 128, TEAMS = 2, APPEND_THREADS = TEAM * TEAMS;
+// (16,384 tokens of 16 + 4 heads of 256: 82 us, 117 with loads into registers).
+constexpr int APPEND_THREADS = 256, FEW_TEAM = 128;
 
+template <int TEAM>
 __device__ __forceinline__ void team_bar(int team) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TEAM) : "memory");
 }
 
-template <int D>
+template <int D, int TEAM>
 struct AppendCfg {
+  static constexpr int TEAMS = APPEND_THREADS / TEAM;
   static constexpr int N = KV8_BLOCK * (D / 8) / TEAM;   // rows of a lane
   static constexpr int CS = D / 2 * 3;                   // a slot's cosines, sines, negated sines
   static constexpr uint32_t ANGLES = KV8_BLOCK * CS * 4;
@@ -186,7 +188,7 @@ __device__ __forceinline__ void put_angles(const GdnRopeArgs& a, const RunPlace&
   if (u0 >= per) return;
   const int32_t* pos = a.positions + (a.axes.count ? a.axes.pair[i] * a.n : 0) + w.run.t0;
   for (int u = u0; u < w.run.rows; u += per)
-    put_angle<IO, D>(cs + (w.r + u) * AppendCfg<D>::CS, i, pos[u], fraction[i], a.rope_scale);
+    put_angle<IO, D>(cs + (w.r + u) * AppendCfg<D, FEW_TEAM>::CS, i, pos[u], fraction[i], a.rope_scale);
 }
 
 // A lane's weights of the norm that a tile's rows have.
@@ -200,13 +202,13 @@ __device__ __forceinline__ void load_weights(const GdnRopeArgs& a, int tile, int
 
 // One tile's rows x (of slots slot0 .., others zeros), normed with the weights wt, rotated and stored; by a team (the block's
 // largest value passes through red).  live: false leaves the stores out.
-template <typename IO, int D>
+template <typename IO, int D, int TEAM>
 __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const RunPlace& w,
                                             const LanePlace<D>& at, int tile, int nq, int slot0,
                                             int team, const float* cs, float (&red)[TEAM / 32],
-                                            const float4 (&wt)[2], const Vec8<IO> (&x)[AppendCfg<D>::N],
+                                            const float4 (&wt)[2], const Vec8<IO> (&x)[AppendCfg<D, TEAM>::N],
                                             bool live) {
-  constexpr int N = AppendCfg<D>::N, CS = AppendCfg<D>::CS;
+  constexpr int N = AppendCfg<D, TEAM>::N, CS = AppendCfg<D, TEAM>::CS;
   const GdnRopeArgs& a = p.r;
   const int tt = threadIdx.x % TEAM, lane = threadIdx.x & 31;
   const Run& run = w.run;
@@ -264,7 +266,7 @@ __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const Run
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) red[tt >> 5] = top;
-    team_bar(team);
+    team_bar<TEAM>(team);
 #pragma unroll
     for (int i = 0; i < TEAM / 32; ++i) top = fmaxf(top, red[i]);
   };
@@ -282,7 +284,7 @@ __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const Run
         y[u][i] = pk(f0, f1);
         top = max3(top, fabsf(f0), fabsf(f1));
       }
-    team_bar(team);   // all have read red
+    team_bar<TEAM>(team);   // all have read red
     over_team();
   }
   if (!live) return;
@@ -321,7 +323,7 @@ __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const Run
 template <typename IO, int D>
 __global__ void __launch_bounds__(APPEND_THREADS)
     kv8_append_kernel(const __grid_constant__ GdnKv8AppendArgs p) {
-  constexpr int N = AppendCfg<D>::N;
+  constexpr int TEAM = FEW_TEAM, N = AppendCfg<D, TEAM>::N, TEAMS = AppendCfg<D, TEAM>::TEAMS;
   extern __shared__ __align__(16) float cs[];     // [slot][cosines, sines, negated sines]
   __shared__ uint64_t fraction[D / 2];
   __shared__ float red[2][TEAMS][TEAM / 32];      // of every other tile: one barrier per tile
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(APPEND_THREADS)
     float4 wt[2] = {};
     load(tile, x);
     load_weights(a, tile, nq, at.part, wt);
-    append_tile<IO, D>(p, w, at, tile, nq, slot0, team, cs, red[it & 1][team], wt, x, true);
+    append_tile<IO, D, TEAM>(p, w, at, tile, nq, slot0, team, cs, red[it & 1][team], wt, x, true);
   }
 }
 
@@ -369,8 +371,12 @@ __global__ void __launch_bounds__(APPEND_THREADS)
 template <int D>
 struct RingCfg {
   static constexpr uint32_t TILE = KV8_BLOCK * D * 2;
-  static constexpr int STAGES = D == 256 ? 8 : 16;      // even: each stage is one team's
-  static constexpr uint32_t ANGLES = (AppendCfg<D>::ANGLES + 127) / 128 * 128;
+  // Four rows a lane: what is done once per tile and lane is as much as a row (16,384 tokens of
+  // 32 + 8 heads of 128: 96 us, 113 with two rows, of 16 + 16 heads of 64 56, 85 with one).
+  static constexpr int TEAM = D / 2;
+  static constexpr int STAGES = D == 256 ? 8 : 16;
+  static_assert(STAGES % (APPEND_THREADS / TEAM) == 0, "each stage is one team's");
+  static constexpr uint32_t ANGLES = (AppendCfg<D, TEAM>::ANGLES + 127) / 128 * 128;
   static constexpr uint32_t SMEM = ANGLES + STAGES * TILE;
   static constexpr int PER_SM = 2, CTAS = SMS * PER_SM;
 };
@@ -387,7 +393,7 @@ __global__ void __launch_bounds__(RING_THREADS, RingCfg<D>::PER_SM)
                            const __grid_constant__ CUtensorMap vmap) {
   using C = RingCfg<D>;
   using namespace gdn::tc;
-  constexpr int N = AppendCfg<D>::N;
+  constexpr int TEAM = C::TEAM, N = AppendCfg<D, TEAM>::N, TEAMS = AppendCfg<D, TEAM>::TEAMS;
   extern __shared__ __align__(128) unsigned char ring_smem[];
   __shared__ uint64_t fraction[D / 2];
   __shared__ float red[2][TEAMS][TEAM / 32];
@@ -451,9 +457,9 @@ __global__ void __launch_bounds__(RING_THREADS, RingCfg<D>::PER_SM)
       for (int tile = x0, left = x1, k = 0; left > 0; left -= tiles, tile = 0, ++k) {
         const RunPlace w = places[k];
         const int last = min(left, tiles);
-        if (k > 0) asm volatile("bar.sync 3, %0;" ::"n"(APPEND_THREADS) : "memory");   // the run before is done with
+        if (k > 0) asm volatile("bar.sync 15, %0;" ::"n"(APPEND_THREADS) : "memory");   // the run before is done with
         put_angles<IO, D>(a, w, fraction, cs, APPEND_THREADS);
-        asm volatile("bar.sync 3, %0;" ::"n"(APPEND_THREADS) : "memory");
+        asm volatile("bar.sync 15, %0;" ::"n"(APPEND_THREADS) : "memory");
         for (; tile < last; ++tile, ++j) {
           if (j % TEAMS != team) continue;
           const int s = j % C::STAGES;
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(RING_THREADS, RingCfg<D>::PER_SM)
           }
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(&empty[s]);
-          append_tile<IO, D>(p, w, at, tile, nq, slot0, team, cs, red[j / TEAMS & 1][team], wt, v, ok);
+          append_tile<IO, D, TEAM>(p, w, at, tile, nq, slot0, team, cs, red[j / TEAMS & 1][team], wt, v, ok);
         }
       }
     }
@@ -527,10 +533,11 @@ static cudaError_t launch_append_d(const GdnKv8AppendArgs& a, cudaStream_t s) {
     return launch_behind(kernel, dim3(ctas), RING_THREADS, RingCfg<D>::SMEM, s, a, map[0], map[1], map[2]);
   }
   // few runs: their tiles over several CTAs
+  constexpr int TEAMS = AppendCfg<D, FEW_TEAM>::TEAMS;
   const int most = (tiles + TEAMS - 1) / TEAMS;
   int split = 1;
   while (split < most && runs * split < 8 * SMS) ++split;
-  const size_t smem = a.r.rot_dim > 0 ? AppendCfg<D>::ANGLES : 0;
+  const size_t smem = a.r.rot_dim > 0 ? AppendCfg<D, FEW_TEAM>::ANGLES : 0;
   return launch_behind(kv8_append_kernel<IO, D>, dim3((unsigned)runs, (unsigned)split), APPEND_THREADS,
                        smem, s, a);
 }
