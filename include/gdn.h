@@ -129,7 +129,7 @@ typedef enum { GDN_FP32 = 0, GDN_BF16 = 1, GDN_FP16 = 2 } gdn_dtype;
  *   the output rows of the items those pairs had taken are not written.
  *   gdn_qk_norm_rope and gdn_kv_append alike from 640 tokens on (the rows of the
  *   first CTA's tokens are not written), gdn_kv8_append where many whole blocks go
- *   in (the first block's rows are not valid, in the cache neither), and
+ *   in (the first CTA's rows are not valid, in the cache neither), and
  *   gdn_attn_decode and gdn_attn_decode_kv8 (one CTA goes without a block of
  *   keys; the rows that it had a share in, and what their weights receive, are not valid). */
 #define GDN_TEST_WAIT_TIMEOUT 0x4
