@@ -188,7 +188,8 @@ __device__ __forceinline__ void put_angles(const GdnRopeArgs& a, const RunPlace&
   if (u0 >= per) return;
   const int32_t* pos = a.positions + (a.axes.count ? a.axes.pair[i] * a.n : 0) + w.run.t0;
   for (int u = u0; u < w.run.rows; u += per)
-    put_angle<IO, D>(cs + (w.r + u) * AppendCfg<D, FEW_TEAM>::CS, i, pos[u], fraction[i], a.rope_scale);
+    put_angle<IO, D>(cs + (w.r + u) * AppendCfg<D, FEW_TEAM>::CS, angle_place<D>(a.interleaved, i), pos[u],
+                     fraction[i], a.rope_scale);
 }
 
 // A lane's weights of the norm that a tile's rows have.

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(FEW_THREADS)
   const int32_t pos = a.positions[t];
   const int64_t dst = a.v.data ? cache_row(a, t, pos) : -1;
   for (int i = threadIdx.x; i < a.rot_dim / 2; i += FEW_THREADS)
-    put_angle<IO, D>(cs, i, a.axes.count ? a.positions[a.axes.pair[i] * a.n + t] : pos,
+    put_angle<IO, D>(cs, angle_place<D>(a.interleaved, i), a.axes.count ? a.positions[a.axes.pair[i] * a.n + t] : pos,
                      turn_fraction(a.inv_freq[i]), a.rope_scale);
   __syncthreads();
   for (; r < per; r += step) {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
       }
       if (axes) {
         // this batch's, and the next one's on their way (16,411 tokens of 40
-        // heads of 128, all pairs rotated: 77.4 us with three axes, 76.8 with one)
+        // heads of 128, all pairs rotated: 64 us with three axes as with one)
         __syncwarp();
 #pragma unroll
         for (int x = 0; x < GDN_ROPE_MAX_AXES; ++x) sh.axis_pos[x][lane] = axis_next[x];
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
         }
         for (int i = lane; i < half; i += 32) {
           const uint64_t f = fraction[i];
+          const int place = angle_place<D>(a.interleaved, i);
           if (axes) {   // this pair's positions, four tokens at a time
             const int4 v = *reinterpret_cast<const int4*>(&sh.axis_pos[axis_of[i]][k * N]);
             p[0] = v.x;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(MANY_THREADS, MANY_PER_SM)
             p[3] = v.w;
           }
 #pragma unroll
-          for (int tt = 0; tt < N; ++tt) put_angle<IO, D>(cs + tt * CS, i, p[tt], f, scale);
+          for (int tt = 0; tt < N; ++tt) put_angle<IO, D>(cs + tt * CS, place, p[tt], f, scale);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.full[s]);
