@@ -373,7 +373,7 @@ template <int D>
 struct RingCfg {
   static constexpr uint32_t TILE = KV8_BLOCK * D * 2;
   // Four rows a lane: what is done once per tile and lane is as much as a row (16,384 tokens of
-  // 32 + 8 heads of 128: 96 us, 113 with two rows, of 16 + 16 heads of 64 56, 85 with one).
+  // 16 + 16 heads of 64: 56 us, 85 with one row a lane).
   static constexpr int TEAM = D / 2;
   static constexpr int STAGES = D == 256 ? 8 : 16;
   static_assert(STAGES % (APPEND_THREADS / TEAM) == 0, "each stage is one team's");
