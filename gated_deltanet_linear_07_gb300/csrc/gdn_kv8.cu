@@ -252,7 +252,7 @@ __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const Run
   float* sp = (is_v ? p.cache.v_scale : p.cache.k_scale) + first / KV8_BLOCK + w.block;
   unsigned char* codes = reinterpret_cast<unsigned char*>(is_v ? p.cache.v : p.cache.k) +
                          (first + w.block * KV8_BLOCK) * D + 8 * at.part;
-  const float held = r > 0 ? *sp : 0.f;
+  const float held = r > 0 ? *sp : -1.f;   // < 0: the block begins here
   // (rows outside the run are zeros; a maximum passes over NaN)
   float top = 0.f;
 #pragma unroll
@@ -295,7 +295,7 @@ __device__ __forceinline__ void append_tile(const GdnKv8AppendArgs& p, const Run
     if (held >= scale) {
       scale = held;
       inv = 1.0f / held;
-    } else {   // what the block holds already, at the new scale
+    } else {   // what the block holds already, at the new scale (zeros, where it stood for zeros)
       const float f = held * inv;
 #pragma unroll
       for (int u = 0; u < N; ++u)

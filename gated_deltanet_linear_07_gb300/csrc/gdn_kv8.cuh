@@ -47,8 +47,9 @@ __device__ __forceinline__ int kv8_exponent(float top) {
   const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
   return min(max(e, KV8_MIN_EXP), KV8_MAX_EXP);
 }
+// A block's scale as the calls take it (0: all that it holds stands for 0).
 __device__ __forceinline__ bool kv8_scale_ok(float s) {
-  return s >= 0x1p-40f && s <= 0x1p40f;
+  return s == 0.f || (s >= 0x1p-40f && s <= 0x1p40f);
 }
 
 }  // namespace attn

@@ -686,8 +686,11 @@ typedef struct {
  * A row whose place its block table row cannot hold sets GDN_DEV_BAD_LENGTH, one whose
  * page is outside [0, num_pages) GDN_DEV_BAD_PAGE; such a row is not stored (its
  * q_out and k_out are written).  A place at a multiple of GDN_KV8_BLOCK starts its
- * block anew; places behind the appended ones are left as they were.  No two
- * sequences of a call may store into one page.
+ * block anew; places behind the appended ones are left as they were.  Where a sequence
+ * goes on inside a block, the block's scale has to be one that gdn_attn_decode_kv8
+ * takes: what it holds under a scale of 0 is stored as zeros (NaN as NaN) beside the
+ * new rows; under anything else it is not valid, and the new rows are stored as
+ * if the block began with them.  No two sequences of a call may store into one page.
  */
 int gdn_kv8_append(const gdn_attn_dims* dims, const gdn_rope_params* params,
                    const gdn_rope_axes* axes, const gdn_view* q, const gdn_view* k,
