@@ -681,13 +681,18 @@ def rope_sections(sections, interleaved=False):
     return out
 
 
-def make_rope_axes(axis_of_pair) -> gdn_rope_axes:
+def make_rope_axes(axis_of_pair, count=None) -> gdn_rope_axes:
     """gdn_rope_axes from the axis of each pair of channels (rot_dim / 2 of them; see
-    rope_sections)."""
+    rope_sections).  count: the axes that positions have, where that is more than
+    the pairs use (None: up to the last one that a pair turns by)."""
     axis = [int(a) for a in axis_of_pair]
     if len(axis) > 128 or any(not 0 <= a < GDN_ROPE_MAX_AXES for a in axis):
         raise ValueError(f"at most 128 pairs, of axes 0 to {GDN_ROPE_MAX_AXES - 1}")
-    return gdn_rope_axes(max(axis, default=0) + 1, (ctypes.c_uint8 * 128)(*axis))
+    used = max(axis, default=0) + 1
+    count = used if count is None else int(count)
+    if not used <= count <= GDN_ROPE_MAX_AXES:
+        raise ValueError(f"count must be {used} (the pairs') to {GDN_ROPE_MAX_AXES}, got {count}")
+    return gdn_rope_axes(count, (ctypes.c_uint8 * 128)(*axis))
 
 
 class _Kv8Tensors(NamedTuple):

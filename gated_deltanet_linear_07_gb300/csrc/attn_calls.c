@@ -605,7 +605,7 @@ static PyObject* qk_norm_rope_axes(PyObject* self, PyObject* const* a, Py_ssize_
   const gdn_rope_axes* ax;
   gdn_view q, k;
   PyObject *dt, *other;
-  int64_t total;
+  int64_t total, rows[4] = {0};
   void *pos, *status, *qp = NULL, *kp = NULL;
   gdn_stream_t s;
   if (count(na, 13) || dims_of(a[0], &d, &dt) || axes_of(a[7], &axes, &ax) ||
@@ -615,7 +615,10 @@ static PyObject* qk_norm_rope_axes(PyObject* self, PyObject* const* a, Py_ssize_
     PyErr_SetString(PyExc_TypeError, "axes must be a gdn_rope_axes");
     return NULL;
   }
-  const int64_t n = per_token(ax) ? total / per_token(ax) : 0;
+  /* as many tokens as q or k has: where the axes are not as many as the positions', those are at fault */
+  PyObject* const some = a[1] != Py_None ? a[1] : a[2];
+  if (some != Py_None && shape_of(some, rows) < 0) return NULL;
+  const int64_t n = some != Py_None ? rows[0] : per_token(ax) ? total / per_token(ax) : 0;
   if (view(a[1], "q", dt, n, d.h_q, d.d, &q) || view(a[2], "k", dt, n, d.h_kv, d.d, &k) ||
       rope_params(a + 3, &d, a[10], &p) ||
       flat(a[6], "positions", t_int32, n * per_token(ax), &pos) ||
