@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 2)
     for (int64_t i = now + tid; i < cap_to; i += SELECT_THREADS) w_out[i] = 0.f;
 }
 
-constexpr int MOVE_WARPS = 8, MOVE_BLOCKS = 16;   // of a CTA, at most
+constexpr int MOVE_WARPS = GdnKv8MoveGrid::WARPS, MOVE_BLOCKS = GdnKv8MoveGrid::BLOCKS;
 static_assert(MOVE_BLOCKS * KV8_BLOCK <= 32 * MOVE_WARPS, "a thread per row");
 
 // A CTA has some blocks of the new pages of one sequence and head.  Where their up to 16 kept rows
@@ -877,13 +877,9 @@ __global__ void __launch_bounds__(32 * MOVE_WARPS, D == 256 ? 4 : 5)
 
 template <int D>
 static cudaError_t launch_move_d(const GdnKv8EvictArgs& a, cudaStream_t s) {
-  const int64_t items = (int64_t)a.n * a.h_kv, all = (a.keep + KV8_BLOCK - 1) / KV8_BLOCK;
-  int blocks = MOVE_BLOCKS;   // fewer where that leaves SMs idle, down to a unit per warp
-  while (blocks > MOVE_WARPS / 2 && items * ((all + blocks - 1) / blocks) < 4 * SMS) blocks /= 2;
-  const int64_t across = (all + blocks - 1) / blocks;
-  if (items * across > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_behind(kv8_move_kernel<D>, dim3((unsigned)(items * across)), 32 * MOVE_WARPS, 0, s, a,
-                       blocks, (int)across);   // (on its way while the selection ends)
+  const GdnKv8MoveGrid grid((int64_t)a.n * a.h_kv, a.keep);
+  return launch_behind(kv8_move_kernel<D>, dim3((unsigned)grid.ctas), 32 * MOVE_WARPS, 0, s, a,
+                       grid.blocks, (int)grid.across);   // (on its way while the selection ends)
 }
 
 template <typename IO>

@@ -84,6 +84,21 @@ struct GdnKv8EvictArgs {
   int32_t n, keep, first, last, h_kv, d, page_shift;
 };
 
+// The eviction's copy: each CTA has `blocks` blocks of the new pages of one sequence and head,
+// `across` CTAs each of these; ctas in all.
+struct GdnKv8MoveGrid {
+  static constexpr int WARPS = 8, BLOCKS = 16;   // of a CTA, at most
+  int blocks;
+  int64_t across, ctas;
+  GdnKv8MoveGrid(int64_t items, int32_t keep) : blocks(BLOCKS) {
+    const int64_t all = ((int64_t)keep + GDN_KV8_BLOCK - 1) / GDN_KV8_BLOCK;
+    // fewer where that leaves SMs idle, down to a unit (a block's keys or values) per warp
+    while (blocks > WARPS / 2 && items * ((all + blocks - 1) / blocks) < 4 * gdn::attn::SMS) blocks /= 2;
+    across = (all + blocks - 1) / blocks;
+    ctas = items * across;
+  }
+};
+
 struct GdnKv8DecodeArgs {
   gdn_view q, gate;
   gdn_kv8_cache cache;

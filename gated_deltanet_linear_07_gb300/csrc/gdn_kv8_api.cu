@@ -166,9 +166,9 @@ GDN_EXPORT int gdn_kv8_evict(const gdn_attn_dims* dims, const gdn_kv8_cache* fro
   if (!weights || !seq_lens || !new_lens || !kept) return GDN_EINVAL;
   if (weights_out == weights || new_lens == seq_lens) return GDN_EINVAL;
   if (!aligned16(weights)) return GDN_EALIGN;
-  // one CTA per (sequence, head); eight warps of 16 rows' keys or values
-  const int64_t units = (int64_t)n * dims->h_kv * ((keep + KV8_BLOCK - 1) / KV8_BLOCK) * 2;
-  if ((int64_t)n * dims->h_kv > 0x7fffffffLL || units / 8 >= 0x7fffffffLL) return GDN_EUNSUPPORTED;
+  // the selection takes a CTA per sequence and head, the copy several: all of both, or nothing is launched
+  const int64_t items = (int64_t)n * dims->h_kv;
+  if (items > 0x7fffffffLL || GdnKv8MoveGrid(items, keep).ctas > 0x7fffffffLL) return GDN_EUNSUPPORTED;
   GdnKv8EvictArgs a;
   memset(&a, 0, sizeof(a));
   a.from = *from;
