@@ -22,8 +22,8 @@
 // contribution s_p + log2 b_p, by which the weights are scaled for the product with v
 // in fp16: blocks of large and small values may follow each other in any order
 // without either leaving fp16's range unless it is negligible beside the other.  Both may
-// lag behind the true maxima by 2^3.9 (M by more), so that they move at the first keys only
-// and no lane asks the others for a maximum in between.
+// lag behind the true maxima by 2^3.9, so that they move at the first keys only and no
+// lane asks the others for a maximum in between.
 //
 // The work is cut by bytes: all units of 32 KB (64 keys of 256, 128 of 128, 256 of 64) of
 // all (sequence, key/value head) items form one line, with a little added for the beginning
@@ -50,7 +50,10 @@ constexpr int K8_TILE = 32;              // keys of a warp's tile: two blocks
 constexpr int K8_MAX_WARPS = 8;          // that consume; two more warps load
 constexpr int K8_MAX_BARS = 8;
 // Keys of a CTA of a cluster, at most (replayed, 16 + 4 heads of 256: 16 sequences of 2048 21 us in
-// clusters, 25 as runs with a merge; one of 4096 13.9 and 14.1, where the two meet).
+// clusters, 25 as runs with a merge; one of 4096 13.9 and 14.1, where the two meet).  The block
+// table's width decides, not the lengths, which the host does not know: a short sequence under a
+// wide table is cut in runs (one of 700 keys under a table of 704 or 4096 places 9.9 us, of 8192 or
+// 131,072 12.1; of 3000 keys 12.8 and 13.9; of 64 keys 9.4 both; 32 + 8 heads of 128, 700 keys 7.9 and 9.6).
 constexpr int K8_FEW_KEYS = 512;
 constexpr int K8_SCALES = 16;            // units whose scales are kept: the stages' and two batches
 // What a unit and the ends of an item cost, as far as the cut goes: the ends as much as four units
@@ -669,7 +672,9 @@ __global__ void __launch_bounds__(K8Cfg<D, NT>::THREADS, K8Cfg<D, NT>::PER_SM)
                     f[e] = ex2(mv[nt][e] - topv);
                     mv[nt][e] = topv;
                   }
-                  // (with a weight of 0 until there is a contribution; far below it, 0 too)
+                  // (a weight of 0 until there is a contribution.  M - M' is 44 at most where the
+                  // largest weights' scales are not 0; else 80 of it are kept, and what is less
+                  // than 2^-76 of the largest weight comes out smaller or as 0.)
                   pf[nt][e] = mv[nt][e] == -INFINITY ? 0.f : ex2(fminf(m[nt][e] - mv[nt][e], 80.f) + UP);
                 }
 #pragma unroll
@@ -1257,7 +1262,9 @@ static cudaError_t launch_decode(const GdnKv8DecodeArgs& a, cudaStream_t s) {
                        s, a, across);
 }
 
-// Up to eight query heads of a key/value head: one eight of them; more: two.
+// Up to eight query heads of a key/value head: one eight of them; more: two (64 sequences of up to
+// 8192, 4 key/value heads of 256, replayed: 96 us with 4 query heads each, 102 with 8, 114 with 12, 118
+// with 16; 8 of 128: 92 with 8, 99 with 12, 100 with 16; 64 of up to 16,384, 4 of 64: 56 with 8, 85 with 16).
 template <typename IO, int D>
 static cudaError_t launch_decode_n(const GdnKv8DecodeArgs& a, cudaStream_t s) {
   return a.h_q / a.h_kv <= 8 ? launch_decode<IO, D, 1>(a, s) : launch_decode<IO, D, 2>(a, s);

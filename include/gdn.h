@@ -729,7 +729,8 @@ size_t gdn_attn_decode_kv8_workspace_size(const gdn_attn_dims* dims, int32_t n, 
  * row is taken in fp16, times a power of two of its own (a bf16 one keeps all its
  * bits but those below 2^-24 of its largest element), and the softmax weights, times
  * the values' scale, are rounded to fp16 for the product with v (relative to each,
- * down to 2^-26 of the row's largest contribution).  The stored numbers
+ * down to 2^-26 of the row's largest contribution, or to 2^-76 of its largest
+ * weight where only places of scale 0 have more).  The stored numbers
  * enter both products as they are.  Scales have to be 0, or finite and from 2^-40
  * to 2^40.  What the cache holds beyond a sequence's length never reaches its output.
  */
@@ -746,7 +747,9 @@ int gdn_attn_decode_kv8(const gdn_attn_dims* dims, const gdn_view* q, const gdn_
  * What is kept is copied to the pages of `to`, whose blocks take the largest of
  * their tokens' scales; the old pages are left as they were (a prefix that other
  * sequences share stays theirs) and are the caller's again after the call.
- * A shorter sequence is copied whole.
+ * A shorter sequence is copied whole.  Of the calls here gdn_attn_decode_kv8 alone adds to
+ * weights, nothing does for a prompt's own attention: places that no decoded
+ * token has weighed yet are equal, and the lowest of them, the oldest tokens, stay.
  *   weights      [from->num_seqs][h_kv][from's pages_per_seq * page_size] fp32, 16-byte aligned
  *   seq_lens     [n] int32 (device), n <= from->num_seqs, to->num_seqs; 0 or less: nothing
  *   to           cache with pages_per_seq * page_size >= keep, none of whose pages

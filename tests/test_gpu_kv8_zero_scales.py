@@ -208,3 +208,34 @@ def test_not_a_number_under_a_scale_of_zero_stays_one(gpu_lib):
             assert torch.isnan(rows[:, 3, 10]).all()
             rows[:, 3, 10] = 0
             assert not rows.any()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("exp", [0, -40, 40])
+@pytest.mark.parametrize("ahead", [1.0, 3.5, 5.0, 6.0, 8.0, 10.0])
+def test_what_places_of_scale_zero_outweigh(gpu_lib, ahead, exp, wide):
+    """Every other block has values of scale 0 and keys whose scores lead by 8 `ahead` (2^11.5 to
+    2^115): what the rest contributes is right down to 2^-76 of the largest weight."""
+    g = torch.Generator().manual_seed(int(ahead))
+    d, page, lens = 64, 16, [64, 16, 41, 32]
+    n, width = len(lens), 4
+    dims = gdn.make_attn_dims(2, 1, d, page_size=page)
+    _, v, ks, vs, _ = _kv8.paged(g, [width * page] * n, 1, d, page, spare=0)
+    k, ks = torch.zeros(n * width, 1, page, d), torch.ones_like(ks)
+    vs = torch.full_like(vs, 2.0 ** exp)
+    leads = torch.tensor([[1, 0, 0, 1], [0, 0, 0, 0], [0, 1, 0, 1], [0, 1, 1, 0]]).flatten() > 0
+    k[leads], vs[leads] = ahead, 0.0
+    table = torch.arange(n * width, dtype=torch.int32).view(n, width)
+    q = torch.ones(n, 2, d).bfloat16()
+    host = (_kv8.codes_of(k), v, ks, vs, table)
+    ref, slack, w, _ = _kv8.decode(q, host, lens, None, _attn.scale_of(d), torch.bfloat16)
+    for b, length in enumerate(lens):
+        codes, _ = _kv8.of_sequence(v, vs, table[b, :-(-length // page)], length, 0)
+        slack[b] += 2.0 ** -76 * float(w[b].max()) * codes.abs().sum(0)
+    if wide:
+        table = torch.cat([table, torch.full((n, 1020), -1, dtype=torch.int32)], 1)
+    cache = gdn.Kv8Cache(*(x.cuda() for x in (*host[:4], table)))
+    ws = torch.empty(gdn.gdn_attn_decode_kv8_workspace_size(dims, n), dtype=torch.uint8, device="cuda")
+    o = gdn.gdn_attn_decode_kv8(dims, q.cuda(), cache, _ints(lens), ws)
+    torch.cuda.synchronize()
+    _attn.check(o, ref, slack, torch.bfloat16, "o")
