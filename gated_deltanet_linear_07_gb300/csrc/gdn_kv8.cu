@@ -121,7 +121,8 @@ static int64_t most_runs(int64_t n, int64_t num_seqs) {
 
 // ---- append --------------------------------------------------------------------
 
-// A CTA has one run, of up to 16 rows, and forms its rows' cosines and sines once.  A tile
+// A CTA has one run at a time, of up to 16 rows, and forms its rows' cosines and sines once for all
+// the heads that it has of them (all, or a share where runs are few).  A tile
 // is a run's rows of one head (q, k or v), by a team of threads: eight channels
 // per lane, D / 8 lanes per row, the rows at their slots of the block, so that what
 // the block held before lies in the lanes of its own slots.
@@ -499,7 +500,10 @@ template <typename IO, int D>
 static cudaError_t launch_append_d(const GdnKv8AppendArgs& a, cudaStream_t s) {
   const int64_t runs = a.cu ? most_runs(a.r.n, a.num_seqs) : a.r.n;
   const int tiles = (a.r.q.data ? a.r.h_q : 0) + 2 * a.r.h_kv;
-  // Whole blocks for the most part, and enough of them for all SMs.
+  // Whole blocks for the most part, and enough of them for all SMs.  (Replayed, one sequence, 64 channels
+  // rotated, registers and ring: 2400 tokens of 16 + 4 heads of 256 22 and 24 us, 2600 22 and 29, 4000 30
+  // and 30, 8000 52 and 46; 32 + 8 of 128 22 and 26, 26 and 31, 35 and 32, 57 and 48; 16 + 16 of 64 15 and
+  // 17, 20 and 21, 29 and 22, 47 and 32.  They meet at 4000, 3500 and 2700 tokens, above this border.)
   if (a.r.n >= 8 * runs && runs >= SMS) {
     const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn_tensor_map_encoder());
     if (!enc) return cudaErrorNotSupported;
