@@ -671,9 +671,9 @@ typedef struct {
 /*
  * gdn_kv8_append -- norm and rotate q and k as gdn_qk_norm_rope (axes null) or
  * gdn_qk_norm_rope_axes does, and store k and v in the cache (from fp32, rounded
- * once).  Sequence b of the call, 0 <= b < num_seqs <= cache->num_seqs, has the
- * rows cu_seqlens[b] .. cu_seqlens[b+1], which go to its places starts[b],
- * starts[b] + 1, ...
+ * once; a key's fp32 has the 16-bit types' cosine and sine, within 2^-20.5).
+ * Sequence b of the call, 0 <= b < num_seqs <= cache->num_seqs, has the rows
+ * cu_seqlens[b] .. cu_seqlens[b+1], which go to its places starts[b], starts[b] + 1, ...
  *   positions  [axes' count, or 1][n] int32 (device): for the rotation alone
  *   cu_seqlens [num_seqs+1] int32 (device): 0 = cu[0] <= cu[1] <= ... = n, else
  *              GDN_DEV_BAD_CU_SEQLENS and nothing is written.  NULL: row t is
